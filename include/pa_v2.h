@@ -79,6 +79,9 @@ typedef enum pa_dtype { PA_F32 = 0, PA_F16 = 1, PA_BF16 = 2 } pa_dtype;
 #define PA_DEVICE_BAD_INDPTR    0x8  /* o_indptr decreasing or outside [0, num_partials] */
 #define PA_DEVICE_WAIT_TIMEOUT  0x10 /* a bounded wait (staged K/V, a tensor-memory kernel role) gave up */
 #define PA_DEVICE_BAD_BLOCK     0x20 /* a selected block id outside the scored range */
+#define PA_DEVICE_BAD_LENGTH    0x40 /* a request's lengths are negative or pass a capacity */
+#define PA_DEVICE_NO_PAGES      0x80 /* the free list ran out of pages */
+#define PA_DEVICE_BAD_TREE      0x100 /* a drafted token's parent, or a tree's size, out of range */
 
 /* Largest chunk count of any plan: the 65535 grid-z bound of the pages'
  * launch shape (PR #984, What changed 4), kept as a plan invariant. */
@@ -603,6 +606,136 @@ pa_status pa_v2_decode_noalloc(const pa_v2_plan_t* plan, const float* q, const v
                                const int32_t* last_page_len, const int32_t* first_page_offset,
                                const int32_t* request_indices, const int32_t* kv_tile_indices,
                                const int32_t* o_indptr, float sm_scale, float* out, float* lse2_out,
+                               int32_t* status, void* cuda_stream);
+
+/* ---- one step of several new tokens per request (speculative decoding) ----
+ *
+ * Three calls make the step around the cache: pa_v2_build_tables (page table,
+ * slots, positions and tree masks from the requests' lengths, on the device),
+ * pa_v2_qk_rope_append (per-head norm and rotation of q and k, k and v into the
+ * pools) and pa_v2_tree_attention (the new tokens over their cached pages).
+ * The tables also feed the single-token decode calls above.  Nothing is read
+ * back, so a step can be captured into a CUDA graph and replayed while the
+ * lengths change.  Inference only: none of them has a backward pass.
+ *
+ * pa_v2_build_tables: request r has cached_lens[r] tokens in the cache and
+ * appends new_lens[r].  With c, n those lengths, s = page_size, t = c + n:
+ *  - Pages.  The request's physical pages are block_table[r, 0 .. ceil(t/s)),
+ *    a row of table_width int32.  With a free list, entries from ceil(c/s) on
+ *    are taken from it, requests in order (request r's first new page is
+ *    free_pages[sum of the pages earlier requests take]), and written into
+ *    block_table; with free_pages null every entry is the caller's already.
+ *    pages_needed[0] receives the number of pages the step takes.
+ *  - Page table.  The visible window is the last min(t, window) tokens (all of
+ *    them when window is 0): indices[indptr[r] ..) lists its pages,
+ *    first_page_offset[r] is the entry it starts at, last_page_len[r] the
+ *    entries used of its last page, as the decode calls read them.  A request
+ *    with t = 0 has no page.
+ *  - Tokens.  The new tokens are packed request by request, qo_indptr[batch+1]
+ *    their prefix sums.  Token i of request r goes to pool row slots[] =
+ *    block_table[r, (c + i) / s] * s + (c + i) % s.  Without `parents` the new
+ *    tokens are a chain: positions[] = c + i.  With it they are a tree:
+ *    parents[] (packed like the tokens) is the index, within the request, of an
+ *    earlier new token, or -1 for a root; positions[] = c + depth.  tree_mask
+ *    (nullable) [token_capacity, mask_words] receives each token's visible new
+ *    tokens, bit j % 32 of word j / 32 for token j: its ancestors and itself
+ *    (a chain: every token up to itself).
+ *  - Padding.  slots / positions behind the last token are set to -1 / 0
+ *    (pa_v2_qk_rope_append skips such tokens); indices and tree_mask rows
+ *    behind the last are left as they were.
+ * The lengths are read, not advanced: the same call again gives the same
+ * result.  DEVICE pointers; indices [index_capacity], slots and positions (and
+ * parents) [token_capacity].  Bad data is recorded in `status` and contained:
+ * negative lengths count as 0 and a request that needs more pages than
+ * table_width gets no page and slots -1 (PA_DEVICE_BAD_LENGTH); pages or tokens
+ * past a capacity are not written (the same bit); a page the free list does not
+ * have is -1 (PA_DEVICE_NO_PAGES), as are the slots on it; a parent outside
+ * [-1, i) makes token i a root, and a tree of more than 32 * mask_words tokens
+ * loses the bits that do not fit (PA_DEVICE_BAD_TREE).
+ * PA_EINVAL: null pointers, negative sizes, page_size < 1, window < 0,
+ * mask_words < 1 with a tree_mask.  PA_EUNSUPPORTED: batch above
+ * PA_V2_MAX_TABLE_BATCH, batch * table_width or token_capacity * mask_words
+ * above INT32_MAX, index_capacity or token_capacity above INT32_MAX. */
+#define PA_V2_MAX_TABLE_BATCH 16384
+pa_status pa_v2_build_tables(const int32_t* cached_lens, const int32_t* new_lens, int32_t batch,
+                             int32_t* block_table, int32_t table_width, const int32_t* free_pages,
+                             int32_t num_free, const int32_t* parents, int32_t page_size, int32_t window,
+                             int32_t* indptr, int32_t* indices, int64_t index_capacity, int32_t* last_page_len,
+                             int32_t* first_page_offset, int32_t* qo_indptr, int32_t* slots, int32_t* positions,
+                             int64_t token_capacity, int32_t* tree_mask, int32_t mask_words,
+                             int32_t* pages_needed, int32_t* status, void* cuda_stream);
+
+/* pa_v2_qk_rope_append: what stands between the projections and the attention,
+ * in one pass.  For every token t with slots[t] >= 0 and every head:
+ *  - norm (q when q_weight is given, k when k_weight is): x <- x * w /
+ *    sqrt(mean(x^2) + eps) over the head's head_dim elements;
+ *  - rotation by position: with angle a_j = positions[t] * inv_freq[j],
+ *    j < rot_dim / 2, the pair (x_j, x_{j + rot_dim/2}) -- interleaved: (x_2j,
+ *    x_2j+1) -- becomes (x cos a - y sin a, y cos a + x sin a); elements from
+ *    rot_dim on are not rotated.  Angles are reduced in 64 bits, so far
+ *    positions keep f32 accuracy; norm and rotation run in f32 and each result
+ *    is rounded once;
+ *  - q -> q_out[t]; k and v -> row slots[t] of k_pool and v_pool (v unchanged).
+ * A token with a negative slot is padding: nothing of it is read or written.
+ * A slot at or past num_pages * page_size is skipped like one and recorded as
+ * PA_DEVICE_BAD_SLOT.  Slots must be distinct; q_out must not overlap an input.
+ *   q [num_tokens, num_qo_heads, head_dim], k / v [num_tokens, num_kv_heads,
+ *     head_dim] of `dtype` (f32, f16, bf16: also the pools'), rows of a token
+ *     contiguous, tokens q_stride / k_stride / v_stride elements apart (views of
+ *     one packed projection output);
+ *   q_out contiguous, of q_dtype: `dtype`, or PA_F32 (what the decode calls read);
+ *   q_weight, k_weight [head_dim] of `dtype`, or null; inv_freq [rot_dim / 2] f32;
+ *   positions, slots [num_tokens] int32.
+ * head_dim 64 or 128; rot_dim a multiple of 16 up to head_dim, or 0 (no
+ * rotation).  Pointers and token strides 16-byte aligned (PA_EINVAL).
+ * DEVICE pointers; PA_EUNSUPPORTED for other dims or dtypes, and for pools of
+ * 2^31 rows or more. */
+pa_status pa_v2_qk_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, int32_t dtype, int32_t num_tokens, int32_t num_qo_heads,
+                               int32_t num_kv_heads, int32_t head_dim, const int32_t* positions,
+                               const int32_t* slots, const float* inv_freq, int32_t rot_dim, int32_t interleaved,
+                               const void* q_weight, const void* k_weight, float eps, void* q_out,
+                               int32_t q_dtype, void* k_pool, void* v_pool, int64_t num_pages, int32_t page_size,
+                               int32_t* status, void* cuda_stream);
+
+/* pa_v2_tree_attention: attention of several query tokens per request over the
+ * paged cache.  Request r's page table lists L_r visible tokens (the geometry
+ * of the decode calls); the last n_r = qo_indptr[r+1] - qo_indptr[r] of them
+ * are its new tokens, whose K and V are already in the pools.  Query token i of
+ * the request sees the L_r - n_r tokens before them, and new token j when bit
+ * j % 32 of word j / 32 of its tree_mask row is set (tree_mask null: a chain, j
+ * <= i).  With s the scaled scores over what it sees,
+ *   out = sum softmax(s) v,   lse2 = log2(sum exp(s));
+ * a token that sees nothing gets zeros and -inf.  Values behind a cleared bit or
+ * outside the visible rows never reach a result, NaN and infinities included.
+ *   q, out [num_tokens, num_qo_heads, head_dim] of kv_dtype (f16 or bf16;
+ *     16-byte aligned), lse2_out [num_tokens, num_qo_heads] f32;
+ *   tree_mask [num_tokens, mask_words] int32, mask_words <= PA_V2_MAX_MASK_WORDS;
+ *   qo_indptr [batch + 1] int32; rows of out / lse2_out at or past
+ *     qo_indptr[batch] are left as they were.
+ *   workspace  device scratch of pa_v2_tree_attention_workspace's size, 16-byte
+ *     aligned; its contents need no initialisation.  Two calls sharing it must
+ *     not overlap on the GPU.
+ * Bad data is recorded in `status`: a page slot or page id out of range
+ * (PA_DEVICE_BAD_SLOT, the request's rows become zeros and -inf;
+ * PA_DEVICE_BAD_PAGE, its rows are not read and that request's result is finite
+ * but meaningless), a qo_indptr that decreases or passes
+ * num_tokens (PA_DEVICE_BAD_INDPTR, the request is skipped), last_page_len or
+ * first_page_offset outside the geometry rules, or n_r above L_r or above
+ * 32 * mask_words (PA_DEVICE_BAD_TREE, the request's rows become zeros and -inf).
+ * P = exp(s) enters the second product rounded to kv_dtype; scores, statistics
+ * and sums are f32.  head_dim 64 or 128, page_size 1..16 or a multiple of 16 up
+ * to 256, pools below 2^31 rows (else PA_EUNSUPPORTED).  DEVICE pointers. */
+#define PA_V2_MAX_MASK_WORDS 32
+pa_status pa_v2_tree_attention_workspace(int32_t device, int32_t num_tokens, int32_t batch, int32_t num_qo_heads,
+                                         int32_t num_kv_heads, int32_t head_dim, int64_t* bytes);
+pa_status pa_v2_tree_attention(const void* q, const void* k_pool, const void* v_pool, int32_t kv_dtype,
+                               int64_t num_pages, int32_t page_size, int32_t num_qo_heads, int32_t num_kv_heads,
+                               int32_t head_dim, const int32_t* indices, int64_t num_indices,
+                               const int32_t* indptr, const int32_t* last_page_len,
+                               const int32_t* first_page_offset, int32_t batch, const int32_t* qo_indptr,
+                               int32_t num_tokens, const int32_t* tree_mask, int32_t mask_words, float sm_scale,
+                               void* out, float* lse2_out, void* workspace, int64_t workspace_bytes,
                                int32_t* status, void* cuda_stream);
 
 /* The variable-length merge (issue #898, design piece 3 and Task 3; PR

@@ -60,6 +60,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+}  // namespace
+
 // Tensor map over a pool viewed as [rows = num_pages * page_size, Hkv, D]
 // (innermost first: D, Hkv, rows); a box is one KV head x `box_rows` rows x
 // `box_d` elements of the head dim.
@@ -79,6 +81,8 @@ bool make_pool_map(CUtensorMap* map, const void* base, int dtype, int64_t rows, 
                    swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return rc == CUDA_SUCCESS;
 }
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -11,6 +11,7 @@ split-KV, and variable-length merge kernels", design pieces 2-4).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -25,6 +26,8 @@ PA_F32, PA_F16, PA_BF16 = 0, 1, 2
 PA_V2_MAX_CHUNKS = 65535
 DEVICE_BAD_REQUEST, DEVICE_BAD_SLOT, DEVICE_BAD_PAGE, DEVICE_BAD_INDPTR, DEVICE_WAIT_TIMEOUT = 1, 2, 4, 8, 16
 DEVICE_BAD_BLOCK = 32
+DEVICE_BAD_LENGTH, DEVICE_NO_PAGES, DEVICE_BAD_TREE = 64, 128, 256
+MAX_TABLE_BATCH, MAX_MASK_WORDS = 16384, 32
 
 KV_DTYPES = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
 
@@ -36,7 +39,8 @@ ABI_SYMBOLS = ("pa_v2_q_heads_per_cta", "pa_v2_default_target_ctas", "pa_v2_plan
                "pa_v2_decode_partial_extra", "pa_v2_selftest_wait", "pa_v2_host_graph_create",
                "pa_v2_host_graph_run", "pa_v2_host_graph_destroy", "pa_v2_decode_host_mapped",
                "pa_v2_host_graph_create_mapped", "pa_v2_wave_fit_pages_per_chunk",
-               "pa_v2_balanced_pages_per_chunk", "pa_v2_cascade_plan", "pa_v2_cascade_decode",
+               "pa_v2_balanced_pages_per_chunk", "pa_v2_cascade_plan", "pa_v2_cascade_decode", "pa_v2_build_tables",
+               "pa_v2_qk_rope_append", "pa_v2_tree_attention_workspace", "pa_v2_tree_attention",
                "pa_status_from_device", "pa_status_string", "pa_version")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -135,6 +139,17 @@ def lib() -> ctypes.CDLL:
         L.pa_sparse_csr.restype = i32
         L.pa_selection_from_blocks.argtypes = [P, i32, i32, i32, i32, i64, P, P, P]
         L.pa_selection_from_blocks.restype = i32
+        L.pa_v2_build_tables.argtypes = [P, P, i32, P, i32, P, i32, P, i32, i32, P, P, i64, P, P, P, P, P, i64, P, i32,
+                                         P, P, P]
+        L.pa_v2_build_tables.restype = i32
+        L.pa_v2_qk_rope_append.argtypes = [P, i64, P, i64, P, i64, i32, i32, i32, i32, i32, P, P, P, i32, i32, P, P, f32,
+                                           P, i32, P, P, i64, i32, P, P]
+        L.pa_v2_qk_rope_append.restype = i32
+        L.pa_v2_tree_attention_workspace.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.POINTER(i64)]
+        L.pa_v2_tree_attention_workspace.restype = i32
+        L.pa_v2_tree_attention.argtypes = [P, P, P, i32, i64, i32, i32, i32, i32, P, i64, P, P, P, i32, P, i32, P, i32,
+                                           f32, P, P, P, i64, P, P]
+        L.pa_v2_tree_attention.restype = i32
         L.pa_status_from_device.argtypes = [i32]
         L.pa_status_from_device.restype = i32
         L.pa_status_string.argtypes = [i32]
@@ -600,6 +615,221 @@ def pa_selection_from_blocks(block_ids, block_size: int, kv_len: int, request_st
     if rc != PA_OK:
         raise PaError(rc, "pa_selection_from_blocks")
     return indices[:R * per]
+
+
+# ---------------------------------------------------------------------------
+# one step of several new tokens per request: tables, q/k preparation, tree attention
+# ---------------------------------------------------------------------------
+
+@contextlib.contextmanager
+def _launch_on(device, stream):
+    """Make `device` and the launch stream current (new tensors then belong to that stream); yields its
+    handle.  stream: a torch stream, a raw handle, or None for the device's current stream."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+            return
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(s):
+            yield s.cuda_stream
+
+
+def _step_ptr(t, name: str, device, dtype=None, shape=None) -> int | None:
+    """Pointer of a contiguous tensor on `device`, its dtype and shape checked; None stays None."""
+    p = _dev_ptr(t, name, dtype)
+    if t is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t is not None and shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return p
+
+
+@dataclass
+class StepTables:
+    """Outputs of pa_v2_build_tables: device int32 buffers a program keeps and reuses from step to step."""
+
+    indptr: torch.Tensor             # [batch + 1]
+    indices: torch.Tensor            # [index capacity]
+    last_page_len: torch.Tensor      # [batch]
+    first_page_offset: torch.Tensor  # [batch]
+    qo_indptr: torch.Tensor          # [batch + 1]
+    slots: torch.Tensor              # [token capacity]
+    positions: torch.Tensor          # [token capacity]
+    tree_mask: torch.Tensor | None   # [token capacity, mask words], or None
+    pages_needed: torch.Tensor       # [1]
+
+    @classmethod
+    def empty(cls, batch: int, index_capacity: int, token_capacity: int, mask_words: int = 0,
+              device="cuda") -> "StepTables":
+        def z(*shape):
+            return torch.zeros(*shape, dtype=torch.int32, device=device)
+
+        return cls(z(batch + 1), z(index_capacity), z(batch), z(batch), z(batch + 1), z(token_capacity),
+                   z(token_capacity), z(token_capacity, mask_words) if mask_words else None, z(1))
+
+
+def pa_v2_build_tables(cached_lens, new_lens, block_table, page_size: int, tables: StepTables, free_pages=None,
+                       parents=None, window: int = 0, status=None, stream=None) -> StepTables:
+    """Page table, slots, positions and tree masks of one step (pa_v2_build_tables), on the device.
+
+    cached_lens, new_lens [B]; block_table [B, width], extended in place from free_pages when given;
+    parents [token capacity] (request-relative, -1 a root) for trees, None for chains.  Fills and returns
+    `tables`."""
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, width]")
+    dev, (B, width) = block_table.device, block_table.shape
+    i32 = torch.int32
+    cap_i, cap_t = tables.indices.numel(), tables.slots.numel()
+    mask = tables.tree_mask
+    if mask is not None and mask.dim() != 2:
+        raise ValueError("tree_mask must be [token capacity, mask words]")
+    words = mask.shape[1] if mask is not None else 0
+    args = (_step_ptr(cached_lens, "cached_lens", dev, i32, (B,)), _step_ptr(new_lens, "new_lens", dev, i32, (B,)), B,
+            _step_ptr(block_table, "block_table", dev, i32), width,
+            _step_ptr(free_pages, "free_pages", dev, i32), free_pages.numel() if free_pages is not None else 0,
+            _step_ptr(parents, "parents", dev, i32, (cap_t,)), int(page_size), int(window),
+            _step_ptr(tables.indptr, "indptr", dev, i32, (B + 1,)), _step_ptr(tables.indices, "indices", dev, i32),
+            cap_i, _step_ptr(tables.last_page_len, "last_page_len", dev, i32, (B,)),
+            _step_ptr(tables.first_page_offset, "first_page_offset", dev, i32, (B,)),
+            _step_ptr(tables.qo_indptr, "qo_indptr", dev, i32, (B + 1,)),
+            _step_ptr(tables.slots, "slots", dev, i32, (cap_t,)),
+            _step_ptr(tables.positions, "positions", dev, i32, (cap_t,)), cap_t,
+            _step_ptr(mask, "tree_mask", dev, i32, (cap_t, words)), words,
+            _step_ptr(tables.pages_needed, "pages_needed", dev, i32, (1,)), _step_ptr(status, "status", dev, i32))
+    with _launch_on(dev, stream) as handle:
+        rc = lib().pa_v2_build_tables(*args, handle)
+    if rc != PA_OK:
+        raise PaError(rc, "pa_v2_build_tables")
+    return tables
+
+
+def _token_rows(t, name: str, tokens: int, head_dim: int, dtype, device) -> tuple[int, int, int]:
+    """(pointer, token stride in elements, heads) of a [tokens, heads, head_dim] view with contiguous token rows."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype or t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != head_dim:
+        raise ValueError(f"{name} must be [{tokens}, heads, {head_dim}] {dtype}, got {list(t.shape)} {t.dtype}")
+    heads = t.shape[1]
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), (t.stride(0) if tokens > 1 else heads * head_dim), heads
+
+
+def _pools(k_pool, v_pool, device) -> None:
+    if k_pool.dtype not in KV_DTYPES or v_pool.dtype != k_pool.dtype or k_pool.shape != v_pool.shape:
+        raise ValueError("k_pool and v_pool must share one of float32/float16/bfloat16 and a shape")
+    if k_pool.dim() != 4:
+        raise ValueError("pools must be [num_pages, page_size, num_kv_heads, head_dim]")
+    if k_pool.device != device or v_pool.device != device:
+        raise ValueError(f"pools must be on {device}")
+
+
+def pa_v2_qk_rope_append(q, k, v, positions, slots, inv_freq, k_pool, v_pool, q_out=None, q_weight=None,
+                         k_weight=None, eps: float = 1e-6, interleaved: bool = False, q_dtype=None, status=None,
+                         stream=None):
+    """Per-head norm and rotation of q and k, k and v appended to the pools (pa_v2_qk_rope_append).
+
+    q [T, Hq, D], k and v [T, Hkv, D] (views of one packed projection output will do), positions and slots [T]
+    int32, inv_freq [rot_dim / 2] float32 or None (no rotation).  Returns q_out [T, Hq, D] in q_dtype (the
+    activations' dtype by default, or float32 for the decode calls); its padded rows are not written."""
+    dev = q.device
+    _pools(k_pool, v_pool, dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    T, _, D = q.shape
+    dt = k_pool.dtype
+    qp, qs, hq = _token_rows(q, "q", T, D, dt, dev)
+    kp, ks, hkv = _token_rows(k, "k", T, D, dt, dev)
+    vp, vs, hv = _token_rows(v, "v", T, D, dt, dev)
+    if hv != hkv or tuple(k_pool.shape[2:]) != (hkv, D):
+        raise ValueError(f"k, v and the pools must agree on heads and head_dim: {hkv}, {hv}, {list(k_pool.shape)}")
+    rot = 2 * inv_freq.numel() if inv_freq is not None else 0
+    if q_out is not None:
+        q_dtype = q_out.dtype
+    elif q_dtype is None:
+        q_dtype = dt
+    if q_dtype not in KV_DTYPES:
+        raise ValueError(f"q_dtype must be one of {list(KV_DTYPES)}")
+    i32 = torch.int32
+    tail = (KV_DTYPES[dt], T, hq, hkv, D, _step_ptr(positions, "positions", dev, i32, (T,)),
+            _step_ptr(slots, "slots", dev, i32, (T,)), _step_ptr(inv_freq, "inv_freq", dev, torch.float32), rot,
+            int(bool(interleaved)), _step_ptr(q_weight, "q_weight", dev, dt, (D,)),
+            _step_ptr(k_weight, "k_weight", dev, dt, (D,)), float(eps))
+    pools = (_step_ptr(k_pool, "k_pool", dev), _step_ptr(v_pool, "v_pool", dev), k_pool.shape[0], k_pool.shape[1],
+             _step_ptr(status, "status", dev, i32))
+    with _launch_on(dev, stream) as handle:
+        if q_out is None:
+            q_out = torch.empty(T, hq, D, dtype=q_dtype, device=dev)
+        rc = lib().pa_v2_qk_rope_append(qp, qs, kp, ks, vp, vs, *tail, _step_ptr(q_out, "q_out", dev, None, (T, hq, D)),
+                                        KV_DTYPES[q_dtype], *pools, handle)
+    if rc != PA_OK:
+        raise PaError(rc, "pa_v2_qk_rope_append")
+    return q_out
+
+
+def pa_v2_tree_attention_workspace(num_tokens: int, batch: int, num_qo_heads: int, num_kv_heads: int, head_dim: int,
+                                   device: int | None = None) -> int:
+    """Bytes of device scratch pa_v2_tree_attention needs for these sizes."""
+    dev = torch.cuda.current_device() if device is None else device
+    out = ctypes.c_int64()
+    rc = lib().pa_v2_tree_attention_workspace(dev, num_tokens, batch, num_qo_heads, num_kv_heads, head_dim,
+                                              ctypes.byref(out))
+    if rc != PA_OK:
+        raise PaError(rc, "pa_v2_tree_attention_workspace")
+    return int(out.value)
+
+
+def tree_attention_workspace(num_tokens: int, batch: int, num_qo_heads: int, num_kv_heads: int, head_dim: int,
+                             device="cuda") -> torch.Tensor:
+    """A workspace tensor for pa_v2_tree_attention calls of up to these sizes."""
+    dev = torch.device(device)
+    index = dev.index if dev.index is not None else torch.cuda.current_device()
+    n = pa_v2_tree_attention_workspace(num_tokens, batch, num_qo_heads, num_kv_heads, head_dim, index)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+
+
+def pa_v2_tree_attention(q, k_pool, v_pool, indices, indptr, last_page_len, first_page_offset, qo_indptr,
+                         sm_scale: float, tree_mask=None, out=None, lse2_out=None, workspace=None, status=None,
+                         stream=None):
+    """Attention of each request's new tokens over its paged cache (pa_v2_tree_attention).
+
+    q [T, Hq, D] of the pools' 16-bit dtype, packed request by request (qo_indptr [B + 1]); tree_mask
+    [T, words] int32 ancestor bits, or None for chains.  Returns (out [T, Hq, D], lse2 [T, Hq] float32); rows
+    behind the last token are not written."""
+    dev = q.device
+    _pools(k_pool, v_pool, dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    T, hq, D = q.shape
+    P, ps, hkv, pd = k_pool.shape
+    if pd != D:
+        raise ValueError(f"pools must be [P, page_size, Hkv, {D}]")
+    B = last_page_len.numel()
+    i32 = torch.int32
+    if tree_mask is not None and tree_mask.dim() != 2:
+        raise ValueError("tree_mask must be [tokens, mask words]")
+    words = tree_mask.shape[1] if tree_mask is not None else 0
+    args = (_step_ptr(q, "q", dev, k_pool.dtype), _step_ptr(k_pool, "k_pool", dev), _step_ptr(v_pool, "v_pool", dev),
+            KV_DTYPES[k_pool.dtype], P, ps, hq, hkv, D, _step_ptr(indices, "indices", dev, i32), indices.numel(),
+            _step_ptr(indptr, "indptr", dev, i32, (B + 1,)), _step_ptr(last_page_len, "last_page_len", dev, i32, (B,)),
+            _step_ptr(first_page_offset, "first_page_offset", dev, i32, (B,)), B,
+            _step_ptr(qo_indptr, "qo_indptr", dev, i32, (B + 1,)), T,
+            _step_ptr(tree_mask, "tree_mask", dev, i32, (T, words)), words, float(sm_scale))
+    st = _step_ptr(status, "status", dev, i32)
+    with _launch_on(dev, stream) as handle:
+        if workspace is None and hkv > 0 and hq % hkv == 0 and D in (64, 128):
+            workspace = tree_attention_workspace(T, B, hq, hkv, D, dev)
+        if out is None:
+            out = torch.empty(T, hq, D, dtype=q.dtype, device=dev)
+        if lse2_out is None:
+            lse2_out = torch.empty(T, hq, dtype=torch.float32, device=dev)
+        rc = lib().pa_v2_tree_attention(
+            *args, _step_ptr(out, "out", dev, q.dtype, (T, hq, D)),
+            _step_ptr(lse2_out, "lse2_out", dev, torch.float32, (T, hq)), _step_ptr(workspace, "workspace", dev),
+            workspace.numel() * workspace.element_size() if workspace is not None else 0, st, handle)
+    if rc != PA_OK:
+        raise PaError(rc, "pa_v2_tree_attention")
+    return out, lse2_out
 
 
 # ---------------------------------------------------------------------------
