@@ -408,6 +408,27 @@ def test_tree_long_context_split_over_the_machine(dtype):
     _check_tree(_tree_case(8, [(6000, 6), (2500, 2)], 4, 2, 128, 16, dtype))
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("reqs,hq,hkv,D,chain,page_size", [
+    ([(4095, 20)] * 3, 32, 8, 128, True, 16),            # runs of several tiles, one tile of query rows
+    ([(4000, 64), (1, 3), (2500, 64)], 32, 8, 128, False, 16),   # two tiles of query rows
+    ([(3000, 37), (2900, 8)], 32, 8, 128, False, 5),     # the same through the gathering loader
+    ([(700, 1)] * 60, 8, 8, 128, True, 16),              # several whole heads per run
+    ([(300, 1), (90, 2)] * 90, 4, 2, 64, True, 8),
+    ([(20000, 3)], 4, 1, 64, False, 64)])
+def test_tree_runs_of_several_tiles_and_pieces(reqs, hq, hkv, D, chain, page_size, dtype):
+    _check_tree(_tree_case(D + len(reqs), reqs, hq, hkv, D, page_size, dtype, chain=chain))
+
+
+@pytest.mark.parametrize("reqs,hq,hkv,chain,page_size", [
+    ([(9000, 200)], 8, 2, False, 16),                    # four blocks of query rows, the keys cut into segments
+    ([(9000, 200), (50, 1), (3000, 90)], 8, 2, True, 16),
+    ([(6000, 330)], 8, 2, True, 3),
+    ([(0, 700)], 8, 2, True, 16)])                       # nothing but new tokens: blocks that stop at their last one
+def test_tree_several_blocks_of_query_rows(reqs, hq, hkv, chain, page_size):
+    _check_tree(_tree_case(len(reqs) + page_size, reqs, hq, hkv, 64, page_size, torch.float16, chain=chain))
+
+
 def test_tree_many_ragged_requests():
     rng = random.Random(4)
     reqs = [(rng.choice([0, 1, 15, 16, rng.randint(0, 700)]), rng.randint(0, 9)) for _ in range(90)]
