@@ -10,14 +10,14 @@
 // Work.  The query rows of a KV head are its n * G (token, head) pairs; a block
 // of up to 256 of them meets the request's keys in tiles of 128 pool rows (page
 // order, so a tile is whole pages or whole slices of one).  One block against
-// one tile is a unit; the units of all (request, KV head, block) in order are
-// cut into equal runs, one per CTA and one CTA per SM, whatever the lengths: no
-// host plan, no wave tail.  A CTA's run meets several blocks or a part of one;
-// a block whole inside a run is written as the result, parts go to the
-// workspace and pa_v2_tree_merge_kernel folds them.  When a request has several
-// blocks, its keys are cut into segments of about one run and the order is
-// segment by segment, so the CTAs at work on one segment's blocks read the same
-// keys at about the same time (out of L2).
+// one tile is a unit, and every CTA (one per SM) gets the same number of them,
+// `run`, whatever the lengths: no host plan, no wave tail.  A block's keys are
+// cut into chunks of `run` tiles, one CTA each; what is left of the blocks (all
+// of a short request) is strung together and dealt out in equal stretches to
+// the other CTAs.  So the blocks of one request meet the same keys at the same
+// time, out of L2, and a block costs one partial result more than it must.  A
+// block that one CTA meets alone is written as the result; parts go to the
+// workspace, and pa_v2_tree_merge_kernel folds them.
 //
 // A CTA holds a 256-row block as two M=128 tiles, A and B.  With 128 rows or
 // fewer, A and B are the same rows against alternate key tiles (two streams,
@@ -28,10 +28,12 @@
 //    rescaled in place only when a row's maximum grows by more than kLazy);
 //  - warp 8: one thread issues S = Q K^T (both operands in shared memory) and
 //    O += P V (P in tensor memory);
-//  - warp 9 (and 10): loads K and V tiles through a ring of shared-memory
-//    stages, TMA boxes of up to 16 rows x 64 elements per page, or cp.async for
-//    page sizes whose pages do not start on 8-row boundaries; it also walks the
-//    CTA's run and hands the pieces to the other roles;
+//  - warps 9 and 10: load K and V tiles through a ring of shared-memory stages,
+//    TMA boxes of up to 16 rows x 64 elements per page (K by warp 9, V by warp
+//    10: issuing a tile's 16 boxes takes a thread about 1200 cycles), or
+//    cp.async by both for page sizes whose pages do not start on 8-row
+//    boundaries; both walk the CTA's share of the work, and warp 9 hands its
+//    pieces to the other roles;
 //  - warp 11: makes V tiles that hold rows outside the visible range or new
 //    tokens safe: 0 * NaN is NaN, so what a mask hides must not be left in V.
 //    Outside rows become zeros; non-finite elements of new tokens become zeros
@@ -55,7 +57,8 @@ namespace {
 constexpr int kTrThreads = 384;
 constexpr int kTrTile = 128;      // query rows of a tensor-core tile, and keys of a key tile
 constexpr int kTrBlock = 256;     // query rows of a block
-constexpr int kTrSlots = 3;       // partial results a CTA can leave (see piece_slot)
+constexpr int kTrSlots = 2;       // partial results per CTA (see rest_slot)
+constexpr int kTrRestCost = 4;    // what starting a left-over stretch costs, in key tiles
 constexpr int kTrMmaWarp = 8, kTrLoadWarp = 9, kTrFixWarp = 11;
 constexpr int kTrLoadThreads = 64;  // loader threads without TMA
 constexpr int kTrRing = 2;        // pieces handed out ahead
@@ -98,10 +101,10 @@ struct TreeParams {
   const int32_t* tree_mask;
   void* out;
   float* lse_out;
-  float* slots;    // partial results: kTrSlots per CTA
+  float* slots;    // partial results: kTrSlots * ctas
   int32_t* status;
   int64_t num_pages, num_indices;
-  int32_t batch, num_tokens, mask_words, page_size, hq, hkv, group, ctas;
+  int32_t batch, num_tokens, mask_words, page_size, box_rows, hq, hkv, group, ctas;
   uint32_t ps_magic, ps_shift, g_magic, g_shift;
   float scale_log2;   // |sm_scale| * log2(e), or 1 for a zero scale
   uint32_t q_xor;     // sign flip of both halves of a q word for a negative scale
@@ -110,140 +113,278 @@ struct TreeParams {
 
 // One request's share of the work.
 struct TreeReq {
-  int32_t slot_base, pages;
+  int32_t slot_base;
   int32_t t0, n;       // its query tokens
   int32_t lo, hi, ds;  // pool rows in page order: visible [lo, hi), new tokens [ds, hi)
   int32_t blocks;      // blocks of query rows per KV head
   int32_t tile0;       // first key tile
   int32_t common;      // key tiles every block meets
-  int32_t sum_tail;    // further key tiles, over all blocks (chains: a block stops at its last token)
-  bool chain, empty;   // empty: nothing visible or a bad table: zeros and -inf
+  int32_t units;       // per KV head: blocks * common, and what chains add per block (a block stops at its last token)
+  int32_t kind;        // 0 (no query), kReqEmpty (nothing visible or a bad table: zeros and -inf), kReqEven, kReqChain
 
-  __device__ __forceinline__ int64_t units() const { return (int64_t)blocks * common + sum_tail; }  // per KV head
+  __device__ __forceinline__ bool tails() const { return units != blocks * common; }
 };
+constexpr int kReqEmpty = 1, kReqEven = 2, kReqChain = 3;
 
+// Key tiles of block b behind the common ones.
 __device__ __forceinline__ int32_t tail_of(const TreeReq& g, int group, int b) {
-  if (!g.chain || g.empty) return 0;
-  const int64_t tok = min((int64_t)g.n, ((int64_t)kTrBlock * (b + 1) + group - 1) / group);
-  return (int32_t)((g.ds + tok + kTrTile - 1) / kTrTile) - g.tile0 - g.common;
+  if (g.kind != kReqChain) return 0;
+  const int32_t tok = (int32_t)min((int64_t)g.n, ((int64_t)kTrBlock * (b + 1) + group - 1) / group);
+  return (g.ds + tok + kTrTile - 1) / kTrTile - g.tile0 - g.common;
 }
 
 __device__ __forceinline__ TreeReq tree_req(const TreeParams& p, int r, bool tell) {
-  TreeReq g;
+  TreeReq g = {};
   const int32_t a = p.qo_indptr[r], b = p.qo_indptr[r + 1];
   const int32_t s0 = p.indptr[r], s1 = p.indptr[r + 1];
   const int32_t lpl = p.last_page_len[r], fpo = p.first_page_offset[r];
-  g.t0 = a;
-  g.n = b - a;
-  g.lo = g.hi = g.ds = g.tile0 = g.sum_tail = 0;
-  g.slot_base = s0;
-  g.pages = 0;
-  g.blocks = g.common = 0;
-  g.chain = p.tree_mask == nullptr;
-  g.empty = true;
   if (a < 0 || b < a || b > p.num_tokens) {
     if (tell) report(p.status, PA_DEVICE_BAD_INDPTR);
-    g.n = 0;
+    return g;
   }
-  if (g.n == 0) return g;
-  g.blocks = (int32_t)(((int64_t)g.n * p.group + kTrBlock - 1) / kTrBlock);
+  if (a == b) return g;
+  g.slot_base = s0;
+  g.t0 = a;
+  g.n = b - a;
+  g.blocks = (g.n * p.group + kTrBlock - 1) / kTrBlock;  // num_tokens * group fits (checked by the host)
+  g.kind = kReqEmpty;
   g.common = 1;  // one unit for an empty block
+  g.units = g.blocks;
   const int64_t pages = (int64_t)s1 - s0;
   if (s0 < 0 || pages < 0 || s1 > p.num_indices || pages * p.page_size > INT32_MAX - 2 * kTrTile) {
     if (tell) report(p.status, PA_DEVICE_BAD_SLOT);
     return g;
   }
-  const int64_t hi = pages > 0 ? (pages - 1) * p.page_size + lpl : 0;
+  const int32_t hi = pages > 0 ? ((int32_t)pages - 1) * p.page_size + lpl : 0;
+  const int32_t tile0 = fpo / kTrTile;
+  const int32_t all = (hi + kTrTile - 1) / kTrTile - tile0;
   if (pages == 0 || lpl < 1 || lpl > p.page_size || fpo < 0 || fpo >= p.page_size || hi - fpo < g.n ||
-      (p.tree_mask && g.n > 32 * p.mask_words)) {
+      (p.tree_mask && g.n > 32 * p.mask_words) || (int64_t)g.blocks * (all + kTrRestCost) > INT32_MAX) {
     if (tell) report(p.status, PA_DEVICE_BAD_TREE);
     return g;
   }
-  g.empty = false;
-  g.pages = (int32_t)pages;
   g.lo = fpo;
-  g.hi = (int32_t)hi;
-  g.ds = g.hi - g.n;
-  g.tile0 = g.lo / kTrTile;
-  const int32_t all = (g.hi + kTrTile - 1) / kTrTile - g.tile0;
-  if (g.blocks == 1 || !g.chain) {
-    g.common = all;
-    g.chain = g.chain && g.blocks > 1;
-  } else {
-    g.common = max(g.ds / kTrTile - g.tile0, 0);
-    for (int b2 = 0; b2 < g.blocks; ++b2) g.sum_tail += tail_of(g, p.group, b2);
+  g.hi = hi;
+  g.ds = hi - g.n;
+  g.tile0 = tile0;
+  g.kind = kReqEven;
+  g.common = all;
+  g.units = g.blocks * all;
+  if (!p.tree_mask && g.blocks > 1) {
+    g.kind = kReqChain;
+    g.common = g.ds / kTrTile - tile0;
+    g.units = g.blocks * g.common;
+    for (int i = 0; i < g.blocks; ++i) g.units += tail_of(g, p.group, i);
   }
   return g;
 }
 
-// Segments of a request's common key tiles: one when it has one block, else about one CTA's run each.
-__device__ __forceinline__ int32_t segments(const TreeReq& g, int64_t run) {
-  if (g.blocks <= 1 || g.common == 0) return 1;
-  return (int32_t)((g.common + run - 1) / run);
-}
-__device__ __forceinline__ int32_t seg_begin(const TreeReq& g, int32_t S, int32_t s) {
-  return (int32_t)((int64_t)s * g.common / S);
+// Key tiles that block b meets.
+__device__ __forceinline__ int32_t tiles_of(const TreeReq& g, int group, int b) { return g.common + tail_of(g, group, b); }
+
+// A block's left-over tiles, weighed with the cost of starting on them.
+__device__ __forceinline__ int32_t rest_weight(int32_t tiles, int32_t run) {
+  const int32_t rest = tiles % run;
+  return rest ? rest + kTrRestCost : 0;
 }
 
-// Place of a partial result that starts `pos` units into its CTA's run of `run` units.  A run meets at most one
-// piece at its start (pos 0) and pieces of at least ceil(run / 2) units, or the run's last one, after it: a block
-// in one segment is cut only by the ends of a run, and a request is cut into several segments only when its
-// common tiles exceed a run, which makes each at least ceil(run / 2) long.
-__device__ __forceinline__ int piece_slot(int64_t pos, int64_t run) {
-  return pos == 0 ? 0 : 1 + (int)((pos - 1) / ((run + 1) / 2));
+// Chunks of `run` tiles and left-over weight per KV head.
+struct HeadCut {
+  int32_t chunks, weight;
+};
+__device__ __forceinline__ HeadCut head_cut(const TreeReq& g, int group, int32_t run) {
+  HeadCut h = {g.blocks * (g.common / run), g.blocks * rest_weight(g.common, run)};
+  if (g.kind == kReqChain) {
+    h.chunks = h.weight = 0;
+    for (int b = 0; b < g.blocks; ++b) {
+      const int32_t t = tiles_of(g, group, b);
+      h.chunks += t / run;
+      h.weight += rest_weight(t, run);
+    }
+  }
+  return h;
 }
 
-// Where the block-wide scan below found a unit.
-struct TreeStart {
-  int64_t total, run;  // all units; units per CTA
-  int64_t off;         // the unit's offset inside request r
-  int32_t r;           // batch when the unit is past the end
+// a / b for 0 <= a, 0 < b; in 32 bits where a allows.
+__device__ __forceinline__ int64_t div_units(int64_t a, int32_t b) {
+  return (a >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The cut of the whole batch, and the place of one chunk or left-over position in it.  CTAs [0, chunks) take a
+// chunk each, the others a stretch of `stretch` left-over weight.  run counts the start of every block in, so
+// chunks * run + weight <= ctas * run, and as there is a block, chunks < ctas.
+struct TreeCut {
+  int64_t weight;         // all left-over weight
+  int64_t off;            // the position inside request r: of chunks, or of left-over weight
+  int64_t r_weight;       // left-over weight of the requests before r
+  int32_t run, chunks, stretch;
+  int32_t r, r_chunks;    // r: batch when the position is past the end; chunks of the requests before it
 };
 
-// Every thread of the block: units of all requests, the run length, and the request of unit `cta * run`.
-template <int THREADS>
-__device__ __forceinline__ void tree_schedule(const TreeParams& p, int64_t cta, bool tell, TreeStart* out,
-                                              int64_t* warp_sum) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.batch + THREADS - 1) / THREADS;
-  const int r0 = min((int64_t)tid * per, (int64_t)p.batch), r1 = min(r0 + per, p.batch);
-  int64_t mine = 0;
-  for (int r = r0; r < r1; ++r) mine += tree_req(p, r, tell).units() * p.hkv;
-  int64_t v = mine;
+// The run length for `tiles` units in `blocks` blocks.
+__device__ __forceinline__ int32_t run_of(int64_t tiles, int64_t blocks, int32_t ctas) {
+  return (int32_t)max(div_units(tiles + kTrRestCost * blocks + ctas - 1, ctas), (int64_t)1);
+}
+// Position of CTA (or of its end, when `past` is 1) among the chunks (c < chunks) or the left-over weight.
+__device__ __forceinline__ void set_stretch(TreeCut* t, int32_t ctas) {
+  t->stretch = t->chunks < ctas ? (int32_t)div_units(t->weight + (ctas - t->chunks) - 1, ctas - t->chunks) : 0;
+}
+
+__device__ __forceinline__ int64_t scan_add(int64_t v, int lane) {
 #pragma unroll
   for (int w = 1; w < 32; w <<= 1) {
     const int64_t u = __shfl_up_sync(0xffffffffu, v, w);
     if (lane >= w) v += u;
   }
-  if (lane == 31) warp_sum[warp] = v;
+  return v;
+}
+
+// The cut for a batch of up to 32 requests, by one warp: lane r holds request r in `mine`.  c < chunks: chunk c;
+// else left-over position (c - chunks + past) * stretch.
+__device__ __forceinline__ TreeCut cut_warp(const TreeParams& p, int c, int past, const TreeReq& mine, int lane) {
+  int64_t tiles = (int64_t)mine.units * p.hkv, blocks = (int64_t)mine.blocks * p.hkv;
+  if (p.batch > 1) {
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) {
+      tiles += __shfl_xor_sync(0xffffffffu, tiles, w);
+      blocks += __shfl_xor_sync(0xffffffffu, blocks, w);
+    }
+  } else {
+    tiles = __shfl_sync(0xffffffffu, tiles, 0);
+    blocks = __shfl_sync(0xffffffffu, blocks, 0);
+  }
+  TreeCut t;
+  t.run = run_of(tiles, blocks, p.ctas);
+  const HeadCut h = head_cut(mine, p.group, t.run);
+  const int64_t chunks = (int64_t)h.chunks * p.hkv, weight = (int64_t)h.weight * p.hkv;
+  const int64_t chunks_to = p.batch > 1 ? scan_add(chunks, lane) : chunks;
+  const int64_t weight_to = p.batch > 1 ? scan_add(weight, lane) : weight;
+  const int last = p.batch - 1;
+  t.chunks = (int32_t)__shfl_sync(0xffffffffu, chunks_to, last);
+  t.weight = __shfl_sync(0xffffffffu, weight_to, last);
+  set_stretch(&t, p.ctas);
+  const bool chunk = c < t.chunks;
+  const int64_t at = chunk ? c : (int64_t)(c - t.chunks + past) * t.stretch;
+  const uint32_t after = __ballot_sync(0xffffffffu, lane <= last && at < (chunk ? chunks_to : weight_to));
+  t.r = after ? __ffs(after) - 1 : p.batch;
+  const int src = after ? t.r : 0;
+  t.r_chunks = (int32_t)__shfl_sync(0xffffffffu, chunks_to - chunks, src);
+  t.r_weight = __shfl_sync(0xffffffffu, weight_to - weight, src);
+  t.off = at - (chunk ? t.r_chunks : t.r_weight);
+  return t;
+}
+
+// Exclusive prefix of v over the block's threads; *total receives the sum.  Two barriers.
+template <int THREADS>
+__device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* warp_sum, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t upto = scan_add(v, lane);
+  if (lane == 31) warp_sum[warp] = upto;
   __syncthreads();
-  int64_t before = v - mine, total = 0;
+  int64_t before = upto - v, sum = 0;
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
-  }
-  const int64_t run = (total + p.ctas - 1) / p.ctas;
-  const int64_t unit = cta * run;
-  if (tid == 0) {
-    out->total = total;
-    out->run = run;
-    if (unit >= total) {
-      out->r = p.batch;
-      out->off = 0;
-    }
-  }
-  if (unit < total && unit >= before && unit < before + mine) {
-    int64_t off = unit - before;
-    int r = r0;
-    for (; r < r1; ++r) {
-      const int64_t u = tree_req(p, r, false).units() * p.hkv;
-      if (off < u) break;
-      off -= u;
-    }
-    out->r = r;
-    out->off = off;
+    sum += warp_sum[w];
   }
   __syncthreads();
+  *total = sum;
+  return before;
+}
+
+// The same for any batch, by every thread of the block (each a run of consecutive requests).
+template <int THREADS>
+__device__ __forceinline__ void cut_block(const TreeParams& p, int c, int past, bool tell, TreeCut* out,
+                                          int64_t* warp_sum) {
+  const int per = (p.batch + THREADS - 1) / THREADS;
+  const int r0 = (int)min((int64_t)threadIdx.x * per, (int64_t)p.batch), r1 = min(r0 + per, p.batch);
+  int64_t tiles = 0, blocks = 0;
+  for (int r = r0; r < r1; ++r) {
+    const TreeReq g = tree_req(p, r, tell);
+    tiles += (int64_t)g.units * p.hkv;
+    blocks += (int64_t)g.blocks * p.hkv;
+  }
+  int64_t all_tiles, all_blocks, all_chunks, all_weight;
+  block_prefix<THREADS>(tiles, warp_sum, &all_tiles);
+  block_prefix<THREADS>(blocks, warp_sum, &all_blocks);
+  TreeCut t;
+  t.run = run_of(all_tiles, all_blocks, p.ctas);
+  int64_t chunks = 0, weight = 0;
+  for (int r = r0; r < r1; ++r) {
+    const HeadCut h = head_cut(tree_req(p, r, false), p.group, t.run);
+    chunks += (int64_t)h.chunks * p.hkv;
+    weight += (int64_t)h.weight * p.hkv;
+  }
+  int64_t chunks_at = block_prefix<THREADS>(chunks, warp_sum, &all_chunks);
+  int64_t weight_at = block_prefix<THREADS>(weight, warp_sum, &all_weight);
+  t.chunks = (int32_t)all_chunks;
+  t.weight = all_weight;
+  set_stretch(&t, p.ctas);
+  const bool chunk = c < t.chunks;
+  const int64_t at = chunk ? c : (int64_t)(c - t.chunks + past) * t.stretch;
+  const int64_t begin = chunk ? chunks_at : weight_at;
+  const int64_t mine = chunk ? chunks : weight;
+  t.r = p.batch;
+  t.off = t.r_weight = t.r_chunks = 0;
+  if (at >= begin && at < begin + mine) {
+    for (t.r = r0; t.r < r1; ++t.r) {
+      const HeadCut h = head_cut(tree_req(p, t.r, false), p.group, t.run);
+      const int64_t u = (int64_t)(chunk ? h.chunks : h.weight) * p.hkv;
+      t.off = at - (chunk ? chunks_at : weight_at);
+      if (t.off < u) break;
+      chunks_at += (int64_t)h.chunks * p.hkv;
+      weight_at += (int64_t)h.weight * p.hkv;
+    }
+    t.r_chunks = (int32_t)chunks_at;
+    t.r_weight = weight_at;
+    *out = t;
+  } else if (threadIdx.x == 0 && at >= (chunk ? all_chunks : all_weight)) {
+    *out = t;
+  }
+  __syncthreads();
+}
+
+// Block, and what is before it in its KV head, of chunk or left-over position x of the head.
+struct BlockAt {
+  int32_t b, tiles, x;     // the block, its key tiles, the position inside it
+  int32_t chunks, weight;  // of the head's blocks before it
+};
+__device__ __forceinline__ BlockAt block_at(const TreeReq& g, int group, int32_t run, int32_t x, bool chunk) {
+  BlockAt k = {0, g.common, x, 0, 0};
+  if (g.kind != kReqChain) {
+    const int32_t chunks = g.common / run, weight = rest_weight(g.common, run);
+    const int32_t each = chunk ? chunks : weight;
+    k.b = x / each;
+    k.x = x - k.b * each;
+    k.chunks = k.b * chunks;
+    k.weight = k.b * weight;
+    return k;
+  }
+  for (;; ++k.b) {
+    k.tiles = tiles_of(g, group, k.b);
+    const int32_t chunks = k.tiles / run, weight = rest_weight(k.tiles, run);
+    const int32_t each = chunk ? chunks : weight;
+    if (k.x < each || k.b + 1 >= g.blocks) return k;
+    k.x -= each;
+    k.chunks += chunks;
+    k.weight += weight;
+  }
+}
+
+// Slot of a partial result.  A chunk's is its CTA's first, and so is that of a left-over piece that its CTA's
+// stretch cuts off (only the stretch's last piece can be, and such a CTA has no chunk).  The piece that ends a
+// block goes to a second slot: of the CTA of the block's first chunk, or, when it has none, of its own CTA (then
+// it opens the stretch: the block was cut at the end of the stretch before).
+__device__ __forceinline__ int rest_slot(bool ends, int32_t chunks, int first_chunk, int cta, int ctas) {
+  return !ends ? cta : ctas + (chunks > 0 ? first_chunk : cta);
+}
+
+__device__ __forceinline__ TreeReq shfl_req(const TreeReq& g, int r) {
+  TreeReq o;
+  const int32_t* src = reinterpret_cast<const int32_t*>(&g);
+  int32_t* dst = reinterpret_cast<int32_t*>(&o);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(TreeReq) / 4); ++i) dst[i] = __shfl_sync(0xffffffffu, src[i], r);
+  return o;
 }
 
 // A run of key tiles of one block, as the loader hands it to the other roles.
@@ -264,6 +405,10 @@ __device__ __forceinline__ bool needs_fix(const TreePiece& d, int tile) {
   return tile * kTrTile < d.lo || (tile + 1) * kTrTile > d.ds;
 }
 
+__device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // Bits [a, b) of a word, a and b clamped to [0, 32].
 __device__ __forceinline__ uint32_t bit_range(int a, int b) {
   a = max(a, 0);
@@ -272,30 +417,45 @@ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
   return (b >= 32 ? 0xffffffffu : ((1u << b) - 1u)) & ~((1u << a) - 1u);
 }
 
-// Which of the keys base .. base+31 (page order) query token i of the piece sees.
-__device__ __forceinline__ uint32_t visible_bits(const TreeParams& p, const TreePiece& d, int i, int base) {
-  uint32_t bits = bit_range(d.lo - base, d.ds - base);
-  if (base + 32 > d.ds && base < d.hi) {
+// Which of the keys base .. base+31 (page order) a query token sees: token `token` of the batch, new token i of a
+// request whose visible rows are [lo, hi) and whose new tokens are [ds, hi).
+__device__ __forceinline__ uint32_t visible_bits(const TreeParams& p, int lo, int ds, int hi, int token, int i,
+                                                 int base) {
+  uint32_t bits = bit_range(lo - base, ds - base);
+  if (base + 32 > ds && base < hi) {
     if (p.tree_mask) {
-      const int32_t* row = p.tree_mask + (int64_t)(d.t0 + i) * p.mask_words;
-      const int at = base - d.ds;  // new-token index of bit 0
+      const int32_t* row = p.tree_mask + (int64_t)token * p.mask_words;
+      const int at = base - ds;  // new-token index of bit 0
       const int w = at >> 5, sh = at & 31;
       const uint32_t x0 = w >= 0 && w < p.mask_words ? (uint32_t)__ldg(row + w) : 0u;
       const uint32_t x1 = w + 1 >= 0 && w + 1 < p.mask_words ? (uint32_t)__ldg(row + w + 1) : 0u;
-      bits |= __funnelshift_r(x0, x1, sh) & bit_range(d.ds - base, d.hi - base);
+      bits |= __funnelshift_r(x0, x1, sh) & bit_range(ds - base, hi - base);
     } else {
-      bits |= bit_range(d.ds - base, min(d.ds + i + 1, d.hi) - base);
+      bits |= bit_range(ds - base, min(ds + i + 1, hi) - base);
     }
   }
   return bits;
 }
 
-// D[128 x N] (+)= A[128 x 16] B[16 x N], A in tensor memory.
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+// A shared-memory matrix descriptor (smem_desc) as two words: the upper one is the same for every operand here
+// (stride 1024 bytes between 8-row groups, version 1, 128-byte swizzle), so only the lower one, address and
+// leading offset in 16-byte units, is computed per product, in 32 bits.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
+
+// D[128 x N] (+)= A[128 x 16] B[16 x N]; A in shared memory, or in tensor memory.
+__device__ __forceinline__ void umma_lo(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b), "r"(idesc), "r"(acc), "n"(kDescHi)
       : "memory");
 }
 
@@ -316,6 +476,36 @@ template <> struct ExpBits<__nv_bfloat16> { static constexpr uint32_t k = 0x7f80
 __device__ __forceinline__ float half_of(const __half* x) { return __half2float(*x); }
 __device__ __forceinline__ float half_of(const __nv_bfloat16* x) { return __bfloat162float(*x); }
 
+// No key was visible to the row (a NaN sum stays NaN).
+__device__ __forceinline__ bool nothing_seen(float l) { return l == 0.f; }
+
+// The non-finite values of new tokens that the fix warp took out of V, back into the O of the rows that see them
+// (a converged warp; query token tok of the piece's request on this thread's lane).
+template <typename T, int D>
+__device__ __noinline__ void put_back(const TreeParams& p, const TreePiece& d, int tok, uint32_t t_o) {
+  const int k0 = max(d.tile * kTrTile, d.ds), k1 = min((d.tile + d.tiles) * kTrTile, d.hi);
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t o[32];
+    __syncwarp();
+    tmem_ld32(t_o + 32 * c, o);
+    for (int k = k0; k < k1; ++k) {
+      if (!(visible_bits(p, d.lo, d.ds, d.hi, d.t0 + tok, tok, k) & 1u)) continue;
+      const int sl = (int)fast_div((uint32_t)k, p.ps_magic, p.ps_shift);
+      const int32_t page = __ldg(p.indices + d.slot_base + sl);
+      if (page < 0 || page >= p.num_pages) continue;
+      const T* src = static_cast<const T*>(p.v_pool) +
+                     (((int64_t)page * p.page_size + (k - sl * p.page_size)) * p.hkv + d.kvh) * D + 32 * c;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float y = half_of(src + i);
+        if (!isfinite(y)) o[i] = __float_as_uint(__uint_as_float(o[i]) + y);
+      }
+    }
+    __syncwarp();
+    tmem_st32(t_o + 32 * c, o);
+  }
+}
+
 template <typename T, int D, bool TMA>
 __global__ void __launch_bounds__(kTrThreads, 1)
     pa_v2_tree_attention_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tm_k,
@@ -328,8 +518,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   uint64_t* b_full = bars;
   uint64_t* b_empty = b_full + C::kStages;
   uint64_t* b_s = b_empty + C::kStages;   // 2: S of a stream is complete
-  uint64_t* b_p = b_s + 2;                // 2: P of a stream is written (one arrival per warp)
-  uint64_t* b_o = b_p + 2;                // the piece's products are complete
+  uint64_t* b_p = b_s + 2;                // 4: a half of a stream's P is written (one arrival per warp)
+  uint64_t* b_o = b_p + 4;                // the piece's products are complete
   uint64_t* b_q = b_o + 1;                // the piece's Q is in shared memory
   uint64_t* b_fix = b_q + 1;              // kStages: the V tile in a stage was made safe
   uint64_t* b_x = b_fix + C::kStages;     // stream B's state is in shared memory
@@ -338,13 +528,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   uint64_t* b_pe = b_pf + kTrRing;        // kTrRing: every role is done with it
   uint64_t* b_drain = b_pe + kTrRing;
   TreePiece* ring = reinterpret_cast<TreePiece*>(b_drain + 1);
-  TreeStart* start = reinterpret_cast<TreeStart*>(ring + kTrRing);
+  TreeCut* start = reinterpret_cast<TreeCut*>(ring + kTrRing);
   int64_t* warp_sum = reinterpret_cast<int64_t*>(start + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(warp_sum + kTrThreads / 32);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(tmem_slot + 1);
   float* xstate = reinterpret_cast<float*>(tmem_slot + 2);  // [2][128]: stream B's maxima and sums
-  static_assert((3 * C::kStages + 9 + 2 * kTrRing) * 8 + kTrRing * sizeof(TreePiece) + sizeof(TreeStart) +
-                        kTrThreads / 32 * 8 + 8 + 2 * kTrTile * 4 <=
+  int32_t(*boxes_of)[16] = reinterpret_cast<int32_t(*)[16]>(xstate + 2 * kTrTile);  // the loader warps' box rows
+  static_assert((3 * C::kStages + 11 + 2 * kTrRing) * 8 + kTrRing * sizeof(TreePiece) + sizeof(TreeCut) +
+                        kTrThreads / 32 * 8 + 8 + 2 * kTrTile * 4 + 2 * 16 * 4 <=
                     2048,
                 "the area behind the stages");
 
@@ -353,6 +544,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   const uint32_t sbase = smem_addr(smem);
 
   pdl_launch_dependents();
+  if (TMA && threadIdx.x == kTrLoadWarp * 32) {
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&b_full[i], TMA ? 1 : kTrLoadThreads);
@@ -361,7 +556,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&b_s[w], 1);
-      mbar_init(&b_p[w], 4);
+      mbar_init(&b_p[2 * w], 4);
+      mbar_init(&b_p[2 * w + 1], 4);
     }
     mbar_init(b_o, 1);
     mbar_init(b_q, 8);
@@ -387,379 +583,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait_prerequisites();
-  tree_schedule<kTrThreads>(p, blockIdx.x, blockIdx.x == 0, start, warp_sum);
+  // the loader warp finds the CTA's place alone when a request fits a lane, else all threads do
+  const bool small = p.batch <= 32;
+  if (!small) cut_block<kTrThreads>(p, blockIdx.x, 0, blockIdx.x == 0, start, warp_sum);
 
-  if (warp == kTrLoadWarp || (!TMA && warp == kTrLoadWarp + 1)) {
-    // ------------------------------------------------------------------ loader
-    const bool leader = warp == kTrLoadWarp;
-    const int64_t run = start->run;
-    int64_t left = min(run, start->total - (int64_t)blockIdx.x * run);  // units to go (<= 0: none)
-    int r = start->r;
-    int64_t off = start->off;
-    int stage = 0, pieces = 0, ops = 0;
-    int pend = -1;  // without TMA: the stage whose copies are not published yet
-    bool alive = true;
-    const int u = (warp - kTrLoadWarp) * 32 + lane;
-    TreeReq g = {};
-    const int box_rows = p.page_size < 16 ? p.page_size : 16;
-    const uint64_t policy = policy_evict_first();
-
-    auto publish = [&]() {  // without TMA: the pending stage's copies have landed
-      fence_proxy_async_smem();
-      mbar_arrive(&b_full[pend]);
-      pend = -1;
-    };
-    // K (or V) rows [128 tile, 128 tile + 128) of the request's pages into the next stage
-    auto load = [&](int tile, int kvh, bool is_v) {
-      if (!wait_phase(&b_empty[stage], ((ops / C::kStages) & 1) ^ 1, abort_flag, p.status)) {
-        alive = false;
-        return;
-      }
-      const uint32_t dst = sbase + C::kOffKv + stage * C::kTileBytes;
-      const int row0 = tile * kTrTile;
-      const int rows = min(kTrTile, g.hi - row0);
-      if (TMA) {
-        const int boxes = (rows + box_rows - 1) / box_rows;
-        if (lane == 0) mbar_arrive_expect_tx(&b_full[stage], (uint32_t)(boxes * box_rows * D * 2));
-        __syncwarp();
-        for (int i = lane; i < boxes * C::kHalves; i += 32) {
-          const int box = i / C::kHalves, half = i % C::kHalves;
-          const int at = row0 + box * box_rows;
-          const int slot = (int)fast_div((uint32_t)at, p.ps_magic, p.ps_shift);
-          const int32_t page = __ldg(p.indices + g.slot_base + slot);
-          int32_t row;
-          if (page >= 0 && page < p.num_pages) {
-            row = page * p.page_size + (at - slot * p.page_size);
-          } else {
-            row = (int32_t)(p.num_pages * p.page_size);  // past the pool: the box is zero-filled
-            if (!is_v && half == 0) report(p.status, PA_DEVICE_BAD_PAGE);
-          }
-          tma_load_3d(smem + C::kOffKv + stage * C::kTileBytes + half * (kTrTile * 128) + box * box_rows * 128,
-                      is_v ? &tm_v : &tm_k, &b_full[stage], half * 64, kvh, row, policy);
-        }
-        __syncwarp();
-      } else {
-        constexpr int kChunks = D / 8;                       // 16-byte pieces of a row
-        constexpr int kPass = kTrLoadThreads / kChunks;      // rows per pass
-        const int ch = u % kChunks;
-        const uint32_t col = (uint32_t)(ch >> 3) * (kTrTile * 128);
-        const T* pool = static_cast<const T*>(is_v ? p.v_pool : p.k_pool) + (int64_t)kvh * D + ch * 8;
-#pragma unroll 8
-        for (int i = 0; i < kTrTile / kPass; ++i) {
-          const int row = i * kPass + u / kChunks;
-          const int at = row0 + row;
-          const uint32_t to = dst + col + sw128(row, ch & 7);
-          bool have = at >= g.lo && at < g.hi;
-          if (have) {
-            const int slot = (int)fast_div((uint32_t)at, p.ps_magic, p.ps_shift);
-            const int32_t page = __ldg(p.indices + g.slot_base + slot);
-            have = page >= 0 && page < p.num_pages;
-            if (have)
-              cp_async_16(to, pool + ((int64_t)page * p.page_size + (at - slot * p.page_size)) * p.hkv * D, policy);
-            else if (ch == 0 && !is_v)
-              report(p.status, PA_DEVICE_BAD_PAGE);
-          }
-          if (!have) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0u) : "memory");
-        }
-        cp_async_commit();
-        if (pend >= 0) {
-          cp_async_wait<1>();
-          publish();
-        }
-        pend = stage;
-      }
-      ++ops;
-      stage = stage + 1 == C::kStages ? 0 : stage + 1;
-    };
-    auto hand_out = [&](const TreePiece& d) {
-      const int at = pieces % kTrRing;
-      // (a second loader warp does not wait here: pieces without key tiles could pass it by)
-      if (leader && !wait_phase(&b_pe[at], ((pieces / kTrRing) & 1) ^ 1, abort_flag, p.status)) {
-        alive = false;
-        return;
-      }
-      if (leader && lane == 0) {
-        ring[at] = d;
-        mbar_arrive(&b_pf[at]);
-      }
-      __syncwarp();
-      ++pieces;
-    };
-
-    int64_t pos = 0;  // units done
-    while (left > 0 && alive && r < p.batch) {
-      g = tree_req(p, r, false);
-      const int64_t per_head = g.units();
-      const int32_t S = segments(g, run);
-      int kvh = per_head > 0 ? (int)(off / per_head) : p.hkv;
-      int64_t x = per_head > 0 ? off % per_head : 0;
-      for (; kvh < p.hkv && left > 0 && alive; ++kvh, x = 0) {
-        for (int s = 0; s < S && left > 0 && alive; ++s) {
-          const int32_t t_begin = seg_begin(g, S, s);
-          const int32_t len_s = seg_begin(g, S, s + 1) - t_begin;
-          const int64_t seg_units = (int64_t)g.blocks * len_s + (s == S - 1 ? g.sum_tail : 0);
-          if (x >= seg_units) {
-            x -= seg_units;
-            continue;
-          }
-          int b = 0;
-          if (len_s > 0 && (s < S - 1 || g.sum_tail == 0)) {
-            b = (int)(x / len_s);
-            x -= (int64_t)b * len_s;
-          }
-          for (; b < g.blocks && left > 0 && alive; ++b) {
-            const int32_t len = len_s + (s == S - 1 ? tail_of(g, p.group, b) : 0);
-            if (x >= len) {
-              x -= len;
-              continue;
-            }
-            TreePiece d;
-            d.kind = g.empty ? kPieceEmpty : kPieceTiles;
-            d.tile = g.tile0 + t_begin + (int32_t)x;
-            d.tiles = (int32_t)min((int64_t)len - x, left);
-            d.lo = g.lo;
-            d.hi = g.hi;
-            d.ds = g.ds;
-            d.t0 = g.t0;
-            d.n = g.n;
-            d.slot_base = g.slot_base;
-            d.row0 = b * kTrBlock;
-            d.rows = min(kTrBlock, g.n * p.group - d.row0);
-            d.kvh = kvh;
-            d.slot = S == 1 && x == 0 && d.tiles == len ? -1 : (int)blockIdx.x * kTrSlots + piece_slot(pos, run);
-            d.tainted = 0;
-            hand_out(d);
-            if (!alive) break;
-            if (d.kind == kPieceTiles) {
-              const int ahead = d.rows > kTrTile ? 1 : 2;  // key tiles S runs ahead of O (as the MMA warp takes them)
-              for (int j = 0; j < min(ahead, d.tiles) && alive; ++j) load(d.tile + j, kvh, false);
-              for (int j = 0; j < d.tiles && alive; ++j) {
-                load(d.tile + j, kvh, true);
-                if (j + ahead < d.tiles && alive) load(d.tile + j + ahead, kvh, false);
-              }
-              if (!TMA && pend >= 0) {
-                cp_async_wait<0>();
-                publish();
-              }
-            }
-            left -= d.tiles;
-            pos += d.tiles;
-            x = 0;
-          }
-          x = 0;
-        }
-      }
-      ++r;
-      off = 0;
-    }
-    if (alive) {
-      TreePiece d = {};
-      d.kind = kPieceEnd;
-      hand_out(d);
-    }
-    if (TMA) {  // no copy of this CTA is left in flight, whatever ended the loop
-      for (int i = max(ops - C::kStages, 0); i < ops; ++i)
-        mbar_wait_bounded(&b_full[i % C::kStages], (uint32_t)((i / C::kStages) & 1), kWaitLimitCycles);
-    } else {
-      cp_async_wait<0>();
-    }
-  } else if (warp == kTrMmaWarp) {
-    // --------------------------------------------------------------------- MMA
-    constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-    constexpr uint32_t id_s = tree_idesc(fmt, kTrTile, false);
-    constexpr uint32_t id_o = tree_idesc(fmt, D, true);
-    int op = 0;
-    uint32_t par_p[2] = {0, 0}, par_q = 0, par_fix = 0;  // par_fix: a bit per stage
-    bool alive = true, issued = false;
-    auto take = [&]() -> int {  // the next loaded stage
-      const int st = op % C::kStages;
-      if (!wait_phase(&b_full[st], (uint32_t)((op / C::kStages) & 1), abort_flag, p.status)) alive = false;
-      ++op;
-      return st;
-    };
-    auto scores = [&](int w, int qt, int st) {
-      if (lane == 0) {
-        const uint32_t qa = sbase + qt * C::kTileBytes, ka = sbase + C::kOffKv + st * C::kTileBytes;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t at = (kk >> 2) * (kTrTile * 128) + (kk & 3) * 32;
-          umma(tmem + col_s(w), smem_desc(qa + at, 16, 1024), smem_desc(ka + at, 16, 1024), id_s, kk != 0);
-        }
-        umma_commit(&b_s[w]);
-        issued = true;
-      }
-      __syncwarp();
-    };
-    auto values = [&](int w, int st, bool acc) {
-      if (!wait_phase(&b_p[w], par_p[w], abort_flag, p.status)) {
-        alive = false;
-        return;
-      }
-      par_p[w] ^= 1;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t va = sbase + C::kOffKv + st * C::kTileBytes;
-#pragma unroll
-        for (int kt = 0; kt < kTrTile / 16; ++kt)
-          umma_ts(tmem + col_o(w), tmem + col_s(w) + 8 * kt, smem_desc(va + kt * 2048, kTrTile * 128, 1024), id_o,
-                  acc || kt != 0);
-      }
-      __syncwarp();
-    };
-    auto release = [&](int st) {
-      if (lane == 0) umma_commit(&b_empty[st]);
-      __syncwarp();
-    };
-    for (int pc = 0; alive; ++pc) {
-      const int at = pc % kTrRing;
-      if (!wait_phase(&b_pf[at], (uint32_t)((pc / kTrRing) & 1), abort_flag, p.status)) break;
-      const TreePiece d = ring[at];
-      if (d.kind == kPieceEnd) break;
-      if (d.kind == kPieceTiles) {
-        const bool dual = d.rows > kTrTile;
-        // Q is written, and both streams are done with the piece before
-        if (!wait_phase(b_q, par_q, abort_flag, p.status)) break;
-        par_q ^= 1;
-        tc_fence_after();
-        auto wait_fix = [&](int tile, int st) {
-          if (!needs_fix(d, tile)) return;
-          if (!wait_phase(&b_fix[st], par_fix >> st & 1u, abort_flag, p.status)) alive = false;
-          par_fix ^= 1u << st;
-        };
-        if (dual) {
-          int k = take();
-          if (!alive) break;
-          scores(0, 0, k);
-          scores(1, 1, k);
-          release(k);
-          for (int j = 0; j < d.tiles && alive; ++j) {
-            const int v = take();
-            if (alive) wait_fix(d.tile + j, v);
-            if (alive) values(0, v, j > 0);
-            if (alive && j + 1 < d.tiles) {
-              k = take();
-              if (alive) scores(0, 0, k);
-            }
-            if (alive) values(1, v, j > 0);
-            if (!alive) break;
-            release(v);
-            if (j + 1 < d.tiles) {
-              scores(1, 1, k);
-              release(k);
-            }
-          }
-        } else {
-          for (int w = 0; w < min(2, d.tiles) && alive; ++w) {
-            const int k = take();
-            if (!alive) break;
-            scores(w, 0, k);
-            release(k);
-          }
-          for (int j = 0; j < d.tiles && alive; ++j) {
-            const int v = take();
-            if (alive) wait_fix(d.tile + j, v);
-            if (alive) values(j & 1, v, j > 1);
-            if (!alive) break;
-            release(v);
-            if (j + 2 < d.tiles) {
-              const int k = take();
-              if (!alive) break;
-              scores(j & 1, 0, k);
-              release(k);
-            }
-          }
-        }
-        if (!alive) break;
-        if (lane == 0) umma_commit(b_o);
-        __syncwarp();
-      }
-      if (lane == 0) mbar_arrive(&b_pe[at]);
-      __syncwarp();
-    }
-    // every MMA of this CTA has completed before tensor memory is released
-    if (lane == 0 && issued) umma_commit(b_drain);
-    __syncwarp();
-    if (__shfl_sync(0xffffffffu, issued ? 1 : 0, 0)) {
-      if (!mbar_wait_bounded(b_drain, 0, kWaitLimitCycles) && lane == 0) report(p.status, PA_DEVICE_WAIT_TIMEOUT);
-    }
-    __syncwarp();
-  } else if (warp == kTrFixWarp) {
-    // --------------------------------------------------------- V tiles made safe
-    int op = 0;
-    bool alive = true;
-    for (int pc = 0; alive; ++pc) {
-      const int at = pc % kTrRing;
-      if (!wait_phase(&b_pf[at], (uint32_t)((pc / kTrRing) & 1), abort_flag, p.status)) break;
-      const TreePiece d = ring[at];
-      if (d.kind == kPieceEnd) break;
-      if (d.kind == kPieceTiles) {
-        // every stage is waited for and released, K tiles too: a wait names a phase by its parity, which only
-        // tells phases apart that are at most one apart
-        auto stage_of = [&](bool last) -> int {
-          const int st = op % C::kStages;
-          if (!wait_phase(&b_full[st], (uint32_t)((op / C::kStages) & 1), abort_flag, p.status)) alive = false;
-          ++op;
-          if (last && alive && lane == 0) mbar_arrive(&b_empty[st]);
-          return st;
-        };
-        const int ahead = d.rows > kTrTile ? 1 : 2;
-        for (int j = 0; j < min(ahead, d.tiles) && alive; ++j) stage_of(true);
-        for (int j = 0; j < d.tiles && alive; ++j) {
-          const bool fix = needs_fix(d, d.tile + j);
-          const int st = stage_of(!fix);
-          if (!alive) break;
-          const int c0 = (d.tile + j) * kTrTile;
-          if (!fix) {
-            if (j + ahead < d.tiles) stage_of(true);
-            continue;
-          }
-          constexpr int kChunks = D / 8;
-          const uint32_t base = sbase + C::kOffKv + st * C::kTileBytes;
-          const int ch = lane % kChunks;
-          const uint32_t col = base + (uint32_t)(ch >> 3) * (kTrTile * 128);
-          uint32_t any = 0;
-          auto fix_rows = [&](int r0, int r1) {
-#pragma unroll 4
-            for (int row = r0 + lane / kChunks; row < r1; row += 32 / kChunks) {
-              const uint32_t a = col + sw128(row, ch & 7);
-              uint32_t x0, x1, x2, x3;
-              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
-                           : "r"(a)
-                           : "memory");
-              const int pr = c0 + row;
-              const bool inside = pr >= d.lo && pr < d.hi;
-              constexpr uint32_t e = ExpBits<T>::k;
-              const uint32_t n0 = sat_mask(x0, e), n1 = sat_mask(x1, e), n2 = sat_mask(x2, e), n3 = sat_mask(x3, e);
-              const uint32_t bad = n0 | n1 | n2 | n3;
-              if (inside) any |= bad;
-              if (!inside || bad) {
-                const uint32_t keep = inside ? 0xffffffffu : 0u;
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x0 & ~n0 & keep),
-                             "r"(x1 & ~n1 & keep), "r"(x2 & ~n2 & keep), "r"(x3 & ~n3 & keep)
-                             : "memory");
-              }
-            }
-          };
-          const int head = min(max(d.lo - c0, 0), kTrTile), tail = min(max(d.ds - c0, head), kTrTile);
-          fix_rows(0, head);
-          fix_rows(tail, kTrTile);
-          if (__any_sync(0xffffffffu, any != 0) && lane == 0) *reinterpret_cast<volatile int32_t*>(&ring[at].tainted) = 1;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&b_fix[st]);
-            mbar_arrive(&b_empty[st]);
-          }
-          __syncwarp();
-          if (j + ahead < d.tiles) stage_of(true);
-        }
-      }
-      if (!alive) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b_pe[at]);
-    }
-  } else if (warp < 8) {
+  // Registers follow the roles: 208 for the softmax threads, which hold a row of scores, 88 for the others
+  // (256 * 208 + 128 * 88 = 384 * 168).  Each warpgroup sets its own count on its own path.
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ----------------------------------------------------------------- softmax
     const int w = warp >> 2;                 // stream
     const int row = (warp & 3) * 32 + lane;  // tile row = tensor-memory lane
@@ -772,39 +603,49 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     for (int pc = 0; alive; ++pc) {
       const int at = pc % kTrRing;
       if (!wait_phase(&b_pf[at], (uint32_t)((pc / kTrRing) & 1), abort_flag, p.status)) break;
-      const TreePiece d = ring[at];
-      if (d.kind == kPieceEnd) break;
-      const bool dual = d.rows > kTrTile;
+      // read again from shared memory where it is needed: kept in registers across the tiles it would be spilled
+      const volatile TreePiece& d = ring[at];
+      const int kind = d.kind, rows = d.rows;
+      if (kind == kPieceEnd) break;
+      const bool dual = rows > kTrTile;
       const int rr = (dual ? w * kTrTile : 0) + row;         // row of the block
-      const bool valid = rr < d.rows;
-      const bool busy = (rr & ~31) < d.rows;                 // a row of this warp is
-      const int qrow = d.row0 + min(rr, d.rows - 1);         // row of the request
-      const int tok = (int)fast_div((uint32_t)qrow, p.g_magic, p.g_shift);
-      const int64_t orow = (int64_t)(d.t0 + tok) * p.hq + (int64_t)d.kvh * p.group + (qrow - tok * p.group);
+      const bool busy = (rr & ~31) < rows;                   // a row of this warp is of the block
+      const int tok = (int)fast_div((uint32_t)(d.row0 + min(rr, rows - 1)), p.g_magic, p.g_shift);
       float m = -INFINITY, l = 0.f;
-      if (d.kind == kPieceTiles) {
-        // ---- Q, swizzled like the key tiles; rows past the block are zeros
+      if (kind == kPieceTiles) {
+        // ---- Q, swizzled like the key tiles; rows past the block repeat its last one (their results go nowhere)
         if (pending_x) {  // the exchanged state of the piece before shares the Q tiles' memory
           if (!wait_phase(b_xd, par_xd, abort_flag, p.status)) break;
           par_xd ^= 1;
           pending_x = false;
         }
         {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + orow * D);
+          // a row's 16-byte pieces on neighbouring lanes; a warp fills its own 32 rows of its stream's tile, or,
+          // when both streams read tile A, 16 of them
+          constexpr int kChunks = D / 8, kPass = 32 / kChunks;
           unsigned char* dst = smem + (dual ? w : 0) * C::kTileBytes;
-          constexpr int kChunks = D / 8;
-          const int c_begin = dual ? 0 : w * (kChunks / 2), c_end = dual ? kChunks : c_begin + kChunks / 2;
-#pragma unroll 8
-          for (int c = c_begin; c < c_end; ++c) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (valid) {
-              x = __ldg(src + c);
-              x.x = (x.x ^ p.q_xor) & p.q_and;
-              x.y = (x.y ^ p.q_xor) & p.q_and;
-              x.z = (x.z ^ p.q_xor) & p.q_and;
-              x.w = (x.w ^ p.q_xor) & p.q_and;
-            }
-            *reinterpret_cast<uint4*>(dst + (c >> 3) * (kTrTile * 128) + sw128(row, c & 7)) = x;
+          const int c = lane % kChunks;
+          const int first = dual ? (warp & 3) * 32 : warp * 16, count = dual ? 32 : 16;
+          const int row0 = d.row0, t0 = d.t0, kvh = d.kvh;
+          constexpr int kBatch = 32 / kPass;  // all loads before the first store
+          uint4 x[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            if (i * kPass >= count) break;
+            const int br = min((dual ? w * kTrTile : 0) + first + i * kPass + lane / kChunks, rows - 1);
+            const int tk = (int)fast_div((uint32_t)(row0 + br), p.g_magic, p.g_shift);
+            const int64_t qr = (int64_t)(t0 + tk) * p.hq + (int64_t)kvh * p.group + (row0 + br - tk * p.group);
+            x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + qr * D) + c);
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            if (i * kPass >= count) break;
+            const int tr = first + i * kPass + lane / kChunks;
+            x[i].x = (x[i].x ^ p.q_xor) & p.q_and;
+            x[i].y = (x[i].y ^ p.q_xor) & p.q_and;
+            x[i].z = (x[i].z ^ p.q_xor) & p.q_and;
+            x[i].w = (x[i].w ^ p.q_xor) & p.q_and;
+            *reinterpret_cast<uint4*>(dst + (c >> 3) * (kTrTile * 128) + sw128(tr, c & 7)) = x[i];
           }
           fence_proxy_async_smem();
           tc_fence_before();
@@ -812,7 +653,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           if (lane == 0) mbar_arrive(b_q);
         }
         // ---- key tiles
-        for (int j = dual ? 0 : w; j < d.tiles; j += dual ? 1 : 2) {
+        const int tiles = d.tiles, tile0 = d.tile, clear0 = d.lo, clear1 = d.ds;  // no mask inside [clear0, clear1)
+        for (int j = dual ? 0 : w; j < tiles; j += dual ? 1 : 2) {
           if (!wait_phase(&b_s[w], par_s, abort_flag, p.status)) {
             alive = false;
             break;
@@ -820,29 +662,32 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           par_s ^= 1;
           tc_fence_after();
           if (busy) {
-            const int c0 = (d.tile + j) * kTrTile;
-            const bool edge = needs_fix(d, d.tile + j);
-            uint32_t vis[4];
+            const int c0 = (tile0 + j) * kTrTile;
+            const bool edge = c0 < clear0 || c0 + kTrTile > clear1;
+            uint32_t x[2][64];  // the row's scores
+            __syncwarp();
+            tmem_ld64(t_s, x[0]);
+            tmem_ld64(t_s + 64, x[1]);
+            tmem_wait64(x[0]);
+            tmem_wait64(x[1]);
             if (edge) {
+              const int hi = d.hi, t0 = d.t0;
 #pragma unroll
-              for (int c = 0; c < 4; ++c) vis[c] = visible_bits(p, d, tok, c0 + 32 * c);
-            }
-            float mx = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t x[32];
-              __syncwarp();
-              tmem_ld32(t_s + 32 * c, x);
-              if (edge) {
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t vis = visible_bits(p, clear0, clear1, hi, t0 + tok, tok, c0 + 32 * c);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                  mx = fmaxf(mx, (vis[c] >> i) & 1u ? __uint_as_float(x[i]) : -INFINITY);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(x[i]));
+                  x[c >> 1][(c & 1) * 32 + i] = (vis >> i) & 1u ? x[c >> 1][(c & 1) * 32 + i] : 0xff800000u;
               }
             }
-            const float mt = mx * scale;
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 64; i += 4) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mx[k] = max3(mx[k], __uint_as_float(x[0][i + k]), __uint_as_float(x[1][i + k]));
+            }
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
             const bool need = mt > m + kLazy;  // m = -inf at first: any finite maximum
             const float a = need ? (m == -INFINITY ? 0.f : fast_exp2(m - mt)) : 1.f;
             if (need) m = mt;
@@ -860,36 +705,35 @@ __global__ void __launch_bounds__(kTrThreads, 1)
               }
             }
             const float mu = (m == -INFINITY ? 0.f : m) - kShift;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const float2 scale2 = make_float2(scale, scale), off2 = make_float2(-mu, -mu);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t pk[32];
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                uint32_t x[32];
-                __syncwarp();
-                tmem_ld32(t_s + 64 * h + 32 * c, x);
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  float y0 = fast_exp2(fmaf(__uint_as_float(x[i]), scale, -mu));
-                  float y1 = fast_exp2(fmaf(__uint_as_float(x[i + 1]), scale, -mu));
-                  if (edge) {
-                    y0 = (vis[2 * h + c] >> i) & 1u ? y0 : 0.f;
-                    y1 = (vis[2 * h + c] >> (i + 1)) & 1u ? y1 : 0.f;
-                  }
-                  sum[i & 2] += y0;
-                  sum[(i & 2) + 1] += y1;
-                  pk[16 * c + i / 2] = TC<T>::pack(y0, y1);
-                }
+              for (int i = 0; i < 64; i += 2) {
+                float2 y = fma2(make_float2(__uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1])), scale2, off2);
+                y.x = fast_exp2(y.x);
+                y.y = fast_exp2(y.y);
+                sum[i >> 1 & 1] = add2(sum[i >> 1 & 1], y);
+                pk[i / 2] = TC<T>::pack(y.x, y.y);
               }
               __syncwarp();
               tmem_st32(t_s + 32 * h, pk);
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&b_p[2 * w + h]);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            sum[0] = add2(sum[0], sum[1]);
+            l += sum[0].x + sum[0].y;
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&b_p[2 * w]);
+              mbar_arrive(&b_p[2 * w + 1]);
+            }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&b_p[w]);
         }
         if (!alive) break;
         if (!wait_phase(b_o, par_o, abort_flag, p.status)) break;
@@ -898,7 +742,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       }
 
       // ---- the piece's result
-      const bool joined = d.kind == kPieceTiles && !dual && d.tiles > 1;  // two streams to join
+      const bool joined = kind == kPieceTiles && !dual && d.tiles > 1;  // two streams to join
       float4* xo = reinterpret_cast<float4*>(smem);                       // [D / 4][128], over the Q tiles
       if (joined && w == 1) {
         if (busy) {
@@ -934,17 +778,20 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           l = l * s0 + l1 * s1;
           m = M;
         }
-        const bool nothing = l == 0.f;  // no visible key (a NaN sum stays NaN)
-        const float inv = nothing ? 0.f : 1.f / l;
+        const bool nothing = nothing_seen(l);
+        const float inv = nothing ? 0.f : fast_rcp(l);
         const float lse = nothing ? -INFINITY : m - kShift + fast_log2(l);
-        const bool tainted = d.kind == kPieceTiles && *reinterpret_cast<volatile int32_t*>(&ring[at].tainted) != 0;
+        if (kind == kPieceTiles && d.tainted != 0 && !nothing_seen(l)) put_back<T, D>(p, ring[at], tok, t_o);
+        const bool valid = rr < rows, whole = d.slot < 0;
+        const int qrow = d.row0 + min(rr, rows - 1);  // row of the request
+        const int64_t orow = (int64_t)(d.t0 + tok) * p.hq + (int64_t)d.kvh * p.group + (qrow - tok * p.group);
         T* out = static_cast<T*>(p.out) + orow * D;
         float* slot = p.slots + (int64_t)max(d.slot, 0) * C::kSlotFloats;
         float4* part = reinterpret_cast<float4*>(slot) + (rr >> 7) * (D / 4 * kTrTile) + row;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
-          if (d.kind == kPieceTiles) {
+          if (kind == kPieceTiles) {
             __syncwarp();
             tmem_ld32(t_o + 32 * c, o);
           }
@@ -961,24 +808,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
               v[4 * i + 3] = v[4 * i + 3] * s0 + y.w * s1;
             }
           }
-          if (tainted && !nothing) {
-            // the non-finite values the fix warp took out, back to the rows that see them
-            const int k0 = max(d.tile * kTrTile, d.ds), k1 = min((d.tile + d.tiles) * kTrTile, d.hi);
-            for (int k = k0; k < k1; ++k) {
-              if (!(visible_bits(p, d, tok, k) & 1u)) continue;
-              const int sl = (int)fast_div((uint32_t)k, p.ps_magic, p.ps_shift);
-              const int32_t page = __ldg(p.indices + d.slot_base + sl);
-              if (page < 0 || page >= p.num_pages) continue;
-              const T* src = static_cast<const T*>(p.v_pool) +
-                             (((int64_t)page * p.page_size + (k - sl * p.page_size)) * p.hkv + d.kvh) * D + 32 * c;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float y = half_of(src + i);
-                if (!isfinite(y)) v[i] += y;
-              }
-            }
-          }
-          if (valid && d.slot < 0) {
+          if (valid && whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) =
@@ -994,7 +824,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           }
         }
         if (valid) {
-          if (d.slot < 0)
+          if (whole)
             p.lse_out[orow] = lse;
           else
             slot[(int64_t)kTrBlock * D + rr] = lse;
@@ -1006,6 +836,404 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         mbar_arrive(&b_pe[at]);
       }
       __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == kTrLoadWarp || warp == kTrLoadWarp + 1) {
+      // ------------------------------------------------------------------ loader
+      const bool leader = warp == kTrLoadWarp;
+      TreeReq mine = {};
+      TreeCut cut;
+      if (small) {
+        if (lane < p.batch) mine = tree_req(p, lane, leader && blockIdx.x == 0);
+        cut = cut_warp(p, blockIdx.x, 0, mine, lane);
+      } else {
+        cut = *start;
+      }
+      const int32_t run = cut.run;
+      int stage = 0, pieces = 0, ops = 0;
+      int pend = -1;  // without TMA: the stage whose copies are not published yet
+      bool alive = true;
+      const int u = (warp - kTrLoadWarp) * 32 + lane;
+      TreeReq g = {};
+      const int box_rows = p.box_rows;
+const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
+
+      auto publish = [&]() {  // without TMA: the pending stage's copies have landed
+        fence_proxy_async_smem();
+        mbar_arrive(&b_full[pend]);
+        pend = -1;
+      };
+      // (keys that several blocks read stay in L2 as other data does, the others leave it first)
+      // K (or V) rows [128 tile, 128 tile + 128) of the request's pages into the next stage
+      auto load = [&](int tile, int kvh, bool is_v) {
+        if (TMA && is_v == leader) {  // the other warp's
+          ++ops;
+          stage = stage + 1 == C::kStages ? 0 : stage + 1;
+          return;
+        }
+        if (!wait_phase(&b_empty[stage], ((ops / C::kStages) & 1) ^ 1, abort_flag, p.status)) {
+          alive = false;
+          return;
+        }
+        const uint64_t policy = g.blocks > 1 ? normal : first;
+        const uint32_t dst = sbase + C::kOffKv + stage * C::kTileBytes;
+        const int row0 = tile * kTrTile;
+        const int rows = min(kTrTile, g.hi - row0);
+        if (TMA) {
+          // lane i resolves box i; one thread issues them all (copies whose operands differ from lane to lane are
+          // issued one lane at a time anyway, at several times the cost)
+          const int boxes = (rows + box_rows - 1) / box_rows;
+          int32_t mine_row = 0;
+          if (lane < boxes) {
+            const int at = row0 + lane * box_rows;
+            const int slot = (int)fast_div((uint32_t)at, p.ps_magic, p.ps_shift);
+            const int32_t page = __ldg(p.indices + g.slot_base + slot);
+            if (page >= 0 && page < p.num_pages) {
+              mine_row = page * p.page_size + (at - slot * p.page_size);
+            } else {
+              mine_row = (int32_t)(p.num_pages * p.page_size);  // past the pool: the box is zero-filled
+              if (!is_v) report(p.status, PA_DEVICE_BAD_PAGE);
+            }
+          }
+          volatile int32_t* box_row = boxes_of[u >> 5];
+          if (lane < 16) box_row[lane] = mine_row;
+          __syncwarp();
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&b_full[stage], (uint32_t)(boxes * box_rows * D * 2));
+            unsigned char* to = smem + C::kOffKv + stage * C::kTileBytes;
+#pragma unroll 2
+            for (int i = 0; i < boxes; ++i, to += box_rows * 128) {
+              const int32_t row = box_row[i];
+#pragma unroll
+              for (int half = 0; half < C::kHalves; ++half)
+                tma_load_3d(to + half * (kTrTile * 128), is_v ? &tm_v : &tm_k, &b_full[stage], half * 64, kvh, row,
+                            policy);
+            }
+          }
+          __syncwarp();
+        } else {
+          constexpr int kChunks = D / 8;                       // 16-byte pieces of a row
+          constexpr int kPass = kTrLoadThreads / kChunks;      // rows per pass
+          const int ch = u % kChunks;
+          const uint32_t col = (uint32_t)(ch >> 3) * (kTrTile * 128);
+          const T* pool = static_cast<const T*>(is_v ? p.v_pool : p.k_pool) + (int64_t)kvh * D + ch * 8;
+  #pragma unroll 8
+          for (int i = 0; i < kTrTile / kPass; ++i) {
+            const int row = i * kPass + u / kChunks;
+            const int at = row0 + row;
+            const uint32_t to = dst + col + sw128(row, ch & 7);
+            bool have = at >= g.lo && at < g.hi;
+            if (have) {
+              const int slot = (int)fast_div((uint32_t)at, p.ps_magic, p.ps_shift);
+              const int32_t page = __ldg(p.indices + g.slot_base + slot);
+              have = page >= 0 && page < p.num_pages;
+              if (have)
+                cp_async_16(to, pool + ((int64_t)page * p.page_size + (at - slot * p.page_size)) * p.hkv * D, policy);
+              else if (ch == 0 && !is_v)
+                report(p.status, PA_DEVICE_BAD_PAGE);
+            }
+            if (!have) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0u) : "memory");
+          }
+          cp_async_commit();
+          if (pend >= 0) {
+            cp_async_wait<1>();
+            publish();
+          }
+          pend = stage;
+        }
+        ++ops;
+        stage = stage + 1 == C::kStages ? 0 : stage + 1;
+      };
+      auto hand_out = [&](const TreePiece& d) {
+        const int at = pieces % kTrRing;
+        // (a second loader warp does not wait here: pieces without key tiles could pass it by)
+        if (leader && !wait_phase(&b_pe[at], ((pieces / kTrRing) & 1) ^ 1, abort_flag, p.status)) {
+          alive = false;
+          return;
+        }
+        if (leader && lane == 0) {
+          ring[at] = d;
+          mbar_arrive(&b_pf[at]);
+        }
+        __syncwarp();
+        ++pieces;
+      };
+
+      // key tiles [t0, t0 + tiles) of block b
+      auto piece = [&](int kvh, int b, int32_t t0, int32_t tiles, int slot) {
+        TreePiece d;
+        d.kind = g.kind == kReqEmpty ? kPieceEmpty : kPieceTiles;
+        d.tile = g.tile0 + t0;
+        d.tiles = tiles;
+        d.lo = g.lo;
+        d.hi = g.hi;
+        d.ds = g.ds;
+        d.t0 = g.t0;
+        d.n = g.n;
+        d.slot_base = g.slot_base;
+        d.row0 = b * kTrBlock;
+        d.rows = min(kTrBlock, g.n * p.group - d.row0);
+        d.kvh = kvh;
+        d.slot = slot;
+        d.tainted = 0;
+        hand_out(d);
+        if (!alive || d.kind == kPieceEmpty) return;
+        const int ahead = d.rows > kTrTile ? 1 : 2;  // key tiles S runs ahead of O (as the MMA warp takes them)
+        for (int j = 0; j < tiles + ahead && alive; ++j) {
+          if (j >= ahead) load(d.tile + j - ahead, kvh, true);
+          if (j < tiles && alive) load(d.tile + j, kvh, false);
+        }
+        if (!TMA && pend >= 0) {
+          cp_async_wait<0>();
+          publish();
+        }
+      };
+
+      int r = cut.r;
+      if (r < p.batch && (int)blockIdx.x < cut.chunks) {
+        g = small ? shfl_req(mine, r) : tree_req(p, r, false);
+        const HeadCut h = head_cut(g, p.group, run);
+        const int kvh = (int)div_units(cut.off, h.chunks);
+        const BlockAt k = block_at(g, p.group, run, (int32_t)(cut.off - (int64_t)kvh * h.chunks), true);
+        piece(kvh, k.b, k.x * run, run, k.tiles == run ? -1 : (int)blockIdx.x);
+      } else {
+        int64_t off = cut.off;
+        int32_t left = (int32_t)min((int64_t)cut.stretch,
+                                    cut.weight - (int64_t)((int)blockIdx.x - cut.chunks) * cut.stretch);
+        int chunks_before = cut.r_chunks;
+        for (; r < p.batch && left > 0 && alive; ++r, off = 0) {
+          g = small ? shfl_req(mine, r) : tree_req(p, r, false);
+          const HeadCut h = head_cut(g, p.group, run);
+          int kvh = h.weight > 0 ? (int)div_units(off, h.weight) : p.hkv;
+          int32_t in_head = (int32_t)(off - (int64_t)kvh * h.weight);
+          for (; kvh < p.hkv && left > 0 && alive; ++kvh, in_head = 0) {
+            BlockAt k = block_at(g, p.group, run, in_head, false);
+            while (left > 0 && alive) {
+              const int32_t chunks = k.tiles / run;
+              const int32_t weight = rest_weight(k.tiles, run);
+              const int32_t take = min(weight - k.x, left);
+              const int32_t t0 = max(k.x - kTrRestCost, 0), t1 = max(k.x + take - kTrRestCost, 0);
+              const bool ends = k.x + take == weight;
+              if (t1 > t0)
+                piece(kvh, k.b, chunks * run + t0, t1 - t0,
+                      ends && t0 == 0 && chunks == 0
+                          ? -1
+                          : rest_slot(ends, chunks, chunks_before + kvh * h.chunks + k.chunks, blockIdx.x, p.ctas));
+              left -= take;
+              if (k.b + 1 >= g.blocks) break;
+              k.chunks += chunks;
+              ++k.b;
+              k.tiles = tiles_of(g, p.group, k.b);
+              k.x = 0;
+            }
+          }
+          chunks_before += p.hkv * h.chunks;
+        }
+      }
+      if (alive) {
+        TreePiece d = {};
+        d.kind = kPieceEnd;
+        hand_out(d);
+      }
+      if (TMA) {  // no copy of this CTA is left in flight, whatever ended the loop
+        for (int i = max(ops - C::kStages, 0); i < ops; ++i)
+          mbar_wait_bounded(&b_full[i % C::kStages], (uint32_t)((i / C::kStages) & 1), kWaitLimitCycles);
+      } else {
+        cp_async_wait<0>();
+      }
+    } else if (warp == kTrMmaWarp) {
+      // --------------------------------------------------------------------- MMA
+      constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+      constexpr uint32_t id_s = tree_idesc(fmt, kTrTile, false);
+      constexpr uint32_t id_o = tree_idesc(fmt, D, true);
+      if (elect_one()) {
+        int op = 0;
+        uint32_t par_p[2] = {0, 0}, par_q = 0, par_fix = 0;  // par_fix: a bit per stage
+        bool alive = true, issued = false;
+        auto take = [&]() -> int {  // the next loaded stage
+          const int st = op % C::kStages;
+          if (!wait_one(&b_full[st], (uint32_t)((op / C::kStages) & 1), abort_flag, p.status)) alive = false;
+          ++op;
+          return st;
+        };
+        auto scores = [&](int w, int qt, int st) {
+          const uint32_t qa = desc_lo(sbase + qt * C::kTileBytes, 16);
+          const uint32_t ka = desc_lo(sbase + C::kOffKv + st * C::kTileBytes, 16);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t at = ((kk >> 2) * (kTrTile * 128) + (kk & 3) * 32) >> 4;
+            umma_lo(tmem + col_s(w), qa + at, ka + at, id_s, kk != 0);
+          }
+          umma_commit(&b_s[w]);
+          issued = true;
+        };
+        auto values = [&](int w, int st, bool acc) {
+          const uint32_t va = desc_lo(sbase + C::kOffKv + st * C::kTileBytes, kTrTile * 128);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // the first half of the keys while the softmax still works on the second
+            if (!wait_one(&b_p[2 * w + h], par_p[w], abort_flag, p.status)) {
+              alive = false;
+              return;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int kt = 4 * h; kt < 4 * h + 4; ++kt)
+              umma_ts(tmem + col_o(w), tmem + col_s(w) + 8 * kt, va + kt * (2048 >> 4), id_o, acc || kt != 0);
+          }
+          par_p[w] ^= 1;
+        };
+        auto release = [&](int st) { umma_commit(&b_empty[st]); };
+        for (int pc = 0; alive; ++pc) {
+          const int at = pc % kTrRing;
+          if (!wait_one(&b_pf[at], (uint32_t)((pc / kTrRing) & 1), abort_flag, p.status)) break;
+          const TreePiece d = ring[at];
+          if (d.kind == kPieceEnd) break;
+          if (d.kind == kPieceTiles) {
+            const bool dual = d.rows > kTrTile;
+            // Q is written, and both streams are done with the piece before
+            if (!wait_one(b_q, par_q, abort_flag, p.status)) break;
+            par_q ^= 1;
+            tc_fence_after();
+            auto wait_fix = [&](int tile, int st) {
+              if (!needs_fix(d, tile)) return;
+              if (!wait_one(&b_fix[st], par_fix >> st & 1u, abort_flag, p.status)) alive = false;
+              par_fix ^= 1u << st;
+            };
+            if (dual) {
+              // the next tile is waited for while the products before it still run
+              int k = take();
+              if (!alive) break;
+              scores(0, 0, k);
+              scores(1, 1, k);
+              release(k);
+              int v = take();
+              for (int j = 0; j < d.tiles && alive; ++j) {
+                const bool more = j + 1 < d.tiles;
+                wait_fix(d.tile + j, v);
+                if (alive) values(0, v, j > 0);
+                if (alive && more) k = take();
+                if (!alive) break;
+                if (more) scores(0, 0, k);
+                values(1, v, j > 0);
+                if (!alive) break;
+                release(v);
+                if (more) {
+                  v = take();
+                  if (!alive) break;
+                  scores(1, 1, k);
+                  release(k);
+                }
+              }
+            } else {
+              for (int w = 0; w < min(2, d.tiles) && alive; ++w) {
+                const int k = take();
+                if (!alive) break;
+                scores(w, 0, k);
+                release(k);
+              }
+              for (int j = 0; j < d.tiles && alive; ++j) {
+                const int v = take();
+                if (alive) wait_fix(d.tile + j, v);
+                if (alive) values(j & 1, v, j > 1);
+                if (!alive) break;
+                release(v);
+                if (j + 2 < d.tiles) {
+                  const int k = take();
+                  if (!alive) break;
+                  scores(j & 1, 0, k);
+                  release(k);
+                }
+              }
+            }
+            if (!alive) break;
+            umma_commit(b_o);
+          }
+          mbar_arrive(&b_pe[at]);
+        }
+        // every MMA of this CTA has completed before tensor memory is released
+        if (issued) {
+          umma_commit(b_drain);
+          if (!mbar_wait_bounded(b_drain, 0, kWaitLimitCycles)) report(p.status, PA_DEVICE_WAIT_TIMEOUT);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kTrFixWarp) {
+      // --------------------------------------------------------- V tiles made safe
+      int op = 0;
+      bool alive = true;
+      for (int pc = 0; alive; ++pc) {
+        const int at = pc % kTrRing;
+        if (!wait_phase(&b_pf[at], (uint32_t)((pc / kTrRing) & 1), abort_flag, p.status)) break;
+        const TreePiece d = ring[at];
+        if (d.kind == kPieceEnd) break;
+        if (d.kind == kPieceTiles) {
+          // every stage is waited for and released, K tiles too: a wait names a phase by its parity, which only
+          // tells phases apart that are at most one apart
+          auto stage_of = [&](bool last) -> int {
+            const int st = op % C::kStages;
+            if (!wait_phase(&b_full[st], (uint32_t)((op / C::kStages) & 1), abort_flag, p.status)) alive = false;
+            ++op;
+            if (last && alive && lane == 0) mbar_arrive(&b_empty[st]);
+            return st;
+          };
+          const int ahead = d.rows > kTrTile ? 1 : 2;
+          for (int j = 0; j < min(ahead, d.tiles) && alive; ++j) stage_of(true);
+          for (int j = 0; j < d.tiles && alive; ++j) {
+            const bool fix = needs_fix(d, d.tile + j);
+            const int st = stage_of(!fix);
+            if (!alive) break;
+            const int c0 = (d.tile + j) * kTrTile;
+            if (!fix) {
+              if (j + ahead < d.tiles) stage_of(true);
+              continue;
+            }
+            constexpr int kChunks = D / 8;
+            const uint32_t base = sbase + C::kOffKv + st * C::kTileBytes;
+            const int ch = lane % kChunks;
+            const uint32_t col = base + (uint32_t)(ch >> 3) * (kTrTile * 128);
+            uint32_t any = 0;
+            auto fix_rows = [&](int r0, int r1) {
+  #pragma unroll 4
+              for (int row = r0 + lane / kChunks; row < r1; row += 32 / kChunks) {
+                const uint32_t a = col + sw128(row, ch & 7);
+                uint32_t x0, x1, x2, x3;
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
+                             : "r"(a)
+                             : "memory");
+                const int pr = c0 + row;
+                const bool inside = pr >= d.lo && pr < d.hi;
+                constexpr uint32_t e = ExpBits<T>::k;
+                const uint32_t n0 = sat_mask(x0, e), n1 = sat_mask(x1, e), n2 = sat_mask(x2, e), n3 = sat_mask(x3, e);
+                const uint32_t bad = n0 | n1 | n2 | n3;
+                if (inside) any |= bad;
+                if (!inside || bad) {
+                  const uint32_t keep = inside ? 0xffffffffu : 0u;
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x0 & ~n0 & keep),
+                               "r"(x1 & ~n1 & keep), "r"(x2 & ~n2 & keep), "r"(x3 & ~n3 & keep)
+                               : "memory");
+                }
+              }
+            };
+            const int head = min(max(d.lo - c0, 0), kTrTile), tail = min(max(d.ds - c0, head), kTrTile);
+            fix_rows(0, head);
+            fix_rows(tail, kTrTile);
+            if (__any_sync(0xffffffffu, any != 0) && lane == 0) *reinterpret_cast<volatile int32_t*>(&ring[at].tainted) = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&b_fix[st]);
+              mbar_arrive(&b_empty[st]);
+            }
+            __syncwarp();
+            if (j + ahead < d.tiles) stage_of(true);
+          }
+        }
+        if (!alive) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_pe[at]);
+    }
     }
   }
 
@@ -1020,72 +1248,84 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 }
 
 // Folds the partial results of blocks that were cut: weights 2^(lse_i - max) of the normalized parts, in the
-// order of the keys.  A KV head of a request with cuts is shared out over the CTAs of the cuts inside it (cut c
-// is unit c * run); a warp takes 32 rows x 8 columns, one row per lane (the parts are stored column by column, so
-// a warp's loads are contiguous), eight parts in flight.
+// order of the keys.  A block with chunks is shared out over the CTAs of its chunks, one without over the CTAs
+// whose stretches cut it; a warp takes 32 rows x 8 columns, one row per lane (the parts are stored column by
+// column, so a warp's loads are contiguous), eight parts in flight.
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads) pa_v2_tree_merge_kernel(const TreeParams p) {
-  __shared__ TreeStart start;
+  __shared__ TreeCut start;
   __shared__ int64_t warp_sum[kMergeThreads / 32];
+  using C = TreeCfg<D>;
+  const int lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait_prerequisites();
-  const int64_t cut = (int64_t)blockIdx.x + 1;
-  tree_schedule<kMergeThreads>(p, cut, false, &start, warp_sum);
-  if (start.r >= p.batch) return;
-  const int64_t run = start.run, unit = cut * run;
-  const TreeReq g = tree_req(p, start.r, false);
-  if (g.empty) return;
-  const int64_t per_head = g.units();
-  const int kvh = (int)(start.off / per_head);
-  const int64_t first = unit - start.off % per_head;  // first unit of this KV head
-  if (first == unit) return;                          // the cut falls between two heads
-  const int64_t c_first = first / run + 1, c_last = (first + per_head - 1) / run;
-  const int32_t S = segments(g, run);
-  const int rows = g.n * p.group;
-  const int64_t jobs = (int64_t)((rows + 31) / 32) * (D / 8);
-  const int64_t workers = (c_last - c_first + 1) * gridDim.y * (kMergeThreads / 32);
-  const int64_t me = ((cut - c_first) * gridDim.y + blockIdx.y) * (kMergeThreads / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  using C = TreeCfg<D>;
-  for (int64_t job = me; job < jobs; job += workers) {
-    const int rg = (int)(job / (D / 8)), oct = (int)(job % (D / 8));
-    const int row = rg * 32 + lane;
-    const int b = rg * 32 / kTrBlock;
-    const int in_block = row - b * kTrBlock;
-    const bool valid = row < rows;
-    // the block's parts: for each segment, the runs its units fall into
-    int s = 0;
-    int64_t at = 0, end = 0;  // units of the current segment still to visit
-    int64_t seg_first = 0;
-    bool more = true, whole = false;
-    auto enter = [&]() {  // unit range of block b in segment s
-      const int32_t t0 = seg_begin(g, S, s), len_s = seg_begin(g, S, s + 1) - t0;
-      int64_t lead = (int64_t)b * len_s;
-      int32_t len = len_s;
-      if (s == S - 1) {
-        for (int i = 0; g.sum_tail && i < b; ++i) lead += tail_of(g, p.group, i);
-        len += tail_of(g, p.group, b);
+  const int c = blockIdx.x;
+  TreeCut cut;
+  TreeReq g = {};
+  if (p.batch <= 32) {
+    if (lane < p.batch) g = tree_req(p, lane, false);
+    cut = cut_warp(p, c, 1, g, lane);
+    if (cut.r >= p.batch) return;
+    g = shfl_req(g, cut.r);
+  } else {
+    cut_block<kMergeThreads>(p, c, 1, false, &start, warp_sum);
+    cut = start;
+    if (cut.r >= p.batch) return;
+    g = tree_req(p, cut.r, false);
+  }
+  if (g.kind == kReqEmpty) return;
+  const int32_t run = cut.run, stretch = cut.stretch;
+  const bool chunk = c < cut.chunks;
+  const HeadCut h = head_cut(g, p.group, run);
+  const int kvh = (int)div_units(cut.off, chunk ? h.chunks : h.weight);
+  const BlockAt k = block_at(g, p.group, run, (int32_t)(cut.off - (int64_t)kvh * (chunk ? h.chunks : h.weight)), chunk);
+  const int32_t chunks = k.tiles / run, weight = rest_weight(k.tiles, run);
+  const int first_chunk = cut.r_chunks + kvh * h.chunks + k.chunks;
+  // the block's left-over weight begins `lead` into the stretch of CTA cta0
+  int cta0 = 0;
+  int32_t lead = 0;
+  if (weight > 0) {
+    const int64_t at = cut.r_weight + (int64_t)kvh * h.weight + k.weight;
+    const int64_t i = div_units(at, stretch);
+    cta0 = cut.chunks + (int)i;
+    lead = (int32_t)(at - i * stretch);
+  }
+  int share = k.x, shares = chunks;  // of the block's rows and columns
+  if (chunk) {
+    if (chunks == 1 && weight == 0) return;  // one piece: already written as the result
+  } else {
+    // the end of c's stretch lies k.x into the block's weight; only ends behind its first tile cut it
+    if (chunks > 0 || k.x <= kTrRestCost) return;
+    shares = (lead + weight - 1) / stretch;
+    const int idle = (lead + kTrRestCost) / stretch;  // ends at or before the first tile
+    share = c - cta0 - idle;
+    shares -= idle;
+  }
+  const int rows = min(kTrBlock, g.n * p.group - k.b * kTrBlock);
+  const int jobs = (rows + 31) / 32 * (D / 8);
+  const int workers = shares * (int)gridDim.y * (kMergeThreads / 32);
+  const int me = (share * (int)gridDim.y + (int)blockIdx.y) * (kMergeThreads / 32) + (int)(threadIdx.x >> 5);
+  for (int job = me; job < jobs; job += workers) {
+    const int rg = job / (D / 8), oct = job % (D / 8);
+    const int in_block = rg * 32 + lane;
+    const int row = k.b * kTrBlock + in_block;
+    const bool valid = in_block < rows;
+    int i = 0;          // chunks taken
+    int32_t at = 0;     // left-over weight taken
+    int cta = cta0;
+    auto next = [&]() -> int {  // slot of the next part in the order of the keys, or -1
+      if (i < chunks) return first_chunk + i++;
+      while (at < weight) {
+        const int32_t end = min((cta - cta0 + 1) * stretch - lead, weight);
+        const bool some = end > max(at, kTrRestCost);
+        const int slot = rest_slot(end == weight, chunks, first_chunk, cta, p.ctas);
+        at = end;
+        ++cta;
+        if (some) return slot;
       }
-      seg_first = at = first + (int64_t)g.blocks * t0 + lead;
-      end = at + len;
+      return -1;
     };
-    enter();
-    whole = S == 1 && at / run == (end - 1) / run;  // one piece: already written as the result
-    if (whole) continue;
-    auto next = [&]() -> int64_t {  // slot of the next part, or -1
-      while (more && at >= end) {
-        if (++s >= S) {
-          more = false;
-          break;
-        }
-        enter();
-      }
-      if (!more) return -1;
-      const int64_t cta = at / run;
-      const int64_t slot = cta * kTrSlots + piece_slot(at - cta * run, run);
-      at = min((cta + 1) * run, end);
-      return slot;
-    };
+    bool more = true;
     float M = -INFINITY, L = 0.f;
     float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     while (more) {
@@ -1093,16 +1333,17 @@ __global__ void __launch_bounds__(kMergeThreads) pa_v2_tree_merge_kernel(const T
       float lse[kBatch];
       float4 x[kBatch][2];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int64_t slot = next();
-        lse[i] = -INFINITY;
-        x[i][0] = x[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q = 0; q < kBatch; ++q) {
+        const int slot = next();
+        more = slot >= 0;
+        lse[q] = -INFINITY;
+        x[q][0] = x[q][1] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (slot >= 0 && valid) {
-          const float* base = p.slots + slot * C::kSlotFloats;
-          lse[i] = __ldcg(base + (int64_t)kTrBlock * D + in_block);
+          const float* base = p.slots + (int64_t)slot * C::kSlotFloats;
+          lse[q] = __ldcg(base + (int64_t)kTrBlock * D + in_block);
           const float4* v = reinterpret_cast<const float4*>(base) + (in_block >> 7) * (D / 4 * kTrTile) + (in_block & 127);
-          x[i][0] = __ldcg(v + (2 * oct) * kTrTile);
-          x[i][1] = __ldcg(v + (2 * oct + 1) * kTrTile);
+          x[q][0] = __ldcg(v + (2 * oct) * kTrTile);
+          x[q][1] = __ldcg(v + (2 * oct + 1) * kTrTile);
         }
       }
       float mb = M;
@@ -1219,8 +1460,9 @@ extern "C" pa_status pa_v2_tree_attention(const void* q, const void* k_pool, con
   std::memset(&tm_k, 0, sizeof(tm_k));
   std::memset(&tm_v, 0, sizeof(tm_v));
   const bool tma = pa::tc_uses_tma(page_size);
+  int box_rows = 8;  // rows of a TMA box: the largest power of two that divides a page, up to a whole tile
+  while (box_rows < pa::kTrTile && page_size % (2 * box_rows) == 0) box_rows *= 2;
   if (tma) {
-    const int box_rows = page_size < 16 ? page_size : 16;
     if (!pa::make_pool_map(&tm_k, k_pool, kv_dtype, num_pages * page_size, num_kv_heads, head_dim, 64, box_rows,
                            CU_TENSOR_MAP_SWIZZLE_128B) ||
         !pa::make_pool_map(&tm_v, v_pool, kv_dtype, num_pages * page_size, num_kv_heads, head_dim, 64, box_rows,
@@ -1248,6 +1490,7 @@ extern "C" pa_status pa_v2_tree_attention(const void* q, const void* k_pool, con
   p.num_tokens = num_tokens;
   p.mask_words = mask_words;
   p.page_size = page_size;
+  p.box_rows = box_rows;
   p.hq = num_qo_heads;
   p.hkv = num_kv_heads;
   p.group = num_qo_heads / num_kv_heads;
@@ -1276,7 +1519,7 @@ extern "C" pa_status pa_v2_tree_attention(const void* q, const void* k_pool, con
           : (head_dim == 64 ? pa::pa_v2_tree_merge_kernel<__nv_bfloat16, 64>
                             : pa::pa_v2_tree_merge_kernel<__nv_bfloat16, 128>);
   if (p.ctas > 1) {
-    const cudaError_t rc = pa::launch_dependent(merge, dim3(p.ctas - 1, 2), dim3(pa::kMergeThreads), 0, stream, p);
+    const cudaError_t rc = pa::launch_dependent(merge, dim3(p.ctas, 2), dim3(pa::kMergeThreads), 0, stream, p);
     if (rc != cudaSuccess) {
       cudaGetLastError();
       return PA_ECUDA;
