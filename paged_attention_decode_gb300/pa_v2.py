@@ -621,27 +621,62 @@ def pa_selection_from_blocks(block_ids, block_size: int, kv_len: int, request_st
 # one step of several new tokens per request: tables, q/k preparation, tree attention
 # ---------------------------------------------------------------------------
 
-@contextlib.contextmanager
-def _launch_on(device, stream):
-    """Make `device` and the launch stream current (new tensors then belong to that stream); yields its
-    handle.  stream: a torch stream, a raw handle, or None for the device's current stream."""
-    with torch.cuda.device(device):
+class _LaunchOn:
+    """Make a device and the launch stream current (new tensors then belong to that stream); entering gives the
+    stream's handle.  stream: a torch stream, a raw handle, or None for the device's current stream, which on the
+    current device needs no change at all."""
+
+    __slots__ = ("index", "stream", "scopes")
+
+    def __init__(self, index: int, stream):
+        self.index, self.stream, self.scopes = index, stream, None
+
+    def __enter__(self) -> int:
+        stream = self.stream
+        if stream is None and torch.cuda.current_device() == self.index:
+            return torch.cuda.current_stream(self.index).cuda_stream
+        self.scopes = contextlib.ExitStack()
+        self.scopes.enter_context(torch.cuda.device(self.index))
         if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-            return
-        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
-        with torch.cuda.stream(s):
-            yield s.cuda_stream
+            return torch.cuda.current_stream(self.index).cuda_stream
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.index)
+        self.scopes.enter_context(torch.cuda.stream(stream))
+        return stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.scopes is not None:
+            self.scopes.close()
 
 
-def _step_ptr(t, name: str, device, dtype=None, shape=None) -> int | None:
-    """Pointer of a contiguous tensor on `device`, its dtype and shape checked; None stays None."""
-    p = _dev_ptr(t, name, dtype)
-    if t is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t is not None and shape is not None and tuple(t.shape) != tuple(shape):
+def _refuse(t, name: str, index: int, dtype, shape) -> None:
+    """Say what is wrong with an argument that _step_ptr does not pass."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return p
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _step_ptr(t, name: str, index: int, dtype=None, shape=None) -> int | None:
+    """Pointer of a contiguous tensor on device `index`, its dtype and shape checked; None stays None."""
+    if t is None:
+        return None
+    if (t.get_device() != index or (dtype is not None and t.dtype is not dtype) or
+            (shape is not None and t.shape != shape) or not t.is_contiguous()):
+        _refuse(t, name, index, dtype, shape)
+    return t.data_ptr()
+
+
+def _device_index(t, name: str) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index
 
 
 @dataclass
@@ -677,51 +712,49 @@ def pa_v2_build_tables(cached_lens, new_lens, block_table, page_size: int, table
     `tables`."""
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch, width]")
-    dev, (B, width) = block_table.device, block_table.shape
-    i32 = torch.int32
-    cap_i, cap_t = tables.indices.numel(), tables.slots.numel()
-    mask = tables.tree_mask
+    dev, (B, width) = _device_index(block_table, "block_table"), block_table.shape
+    i32, ptr = torch.int32, _step_ptr
+    t, mask = tables, tables.tree_mask
+    cap_i, cap_t = t.indices.numel(), t.slots.numel()
     if mask is not None and mask.dim() != 2:
         raise ValueError("tree_mask must be [token capacity, mask words]")
     words = mask.shape[1] if mask is not None else 0
-    args = (_step_ptr(cached_lens, "cached_lens", dev, i32, (B,)), _step_ptr(new_lens, "new_lens", dev, i32, (B,)), B,
-            _step_ptr(block_table, "block_table", dev, i32), width,
-            _step_ptr(free_pages, "free_pages", dev, i32), free_pages.numel() if free_pages is not None else 0,
-            _step_ptr(parents, "parents", dev, i32, (cap_t,)), int(page_size), int(window),
-            _step_ptr(tables.indptr, "indptr", dev, i32, (B + 1,)), _step_ptr(tables.indices, "indices", dev, i32),
-            cap_i, _step_ptr(tables.last_page_len, "last_page_len", dev, i32, (B,)),
-            _step_ptr(tables.first_page_offset, "first_page_offset", dev, i32, (B,)),
-            _step_ptr(tables.qo_indptr, "qo_indptr", dev, i32, (B + 1,)),
-            _step_ptr(tables.slots, "slots", dev, i32, (cap_t,)),
-            _step_ptr(tables.positions, "positions", dev, i32, (cap_t,)), cap_t,
-            _step_ptr(mask, "tree_mask", dev, i32, (cap_t, words)), words,
-            _step_ptr(tables.pages_needed, "pages_needed", dev, i32, (1,)), _step_ptr(status, "status", dev, i32))
-    with _launch_on(dev, stream) as handle:
+    args = (ptr(cached_lens, "cached_lens", dev, i32, (B,)), ptr(new_lens, "new_lens", dev, i32, (B,)), B,
+            ptr(block_table, "block_table", dev, i32), width, ptr(free_pages, "free_pages", dev, i32),
+            free_pages.numel() if free_pages is not None else 0, ptr(parents, "parents", dev, i32, (cap_t,)),
+            page_size, window, ptr(t.indptr, "indptr", dev, i32, (B + 1,)), ptr(t.indices, "indices", dev, i32), cap_i,
+            ptr(t.last_page_len, "last_page_len", dev, i32, (B,)),
+            ptr(t.first_page_offset, "first_page_offset", dev, i32, (B,)),
+            ptr(t.qo_indptr, "qo_indptr", dev, i32, (B + 1,)), ptr(t.slots, "slots", dev, i32, (cap_t,)),
+            ptr(t.positions, "positions", dev, i32, (cap_t,)), cap_t, ptr(mask, "tree_mask", dev, i32, (cap_t, words)),
+            words, ptr(t.pages_needed, "pages_needed", dev, i32, (1,)), ptr(status, "status", dev, i32))
+    with _LaunchOn(dev, stream) as handle:
         rc = lib().pa_v2_build_tables(*args, handle)
     if rc != PA_OK:
         raise PaError(rc, "pa_v2_build_tables")
     return tables
 
 
-def _token_rows(t, name: str, tokens: int, head_dim: int, dtype, device) -> tuple[int, int, int]:
+def _token_rows(t, name: str, tokens: int, head_dim: int, dtype, index: int) -> tuple[int, int, int]:
     """(pointer, token stride in elements, heads) of a [tokens, heads, head_dim] view with contiguous token rows."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != dtype or t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != head_dim:
-        raise ValueError(f"{name} must be [{tokens}, heads, {head_dim}] {dtype}, got {list(t.shape)} {t.dtype}")
-    heads = t.shape[1]
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
+    if t.get_device() != index or t.dtype is not dtype or t.dim() != 3:
+        _refuse(t, name, index, dtype, None)
+    n, heads, d = t.shape
+    if n != tokens or d != head_dim:
+        raise ValueError(f"{name} must be [{tokens}, heads, {head_dim}], got {list(t.shape)}")
+    token, head, elem = t.stride()
+    if elem != 1 or (heads > 1 and head != head_dim):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (t.stride(0) if tokens > 1 else heads * head_dim), heads
+    return t.data_ptr(), (token if tokens > 1 else heads * head_dim), heads
 
 
-def _pools(k_pool, v_pool, device) -> None:
-    if k_pool.dtype not in KV_DTYPES or v_pool.dtype != k_pool.dtype or k_pool.shape != v_pool.shape:
+def _pools(k_pool, v_pool, index: int) -> tuple[int, int]:
+    """(k, v) pointers of the pools of one step."""
+    if k_pool.dtype not in KV_DTYPES or v_pool.dtype is not k_pool.dtype or k_pool.shape != v_pool.shape:
         raise ValueError("k_pool and v_pool must share one of float32/float16/bfloat16 and a shape")
     if k_pool.dim() != 4:
         raise ValueError("pools must be [num_pages, page_size, num_kv_heads, head_dim]")
-    if k_pool.device != device or v_pool.device != device:
-        raise ValueError(f"pools must be on {device}")
+    return _step_ptr(k_pool, "k_pool", index), _step_ptr(v_pool, "v_pool", index)
 
 
 def pa_v2_qk_rope_append(q, k, v, positions, slots, inv_freq, k_pool, v_pool, q_out=None, q_weight=None,
@@ -732,16 +765,17 @@ def pa_v2_qk_rope_append(q, k, v, positions, slots, inv_freq, k_pool, v_pool, q_
     q [T, Hq, D], k and v [T, Hkv, D] (views of one packed projection output will do), positions and slots [T]
     int32, inv_freq [rot_dim / 2] float32 or None (no rotation).  Returns q_out [T, Hq, D] in q_dtype (the
     activations' dtype by default, or float32 for the decode calls); its padded rows are not written."""
-    dev = q.device
-    _pools(k_pool, v_pool, dev)
+    dev = _device_index(q, "q")
+    k_ptr, v_ptr = _pools(k_pool, v_pool, dev)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, head_dim]")
     T, _, D = q.shape
-    dt = k_pool.dtype
+    dt, i32, ptr = k_pool.dtype, torch.int32, _step_ptr
     qp, qs, hq = _token_rows(q, "q", T, D, dt, dev)
     kp, ks, hkv = _token_rows(k, "k", T, D, dt, dev)
     vp, vs, hv = _token_rows(v, "v", T, D, dt, dev)
-    if hv != hkv or tuple(k_pool.shape[2:]) != (hkv, D):
+    pages, page_size, pool_heads, pool_dim = k_pool.shape
+    if hv != hkv or pool_heads != hkv or pool_dim != D:
         raise ValueError(f"k, v and the pools must agree on heads and head_dim: {hkv}, {hv}, {list(k_pool.shape)}")
     rot = 2 * inv_freq.numel() if inv_freq is not None else 0
     if q_out is not None:
@@ -750,18 +784,16 @@ def pa_v2_qk_rope_append(q, k, v, positions, slots, inv_freq, k_pool, v_pool, q_
         q_dtype = dt
     if q_dtype not in KV_DTYPES:
         raise ValueError(f"q_dtype must be one of {list(KV_DTYPES)}")
-    i32 = torch.int32
-    tail = (KV_DTYPES[dt], T, hq, hkv, D, _step_ptr(positions, "positions", dev, i32, (T,)),
-            _step_ptr(slots, "slots", dev, i32, (T,)), _step_ptr(inv_freq, "inv_freq", dev, torch.float32), rot,
-            int(bool(interleaved)), _step_ptr(q_weight, "q_weight", dev, dt, (D,)),
-            _step_ptr(k_weight, "k_weight", dev, dt, (D,)), float(eps))
-    pools = (_step_ptr(k_pool, "k_pool", dev), _step_ptr(v_pool, "v_pool", dev), k_pool.shape[0], k_pool.shape[1],
-             _step_ptr(status, "status", dev, i32))
-    with _launch_on(dev, stream) as handle:
+    head = (qp, qs, kp, ks, vp, vs, KV_DTYPES[dt], T, hq, hkv, D, ptr(positions, "positions", dev, i32, (T,)),
+            ptr(slots, "slots", dev, i32, (T,)), ptr(inv_freq, "inv_freq", dev, torch.float32), rot,
+            1 if interleaved else 0, ptr(q_weight, "q_weight", dev, dt, (D,)), ptr(k_weight, "k_weight", dev, dt, (D,)),
+            eps)
+    st = ptr(status, "status", dev, i32)
+    with _LaunchOn(dev, stream) as handle:
         if q_out is None:
-            q_out = torch.empty(T, hq, D, dtype=q_dtype, device=dev)
-        rc = lib().pa_v2_qk_rope_append(qp, qs, kp, ks, vp, vs, *tail, _step_ptr(q_out, "q_out", dev, None, (T, hq, D)),
-                                        KV_DTYPES[q_dtype], *pools, handle)
+            q_out = torch.empty(T, hq, D, dtype=q_dtype, device=q.device)
+        rc = lib().pa_v2_qk_rope_append(*head, ptr(q_out, "q_out", dev, None, (T, hq, D)), KV_DTYPES[q_dtype], k_ptr,
+                                        v_ptr, pages, page_size, st, handle)
     if rc != PA_OK:
         raise PaError(rc, "pa_v2_qk_rope_append")
     return q_out
@@ -796,37 +828,36 @@ def pa_v2_tree_attention(q, k_pool, v_pool, indices, indptr, last_page_len, firs
     q [T, Hq, D] of the pools' 16-bit dtype, packed request by request (qo_indptr [B + 1]); tree_mask
     [T, words] int32 ancestor bits, or None for chains.  Returns (out [T, Hq, D], lse2 [T, Hq] float32); rows
     behind the last token are not written."""
-    dev = q.device
-    _pools(k_pool, v_pool, dev)
+    dev = _device_index(q, "q")
+    k_ptr, v_ptr = _pools(k_pool, v_pool, dev)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, head_dim]")
     T, hq, D = q.shape
-    P, ps, hkv, pd = k_pool.shape
-    if pd != D:
+    P, ps, hkv, pool_dim = k_pool.shape
+    if pool_dim != D:
         raise ValueError(f"pools must be [P, page_size, Hkv, {D}]")
-    B = last_page_len.numel()
-    i32 = torch.int32
+    B, dt, i32, ptr = last_page_len.numel(), k_pool.dtype, torch.int32, _step_ptr
     if tree_mask is not None and tree_mask.dim() != 2:
         raise ValueError("tree_mask must be [tokens, mask words]")
     words = tree_mask.shape[1] if tree_mask is not None else 0
-    args = (_step_ptr(q, "q", dev, k_pool.dtype), _step_ptr(k_pool, "k_pool", dev), _step_ptr(v_pool, "v_pool", dev),
-            KV_DTYPES[k_pool.dtype], P, ps, hq, hkv, D, _step_ptr(indices, "indices", dev, i32), indices.numel(),
-            _step_ptr(indptr, "indptr", dev, i32, (B + 1,)), _step_ptr(last_page_len, "last_page_len", dev, i32, (B,)),
-            _step_ptr(first_page_offset, "first_page_offset", dev, i32, (B,)), B,
-            _step_ptr(qo_indptr, "qo_indptr", dev, i32, (B + 1,)), T,
-            _step_ptr(tree_mask, "tree_mask", dev, i32, (T, words)), words, float(sm_scale))
-    st = _step_ptr(status, "status", dev, i32)
-    with _launch_on(dev, stream) as handle:
+    head = (ptr(q, "q", dev, dt), k_ptr, v_ptr, KV_DTYPES[dt], P, ps, hq, hkv, D, ptr(indices, "indices", dev, i32),
+            indices.numel(), ptr(indptr, "indptr", dev, i32, (B + 1,)),
+            ptr(last_page_len, "last_page_len", dev, i32, (B,)),
+            ptr(first_page_offset, "first_page_offset", dev, i32, (B,)), B,
+            ptr(qo_indptr, "qo_indptr", dev, i32, (B + 1,)), T, ptr(tree_mask, "tree_mask", dev, i32, (T, words)), words,
+            sm_scale)
+    st = ptr(status, "status", dev, i32)
+    with _LaunchOn(dev, stream) as handle:
         if workspace is None and hkv > 0 and hq % hkv == 0 and D in (64, 128):
-            workspace = tree_attention_workspace(T, B, hq, hkv, D, dev)
+            workspace = tree_attention_workspace(T, B, hq, hkv, D, q.device)
         if out is None:
-            out = torch.empty(T, hq, D, dtype=q.dtype, device=dev)
+            out = torch.empty(T, hq, D, dtype=dt, device=q.device)
         if lse2_out is None:
-            lse2_out = torch.empty(T, hq, dtype=torch.float32, device=dev)
+            lse2_out = torch.empty(T, hq, dtype=torch.float32, device=q.device)
         rc = lib().pa_v2_tree_attention(
-            *args, _step_ptr(out, "out", dev, q.dtype, (T, hq, D)),
-            _step_ptr(lse2_out, "lse2_out", dev, torch.float32, (T, hq)), _step_ptr(workspace, "workspace", dev),
-            workspace.numel() * workspace.element_size() if workspace is not None else 0, st, handle)
+            *head, ptr(out, "out", dev, dt, (T, hq, D)), ptr(lse2_out, "lse2_out", dev, torch.float32, (T, hq)),
+            ptr(workspace, "workspace", dev), workspace.numel() * workspace.element_size() if workspace is not None else 0,
+            st, handle)
     if rc != PA_OK:
         raise PaError(rc, "pa_v2_tree_attention")
     return out, lse2_out
