@@ -676,7 +676,7 @@ pa_status pa_v2_build_tables(const int32_t* cached_lens, const int32_t* new_lens
  *    positions keep f32 accuracy; norm and rotation run in f32 and each result
  *    is rounded once;
  *  - q -> q_out[t]; k and v -> row slots[t] of k_pool and v_pool (v unchanged).
- * A token with a negative slot is padding: nothing of it is read or written.
+ * A token with a negative slot is padding: nothing of it is written.
  * A slot at or past num_pages * page_size is skipped like one and recorded as
  * PA_DEVICE_BAD_SLOT.  Slots must be distinct; q_out must not overlap an input.
  *   q [num_tokens, num_qo_heads, head_dim], k / v [num_tokens, num_kv_heads,

@@ -4,18 +4,25 @@
 //   norm      x <- x * w / sqrt(mean(x^2) + eps)                (f32)
 //   rotation  (x, y) <- (x cos a - y sin a, y cos a + x sin a),  a_j = pos * inv_freq[j]
 //
-// The angle is reduced in 64 bits before the sine is taken: pos * inv_freq in
-// turns, minus its nearest integer, leaves a fraction of a turn that f32 holds
-// to 2^-25, so a position of a million costs no accuracy (in f32 the product
-// alone would be off by 0.06 radians there).
+// The angle is reduced in 64 bits before the sine is taken: a frequency is kept as
+// the fraction of a turn that one position adds, times 2^64, so an integer product
+// with the position wraps around whole turns by itself and leaves a fraction of a
+// turn that f32 holds to 2^-26; a position of a million costs no accuracy (in f32
+// the product alone would be off by 0.06 radians there).
 //
-// One CTA per token.  A head's row is read as 16-byte pieces, one per lane, so
-// a row takes head_dim / (16 / esize) lanes and the CTA's lanes hold several
-// heads at once; a lane keeps the same place in the row for every head, so its
-// cosines and sines are read once from shared memory, where the token's angles
-// were computed once for all heads.  Half-split pairs sit (rot_dim / 2)
-// elements apart, a whole number of lanes (rot_dim is a multiple of 16), and
-// meet through one shuffle per element.
+// HBM bound: every row is read and written once.  A lane holds 16 bytes of a head's
+// row as two 8-byte pieces, so a row takes head_dim / (16 / esize) lanes and a CTA's
+// lanes hold several heads at once.  The two pieces are chosen so that a lane has
+// both elements of each of its pairs: half-split pairs sit rot_dim / 2 elements
+// apart, so its second piece is the first one's partner (with one 16-byte piece per
+// lane every element had to be shuffled across lanes, and the kernel was bound by
+// its instructions: 115 us for 16384 tokens of 48 heads).  A CTA walks
+// tiles of up to four tokens, each lane keeping the same heads and the same places in
+// the row: the next token's pieces are in flight while this one's are worked on, and
+// the next tile's cosines and sines are computed by all threads, one angle each, into
+// the other half of a shared buffer (one barrier per tile; with one per token, behind
+// the two warps that computed its angles, the kernel took 86 us).  A frequency is
+// converted once per CTA.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -31,6 +38,8 @@ namespace pa {
 namespace {
 
 constexpr int kQkThreads = 256;
+constexpr int kQkPasses = 3;  // heads a lane holds at once, at most (four do not fit its registers)
+constexpr int kQkTile = 4;    // tokens per tile, at most: one angle per thread
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
 struct QkParams {
@@ -49,10 +58,10 @@ struct QkParams {
   int32_t* status;
   int64_t num_rows;  // pool rows
   float eps;
-  int32_t hq, hkv, rot, interleaved;
+  int32_t tokens, hq, hkv, rot, tile;
 };
 
-// 16 bytes of T as floats, and back.
+// Two 8-byte pieces of T as floats, and back (one rounding).
 template <typename T> struct Vec;
 template <> struct Vec<float> {
   static constexpr int N = 4;
@@ -108,117 +117,191 @@ template <> struct Vec<__nv_bfloat16> {
   }
 };
 
-// Cosine and sine of pos * inv_freq radians.
-__device__ __forceinline__ float2 rotation(int32_t pos, float inv_freq) {
-  double turns = (double)pos * ((double)inv_freq * kInvTwoPi);
-  turns -= rint(turns);
+// The part of a turn that one position adds, times 2^64.
+__device__ __forceinline__ uint64_t turn_of(float inv_freq) {
+  const double f = (double)inv_freq * kInvTwoPi;
+  return __double2ull_rd((f - floor(f)) * 18446744073709551616.0);
+}
+
+// Cosine and sine after pos positions.
+__device__ __forceinline__ float2 rotation(int32_t pos, uint64_t turn) {
+  const int32_t part = (int32_t)(uint32_t)(((uint64_t)(uint32_t)pos * turn) >> 32);  // [-1/2, 1/2) turns, times 2^32
   float s, c;
-  sincospif(2.0f * (float)turns, &s, &c);
+  sincospif((float)part * 4.656612873077393e-10f, &s, &c);  // 2^-31: sincospif takes half turns
   return make_float2(c, s);
 }
 
-template <typename T, typename TQ, int D>
-__global__ void __launch_bounds__(kQkThreads) pa_v2_qk_rope_append_kernel(const QkParams p) {
-  constexpr int N = Vec<T>::N;
-  constexpr int kLanes = D / N;                    // lanes per head row (8, 16 or 32)
-  constexpr int kRows = kQkThreads / kLanes;       // head rows in flight per CTA
-  __shared__ float2 cs[D / 2];
+__device__ __forceinline__ uint2 load_stream(const void* a) {
+  uint2 x;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(a));
+  return x;
+}
+
+// NP: heads per lane (blockIdx.y takes the next NP * kRows heads).  PAIRED: the lane's pieces are partners (half
+// split); else they are neighbours and pairs are neighbouring elements (interleaved).
+template <typename T, typename TQ, int D, int NP, bool PAIRED>
+__global__ void __launch_bounds__(kQkThreads, 2) pa_v2_qk_rope_append_kernel(const QkParams p) {
+  constexpr int N = Vec<T>::N, P = N / 2;     // elements per lane; per piece, and pairs per lane
+  constexpr int kLanes = D / N;               // lanes per head row (8, 16 or 32)
+  constexpr int kRows = kQkThreads / kLanes;  // head rows in flight per CTA and pass
+  __shared__ __align__(16) float2 cs[2][kQkTile][D / 2];
 
   pdl_launch_dependents();
   pdl_wait_prerequisites();
 
-  const int t = blockIdx.x;
-  const int64_t slot = p.slots[t];
-  if (slot < 0 || slot >= p.num_rows) {  // padding, or a slot outside the pools
-    if (slot >= p.num_rows && threadIdx.x == 0) report(p.status, PA_DEVICE_BAD_SLOT);
-    return;
-  }
   const int half = p.rot / 2;
-  if ((int)threadIdx.x < half) cs[threadIdx.x] = rotation(p.positions[t], p.inv_freq[threadIdx.x]);
-  __syncthreads();
-
-  const int lane = threadIdx.x & (kLanes - 1);     // place in the row
-  const int e0 = lane * N;
-  const bool rotated = e0 < p.rot;                 // rot is a multiple of 2 N or of N: never inside a lane's piece
-  const int hl = half / N;                         // lanes between the halves of a pair
-  float2 r[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    r[i] = make_float2(1.f, 0.f);
-    if (rotated) r[i] = p.interleaved ? cs[(e0 + i) >> 1] : cs[(e0 + i) < half ? e0 + i : e0 + i - half];
-  }
-  const bool upper = !p.interleaved && e0 >= half;
-
+  const int lane = threadIdx.x & (kLanes - 1);
+  const bool rotated = lane * P < half;
+  // the places of the two pieces: partners while there are any, then neighbours
+  const int e0 = PAIRED && rotated ? lane * P : lane * N, e1 = PAIRED && rotated ? e0 + half : e0 + P;
   const int heads = p.hq + 2 * p.hkv;
-  for (int h0 = 0; h0 < heads; h0 += kRows) {
-    const int h = h0 + (int)threadIdx.x / kLanes;
-    const bool live = h < heads;
-    const int kind = h < p.hq ? 0 : h < p.hq + p.hkv ? 1 : 2;  // q, k, v
-    const int hh = kind == 0 ? h : kind == 1 ? h - p.hq : h - p.hq - p.hkv;
-    const T* src = kind == 0   ? static_cast<const T*>(p.q) + t * p.q_stride
-                   : kind == 1 ? static_cast<const T*>(p.k) + t * p.k_stride
-                               : static_cast<const T*>(p.v) + t * p.v_stride;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (live) raw = *reinterpret_cast<const uint4*>(src + (int64_t)hh * D + e0);
-    float x[N];
-    Vec<T>::unpack(raw, x);
-    // norm: every lane of the warp takes part in the shuffles, whatever its head's kind
-    float ss = 0.f;
+
+  // this lane's heads
+  const T* src[NP];
+  uint4 weight[NP];
+  int kind[NP], hh[NP];  // q, k, v or none; the head among its kind
+  bool normed[NP];
 #pragma unroll
-    for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-    for (int w = kLanes / 2; w >= 1; w >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, w);
-    const T* weight = static_cast<const T*>(kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr);
-    if (live && weight) {
-      const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
-      float g[N];
-      Vec<T>::unpack(*reinterpret_cast<const uint4*>(weight + e0), g);
-#pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = x[i] * inv * g[i];
+  for (int i = 0; i < NP; ++i) {
+    const int h = ((int)blockIdx.y * NP + i) * kRows + (int)threadIdx.x / kLanes;
+    kind[i] = h < p.hq ? 0 : h < p.hq + p.hkv ? 1 : h < heads ? 2 : 3;
+    hh[i] = kind[i] == 0 ? h : kind[i] == 1 ? h - p.hq : h - p.hq - p.hkv;
+    const T* base = static_cast<const T*>(kind[i] == 0 ? p.q : kind[i] == 1 ? p.k : p.v);
+    const int64_t step = kind[i] == 0 ? p.q_stride : kind[i] == 1 ? p.k_stride : p.v_stride;
+    src[i] = base + (int64_t)blockIdx.x * p.tile * step + (int64_t)hh[i] * D;
+    const T* w = static_cast<const T*>(kind[i] == 0 ? p.q_weight : kind[i] == 1 ? p.k_weight : nullptr);
+    normed[i] = w != nullptr;
+    weight[i] = make_uint4(0, 0, 0, 0);
+    if (w) {
+      const uint2 a = *reinterpret_cast<const uint2*>(w + e0), b = *reinterpret_cast<const uint2*>(w + e1);
+      weight[i] = make_uint4(a.x, a.y, b.x, b.y);
     }
-    if (p.rot > 0) {
-      float y[N];
-      if (p.interleaved) {
+  }
+
+  // this thread's angle: one frequency of one token of a tile
+  const int angle = threadIdx.x % (D / 2), angle_tok = threadIdx.x / (D / 2);
+  const bool has_angle = angle < half && angle_tok < p.tile;
+  const uint64_t turn = has_angle ? turn_of(p.inv_freq[angle]) : 0;
+  auto angles = [&](int first, int buf) {  // of the tile whose first token is `first`
+    if (has_angle && first + angle_tok < p.tokens)
+      cs[buf][angle_tok][angle] = rotation(p.positions[first + angle_tok], turn);
+  };
+  int t = blockIdx.x * p.tile, in_tile = 0;
+  const int jump = ((int)gridDim.x - 1) * p.tile + 1;  // from a tile's last token to the next tile's first
+  uint4 next[NP];
+  int32_t next_slot = 0;
+  auto fetch = [&](int at, int skip) {  // a token's pieces; src moves on by `skip` tokens
 #pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = x[i ^ 1];
-      } else {
-        const int warp_lane = threadIdx.x & 31;
-        const int from = rotated ? (upper ? warp_lane - hl : warp_lane + hl) : warp_lane;
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], from);
+    for (int i = 0; i < NP; ++i) {
+      next[i] = make_uint4(0, 0, 0, 0);
+      if (kind[i] < 3) {
+        const uint2 a = load_stream(src[i] + e0), b = load_stream(src[i] + e1);
+        next[i] = make_uint4(a.x, a.y, b.x, b.y);
       }
-      if (kind < 2 && rotated) {
+      src[i] += (int64_t)skip * (kind[i] == 0 ? p.q_stride : kind[i] == 1 ? p.k_stride : p.v_stride);
+    }
+    next_slot = p.slots[at];
+  };
+  auto skip_of = [&](int place) { return place + 1 == p.tile ? jump : 1; };
+  if (t < p.tokens) {
+    fetch(t, skip_of(0));
+    angles(t, 0);
+  }
+  __syncthreads();
+  for (int buf = 0; t < p.tokens;) {
+    uint4 raw[NP];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          // first of a pair: x cos - y sin; second: x cos + y sin (y its partner)
-          const bool second = p.interleaved ? (i & 1) : upper;
-          x[i] = fmaf(second ? y[i] : -y[i], r[i].y, x[i] * r[i].x);
+    for (int i = 0; i < NP; ++i) raw[i] = next[i];
+    const int64_t slot = next_slot;
+    const int place = in_tile, after = t + skip_of(place);
+    in_tile = place + 1 == p.tile ? 0 : place + 1;
+    if (after < p.tokens) fetch(after, skip_of(in_tile));
+    if (place == 0) angles(t + (int)gridDim.x * p.tile, buf ^ 1);
+    if (slot >= 0 && slot < p.num_rows) {
+      float2 r[P];  // the pairs' cosines and sines
+#pragma unroll
+      for (int i = 0; i < P; ++i) r[i] = make_float2(1.f, 0.f);
+      if (rotated) {
+        const float4* at = reinterpret_cast<const float4*>(&cs[buf][place][lane * P]);
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i) {
+          const float4 v = at[i];
+          r[2 * i] = make_float2(v.x, v.y);
+          r[2 * i + 1] = make_float2(v.z, v.w);
         }
       }
-    }
-    if (!live) continue;
-    if (kind == 0) {
-      TQ* dst = static_cast<TQ*>(p.q_out) + ((int64_t)t * p.hq + hh) * D + e0;
 #pragma unroll
-      for (int j = 0; j < N / Vec<TQ>::N; ++j) {
-        float z[Vec<TQ>::N];
+      for (int k = 0; k < NP; ++k) {
+        if (__any_sync(0xffffffffu, kind[k] < 2)) {  // a warp of v heads alone has nothing to compute
+          float x[N];
+          Vec<T>::unpack(raw[k], x);
+          if (__any_sync(0xffffffffu, normed[k])) {
+            float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < Vec<TQ>::N; ++i) z[i] = x[j * Vec<TQ>::N + i];
-        reinterpret_cast<uint4*>(dst)[j] = Vec<TQ>::pack(z);
+            for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+            for (int w = kLanes / 2; w >= 1; w >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, w);
+            if (normed[k]) {
+              const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
+              float g[N];
+              Vec<T>::unpack(weight[k], g);
+#pragma unroll
+              for (int i = 0; i < N; ++i) x[i] = x[i] * inv * g[i];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const int a = PAIRED ? i : 2 * i, b = PAIRED ? i + P : 2 * i + 1;
+            const float u = x[a], w = x[b];
+            x[a] = fmaf(-w, r[i].y, u * r[i].x);
+            x[b] = fmaf(u, r[i].y, w * r[i].x);
+          }
+          if (kind[k] == 0) {
+            TQ* dst = static_cast<TQ*>(p.q_out) + ((int64_t)t * p.hq + hh[k]) * D;
+            if (sizeof(TQ) == sizeof(T)) {
+              const uint4 z = Vec<T>::pack(x);
+              *reinterpret_cast<uint2*>(dst + e0) = make_uint2(z.x, z.y);
+              *reinterpret_cast<uint2*>(dst + e1) = make_uint2(z.z, z.w);
+            } else {  // f32 from 16 bits: a piece is 16 bytes
+              *reinterpret_cast<float4*>(dst + e0) = make_float4(x[0], x[1], x[2], x[3]);
+              *reinterpret_cast<float4*>(dst + e1) = make_float4(x[P], x[P + 1], x[N - 2], x[N - 1]);
+            }
+          }
+          if (kind[k] == 1) raw[k] = Vec<T>::pack(x);
+        }
+        if (kind[k] == 1 || kind[k] == 2) {
+          T* dst = static_cast<T*>(kind[k] == 1 ? p.k_pool : p.v_pool) + (slot * p.hkv + hh[k]) * D;
+          *reinterpret_cast<uint2*>(dst + e0) = make_uint2(raw[k].x, raw[k].y);
+          *reinterpret_cast<uint2*>(dst + e1) = make_uint2(raw[k].z, raw[k].w);
+        }
       }
-    } else {
-      T* pool = static_cast<T*>(kind == 1 ? p.k_pool : p.v_pool);
-      *reinterpret_cast<uint4*>(pool + (slot * p.hkv + hh) * D + e0) = kind == 1 ? Vec<T>::pack(x) : raw;
+    } else if (slot >= p.num_rows && threadIdx.x == 0) {
+      report(p.status, PA_DEVICE_BAD_SLOT);
+    }
+    t = after;
+    if (in_tile == 0) {
+      __syncthreads();
+      buf ^= 1;
     }
   }
 }
 
 using QkKernel = void (*)(const QkParams);
 
+template <typename T, typename TQ, int D, bool PAIRED>
+QkKernel pick_passes(int np) {
+  return np == 1   ? pa_v2_qk_rope_append_kernel<T, TQ, D, 1, PAIRED>
+         : np == 2 ? pa_v2_qk_rope_append_kernel<T, TQ, D, 2, PAIRED>
+                   : pa_v2_qk_rope_append_kernel<T, TQ, D, 3, PAIRED>;
+}
+template <typename T, typename TQ>
+QkKernel pick_layout(int D, bool paired, int np) {
+  if (D == 64) return paired ? pick_passes<T, TQ, 64, true>(np) : pick_passes<T, TQ, 64, false>(np);
+  return paired ? pick_passes<T, TQ, 128, true>(np) : pick_passes<T, TQ, 128, false>(np);
+}
 template <typename T>
-QkKernel pick(int D, bool q32) {
-  if (D == 64) return q32 ? pa_v2_qk_rope_append_kernel<T, float, 64> : pa_v2_qk_rope_append_kernel<T, T, 64>;
-  return q32 ? pa_v2_qk_rope_append_kernel<T, float, 128> : pa_v2_qk_rope_append_kernel<T, T, 128>;
+QkKernel pick(int D, bool q32, bool paired, int np) {
+  return q32 ? pick_layout<T, float>(D, paired, np) : pick_layout<T, T>(D, paired, np);
 }
 
 bool aligned(const void* x, int64_t a) { return reinterpret_cast<uintptr_t>(x) % a == 0; }
@@ -241,7 +324,7 @@ extern "C" pa_status pa_v2_qk_rope_append(const void* q, int64_t q_stride, const
   if (q_dtype != dtype && q_dtype != PA_F32) return PA_EUNSUPPORTED;
   if (head_dim != 64 && head_dim != 128) return PA_EUNSUPPORTED;
   if (rot_dim > head_dim || rot_dim % 16 != 0) return PA_EUNSUPPORTED;
-  if (num_qo_heads > 65536 || num_kv_heads > 65536) return PA_EUNSUPPORTED;
+  if (num_qo_heads > 16384 || num_kv_heads > 16384) return PA_EUNSUPPORTED;
   if (num_pages >= (1ll << 31) || num_pages * page_size >= (1ll << 31)) return PA_EUNSUPPORTED;
   if (num_tokens == 0) return PA_OK;
   if (!q || !k || !v || !positions || !slots || !q_out || !k_pool || !v_pool || (rot_dim > 0 && !inv_freq))
@@ -275,12 +358,30 @@ extern "C" pa_status pa_v2_qk_rope_append(const void* q, int64_t q_stride, const
   p.hq = num_qo_heads;
   p.hkv = num_kv_heads;
   p.rot = rot_dim;
-  p.interleaved = interleaved ? 1 : 0;
+  p.tokens = num_tokens;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return PA_ECUDA;
+  // Head passes of a token: as few CTAs per token as hold them, or, while the tokens alone do not fill the GPU, a
+  // CTA per pass (8 tokens of 48 heads: 24 CTAs instead of 8).
   const bool q32 = q_dtype == PA_F32;
-  const pa::QkKernel fn = dtype == PA_F32   ? pa::pick<float>(head_dim, true)
-                          : dtype == PA_F16 ? pa::pick<__half>(head_dim, q32)
-                                            : pa::pick<__nv_bfloat16>(head_dim, q32);
-  const cudaError_t rc = pa::launch_dependent(fn, dim3(num_tokens), dim3(pa::kQkThreads), 0,
-                                              static_cast<cudaStream_t>(cuda_stream), p);
+  const int rows = (int)(pa::kQkThreads / (head_dim * esize / 16));
+  const int passes = (num_qo_heads + 2 * num_kv_heads + rows - 1) / rows;
+  int groups = (passes + pa::kQkPasses - 1) / pa::kQkPasses;
+  if ((int64_t)num_tokens * groups < sms) groups = passes;
+  const int np = (passes + groups - 1) / groups;
+  const pa::QkKernel fn = dtype == PA_F32   ? pa::pick<float>(head_dim, true, !interleaved, np)
+                          : dtype == PA_F16 ? pa::pick<__half>(head_dim, q32, !interleaved, np)
+                                            : pa::pick<__nv_bfloat16>(head_dim, q32, !interleaved, np);
+  int per_sm = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, pa::kQkThreads, 0) != cudaSuccess || per_sm < 1)
+    return PA_ECUDA;
+  const int64_t wave = ((int64_t)sms * per_sm + groups - 1) / groups;  // CTAs along the tokens: one wave
+  int tile = (int)(num_tokens / wave);  // whole tiles only where every CTA still gets some
+  p.tile = tile < 1 ? 1 : tile < pa::kQkTile ? tile : pa::kQkTile;
+  const int64_t tiles = ((int64_t)num_tokens + p.tile - 1) / p.tile;
+  const cudaError_t rc = pa::launch_dependent(fn, dim3((unsigned)(tiles < wave ? tiles : wave), groups),
+                                              dim3(pa::kQkThreads), 0, static_cast<cudaStream_t>(cuda_stream), p);
   return rc == cudaSuccess && cudaGetLastError() == cudaSuccess ? PA_OK : PA_ECUDA;
 }

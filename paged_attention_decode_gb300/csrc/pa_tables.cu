@@ -48,6 +48,7 @@ struct TableParams {
   int32_t* status;
   int32_t batch, width, num_free, page_size, window, mask_words;
   int32_t index_cap, token_cap;
+  uint32_t ps_magic, ps_shift;
 };
 
 // One request's share of the step.
@@ -61,25 +62,37 @@ struct ReqGeom {
   bool bad;         // lengths out of range: no pages, no slots
 };
 
+__device__ __forceinline__ int32_t pages_of(const TableParams& p, int32_t rows) {  // ceil(rows / page_size)
+  return rows > 0 ? (int32_t)fast_div((uint32_t)(rows - 1), p.ps_magic, p.ps_shift) + 1 : 0;
+}
+
 __device__ __forceinline__ ReqGeom request_geom(const TableParams& p, int r) {
   ReqGeom g;
   const int32_t c = p.cached[r], n = p.fresh[r];
-  const int64_t s = p.page_size;
-  const int64_t t = (int64_t)max(c, 0) + max(n, 0);
-  const int64_t need = (t + s - 1) / s;
-  g.bad = c < 0 || n < 0 || need > p.width;
   g.cached = max(c, 0);
   g.tokens = max(n, 0);
   g.have = g.need = g.first = g.fpo = g.lpl = 0;
-  if (!g.bad && t > 0) {
-    const int64_t start = p.window > 0 && t > p.window ? t - p.window : 0;
-    g.have = (int32_t)((c + s - 1) / s);
-    g.need = (int32_t)need;
-    g.first = (int32_t)(start / s);
-    g.fpo = (int32_t)(start - (int64_t)g.first * s);
-    g.lpl = (int32_t)(t - (need - 1) * s);
+  g.bad = c < 0 || n < 0 || (int64_t)c + n > INT32_MAX;
+  if (!g.bad) {
+    const int32_t t = c + n;
+    const int32_t need = pages_of(p, t);
+    g.bad = need > p.width;
+    if (!g.bad && t > 0) {
+      const int32_t start = p.window > 0 && t > p.window ? t - p.window : 0;
+      g.have = pages_of(p, c);
+      g.need = need;
+      g.first = (int32_t)fast_div((uint32_t)start, p.ps_magic, p.ps_shift);
+      g.fpo = start - g.first * p.page_size;
+      g.lpl = t - (need - 1) * p.page_size;
+    }
   }
   return g;
+}
+
+// Sums that stop at the largest value: a batch may claim more tokens than fit.
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) {
+  const uint32_t s = a + b;
+  return s < a ? 0xffffffffu : s;
 }
 
 // Last r in [0, n) with a[r] <= x (a non-decreasing, a[0] <= x).
@@ -111,7 +124,7 @@ __global__ void __launch_bounds__(kTabThreads) pa_v2_build_tables_kernel(const T
   int32_t* ip = sm;               // [B + 1] page-list prefix
   int32_t* taken = ip + B + 1;    // [B + 1] taken-page prefix
   int32_t* qo = taken + B + 1;    // [B + 1] token prefix, clamped to the capacity
-  __shared__ int64_t warp_sum[3][kTabThreads / 32];
+  __shared__ uint32_t warp_sum[3][kTabThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   pdl_launch_dependents();
@@ -120,50 +133,58 @@ __global__ void __launch_bounds__(kTabThreads) pa_v2_build_tables_kernel(const T
   // ---- the three prefix sums: each thread a run of consecutive requests
   const int per = (B + kTabThreads - 1) / kTabThreads;
   const int r0 = min(tid * per, B), r1 = min(r0 + per, B);
-  int64_t sum[3] = {0, 0, 0};
+  // (page counts fit: batch * width does)
+  uint32_t sum[3] = {0, 0, 0};
   for (int r = r0; r < r1; ++r) {
     const ReqGeom g = request_geom(p, r);
     if (g.bad && blockIdx.x == 0) report(p.status, PA_DEVICE_BAD_LENGTH);
     const int32_t pages = g.need - g.first, take = p.free_pages ? g.need - g.have : 0;
     ip[r] = pages;
     taken[r] = take;
+    qo[r] = g.tokens;
     sum[0] += pages;
     sum[1] += take;
-    sum[2] += g.tokens;
+    sum[2] = add_sat(sum[2], g.tokens);
   }
-  int64_t before[3];
+  uint32_t before[3];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    int64_t v = sum[k];
+    uint32_t v = __shfl_up_sync(0xffffffffu, sum[k], 1);
+    if (lane == 0) v = 0;
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, v, w);
-      if (lane >= w) v += u;
+      const uint32_t u = __shfl_up_sync(0xffffffffu, v, w);
+      if (lane >= w) v = add_sat(v, u);
     }
-    before[k] = v - sum[k];
-    if (lane == 31) warp_sum[k][warp] = v;
+    before[k] = v;
+    if (lane == 31) warp_sum[k][warp] = add_sat(v, sum[k]);
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 3; ++k)
-    for (int w = 0; w < warp; ++w) before[k] += warp_sum[k][w];
+  for (int k = 0; k < 3; ++k) {
+    uint32_t earlier = 0;
+#pragma unroll
+    for (int w = 0; w < kTabThreads / 32; ++w)
+      if (w < warp) earlier = add_sat(earlier, warp_sum[k][w]);
+    before[k] = add_sat(earlier, before[k]);
+  }
+  const uint32_t cap = (uint32_t)p.token_cap;
   for (int r = r0; r < r1; ++r) {
-    const int32_t pages = ip[r], take = taken[r];
-    const int32_t n = max(p.fresh[r], 0);
+    const int32_t pages = ip[r], take = taken[r], n = qo[r];
     ip[r] = (int32_t)before[0];
     taken[r] = (int32_t)before[1];
-    qo[r] = (int32_t)min(before[2], (int64_t)p.token_cap);
+    qo[r] = (int32_t)min(before[2], cap);
     before[0] += pages;
     before[1] += take;
-    before[2] += n;
+    before[2] = add_sat(before[2], n);
   }
   if (tid == kTabThreads - 1) {  // the last thread's runs end at B
     ip[B] = (int32_t)before[0];
     taken[B] = (int32_t)before[1];
-    qo[B] = (int32_t)min(before[2], (int64_t)p.token_cap);
+    qo[B] = (int32_t)min(before[2], cap);
     if (blockIdx.x == 0) {
-      if (before[2] > p.token_cap || before[0] > p.index_cap) report(p.status, PA_DEVICE_BAD_LENGTH);
-      if (p.free_pages && before[1] > p.num_free) report(p.status, PA_DEVICE_NO_PAGES);
+      if (before[2] > cap || before[0] > (uint32_t)p.index_cap) report(p.status, PA_DEVICE_BAD_LENGTH);
+      if (p.free_pages && before[1] > (uint32_t)p.num_free) report(p.status, PA_DEVICE_NO_PAGES);
       *p.pages_needed = (int32_t)before[1];
     }
   }
@@ -195,12 +216,23 @@ __global__ void __launch_bounds__(kTabThreads) pa_v2_build_tables_kernel(const T
   const int32_t n_idx = min(ip[B], p.index_cap);
   const int64_t gwarps = (int64_t)gridDim.x * (kTabThreads / 32);
   for (int64_t run = (int64_t)blockIdx.x * (kTabThreads / 32) + warp; run * kTabRun < n_idx; run += gwarps) {
-    int32_t i = (int32_t)(run * kTabRun) + lane;
+    const int32_t i0 = (int32_t)(run * kTabRun);
     const int32_t end = (int32_t)min((run + 1) * (int64_t)kTabRun, (int64_t)n_idx);
-    int r = -1;
-    int32_t r_end = INT_MIN;
-    ReqGeom g;
-    for (; i < end; i += 32) {
+    int r = last_le(ip, B, i0);
+    ReqGeom g = request_geom(p, r);
+    int32_t col = g.first + i0 - ip[r];
+    if (end - i0 == kTabRun && end <= ip[r + 1] && (!p.free_pages || col + kTabRun <= g.have)) {
+      // one request's old pages: a plain copy, all loads in flight at once
+      const int32_t* src = p.block_table + (int64_t)r * p.width + col + lane;
+      int32_t x[kTabRun / 32];
+#pragma unroll
+      for (int k = 0; k < kTabRun / 32; ++k) x[k] = src[32 * k];
+#pragma unroll
+      for (int k = 0; k < kTabRun / 32; ++k) p.indices[i0 + lane + 32 * k] = x[k];
+      continue;
+    }
+    int32_t r_end = ip[r + 1];
+    for (int32_t i = i0 + lane; i < end; i += 32) {
       if (i >= r_end) {
         r = last_le(ip, B, i);
         r_end = ip[r + 1];
@@ -223,9 +255,10 @@ __global__ void __launch_bounds__(kTabThreads) pa_v2_build_tables_kernel(const T
     const int32_t i = (int32_t)t - base;
     int64_t slot = -1;
     if (!g.bad) {
-      const int64_t at = (int64_t)g.cached + i;
-      const int32_t page = page_at(p, taken, g, r, (int32_t)(at / p.page_size));
-      slot = (int64_t)page * p.page_size + at % p.page_size;
+      const int32_t at = g.cached + i;
+      const int32_t entry = (int32_t)fast_div((uint32_t)at, p.ps_magic, p.ps_shift);
+      const int32_t page = page_at(p, taken, g, r, entry);
+      slot = (int64_t)page * p.page_size + (at - entry * p.page_size);
       if (page < 0 || slot > INT32_MAX) {
         slot = -1;
         report(p.status, page == -1 && p.free_pages ? PA_DEVICE_NO_PAGES : PA_DEVICE_BAD_PAGE);
@@ -271,7 +304,7 @@ __global__ void __launch_bounds__(kTabThreads) pa_v2_build_tables_kernel(const T
       depth = i;
     }
     if (bad_tree) report(p.status, PA_DEVICE_BAD_TREE);
-    p.positions[t] = g.bad ? 0 : (int32_t)min((int64_t)g.cached + depth, (int64_t)INT32_MAX);
+    p.positions[t] = g.bad ? 0 : g.cached + depth;
   }
 }
 
@@ -324,6 +357,9 @@ extern "C" pa_status pa_v2_build_tables(const int32_t* cached_lens, const int32_
   p.mask_words = mask_words;
   p.index_cap = (int32_t)index_capacity;
   p.token_cap = (int32_t)token_capacity;
+  const pa::FastDiv fd = pa::FastDiv::make((uint32_t)page_size);
+  p.ps_magic = fd.magic;
+  p.ps_shift = fd.shift;
   const size_t smem = 3 * ((size_t)batch + 1) * sizeof(int32_t);
   constexpr size_t kMaxSmem = 3 * (PA_V2_MAX_TABLE_BATCH + 1) * sizeof(int32_t);
   if (!pa::prepare_kernel(reinterpret_cast<const void*>(pa::pa_v2_build_tables_kernel), kMaxSmem)) return PA_ECUDA;
