@@ -27,11 +27,13 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
 #include "pa_device.cuh"
 #include "pa_internal.cuh"
+#include "pa_tc05.cuh"
 #include "pa_v2.h"
 
 namespace pa {
@@ -156,19 +158,27 @@ __global__ void __launch_bounds__(kQkThreads, 2) pa_v2_qk_rope_append_kernel(con
   const int e0 = PAIRED && rotated ? lane * P : lane * N, e1 = PAIRED && rotated ? e0 + half : e0 + P;
   const int heads = p.hq + 2 * p.hkv;
 
-  // this lane's heads
-  const T* src[NP];
+  // this lane's heads: where they are read and written (bytes; a row's place is base + index * step, both steps
+  // below 2^31), and their norm weights
+  const char* src[NP];
+  char* dst[NP];
+  uint32_t src_step[NP], dst_step[NP];
   uint4 weight[NP];
-  int kind[NP], hh[NP];  // q, k, v or none; the head among its kind
+  int kind[NP];  // q, k, v or none
   bool normed[NP];
+  const int gap = e1 - e0;
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int h = ((int)blockIdx.y * NP + i) * kRows + (int)threadIdx.x / kLanes;
     kind[i] = h < p.hq ? 0 : h < p.hq + p.hkv ? 1 : h < heads ? 2 : 3;
-    hh[i] = kind[i] == 0 ? h : kind[i] == 1 ? h - p.hq : h - p.hq - p.hkv;
-    const T* base = static_cast<const T*>(kind[i] == 0 ? p.q : kind[i] == 1 ? p.k : p.v);
-    const int64_t step = kind[i] == 0 ? p.q_stride : kind[i] == 1 ? p.k_stride : p.v_stride;
-    src[i] = base + (int64_t)blockIdx.x * p.tile * step + (int64_t)hh[i] * D;
+    const int hh = kind[i] == 0 ? h : kind[i] == 1 ? h - p.hq : h - p.hq - p.hkv;
+    const int at = hh * D + e0;
+    const T* base = static_cast<const T*>(kind[i] == 0 ? p.q : kind[i] == 1 ? p.k : p.v) + at;
+    src[i] = reinterpret_cast<const char*>(base);
+    src_step[i] = (uint32_t)((kind[i] == 0 ? p.q_stride : kind[i] == 1 ? p.k_stride : p.v_stride) * sizeof(T));
+    dst[i] = kind[i] == 0 ? reinterpret_cast<char*>(static_cast<TQ*>(p.q_out) + at)
+                          : reinterpret_cast<char*>(static_cast<T*>(kind[i] == 1 ? p.k_pool : p.v_pool) + at);
+    dst_step[i] = kind[i] == 0 ? (uint32_t)(p.hq * D * sizeof(TQ)) : (uint32_t)(p.hkv * D * sizeof(T));
     const T* w = static_cast<const T*>(kind[i] == 0 ? p.q_weight : kind[i] == 1 ? p.k_weight : nullptr);
     normed[i] = w != nullptr;
     weight[i] = make_uint4(0, 0, 0, 0);
@@ -190,21 +200,21 @@ __global__ void __launch_bounds__(kQkThreads, 2) pa_v2_qk_rope_append_kernel(con
   const int jump = ((int)gridDim.x - 1) * p.tile + 1;  // from a tile's last token to the next tile's first
   uint4 next[NP];
   int32_t next_slot = 0;
-  auto fetch = [&](int at, int skip) {  // a token's pieces; src moves on by `skip` tokens
+  auto fetch = [&](int at) {  // a token's pieces
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       next[i] = make_uint4(0, 0, 0, 0);
       if (kind[i] < 3) {
-        const uint2 a = load_stream(src[i] + e0), b = load_stream(src[i] + e1);
+        const char* from = src[i] + (uint64_t)(uint32_t)at * src_step[i];
+        const uint2 a = load_stream(from), b = load_stream(from + gap * (int)sizeof(T));
         next[i] = make_uint4(a.x, a.y, b.x, b.y);
       }
-      src[i] += (int64_t)skip * (kind[i] == 0 ? p.q_stride : kind[i] == 1 ? p.k_stride : p.v_stride);
     }
     next_slot = p.slots[at];
   };
   auto skip_of = [&](int place) { return place + 1 == p.tile ? jump : 1; };
   if (t < p.tokens) {
-    fetch(t, skip_of(0));
+    fetch(t);
     angles(t, 0);
   }
   __syncthreads();
@@ -215,7 +225,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) pa_v2_qk_rope_append_kernel(con
     const int64_t slot = next_slot;
     const int place = in_tile, after = t + skip_of(place);
     in_tile = place + 1 == p.tile ? 0 : place + 1;
-    if (after < p.tokens) fetch(after, skip_of(in_tile));
+    if (after < p.tokens) fetch(after);
     if (place == 0) angles(t + (int)gridDim.x * p.tile, buf ^ 1);
     if (slot >= 0 && slot < p.num_rows) {
       float2 r[P];  // the pairs' cosines and sines
@@ -236,9 +246,10 @@ __global__ void __launch_bounds__(kQkThreads, 2) pa_v2_qk_rope_append_kernel(con
           float x[N];
           Vec<T>::unpack(raw[k], x);
           if (__any_sync(0xffffffffu, normed[k])) {
-            float ss = 0.f;
+            float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
+            for (int i = 0; i < N; i += 2) s2 = fma2(make_float2(x[i], x[i + 1]), make_float2(x[i], x[i + 1]), s2);
+            float ss = s2.x + s2.y;
 #pragma unroll
             for (int w = kLanes / 2; w >= 1; w >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, w);
             if (normed[k]) {
@@ -256,23 +267,18 @@ __global__ void __launch_bounds__(kQkThreads, 2) pa_v2_qk_rope_append_kernel(con
             x[a] = fmaf(-w, r[i].y, u * r[i].x);
             x[b] = fmaf(u, r[i].y, w * r[i].x);
           }
-          if (kind[k] == 0) {
-            TQ* dst = static_cast<TQ*>(p.q_out) + ((int64_t)t * p.hq + hh[k]) * D;
-            if (sizeof(TQ) == sizeof(T)) {
-              const uint4 z = Vec<T>::pack(x);
-              *reinterpret_cast<uint2*>(dst + e0) = make_uint2(z.x, z.y);
-              *reinterpret_cast<uint2*>(dst + e1) = make_uint2(z.z, z.w);
-            } else {  // f32 from 16 bits: a piece is 16 bytes
-              *reinterpret_cast<float4*>(dst + e0) = make_float4(x[0], x[1], x[2], x[3]);
-              *reinterpret_cast<float4*>(dst + e1) = make_float4(x[P], x[P + 1], x[N - 2], x[N - 1]);
-            }
+          if (kind[k] == 0 && sizeof(TQ) != sizeof(T)) {  // f32 from 16 bits: a piece is 16 bytes
+            char* to = dst[k] + (uint64_t)(uint32_t)t * dst_step[k];
+            *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(to + gap * (int)sizeof(TQ)) = make_float4(x[P], x[P + 1], x[N - 2], x[N - 1]);
+          } else if (kind[k] < 2) {
+            raw[k] = Vec<T>::pack(x);
           }
-          if (kind[k] == 1) raw[k] = Vec<T>::pack(x);
         }
-        if (kind[k] == 1 || kind[k] == 2) {
-          T* dst = static_cast<T*>(kind[k] == 1 ? p.k_pool : p.v_pool) + (slot * p.hkv + hh[k]) * D;
-          *reinterpret_cast<uint2*>(dst + e0) = make_uint2(raw[k].x, raw[k].y);
-          *reinterpret_cast<uint2*>(dst + e1) = make_uint2(raw[k].z, raw[k].w);
+        if (kind[k] < 3 && !(kind[k] == 0 && sizeof(TQ) != sizeof(T))) {
+          char* to = dst[k] + (uint64_t)(uint32_t)(kind[k] == 0 ? t : (int)slot) * dst_step[k];
+          *reinterpret_cast<uint2*>(to) = make_uint2(raw[k].x, raw[k].y);
+          *reinterpret_cast<uint2*>(to + gap * (int)sizeof(T)) = make_uint2(raw[k].z, raw[k].w);
         }
       }
     } else if (slot >= p.num_rows && threadIdx.x == 0) {
@@ -331,6 +337,8 @@ extern "C" pa_status pa_v2_qk_rope_append(const void* q, int64_t q_stride, const
     return PA_EINVAL;
   const int64_t esize = dtype == PA_F32 ? 4 : 2;
   const int64_t q_row = (int64_t)num_qo_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
+  if (q_stride * esize > INT32_MAX || k_stride * esize > INT32_MAX || v_stride * esize > INT32_MAX)
+    return PA_EUNSUPPORTED;
   if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride * esize % 16 || k_stride * esize % 16 ||
       v_stride * esize % 16)
     return PA_EINVAL;

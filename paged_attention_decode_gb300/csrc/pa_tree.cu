@@ -89,6 +89,8 @@ template <typename T> struct PRange;
 template <> struct PRange<__half> { static constexpr float kShift = 11.f, kLazy = 4.f; };
 template <> struct PRange<__nv_bfloat16> { static constexpr float kShift = 0.f, kLazy = 8.f; };
 
+struct TreeFold;
+
 struct TreeParams {
   const void* q;
   const void* k_pool;
@@ -102,6 +104,7 @@ struct TreeParams {
   void* out;
   float* lse_out;
   float* slots;    // partial results: kTrSlots * ctas
+  TreeFold* folds;  // what each CTA of the merge kernel has to do
   int32_t* status;
   int64_t num_pages, num_indices;
   int32_t batch, num_tokens, mask_words, page_size, box_rows, hq, hkv, group, ctas;
@@ -386,6 +389,17 @@ __device__ __forceinline__ TreeReq shfl_req(const TreeReq& g, int r) {
   for (int i = 0; i < (int)(sizeof(TreeReq) / 4); ++i) dst[i] = __shfl_sync(0xffffffffu, src[i], r);
   return o;
 }
+
+// A block to fold, and one CTA's share of it, as the attention kernel leaves it for the merge kernel.  The parts lie,
+// in the order of the keys, in slots first_chunk .. first_chunk + chunks - 1 and, for the left-over weight (which
+// begins `lead` into the stretch of CTA cta0), in those of rest_slot.
+struct alignas(16) TreeFold {
+  int32_t shares;  // 0: nothing to fold here
+  int32_t share;
+  int32_t t0, row0, rows, kvh;
+  int32_t first_chunk, chunks;
+  int32_t weight, lead, cta0, stretch;
+};
 
 // A run of key tiles of one block, as the loader hands it to the other roles.
 struct TreePiece {
@@ -990,15 +1004,49 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
         }
       };
 
+      // what the merge kernel's CTA of this number does: blocks with chunks are shared out over the CTAs of their
+      // chunks, blocks without over the CTAs whose stretches cut them.  `at`: where the block's left-over weight
+      // begins; share < 0: counted from the stretch ends behind the block's first tile.
+      const bool writes = leader && lane == 0;
+      if (writes) p.folds[blockIdx.x].shares = 0;
+      auto fold = [&](int kvh, int b, int first_chunk, int32_t chunks, int share, int64_t at, int32_t weight) {
+        TreeFold f;
+        f.stretch = cut.stretch;
+        f.t0 = g.t0;
+        f.kvh = kvh;
+        f.row0 = b * kTrBlock;
+        f.rows = min(kTrBlock, g.n * p.group - f.row0);
+        f.first_chunk = first_chunk;
+        f.chunks = chunks;
+        f.weight = weight;
+        f.cta0 = f.lead = 0;
+        if (weight > 0) {
+          const int64_t i = div_units(at, cut.stretch);
+          f.cta0 = cut.chunks + (int)i;
+          f.lead = (int32_t)(at - i * cut.stretch);
+        }
+        f.shares = chunks;
+        f.share = share;
+        if (share < 0) {
+          const int idle = (f.lead + kTrRestCost) / cut.stretch;  // stretch ends at or before the first tile
+          f.share = (int)blockIdx.x - f.cta0 - idle;
+          f.shares = (f.lead + weight - 1) / cut.stretch - idle;
+        }
+        if (writes) p.folds[blockIdx.x] = f;
+      };
+
       int r = cut.r;
       if (r < p.batch && (int)blockIdx.x < cut.chunks) {
         g = small ? shfl_req(mine, r) : tree_req(p, r, false);
         const HeadCut h = head_cut(g, p.group, run);
         const int kvh = (int)div_units(cut.off, h.chunks);
         const BlockAt k = block_at(g, p.group, run, (int32_t)(cut.off - (int64_t)kvh * h.chunks), true);
+        if (k.tiles != run && g.kind != kReqEmpty)
+          fold(kvh, k.b, (int)blockIdx.x - k.x, k.tiles / run, k.x,
+               cut.r_weight + (int64_t)kvh * h.weight + k.weight, rest_weight(k.tiles, run));
         piece(kvh, k.b, k.x * run, run, k.tiles == run ? -1 : (int)blockIdx.x);
       } else {
-        int64_t off = cut.off;
+        int64_t off = cut.off, r_weight = cut.r_weight;
         int32_t left = (int32_t)min((int64_t)cut.stretch,
                                     cut.weight - (int64_t)((int)blockIdx.x - cut.chunks) * cut.stretch);
         int chunks_before = cut.r_chunks;
@@ -1021,14 +1069,18 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
                           ? -1
                           : rest_slot(ends, chunks, chunks_before + kvh * h.chunks + k.chunks, blockIdx.x, p.ctas));
               left -= take;
+              if (!ends && chunks == 0 && t1 > 0 && g.kind != kReqEmpty)  // the stretch ends inside, behind its first tile
+                fold(kvh, k.b, 0, 0, -1, r_weight + (int64_t)kvh * h.weight + k.weight, weight);
               if (k.b + 1 >= g.blocks) break;
               k.chunks += chunks;
+              k.weight += weight;
               ++k.b;
               k.tiles = tiles_of(g, p.group, k.b);
               k.x = 0;
             }
           }
           chunks_before += p.hkv * h.chunks;
+          r_weight += (int64_t)p.hkv * h.weight;
         }
       }
       if (alive) {
@@ -1248,77 +1300,34 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
 }
 
 // Folds the partial results of blocks that were cut: weights 2^(lse_i - max) of the normalized parts, in the
-// order of the keys.  A block with chunks is shared out over the CTAs of its chunks, one without over the CTAs
-// whose stretches cut it; a warp takes 32 rows x 8 columns, one row per lane (the parts are stored column by
-// column, so a warp's loads are contiguous), eight parts in flight.
+// order of the keys.  CTA c does what CTA c of the attention kernel wrote down for it; a warp takes 32 rows x 8
+// columns, one row per lane (the parts are stored column by column, so a warp's loads are contiguous), eight
+// parts in flight.
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads) pa_v2_tree_merge_kernel(const TreeParams p) {
-  __shared__ TreeCut start;
-  __shared__ int64_t warp_sum[kMergeThreads / 32];
   using C = TreeCfg<D>;
   const int lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait_prerequisites();
-  const int c = blockIdx.x;
-  TreeCut cut;
-  TreeReq g = {};
-  if (p.batch <= 32) {
-    if (lane < p.batch) g = tree_req(p, lane, false);
-    cut = cut_warp(p, c, 1, g, lane);
-    if (cut.r >= p.batch) return;
-    g = shfl_req(g, cut.r);
-  } else {
-    cut_block<kMergeThreads>(p, c, 1, false, &start, warp_sum);
-    cut = start;
-    if (cut.r >= p.batch) return;
-    g = tree_req(p, cut.r, false);
-  }
-  if (g.kind == kReqEmpty) return;
-  const int32_t run = cut.run, stretch = cut.stretch;
-  const bool chunk = c < cut.chunks;
-  const HeadCut h = head_cut(g, p.group, run);
-  const int kvh = (int)div_units(cut.off, chunk ? h.chunks : h.weight);
-  const BlockAt k = block_at(g, p.group, run, (int32_t)(cut.off - (int64_t)kvh * (chunk ? h.chunks : h.weight)), chunk);
-  const int32_t chunks = k.tiles / run, weight = rest_weight(k.tiles, run);
-  const int first_chunk = cut.r_chunks + kvh * h.chunks + k.chunks;
-  // the block's left-over weight begins `lead` into the stretch of CTA cta0
-  int cta0 = 0;
-  int32_t lead = 0;
-  if (weight > 0) {
-    const int64_t at = cut.r_weight + (int64_t)kvh * h.weight + k.weight;
-    const int64_t i = div_units(at, stretch);
-    cta0 = cut.chunks + (int)i;
-    lead = (int32_t)(at - i * stretch);
-  }
-  int share = k.x, shares = chunks;  // of the block's rows and columns
-  if (chunk) {
-    if (chunks == 1 && weight == 0) return;  // one piece: already written as the result
-  } else {
-    // the end of c's stretch lies k.x into the block's weight; only ends behind its first tile cut it
-    if (chunks > 0 || k.x <= kTrRestCost) return;
-    shares = (lead + weight - 1) / stretch;
-    const int idle = (lead + kTrRestCost) / stretch;  // ends at or before the first tile
-    share = c - cta0 - idle;
-    shares -= idle;
-  }
-  const int rows = min(kTrBlock, g.n * p.group - k.b * kTrBlock);
-  const int jobs = (rows + 31) / 32 * (D / 8);
-  const int workers = shares * (int)gridDim.y * (kMergeThreads / 32);
-  const int me = (share * (int)gridDim.y + (int)blockIdx.y) * (kMergeThreads / 32) + (int)(threadIdx.x >> 5);
+  const TreeFold f = p.folds[blockIdx.x];
+  if (f.shares == 0) return;
+  const int jobs = (f.rows + 31) / 32 * (D / 8);
+  const int workers = f.shares * (int)gridDim.y * (kMergeThreads / 32);
+  const int me = (f.share * (int)gridDim.y + (int)blockIdx.y) * (kMergeThreads / 32) + (int)(threadIdx.x >> 5);
   for (int job = me; job < jobs; job += workers) {
     const int rg = job / (D / 8), oct = job % (D / 8);
     const int in_block = rg * 32 + lane;
-    const int row = k.b * kTrBlock + in_block;
-    const bool valid = in_block < rows;
+    const int row = f.row0 + in_block;
+    const bool valid = in_block < f.rows;
     int i = 0;          // chunks taken
     int32_t at = 0;     // left-over weight taken
-    int cta = cta0;
+    int cta = f.cta0;
     auto next = [&]() -> int {  // slot of the next part in the order of the keys, or -1
-      if (i < chunks) return first_chunk + i++;
-      while (at < weight) {
-        const int32_t end = min((cta - cta0 + 1) * stretch - lead, weight);
+      if (i < f.chunks) return f.first_chunk + i++;
+      while (at < f.weight) {
+        const int32_t end = min((cta - f.cta0 + 1) * f.stretch - f.lead, f.weight);
         const bool some = end > max(at, kTrRestCost);
-        const int slot = rest_slot(end == weight, chunks, first_chunk, cta, p.ctas);
+        const int slot = rest_slot(end == f.weight, f.chunks, f.first_chunk, cta, p.ctas);
         at = end;
         ++cta;
         if (some) return slot;
@@ -1376,7 +1385,7 @@ __global__ void __launch_bounds__(kMergeThreads) pa_v2_tree_merge_kernel(const T
     }
     if (!valid) continue;
     const int tok = (int)fast_div((uint32_t)row, p.g_magic, p.g_shift);
-    const int64_t orow = (int64_t)(g.t0 + tok) * p.hq + (int64_t)kvh * p.group + (row - tok * p.group);
+    const int64_t orow = (int64_t)(f.t0 + tok) * p.hq + (int64_t)f.kvh * p.group + (row - tok * p.group);
     const float inv = L == 0.f ? 0.f : 1.f / L;
     *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + orow * D + 8 * oct) =
         make_uint4(TC<T>::pack(acc[0].x * inv, acc[0].y * inv), TC<T>::pack(acc[0].z * inv, acc[0].w * inv),
@@ -1394,6 +1403,11 @@ template <typename T>
 TreeKernel pick_tree(int D, bool tma) {
   if (D == 64) return tma ? pa_v2_tree_attention_kernel<T, 64, true> : pa_v2_tree_attention_kernel<T, 64, false>;
   return tma ? pa_v2_tree_attention_kernel<T, 128, true> : pa_v2_tree_attention_kernel<T, 128, false>;
+}
+
+int64_t slots_bytes(int32_t ctas, int32_t head_dim) {
+  return (int64_t)ctas * kTrSlots * (int64_t)sizeof(float) *
+         (head_dim == 64 ? TreeCfg<64>::kSlotFloats : TreeCfg<128>::kSlotFloats);
 }
 
 // CTAs of the attention kernel: one per SM.
@@ -1420,8 +1434,7 @@ extern "C" pa_status pa_v2_tree_attention_workspace(int32_t device, int32_t num_
   int32_t ctas = 0;
   const pa_status rc = pa::tree_ctas(device, &ctas);
   if (rc != PA_OK) return rc;
-  *bytes = (int64_t)ctas * pa::kTrSlots * (int64_t)sizeof(float) *
-           (head_dim == 64 ? pa::TreeCfg<64>::kSlotFloats : pa::TreeCfg<128>::kSlotFloats);
+  *bytes = pa::slots_bytes(ctas, head_dim) + ctas * (int64_t)sizeof(pa::TreeFold);
   return PA_OK;
 }
 
@@ -1496,6 +1509,7 @@ extern "C" pa_status pa_v2_tree_attention(const void* q, const void* k_pool, con
   p.group = num_qo_heads / num_kv_heads;
   const pa_status sm = pa::tree_ctas(dev, &p.ctas);
   if (sm != PA_OK) return sm;
+  p.folds = reinterpret_cast<pa::TreeFold*>(static_cast<char*>(workspace) + pa::slots_bytes(p.ctas, head_dim));
   const pa::FastDiv fd = pa::FastDiv::make((uint32_t)page_size), fg = pa::FastDiv::make((uint32_t)p.group);
   p.ps_magic = fd.magic;
   p.ps_shift = fd.shift;
