@@ -58,10 +58,11 @@ constexpr int kTrThreads = 384;
 constexpr int kTrTile = 128;      // query rows of a tensor-core tile, and keys of a key tile
 constexpr int kTrBlock = 256;     // query rows of a block
 constexpr int kTrSlots = 2;       // partial results per CTA (see rest_slot)
-constexpr int kTrRestCost = 4;    // what starting a left-over stretch costs, in key tiles
+constexpr int kTrRestCost = 6;    // what starting a left-over stretch costs, in key tiles
 constexpr int kTrMmaWarp = 8, kTrLoadWarp = 9, kTrFixWarp = 11;
 constexpr int kTrLoadThreads = 64;  // loader threads without TMA
 constexpr int kTrRing = 2;        // pieces handed out ahead
+constexpr int kTrLag = 3;         // without TMA: loads in flight behind the newest (below kStages - 1)
 constexpr int kMergeThreads = 256;
 
 // Tensor-memory columns: S of both streams (P over its first 64), then O of both.
@@ -112,6 +113,7 @@ struct TreeParams {
   float scale_log2;   // |sm_scale| * log2(e), or 1 for a zero scale
   uint32_t q_xor;     // sign flip of both halves of a q word for a negative scale
   uint32_t q_and;     // 0 for a zero scale
+  int32_t small;      // the batch's requests fit a warp's lanes and all units 32 bits
 };
 
 // One request's share of the work.
@@ -228,7 +230,7 @@ struct TreeCut {
 __device__ __forceinline__ int32_t run_of(int64_t tiles, int64_t blocks, int32_t ctas) {
   return (int32_t)max(div_units(tiles + kTrRestCost * blocks + ctas - 1, ctas), (int64_t)1);
 }
-// Position of CTA (or of its end, when `past` is 1) among the chunks (c < chunks) or the left-over weight.
+// The stretch length.
 __device__ __forceinline__ void set_stretch(TreeCut* t, int32_t ctas) {
   t->stretch = t->chunks < ctas ? (int32_t)div_units(t->weight + (ctas - t->chunks) - 1, ctas - t->chunks) : 0;
 }
@@ -242,38 +244,42 @@ __device__ __forceinline__ int64_t scan_add(int64_t v, int lane) {
   return v;
 }
 
-// The cut for a batch of up to 32 requests, by one warp: lane r holds request r in `mine`.  c < chunks: chunk c;
-// else left-over position (c - chunks + past) * stretch.
-__device__ __forceinline__ TreeCut cut_warp(const TreeParams& p, int c, int past, const TreeReq& mine, int lane) {
-  int64_t tiles = (int64_t)mine.units * p.hkv, blocks = (int64_t)mine.blocks * p.hkv;
-  if (p.batch > 1) {
-#pragma unroll
-    for (int w = 16; w >= 1; w >>= 1) {
-      tiles += __shfl_xor_sync(0xffffffffu, tiles, w);
-      blocks += __shfl_xor_sync(0xffffffffu, blocks, w);
-    }
-  } else {
-    tiles = __shfl_sync(0xffffffffu, tiles, 0);
-    blocks = __shfl_sync(0xffffffffu, blocks, 0);
+// The cut for a small batch, by one warp: lane r holds request r in `mine`.  c < chunks: chunk c; else left-over
+// position (c - chunks) * stretch.
+__device__ __forceinline__ TreeCut cut_warp(const TreeParams& p, int c, const TreeReq& mine, int lane) {
+  int32_t tiles = mine.units * p.hkv, blocks = mine.blocks * p.hkv;
+#pragma unroll 1
+  for (int w = p.batch > 1 ? 16 : 0; w >= 1; w >>= 1) {
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, w);
+    blocks += __shfl_xor_sync(0xffffffffu, blocks, w);
   }
   TreeCut t;
-  t.run = run_of(tiles, blocks, p.ctas);
+  t.run = (int32_t)max((uint32_t)(tiles + kTrRestCost * blocks + p.ctas - 1) / (uint32_t)p.ctas, 1u);
+  t.run = __shfl_sync(0xffffffffu, t.run, 0);
   const HeadCut h = head_cut(mine, p.group, t.run);
-  const int64_t chunks = (int64_t)h.chunks * p.hkv, weight = (int64_t)h.weight * p.hkv;
-  const int64_t chunks_to = p.batch > 1 ? scan_add(chunks, lane) : chunks;
-  const int64_t weight_to = p.batch > 1 ? scan_add(weight, lane) : weight;
+  const int32_t chunks = h.chunks * p.hkv, weight = h.weight * p.hkv;
+  int32_t chunks_to = chunks, weight_to = weight;
+#pragma unroll 1
+  for (int w = p.batch > 1 ? 1 : 32; w < 32; w <<= 1) {
+    const int32_t a = __shfl_up_sync(0xffffffffu, chunks_to, w), b = __shfl_up_sync(0xffffffffu, weight_to, w);
+    if (lane >= w) {
+      chunks_to += a;
+      weight_to += b;
+    }
+  }
   const int last = p.batch - 1;
-  t.chunks = (int32_t)__shfl_sync(0xffffffffu, chunks_to, last);
-  t.weight = __shfl_sync(0xffffffffu, weight_to, last);
-  set_stretch(&t, p.ctas);
+  t.chunks = __shfl_sync(0xffffffffu, chunks_to, last);
+  const int32_t all = __shfl_sync(0xffffffffu, weight_to, last);
+  t.weight = all;
+  t.stretch = (int32_t)((uint32_t)(all + (p.ctas - t.chunks) - 1) / (uint32_t)(p.ctas - t.chunks));
   const bool chunk = c < t.chunks;
-  const int64_t at = chunk ? c : (int64_t)(c - t.chunks + past) * t.stretch;
+  const int32_t at = chunk ? c : (c - t.chunks) * t.stretch;
   const uint32_t after = __ballot_sync(0xffffffffu, lane <= last && at < (chunk ? chunks_to : weight_to));
   t.r = after ? __ffs(after) - 1 : p.batch;
   const int src = after ? t.r : 0;
-  t.r_chunks = (int32_t)__shfl_sync(0xffffffffu, chunks_to - chunks, src);
+  t.r_chunks = __shfl_sync(0xffffffffu, chunks_to - chunks, src);
   t.r_weight = __shfl_sync(0xffffffffu, weight_to - weight, src);
-  t.off = at - (chunk ? t.r_chunks : t.r_weight);
+  t.off = at - (chunk ? t.r_chunks : (int32_t)t.r_weight);
   return t;
 }
 
@@ -296,7 +302,7 @@ __device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* warp_sum, in
 
 // The same for any batch, by every thread of the block (each a run of consecutive requests).
 template <int THREADS>
-__device__ __forceinline__ void cut_block(const TreeParams& p, int c, int past, bool tell, TreeCut* out,
+__device__ __forceinline__ void cut_block(const TreeParams& p, int c, bool tell, TreeCut* out,
                                           int64_t* warp_sum) {
   const int per = (p.batch + THREADS - 1) / THREADS;
   const int r0 = (int)min((int64_t)threadIdx.x * per, (int64_t)p.batch), r1 = min(r0 + per, p.batch);
@@ -323,7 +329,7 @@ __device__ __forceinline__ void cut_block(const TreeParams& p, int c, int past, 
   t.weight = all_weight;
   set_stretch(&t, p.ctas);
   const bool chunk = c < t.chunks;
-  const int64_t at = chunk ? c : (int64_t)(c - t.chunks + past) * t.stretch;
+  const int64_t at = chunk ? c : (int64_t)(c - t.chunks) * t.stretch;
   const int64_t begin = chunk ? chunks_at : weight_at;
   const int64_t mine = chunk ? chunks : weight;
   t.r = p.batch;
@@ -596,10 +602,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait_prerequisites();
   // the loader warp finds the CTA's place alone when a request fits a lane, else all threads do
-  const bool small = p.batch <= 32;
-  if (!small) cut_block<kTrThreads>(p, blockIdx.x, 0, blockIdx.x == 0, start, warp_sum);
+  const bool small = p.small != 0;
+  if (!small) cut_block<kTrThreads>(p, blockIdx.x, blockIdx.x == 0, start, warp_sum);
 
   // Registers follow the roles: 208 for the softmax threads, which hold a row of scores, 88 for the others
   // (256 * 208 + 128 * 88 = 384 * 168).  Each warpgroup sets its own count on its own path.
@@ -860,23 +865,22 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       TreeCut cut;
       if (small) {
         if (lane < p.batch) mine = tree_req(p, lane, leader && blockIdx.x == 0);
-        cut = cut_warp(p, blockIdx.x, 0, mine, lane);
+        cut = cut_warp(p, blockIdx.x, mine, lane);
       } else {
         cut = *start;
       }
       const int32_t run = cut.run;
       int stage = 0, pieces = 0, ops = 0;
-      int pend = -1;  // without TMA: the stage whose copies are not published yet
+      int published = 0;  // without TMA: the operations whose copies the other roles may use
       bool alive = true;
       const int u = (warp - kTrLoadWarp) * 32 + lane;
       TreeReq g = {};
       const int box_rows = p.box_rows;
 const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
 
-      auto publish = [&]() {  // without TMA: the pending stage's copies have landed
+      auto publish = [&](int upto) {  // without TMA: the copies of the operations before `upto` have landed
         fence_proxy_async_smem();
-        mbar_arrive(&b_full[pend]);
-        pend = -1;
+        for (; published < upto; ++published) mbar_arrive(&b_full[published % C::kStages]);
       };
       // (keys that several blocks read stay in L2 as other data does, the others leave it first)
       // K (or V) rows [128 tile, 128 tile + 128) of the request's pages into the next stage
@@ -950,11 +954,8 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
             if (!have) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0u) : "memory");
           }
           cp_async_commit();
-          if (pend >= 0) {
-            cp_async_wait<1>();
-            publish();
-          }
-          pend = stage;
+          cp_async_wait<kTrLag>();
+          publish(ops + 1 - kTrLag);
         }
         ++ops;
         stage = stage + 1 == C::kStages ? 0 : stage + 1;
@@ -998,9 +999,9 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
           if (j >= ahead) load(d.tile + j - ahead, kvh, true);
           if (j < tiles && alive) load(d.tile + j, kvh, false);
         }
-        if (!TMA && pend >= 0) {
+        if (!TMA && alive) {  // before the ring of pieces is waited for
           cp_async_wait<0>();
-          publish();
+          publish(ops);
         }
       };
 
@@ -1041,10 +1042,10 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
         const HeadCut h = head_cut(g, p.group, run);
         const int kvh = (int)div_units(cut.off, h.chunks);
         const BlockAt k = block_at(g, p.group, run, (int32_t)(cut.off - (int64_t)kvh * h.chunks), true);
+        piece(kvh, k.b, k.x * run, run, k.tiles == run ? -1 : (int)blockIdx.x);
         if (k.tiles != run && g.kind != kReqEmpty)
           fold(kvh, k.b, (int)blockIdx.x - k.x, k.tiles / run, k.x,
                cut.r_weight + (int64_t)kvh * h.weight + k.weight, rest_weight(k.tiles, run));
-        piece(kvh, k.b, k.x * run, run, k.tiles == run ? -1 : (int)blockIdx.x);
       } else {
         int64_t off = cut.off, r_weight = cut.r_weight;
         int32_t left = (int32_t)min((int64_t)cut.stretch,
@@ -1515,6 +1516,10 @@ extern "C" pa_status pa_v2_tree_attention(const void* q, const void* k_pool, con
   p.ps_shift = fd.shift;
   p.g_magic = fg.magic;
   p.g_shift = fg.shift;
+  // the work's units at most: every block of the batch against every key tile of the page table
+  const double units = ((double)num_indices * page_size / pa::kTrTile + 2.0 * batch) *
+                       ((double)num_tokens * p.group / pa::kTrBlock + batch) * num_kv_heads;
+  p.small = batch <= 32 && units < (double)(1 << 28);
   const bool flat = std::fabs(sm_scale) < 1e-30f;  // every score is zero
   p.scale_log2 = flat ? 1.f : std::fabs(sm_scale) * 1.4426950408889634f;
   p.q_xor = sm_scale < 0.f ? 0x80008000u : 0u;
@@ -1524,16 +1529,17 @@ extern "C" pa_status pa_v2_tree_attention(const void* q, const void* k_pool, con
   const pa::TreeKernel fn = f16 ? pa::pick_tree<__half>(head_dim, tma) : pa::pick_tree<__nv_bfloat16>(head_dim, tma);
   if (!pa::prepare_kernel(reinterpret_cast<const void*>(fn), smem)) return PA_ECUDA;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-  if (pa::launch_dependent(fn, dim3(p.ctas), dim3(pa::kTrThreads), smem, stream, p, tm_k, tm_v) != cudaSuccess) {
-    cudaGetLastError();
-    return PA_ECUDA;
-  }
+  // Not a programmatic dependent: its CTAs want an SM each, and taking the SMs as the kernel before it frees them puts
+  // the blocks that share keys far apart (16 ragged requests behind the q/k preparation: a step of 128 us, 150 with
+  // the early launch).
+  fn<<<dim3(p.ctas), dim3(pa::kTrThreads), smem, stream>>>(p, tm_k, tm_v);
+  if (cudaGetLastError() != cudaSuccess) return PA_ECUDA;
   const pa::MergeKernel merge =
       f16 ? (head_dim == 64 ? pa::pa_v2_tree_merge_kernel<__half, 64> : pa::pa_v2_tree_merge_kernel<__half, 128>)
           : (head_dim == 64 ? pa::pa_v2_tree_merge_kernel<__nv_bfloat16, 64>
                             : pa::pa_v2_tree_merge_kernel<__nv_bfloat16, 128>);
   if (p.ctas > 1) {
-    const cudaError_t rc = pa::launch_dependent(merge, dim3(p.ctas, 2), dim3(pa::kMergeThreads), 0, stream, p);
+    const cudaError_t rc = pa::launch_dependent(merge, dim3(p.ctas, 4), dim3(pa::kMergeThreads), 0, stream, p);
     if (rc != cudaSuccess) {
       cudaGetLastError();
       return PA_ECUDA;
