@@ -77,7 +77,8 @@ struct TreeCfg {
   static constexpr int kStages = D == 128 ? 5 : 9;  // all the shared memory that the Q tiles leave
   static constexpr int kOffKv = 2 * kTileBytes;     // Q tiles first
   static constexpr int kOffMisc = kOffKv + kStages * kTileBytes;
-  static constexpr int kSmem = kOffMisc + 2048;
+  static constexpr int kMisc = D == 128 ? 2048 : 3072;  // barriers, pieces, small exchanges
+  static constexpr int kSmem = kOffMisc + kMisc;
   static constexpr int kSmemAlloc = kSmem + 1024;   // room to align the base
   static constexpr int64_t kSlotFloats = (int64_t)kTrBlock * (D + 1);
 };
@@ -553,10 +554,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(warp_sum + kTrThreads / 32);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(tmem_slot + 1);
   float* xstate = reinterpret_cast<float*>(tmem_slot + 2);  // [2][128]: stream B's maxima and sums
-  int32_t(*boxes_of)[16] = reinterpret_cast<int32_t(*)[16]>(xstate + 2 * kTrTile);  // the loader warps' box rows
+  int32_t(*rows_of)[kTrTile / 2] = reinterpret_cast<int32_t(*)[kTrTile / 2]>(xstate + 2 * kTrTile);  // the loaders'
   static_assert((3 * C::kStages + 11 + 2 * kTrRing) * 8 + kTrRing * sizeof(TreePiece) + sizeof(TreeCut) +
-                        kTrThreads / 32 * 8 + 8 + 2 * kTrTile * 4 + 2 * 16 * 4 <=
-                    2048,
+                        kTrThreads / 32 * 8 + 8 + 2 * kTrTile * 4 + kTrTile * 4 <=
+                    C::kMisc,
                 "the area behind the stages");
 
   const int warp = threadIdx.x >> 5;
@@ -914,7 +915,7 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
               if (!is_v) report(p.status, PA_DEVICE_BAD_PAGE);
             }
           }
-          volatile int32_t* box_row = boxes_of[u >> 5];
+          volatile int32_t* box_row = rows_of[u >> 5];
           if (lane < 16) box_row[lane] = mine_row;
           __syncwarp();
           if (elect_one()) {
@@ -931,27 +932,38 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
           }
           __syncwarp();
         } else {
-          constexpr int kChunks = D / 8;                       // 16-byte pieces of a row
-          constexpr int kPass = kTrLoadThreads / kChunks;      // rows per pass
-          const int ch = u % kChunks;
-          const uint32_t col = (uint32_t)(ch >> 3) * (kTrTile * 128);
-          const T* pool = static_cast<const T*>(is_v ? p.v_pool : p.k_pool) + (int64_t)kvh * D + ch * 8;
-  #pragma unroll 8
-          for (int i = 0; i < kTrTile / kPass; ++i) {
-            const int row = i * kPass + u / kChunks;
-            const int at = row0 + row;
-            const uint32_t to = dst + col + sw128(row, ch & 7);
-            bool have = at >= g.lo && at < g.hi;
-            if (have) {
+          // a warp gathers half of the rows: first each lane resolves two, then all copy them, 16 bytes per lane
+          constexpr int kChunks = D / 8, kPass = 32 / kChunks;  // pieces of a row; rows per pass
+          volatile int32_t* row_of = rows_of[u >> 5];
+          const int half0 = (u >> 5) * (kTrTile / 2);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int at = row0 + half0 + 32 * i + lane;
+            int32_t from = -1;
+            if (at >= g.lo && at < g.hi) {
               const int slot = (int)fast_div((uint32_t)at, p.ps_magic, p.ps_shift);
               const int32_t page = __ldg(p.indices + g.slot_base + slot);
-              have = page >= 0 && page < p.num_pages;
-              if (have)
-                cp_async_16(to, pool + ((int64_t)page * p.page_size + (at - slot * p.page_size)) * p.hkv * D, policy);
-              else if (ch == 0 && !is_v)
+              if (page >= 0 && page < p.num_pages)
+                from = page * p.page_size + (at - slot * p.page_size);
+              else if (!is_v)
                 report(p.status, PA_DEVICE_BAD_PAGE);
             }
-            if (!have) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0u) : "memory");
+            row_of[32 * i + lane] = from;
+          }
+          __syncwarp();
+          const int ch = lane % kChunks, sub = lane / kChunks;
+          const T* pool = static_cast<const T*>(is_v ? p.v_pool : p.k_pool) + (int64_t)kvh * D + ch * 8;
+          const uint32_t row_bytes = (uint32_t)p.hkv * D * sizeof(T);
+          const uint32_t to0 = dst + (uint32_t)(ch >> 3) * (kTrTile * 128) + half0 * 128;
+#pragma unroll 8
+          for (int i = 0; i < kTrTile / 2; i += kPass) {
+            const int32_t from = row_of[i + sub];
+            const uint32_t to = to0 + sw128(i + sub, ch & 7);
+            if (from >= 0)
+              cp_async_16(to, reinterpret_cast<const char*>(pool) + (uint64_t)(uint32_t)from * row_bytes, policy);
+            else
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0u) : "memory");
           }
           cp_async_commit();
           cp_async_wait<kTrLag>();
