@@ -11,7 +11,6 @@ split-KV, and variable-length merge kernels", design pieces 2-4).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -621,35 +620,24 @@ def pa_selection_from_blocks(block_ids, block_size: int, kv_len: int, request_st
 # one step of several new tokens per request: tables, q/k preparation, tree attention
 # ---------------------------------------------------------------------------
 
-class _LaunchOn:
-    """Make a device and the launch stream current (new tensors then belong to that stream); entering gives the
-    stream's handle.  stream: a torch stream, a raw handle, or None for the device's current stream, which on the
-    current device needs no change at all."""
-
-    __slots__ = ("index", "stream", "scopes")
-
-    def __init__(self, index: int, stream):
-        self.index, self.stream, self.scopes = index, stream, None
-
-    def __enter__(self) -> int:
-        stream = self.stream
-        if stream is None and torch.cuda.current_device() == self.index:
-            return torch.cuda.current_stream(self.index).cuda_stream
-        self.scopes = contextlib.ExitStack()
-        self.scopes.enter_context(torch.cuda.device(self.index))
+def _run_on(index: int, stream, launch) -> None:
+    """launch(handle) with device `index` and the launch stream current, so that tensors it makes belong to that
+    stream.  stream: a torch stream, a raw handle, or None for the device's current stream, which on the current
+    device needs no change at all."""
+    if stream is None and torch.cuda.current_device() == index:
+        launch(torch._C._cuda_getCurrentRawStream(index))
+        return
+    with torch.cuda.device(index):
         if stream is None:
-            return torch.cuda.current_stream(self.index).cuda_stream
+            launch(torch.cuda.current_stream(index).cuda_stream)
+            return
         if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.index)
-        self.scopes.enter_context(torch.cuda.stream(stream))
-        return stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.scopes is not None:
-            self.scopes.close()
+            stream = torch.cuda.ExternalStream(int(stream), device=index)
+        with torch.cuda.stream(stream):
+            launch(stream.cuda_stream)
 
 
-def _refuse(t, name: str, index: int, dtype, shape) -> None:
+def _refuse(t, name: str, index: int, dtype, numel) -> None:
     """Say what is wrong with an argument that _step_ptr does not pass."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -657,18 +645,18 @@ def _refuse(t, name: str, index: int, dtype, shape) -> None:
         raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if numel >= 0 and t.numel() != numel:
+        raise ValueError(f"{name} must hold {numel} elements, got {list(t.shape)}")
     raise ValueError(f"{name} must be contiguous")
 
 
-def _step_ptr(t, name: str, index: int, dtype=None, shape=None) -> int | None:
-    """Pointer of a contiguous tensor on device `index`, its dtype and shape checked; None stays None."""
+def _step_ptr(t, name: str, index: int, dtype=None, numel: int = -1) -> int | None:
+    """Pointer of a contiguous tensor on device `index`, its dtype and size checked; None stays None."""
     if t is None:
         return None
-    if (t.get_device() != index or (dtype is not None and t.dtype is not dtype) or
-            (shape is not None and t.shape != shape) or not t.is_contiguous()):
-        _refuse(t, name, index, dtype, shape)
+    if (t.get_device() != index or (dtype is not None and t.dtype is not dtype) or not t.is_contiguous() or
+            (numel >= 0 and t.numel() != numel)):
+        _refuse(t, name, index, dtype, numel)
     return t.data_ptr()
 
 
@@ -719,19 +707,21 @@ def pa_v2_build_tables(cached_lens, new_lens, block_table, page_size: int, table
     if mask is not None and mask.dim() != 2:
         raise ValueError("tree_mask must be [token capacity, mask words]")
     words = mask.shape[1] if mask is not None else 0
-    args = (ptr(cached_lens, "cached_lens", dev, i32, (B,)), ptr(new_lens, "new_lens", dev, i32, (B,)), B,
+    args = (ptr(cached_lens, "cached_lens", dev, i32, B), ptr(new_lens, "new_lens", dev, i32, B), B,
             ptr(block_table, "block_table", dev, i32), width, ptr(free_pages, "free_pages", dev, i32),
-            free_pages.numel() if free_pages is not None else 0, ptr(parents, "parents", dev, i32, (cap_t,)),
-            page_size, window, ptr(t.indptr, "indptr", dev, i32, (B + 1,)), ptr(t.indices, "indices", dev, i32), cap_i,
-            ptr(t.last_page_len, "last_page_len", dev, i32, (B,)),
-            ptr(t.first_page_offset, "first_page_offset", dev, i32, (B,)),
-            ptr(t.qo_indptr, "qo_indptr", dev, i32, (B + 1,)), ptr(t.slots, "slots", dev, i32, (cap_t,)),
-            ptr(t.positions, "positions", dev, i32, (cap_t,)), cap_t, ptr(mask, "tree_mask", dev, i32, (cap_t, words)),
-            words, ptr(t.pages_needed, "pages_needed", dev, i32, (1,)), ptr(status, "status", dev, i32))
-    with _LaunchOn(dev, stream) as handle:
+            free_pages.numel() if free_pages is not None else 0, ptr(parents, "parents", dev, i32, cap_t),
+            page_size, window, ptr(t.indptr, "indptr", dev, i32, B + 1), ptr(t.indices, "indices", dev, i32), cap_i,
+            ptr(t.last_page_len, "last_page_len", dev, i32, B),
+            ptr(t.first_page_offset, "first_page_offset", dev, i32, B),
+            ptr(t.qo_indptr, "qo_indptr", dev, i32, B + 1), ptr(t.slots, "slots", dev, i32, cap_t),
+            ptr(t.positions, "positions", dev, i32, cap_t), cap_t, ptr(mask, "tree_mask", dev, i32, cap_t * words),
+            words, ptr(t.pages_needed, "pages_needed", dev, i32, 1), ptr(status, "status", dev, i32))
+    def launch(handle):
         rc = lib().pa_v2_build_tables(*args, handle)
-    if rc != PA_OK:
-        raise PaError(rc, "pa_v2_build_tables")
+        if rc != PA_OK:
+            raise PaError(rc, "pa_v2_build_tables")
+
+    _run_on(dev, stream, launch)
     return tables
 
 
@@ -784,18 +774,24 @@ def pa_v2_qk_rope_append(q, k, v, positions, slots, inv_freq, k_pool, v_pool, q_
         q_dtype = dt
     if q_dtype not in KV_DTYPES:
         raise ValueError(f"q_dtype must be one of {list(KV_DTYPES)}")
-    head = (qp, qs, kp, ks, vp, vs, KV_DTYPES[dt], T, hq, hkv, D, ptr(positions, "positions", dev, i32, (T,)),
-            ptr(slots, "slots", dev, i32, (T,)), ptr(inv_freq, "inv_freq", dev, torch.float32), rot,
-            1 if interleaved else 0, ptr(q_weight, "q_weight", dev, dt, (D,)), ptr(k_weight, "k_weight", dev, dt, (D,)),
+    head = (qp, qs, kp, ks, vp, vs, KV_DTYPES[dt], T, hq, hkv, D, ptr(positions, "positions", dev, i32, T),
+            ptr(slots, "slots", dev, i32, T), ptr(inv_freq, "inv_freq", dev, torch.float32), rot,
+            1 if interleaved else 0, ptr(q_weight, "q_weight", dev, dt, D), ptr(k_weight, "k_weight", dev, dt, D),
             eps)
     st = ptr(status, "status", dev, i32)
-    with _LaunchOn(dev, stream) as handle:
+    if q_out is not None and tuple(q_out.shape) != (T, hq, D):
+        raise ValueError(f"q_out must be [{T}, {hq}, {D}], got {list(q_out.shape)}")
+
+    def launch(handle):
+        nonlocal q_out
         if q_out is None:
             q_out = torch.empty(T, hq, D, dtype=q_dtype, device=q.device)
-        rc = lib().pa_v2_qk_rope_append(*head, ptr(q_out, "q_out", dev, None, (T, hq, D)), KV_DTYPES[q_dtype], k_ptr,
-                                        v_ptr, pages, page_size, st, handle)
-    if rc != PA_OK:
-        raise PaError(rc, "pa_v2_qk_rope_append")
+        rc = lib().pa_v2_qk_rope_append(*head, ptr(q_out, "q_out", dev), KV_DTYPES[q_dtype], k_ptr, v_ptr, pages,
+                                        page_size, st, handle)
+        if rc != PA_OK:
+            raise PaError(rc, "pa_v2_qk_rope_append")
+
+    _run_on(dev, stream, launch)
     return q_out
 
 
@@ -841,25 +837,32 @@ def pa_v2_tree_attention(q, k_pool, v_pool, indices, indptr, last_page_len, firs
         raise ValueError("tree_mask must be [tokens, mask words]")
     words = tree_mask.shape[1] if tree_mask is not None else 0
     head = (ptr(q, "q", dev, dt), k_ptr, v_ptr, KV_DTYPES[dt], P, ps, hq, hkv, D, ptr(indices, "indices", dev, i32),
-            indices.numel(), ptr(indptr, "indptr", dev, i32, (B + 1,)),
-            ptr(last_page_len, "last_page_len", dev, i32, (B,)),
-            ptr(first_page_offset, "first_page_offset", dev, i32, (B,)), B,
-            ptr(qo_indptr, "qo_indptr", dev, i32, (B + 1,)), T, ptr(tree_mask, "tree_mask", dev, i32, (T, words)), words,
+            indices.numel(), ptr(indptr, "indptr", dev, i32, B + 1),
+            ptr(last_page_len, "last_page_len", dev, i32, B),
+            ptr(first_page_offset, "first_page_offset", dev, i32, B), B,
+            ptr(qo_indptr, "qo_indptr", dev, i32, B + 1), T, ptr(tree_mask, "tree_mask", dev, i32, T * words), words,
             sm_scale)
     st = ptr(status, "status", dev, i32)
-    with _LaunchOn(dev, stream) as handle:
+    for t, name, shape in ((out, "out", (T, hq, D)), (lse2_out, "lse2_out", (T, hq))):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+    def launch(handle):
+        nonlocal workspace, out, lse2_out
         if workspace is None and hkv > 0 and hq % hkv == 0 and D in (64, 128):
             workspace = tree_attention_workspace(T, B, hq, hkv, D, q.device)
         if out is None:
             out = torch.empty(T, hq, D, dtype=dt, device=q.device)
         if lse2_out is None:
             lse2_out = torch.empty(T, hq, dtype=torch.float32, device=q.device)
-        rc = lib().pa_v2_tree_attention(
-            *head, ptr(out, "out", dev, dt, (T, hq, D)), ptr(lse2_out, "lse2_out", dev, torch.float32, (T, hq)),
-            ptr(workspace, "workspace", dev), workspace.numel() * workspace.element_size() if workspace is not None else 0,
-            st, handle)
-    if rc != PA_OK:
-        raise PaError(rc, "pa_v2_tree_attention")
+        rc = lib().pa_v2_tree_attention(*head, ptr(out, "out", dev, dt), ptr(lse2_out, "lse2_out", dev, torch.float32),
+                                        ptr(workspace, "workspace", dev),
+                                        workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                        st, handle)
+        if rc != PA_OK:
+            raise PaError(rc, "pa_v2_tree_attention")
+
+    _run_on(dev, stream, launch)
     return out, lse2_out
 
 
