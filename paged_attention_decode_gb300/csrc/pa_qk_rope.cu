@@ -127,7 +127,7 @@ __device__ __forceinline__ uint64_t turn_of(float inv_freq) {
 
 // Cosine and sine after pos positions.
 __device__ __forceinline__ float2 rotation(int32_t pos, uint64_t turn) {
-  const int32_t part = (int32_t)(uint32_t)(((uint64_t)(uint32_t)pos * turn) >> 32);  // [-1/2, 1/2) turns, times 2^32
+  const int32_t part = (int32_t)(uint32_t)(((uint64_t)(int64_t)pos * turn) >> 32);  // [-1/2, 1/2) turns, times 2^32
   float s, c;
   sincospif((float)part * 4.656612873077393e-10f, &s, &c);  // 2^-31: sincospif takes half turns
   return make_float2(c, s);

@@ -42,6 +42,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -229,7 +230,7 @@ struct TreeCut {
 
 // The run length for `tiles` units in `blocks` blocks.
 __device__ __forceinline__ int32_t run_of(int64_t tiles, int64_t blocks, int32_t ctas) {
-  return (int32_t)max(div_units(tiles + kTrRestCost * blocks + ctas - 1, ctas), (int64_t)1);
+  return (int32_t)min(max(div_units(tiles + kTrRestCost * blocks + ctas - 1, ctas), (int64_t)1), (int64_t)INT32_MAX);
 }
 // The stretch length.
 __device__ __forceinline__ void set_stretch(TreeCut* t, int32_t ctas) {
@@ -1528,10 +1529,11 @@ extern "C" pa_status pa_v2_tree_attention(const void* q, const void* k_pool, con
   p.ps_shift = fd.shift;
   p.g_magic = fg.magic;
   p.g_shift = fg.shift;
-  // the work's units at most: every block of the batch against every key tile of the page table
+  // the work's units at most, for tables that list every page and token once: every block of the batch against every
+  // key tile.  A broken table can claim them again for each of 32 requests and must still fit 31 bits.
   const double units = ((double)num_indices * page_size / pa::kTrTile + 2.0 * batch) *
                        ((double)num_tokens * p.group / pa::kTrBlock + batch) * num_kv_heads;
-  p.small = batch <= 32 && units < (double)(1 << 28);
+  p.small = batch <= 32 && units < (double)(1 << 25);
   const bool flat = std::fabs(sm_scale) < 1e-30f;  // every score is zero
   p.scale_log2 = flat ? 1.f : std::fabs(sm_scale) * 1.4426950408889634f;
   p.q_xor = sm_scale < 0.f ? 0x80008000u : 0u;

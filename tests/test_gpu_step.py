@@ -272,6 +272,12 @@ def test_qk_far_positions_keep_their_angles():
     _check_qk(case, False, torch.float32)
 
 
+def test_qk_negative_positions_turn_the_other_way():
+    case = list(_qk_case(4, 2, 1, 64, 64, torch.float32, False, 4, 3))
+    case[3] = i32([-1, -77, 5, -100_000])
+    _check_qk(case, True, torch.float32)
+
+
 def test_qk_only_one_weight():
     case = list(_qk_case(4, 3, 3, 64, 64, torch.float16, True, 4, 9))
     for keep in (0, 1):
@@ -609,6 +615,60 @@ def test_tree_bad_tables_are_contained_and_reported():
     assert st == pa.DEVICE_BAD_INDPTR
     others_ok(out, lse, range(10, 15))
     assert out[10:].eq(5.0).all()
+
+
+def test_tree_tables_that_claim_pages_and_tokens_again_stay_in_bounds():
+    """Prefix sums that fall and rise again: the falling requests are refused, the others stand on their own."""
+    base = _tree_case(47, [(900, 6), (50, 4), (700, 5)], 4, 2, 64, 16, torch.float16)
+    ref = _check_tree(base)
+    one = [int(x) for x in base["indptr"]]
+    c = dict(base, indptr=i32([0, one[1], 0, one[1], 0, one[1]]), lpl=i32([int(base["lpl"][0])] * 5),
+             fpo=i32([0] * 5), qo=i32([0, 6, 0, 6, 0, 6]))
+    st = status_word()
+    out, lse = _run_tree(c, 0, st)
+    assert int(st) == pa.DEVICE_BAD_INDPTR
+    assert (out[:6].double() - ref[0][:6]).abs().max() <= 2e-3 and (lse[:6].double() - ref[1][:6]).abs().max() <= 1e-3
+    assert out[6:].eq(5.0).all()
+
+
+def test_tree_tokens_of_no_request_are_left_alone():
+    c = _tree_case(48, [(100, 6), (50, 4)], 4, 2, 64, 16, torch.float16)
+    shifted = dict(c, q=torch.cat((c["q"][:3], c["q"])), mask=torch.cat((c["mask"][:3], c["mask"])), qo=c["qo"] + 3)
+    ref, got = _run_tree(c), _run_tree(shifted)
+    assert got[0][:3].eq(5.0).all() and got[1][:3].eq(5.0).all()
+    assert torch.equal(got[0][3:], ref[0]) and torch.equal(got[1][3:], ref[1])
+
+
+def test_tree_many_requests_with_several_blocks():
+    reqs = [(1500, 150), (0, 90), (400, 1)] * 13                # more than a warp's lanes, two blocks each
+    _check_tree(_tree_case(49, reqs, 4, 1, 64, 16, torch.bfloat16))
+    _check_tree(_tree_case(49, reqs, 4, 1, 64, 16, torch.bfloat16, chain=True))
+
+
+def test_tree_two_graphs_with_their_own_workspaces_side_by_side():
+    cases = [_tree_case(s, [(2000, 30), (300, 64)], 8, 2, 128, 16, torch.float16) for s in (51, 52)]
+    refs = [_run_tree(c) for c in cases]
+    graphs, outs, keep = [], [], []
+    for c in cases:
+        d = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in c.items()}
+        ws = pa.tree_attention_workspace(c["q"].shape[0], 2, 8, 2, 128)
+        out, lse = torch.zeros_like(d["q"]), torch.zeros(d["q"].shape[:2], device="cuda")
+        torch.cuda.synchronize()
+        g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(g, stream=s):
+            pa.pa_v2_tree_attention(d["q"], d["kp"], d["vp"], d["idx"], d["indptr"], d["lpl"], d["fpo"], d["qo"],
+                                    d["scale"], tree_mask=d["mask"], out=out, lse2_out=lse, workspace=ws)
+        graphs.append((g, s))
+        outs.append((out, lse))
+        keep.append((d, ws))
+    for _ in range(3):
+        for g, s in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (out, lse), ref in zip(outs, refs):
+            assert torch.equal(out.cpu(), ref[0]) and torch.equal(lse.cpu(), ref[1])
+            out.zero_()
 
 
 def test_tree_more_new_tokens_than_visible_ones_or_than_mask_bits():
