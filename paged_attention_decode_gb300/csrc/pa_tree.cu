@@ -129,7 +129,6 @@ struct TreeReq {
   int32_t units;       // per KV head: blocks * common, and what chains add per block (a block stops at its last token)
   int32_t kind;        // 0 (no query), kReqEmpty (nothing visible or a bad table: zeros and -inf), kReqEven, kReqChain
 
-  __device__ __forceinline__ bool tails() const { return units != blocks * common; }
 };
 constexpr int kReqEmpty = 1, kReqEven = 2, kReqChain = 3;
 
@@ -551,13 +550,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   uint64_t* b_drain = b_pe + kTrRing;
   TreePiece* ring = reinterpret_cast<TreePiece*>(b_drain + 1);
   TreeCut* start = reinterpret_cast<TreeCut*>(ring + kTrRing);
-  int64_t* warp_sum = reinterpret_cast<int64_t*>(start + 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(warp_sum + kTrThreads / 32);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(start + 1);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(tmem_slot + 1);
   float* xstate = reinterpret_cast<float*>(tmem_slot + 2);  // [2][128]: stream B's maxima and sums
+  int64_t* warp_sum = reinterpret_cast<int64_t*>(xstate);   // before the first piece
   int32_t(*rows_of)[kTrTile / 2] = reinterpret_cast<int32_t(*)[kTrTile / 2]>(xstate + 2 * kTrTile);  // the loaders'
   static_assert((3 * C::kStages + 11 + 2 * kTrRing) * 8 + kTrRing * sizeof(TreePiece) + sizeof(TreeCut) +
-                        kTrThreads / 32 * 8 + 8 + 2 * kTrTile * 4 + kTrTile * 4 <=
+                        8 + 2 * kTrTile * 4 + kTrTile * 4 <=
                     C::kMisc,
                 "the area behind the stages");
 
@@ -1258,33 +1257,46 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
             const uint32_t base = sbase + C::kOffKv + st * C::kTileBytes;
             const int ch = lane % kChunks;
             const uint32_t col = base + (uint32_t)(ch >> 3) * (kTrTile * 128);
+            constexpr int kPass = 32 / kChunks;  // rows per pass
+            const int sub = lane / kChunks;
+            auto zero_rows = [&](int r0, int r1) {
+#pragma unroll 8
+              for (int row = r0 + sub; row < r1; row += kPass)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(col + sw128(row, ch & 7)), "r"(0u) : "memory");
+            };
             uint32_t any = 0;
-            auto fix_rows = [&](int r0, int r1) {
-  #pragma unroll 4
-              for (int row = r0 + lane / kChunks; row < r1; row += 32 / kChunks) {
-                const uint32_t a = col + sw128(row, ch & 7);
-                uint32_t x0, x1, x2, x3;
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
-                             : "r"(a)
-                             : "memory");
-                const int pr = c0 + row;
-                const bool inside = pr >= d.lo && pr < d.hi;
-                constexpr uint32_t e = ExpBits<T>::k;
-                const uint32_t n0 = sat_mask(x0, e), n1 = sat_mask(x1, e), n2 = sat_mask(x2, e), n3 = sat_mask(x3, e);
-                const uint32_t bad = n0 | n1 | n2 | n3;
-                if (inside) any |= bad;
-                if (!inside || bad) {
-                  const uint32_t keep = inside ? 0xffffffffu : 0u;
-                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x0 & ~n0 & keep),
-                               "r"(x1 & ~n1 & keep), "r"(x2 & ~n2 & keep), "r"(x3 & ~n3 & keep)
+            auto check_rows = [&](int r0, int r1) {  // four passes' loads at once
+              constexpr uint32_t e = ExpBits<T>::k;
+              for (int base_row = r0; base_row < r1; base_row += 4 * kPass) {
+                uint32_t x[4][4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int row = min(base_row + k * kPass + sub, r1 - 1);
+                  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                               : "=r"(x[k][0]), "=r"(x[k][1]), "=r"(x[k][2]), "=r"(x[k][3])
+                               : "r"(col + sw128(row, ch & 7))
                                : "memory");
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  uint32_t n[4], bad = 0;
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) bad |= n[i] = sat_mask(x[k][i], e);
+                  if (bad) {
+                    any = 1;
+                    const int row = min(base_row + k * kPass + sub, r1 - 1);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(col + sw128(row, ch & 7)),
+                                 "r"(x[k][0] & ~n[0]), "r"(x[k][1] & ~n[1]), "r"(x[k][2] & ~n[2]), "r"(x[k][3] & ~n[3])
+                                 : "memory");
+                  }
                 }
               }
             };
-            const int head = min(max(d.lo - c0, 0), kTrTile), tail = min(max(d.ds - c0, head), kTrTile);
-            fix_rows(0, head);
-            fix_rows(tail, kTrTile);
+            // rows of the tile: outside, earlier tokens (left alone), new tokens, outside
+            const int in0 = min(max(d.lo - c0, 0), kTrTile), in1 = min(max(d.hi - c0, in0), kTrTile);
+            zero_rows(0, in0);
+            check_rows(min(max(d.ds - c0, in0), in1), in1);
+            zero_rows(in1, kTrTile);
             if (__any_sync(0xffffffffu, any != 0) && lane == 0) *reinterpret_cast<volatile int32_t*>(&ring[at].tainted) = 1;
             fence_proxy_async_smem();
             __syncwarp();
