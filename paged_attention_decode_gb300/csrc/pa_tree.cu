@@ -59,7 +59,12 @@ constexpr int kTrThreads = 384;
 constexpr int kTrTile = 128;      // query rows of a tensor-core tile, and keys of a key tile
 constexpr int kTrBlock = 256;     // query rows of a block
 constexpr int kTrSlots = 2;       // partial results per CTA (see rest_slot)
-constexpr int kTrRestCost = 6;    // what starting a left-over stretch costs, in key tiles
+// What starting on a left-over costs, in key tiles, for blocks of one and of two tiles of query rows: the result of the
+// piece before written, Q fetched, the first tile's softmax and the edges of the request (5 to 7 us, about 1.5 us a
+// tile), and, with two, keys that no CTA beside reads at the time.  Sweeps over 4 x 256 tokens and 64 tokens over 32K,
+// 16 ragged requests and 32 windowed chains: 2 / 2 gives 493, 44.8, 136 and 92 us, 6 / 6 gives 436, 44.6, 105 and 80,
+// 4 / 12 gives 400, 46.9, 99 and 72.5, 4 / 24 gives 415, 46.9, 104 and 72.6.
+constexpr int kTrCost1 = 4, kTrCost2 = 12;
 constexpr int kTrMmaWarp = 8, kTrLoadWarp = 9, kTrFixWarp = 11;
 constexpr int kTrLoadThreads = 64;  // loader threads without TMA
 constexpr int kTrRing = 2;        // pieces handed out ahead
@@ -127,6 +132,7 @@ struct TreeReq {
   int32_t tile0;       // first key tile
   int32_t common;      // key tiles every block meets
   int32_t units;       // per KV head: blocks * common, and what chains add per block (a block stops at its last token)
+  int32_t cost;        // of starting on a left-over of one of its blocks
   int32_t kind;        // 0 (no query), kReqEmpty (nothing visible or a bad table: zeros and -inf), kReqEven, kReqChain
 
 };
@@ -153,6 +159,7 @@ __device__ __forceinline__ TreeReq tree_req(const TreeParams& p, int r, bool tel
   g.t0 = a;
   g.n = b - a;
   g.blocks = (g.n * p.group + kTrBlock - 1) / kTrBlock;  // num_tokens * group fits (checked by the host)
+  g.cost = g.n * p.group > kTrTile ? kTrCost2 : kTrCost1;
   g.kind = kReqEmpty;
   g.common = 1;  // one unit for an empty block
   g.units = g.blocks;
@@ -165,7 +172,7 @@ __device__ __forceinline__ TreeReq tree_req(const TreeParams& p, int r, bool tel
   const int32_t tile0 = fpo / kTrTile;
   const int32_t all = (hi + kTrTile - 1) / kTrTile - tile0;
   if (pages == 0 || lpl < 1 || lpl > p.page_size || fpo < 0 || fpo >= p.page_size || hi - fpo < g.n ||
-      (p.tree_mask && g.n > 32 * p.mask_words) || (int64_t)g.blocks * (all + kTrRestCost) > INT32_MAX) {
+      (p.tree_mask && g.n > 32 * p.mask_words) || (int64_t)g.blocks * (all + kTrCost2) > INT32_MAX) {
     if (tell) report(p.status, PA_DEVICE_BAD_TREE);
     return g;
   }
@@ -189,9 +196,9 @@ __device__ __forceinline__ TreeReq tree_req(const TreeParams& p, int r, bool tel
 __device__ __forceinline__ int32_t tiles_of(const TreeReq& g, int group, int b) { return g.common + tail_of(g, group, b); }
 
 // A block's left-over tiles, weighed with the cost of starting on them.
-__device__ __forceinline__ int32_t rest_weight(int32_t tiles, int32_t run) {
+__device__ __forceinline__ int32_t rest_weight(const TreeReq& g, int32_t tiles, int32_t run) {
   const int32_t rest = tiles % run;
-  return rest ? rest + kTrRestCost : 0;
+  return rest ? rest + g.cost : 0;
 }
 
 // Chunks of `run` tiles and left-over weight per KV head.
@@ -199,13 +206,13 @@ struct HeadCut {
   int32_t chunks, weight;
 };
 __device__ __forceinline__ HeadCut head_cut(const TreeReq& g, int group, int32_t run) {
-  HeadCut h = {g.blocks * (g.common / run), g.blocks * rest_weight(g.common, run)};
+  HeadCut h = {g.blocks * (g.common / run), g.blocks * rest_weight(g, g.common, run)};
   if (g.kind == kReqChain) {
     h.chunks = h.weight = 0;
     for (int b = 0; b < g.blocks; ++b) {
       const int32_t t = tiles_of(g, group, b);
       h.chunks += t / run;
-      h.weight += rest_weight(t, run);
+      h.weight += rest_weight(g, t, run);
     }
   }
   return h;
@@ -227,9 +234,9 @@ struct TreeCut {
   int32_t r, r_chunks;    // r: batch when the position is past the end; chunks of the requests before it
 };
 
-// The run length for `tiles` units in `blocks` blocks.
-__device__ __forceinline__ int32_t run_of(int64_t tiles, int64_t blocks, int32_t ctas) {
-  return (int32_t)min(max(div_units(tiles + kTrRestCost * blocks + ctas - 1, ctas), (int64_t)1), (int64_t)INT32_MAX);
+// The run length for `tiles` units and the cost of starting on every block's left-over.
+__device__ __forceinline__ int32_t run_of(int64_t tiles, int64_t cost, int32_t ctas) {
+  return (int32_t)min(max(div_units(tiles + cost + ctas - 1, ctas), (int64_t)1), (int64_t)INT32_MAX);
 }
 // The stretch length.
 __device__ __forceinline__ void set_stretch(TreeCut* t, int32_t ctas) {
@@ -248,14 +255,13 @@ __device__ __forceinline__ int64_t scan_add(int64_t v, int lane) {
 // The cut for a small batch, by one warp: lane r holds request r in `mine`.  c < chunks: chunk c; else left-over
 // position (c - chunks) * stretch.
 __device__ __forceinline__ TreeCut cut_warp(const TreeParams& p, int c, const TreeReq& mine, int lane) {
-  int32_t tiles = mine.units * p.hkv, blocks = mine.blocks * p.hkv;
+  int32_t tiles = (mine.units + mine.blocks * mine.cost) * p.hkv;  // and the cost of starting on every left-over
 #pragma unroll 1
   for (int w = p.batch > 1 ? 16 : 0; w >= 1; w >>= 1) {
     tiles += __shfl_xor_sync(0xffffffffu, tiles, w);
-    blocks += __shfl_xor_sync(0xffffffffu, blocks, w);
   }
   TreeCut t;
-  t.run = (int32_t)max((uint32_t)(tiles + kTrRestCost * blocks + p.ctas - 1) / (uint32_t)p.ctas, 1u);
+  t.run = (int32_t)max((uint32_t)(tiles + p.ctas - 1) / (uint32_t)p.ctas, 1u);
   t.run = __shfl_sync(0xffffffffu, t.run, 0);
   const HeadCut h = head_cut(mine, p.group, t.run);
   const int32_t chunks = h.chunks * p.hkv, weight = h.weight * p.hkv;
@@ -307,17 +313,17 @@ __device__ __forceinline__ void cut_block(const TreeParams& p, int c, bool tell,
                                           int64_t* warp_sum) {
   const int per = (p.batch + THREADS - 1) / THREADS;
   const int r0 = (int)min((int64_t)threadIdx.x * per, (int64_t)p.batch), r1 = min(r0 + per, p.batch);
-  int64_t tiles = 0, blocks = 0;
+  int64_t tiles = 0, cost = 0;
   for (int r = r0; r < r1; ++r) {
     const TreeReq g = tree_req(p, r, tell);
     tiles += (int64_t)g.units * p.hkv;
-    blocks += (int64_t)g.blocks * p.hkv;
+    cost += (int64_t)g.blocks * g.cost * p.hkv;
   }
-  int64_t all_tiles, all_blocks, all_chunks, all_weight;
+  int64_t all_tiles, all_cost, all_chunks, all_weight;
   block_prefix<THREADS>(tiles, warp_sum, &all_tiles);
-  block_prefix<THREADS>(blocks, warp_sum, &all_blocks);
+  block_prefix<THREADS>(cost, warp_sum, &all_cost);
   TreeCut t;
-  t.run = run_of(all_tiles, all_blocks, p.ctas);
+  t.run = run_of(all_tiles, all_cost, p.ctas);
   int64_t chunks = 0, weight = 0;
   for (int r = r0; r < r1; ++r) {
     const HeadCut h = head_cut(tree_req(p, r, false), p.group, t.run);
@@ -361,7 +367,7 @@ struct BlockAt {
 __device__ __forceinline__ BlockAt block_at(const TreeReq& g, int group, int32_t run, int32_t x, bool chunk) {
   BlockAt k = {0, g.common, x, 0, 0};
   if (g.kind != kReqChain) {
-    const int32_t chunks = g.common / run, weight = rest_weight(g.common, run);
+    const int32_t chunks = g.common / run, weight = rest_weight(g, g.common, run);
     const int32_t each = chunk ? chunks : weight;
     k.b = x / each;
     k.x = x - k.b * each;
@@ -371,7 +377,7 @@ __device__ __forceinline__ BlockAt block_at(const TreeReq& g, int group, int32_t
   }
   for (;; ++k.b) {
     k.tiles = tiles_of(g, group, k.b);
-    const int32_t chunks = k.tiles / run, weight = rest_weight(k.tiles, run);
+    const int32_t chunks = k.tiles / run, weight = rest_weight(g, k.tiles, run);
     const int32_t each = chunk ? chunks : weight;
     if (k.x < each || k.b + 1 >= g.blocks) return k;
     k.x -= each;
@@ -405,7 +411,7 @@ struct alignas(16) TreeFold {
   int32_t share;
   int32_t t0, row0, rows, kvh;
   int32_t first_chunk, chunks;
-  int32_t weight, lead, cta0, stretch;
+  int32_t weight, lead, cta0, stretch, cost;
 };
 
 // A run of key tiles of one block, as the loader hands it to the other roles.
@@ -1025,6 +1031,7 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
       auto fold = [&](int kvh, int b, int first_chunk, int32_t chunks, int share, int64_t at, int32_t weight) {
         TreeFold f;
         f.stretch = cut.stretch;
+        f.cost = g.cost;
         f.t0 = g.t0;
         f.kvh = kvh;
         f.row0 = b * kTrBlock;
@@ -1041,7 +1048,7 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
         f.shares = chunks;
         f.share = share;
         if (share < 0) {
-          const int idle = (f.lead + kTrRestCost) / cut.stretch;  // stretch ends at or before the first tile
+          const int idle = (f.lead + g.cost) / cut.stretch;  // stretch ends at or before the first tile
           f.share = (int)blockIdx.x - f.cta0 - idle;
           f.shares = (f.lead + weight - 1) / cut.stretch - idle;
         }
@@ -1057,7 +1064,7 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
         piece(kvh, k.b, k.x * run, run, k.tiles == run ? -1 : (int)blockIdx.x);
         if (k.tiles != run && g.kind != kReqEmpty)
           fold(kvh, k.b, (int)blockIdx.x - k.x, k.tiles / run, k.x,
-               cut.r_weight + (int64_t)kvh * h.weight + k.weight, rest_weight(k.tiles, run));
+               cut.r_weight + (int64_t)kvh * h.weight + k.weight, rest_weight(g, k.tiles, run));
       } else {
         int64_t off = cut.off, r_weight = cut.r_weight;
         int32_t left = (int32_t)min((int64_t)cut.stretch,
@@ -1072,9 +1079,9 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
             BlockAt k = block_at(g, p.group, run, in_head, false);
             while (left > 0 && alive) {
               const int32_t chunks = k.tiles / run;
-              const int32_t weight = rest_weight(k.tiles, run);
+              const int32_t weight = rest_weight(g, k.tiles, run);
               const int32_t take = min(weight - k.x, left);
-              const int32_t t0 = max(k.x - kTrRestCost, 0), t1 = max(k.x + take - kTrRestCost, 0);
+              const int32_t t0 = max(k.x - g.cost, 0), t1 = max(k.x + take - g.cost, 0);
               const bool ends = k.x + take == weight;
               if (t1 > t0)
                 piece(kvh, k.b, chunks * run + t0, t1 - t0,
@@ -1352,7 +1359,7 @@ __global__ void __launch_bounds__(kMergeThreads) pa_v2_tree_merge_kernel(const T
       if (i < f.chunks) return f.first_chunk + i++;
       while (at < f.weight) {
         const int32_t end = min((cta - f.cta0 + 1) * f.stretch - f.lead, f.weight);
-        const bool some = end > max(at, kTrRestCost);
+        const bool some = end > max(at, f.cost);
         const int slot = rest_slot(end == f.weight, f.chunks, f.first_chunk, cta, p.ctas);
         at = end;
         ++cta;
