@@ -688,8 +688,9 @@ pa_status pa_v2_build_tables(const int32_t* cached_lens, const int32_t* new_lens
  *   positions, slots [num_tokens] int32.
  * head_dim 64 or 128; rot_dim a multiple of 16 up to head_dim, or 0 (no
  * rotation).  Pointers and token strides 16-byte aligned (PA_EINVAL).
- * DEVICE pointers; PA_EUNSUPPORTED for other dims or dtypes, and for pools of
- * 2^31 rows or more. */
+ * DEVICE pointers; PA_EUNSUPPORTED for other dims or dtypes, pools of 2^31 rows
+ * or more, more than 16384 query or KV heads, and token strides above 2^31 - 1
+ * bytes. */
 pa_status pa_v2_qk_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                                int64_t v_stride, int32_t dtype, int32_t num_tokens, int32_t num_qo_heads,
                                int32_t num_kv_heads, int32_t head_dim, const int32_t* positions,
@@ -721,8 +722,9 @@ pa_status pa_v2_qk_rope_append(const void* q, int64_t q_stride, const void* k, i
  * PA_DEVICE_BAD_PAGE, its rows are not read and that request's result is finite
  * but meaningless), a qo_indptr that decreases or passes
  * num_tokens (PA_DEVICE_BAD_INDPTR, the request is skipped), last_page_len or
- * first_page_offset outside the geometry rules, or n_r above L_r or above
- * 32 * mask_words (PA_DEVICE_BAD_TREE, the request's rows become zeros and -inf).
+ * first_page_offset outside the geometry rules, n_r above L_r or above
+ * 32 * mask_words, or 2^31 or more products of 256 query rows with 128 keys in
+ * one request (PA_DEVICE_BAD_TREE, the request's rows become zeros and -inf).
  * P = exp(s) enters the second product rounded to kv_dtype; scores, statistics
  * and sums are f32.  head_dim 64 or 128, page_size 1..16 or a multiple of 16 up
  * to 256, pools below 2^31 rows (else PA_EUNSUPPORTED).  DEVICE pointers. */

@@ -22,7 +22,11 @@
 // the next tile's cosines and sines are computed by all threads, one angle each, into
 // the other half of a shared buffer (one barrier per tile; with one per token, behind
 // the two warps that computed its angles, the kernel took 86 us).  A frequency is
-// converted once per CTA.
+// converted once per CTA.  With all of it, 16384 tokens of 48 heads take 80 us, 5.0
+// TB/s (74 % of the measured copy rate): instructions issue in half of the cycles,
+// and 16 warps per SM (120 registers a thread) hide the rest no better; three or
+// four CTAs per SM with the registers that leaves, or 384 and 768 threads a CTA,
+// were no faster.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -29,15 +29,29 @@
 //  - warp 8: one thread issues S = Q K^T (both operands in shared memory) and
 //    O += P V (P in tensor memory);
 //  - warps 9 and 10: load K and V tiles through a ring of shared-memory stages,
-//    TMA boxes of up to 16 rows x 64 elements per page (K by warp 9, V by warp
-//    10: issuing a tile's 16 boxes takes a thread about 1200 cycles), or
-//    cp.async by both for page sizes whose pages do not start on 8-row
-//    boundaries; both walk the CTA's share of the work, and warp 9 hands its
-//    pieces to the other roles;
+//    TMA boxes of 64 elements x the largest power of two of rows that divides a
+//    page (K by warp 9, V by warp 10: issuing the 16 boxes of a tile of 16-row
+//    pages takes a thread about 1000 cycles), or cp.async by both for page sizes
+//    whose pages do not start on 8-row boundaries; both walk the CTA's share of
+//    the work, and warp 9 hands its pieces to the other roles;
 //  - warp 11: makes V tiles that hold rows outside the visible range or new
 //    tokens safe: 0 * NaN is NaN, so what a mask hides must not be left in V.
 //    Outside rows become zeros; non-finite elements of new tokens become zeros
 //    and are added back, in the epilogue, to the rows that do see them.
+//
+// What bounds it.  A tile of two streams of 128 rows is 2500 cycles of products
+// (S and PV, D = 128, at the cuBLAS burst rate) and, from HBM, 2900 cycles of K
+// and V when nothing else reads them; it takes 3100-3250: a row's softmax (1550:
+// reading S, the maximum, 128 exponentials, packing, writing P) and the PV and S
+// products that need it and that it needs (1250) follow one another within a
+// stream, and the other stream fills most of the gap.  Around the tiles stand
+// 6.5 us of start (cold code, barriers, tensor memory, the cut, the page list, Q
+// and the first K tile) and, after a cut block, 2-4 us of epilogue and 5 us of
+// merge.  bf16, 32 query heads on 8 KV heads, D = 128, replayed from a graph: 64
+// tokens over 32K 46.6 us (20 us of HBM reads), 4 x 256 tokens over 32K 400 us
+// (1.37 PFLOP/s of 1.92 measured with cuBLAS), 16 ragged requests 99 us (4.4
+// TB/s), 32 chains of 5 tokens with a 4096-token window 72.4 us (5.2 TB/s), 8
+// tokens over 1K 15.5 us (nearly all start and merge).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -134,7 +148,6 @@ struct TreeReq {
   int32_t units;       // per KV head: blocks * common, and what chains add per block (a block stops at its last token)
   int32_t cost;        // of starting on a left-over of one of its blocks
   int32_t kind;        // 0 (no query), kReqEmpty (nothing visible or a bad table: zeros and -inf), kReqEven, kReqChain
-
 };
 constexpr int kReqEmpty = 1, kReqEven = 2, kReqChain = 3;
 
@@ -193,7 +206,9 @@ __device__ __forceinline__ TreeReq tree_req(const TreeParams& p, int r, bool tel
 }
 
 // Key tiles that block b meets.
-__device__ __forceinline__ int32_t tiles_of(const TreeReq& g, int group, int b) { return g.common + tail_of(g, group, b); }
+__device__ __forceinline__ int32_t tiles_of(const TreeReq& g, int group, int b) {
+  return g.common + tail_of(g, group, b);
+}
 
 // A block's left-over tiles, weighed with the cost of starting on them.
 __device__ __forceinline__ int32_t rest_weight(const TreeReq& g, int32_t tiles, int32_t run) {
@@ -883,13 +898,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       const int u = (warp - kTrLoadWarp) * 32 + lane;
       TreeReq g = {};
       const int box_rows = p.box_rows;
-const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
+      // keys that several blocks read stay in L2 as other data does, the others leave it first
+      const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
 
       auto publish = [&](int upto) {  // without TMA: the copies of the operations before `upto` have landed
         fence_proxy_async_smem();
         for (; published < upto; ++published) mbar_arrive(&b_full[published % C::kStages]);
       };
-      // (keys that several blocks read stay in L2 as other data does, the others leave it first)
       // K (or V) rows [128 tile, 128 tile + 128) of the request's pages into the next stage
       auto load = [&](int tile, int kvh, bool is_v) {
         if (TMA && is_v == leader) {  // the other warp's
@@ -1089,7 +1104,8 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
                           ? -1
                           : rest_slot(ends, chunks, chunks_before + kvh * h.chunks + k.chunks, blockIdx.x, p.ctas));
               left -= take;
-              if (!ends && chunks == 0 && t1 > 0 && g.kind != kReqEmpty)  // the stretch ends inside, behind its first tile
+              // the stretch ends inside the block, behind its first tile
+              if (!ends && chunks == 0 && t1 > 0 && g.kind != kReqEmpty)
                 fold(kvh, k.b, 0, 0, -1, r_weight + (int64_t)kvh * h.weight + k.weight, weight);
               if (k.b + 1 >= g.blocks) break;
               k.chunks += chunks;
@@ -1269,7 +1285,8 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
             auto zero_rows = [&](int r0, int r1) {
 #pragma unroll 8
               for (int row = r0 + sub; row < r1; row += kPass)
-                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(col + sw128(row, ch & 7)), "r"(0u) : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(col + sw128(row, ch & 7)), "r"(0u)
+                             : "memory");
             };
             uint32_t any = 0;
             auto check_rows = [&](int r0, int r1) {  // four passes' loads at once
@@ -1304,7 +1321,8 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
             zero_rows(0, in0);
             check_rows(min(max(d.ds - c0, in0), in1), in1);
             zero_rows(in1, kTrTile);
-            if (__any_sync(0xffffffffu, any != 0) && lane == 0) *reinterpret_cast<volatile int32_t*>(&ring[at].tainted) = 1;
+            if (__any_sync(0xffffffffu, any != 0) && lane == 0)
+              *reinterpret_cast<volatile int32_t*>(&ring[at].tainted) = 1;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -1318,7 +1336,7 @@ const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
         if (!alive) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(&b_pe[at]);
-    }
+      }
     }
   }
 
@@ -1383,7 +1401,8 @@ __global__ void __launch_bounds__(kMergeThreads) pa_v2_tree_merge_kernel(const T
         if (slot >= 0 && valid) {
           const float* base = p.slots + (int64_t)slot * C::kSlotFloats;
           lse[q] = __ldcg(base + (int64_t)kTrBlock * D + in_block);
-          const float4* v = reinterpret_cast<const float4*>(base) + (in_block >> 7) * (D / 4 * kTrTile) + (in_block & 127);
+          const float4* v =
+              reinterpret_cast<const float4*>(base) + (in_block >> 7) * (D / 4 * kTrTile) + (in_block & 127);
           x[q][0] = __ldcg(v + (2 * oct) * kTrTile);
           x[q][1] = __ldcg(v + (2 * oct + 1) * kTrTile);
         }
@@ -1549,7 +1568,8 @@ extern "C" pa_status pa_v2_tree_attention(const void* q, const void* k_pool, con
   p.g_magic = fg.magic;
   p.g_shift = fg.shift;
   // the work's units at most, for tables that list every page and token once: every block of the batch against every
-  // key tile.  A broken table can claim them again for each of 32 requests and must still fit 31 bits.
+  // key tile.  The blocks' starting costs are at most 6 / batch times that, and a broken table can claim all of it
+  // again for each of 32 requests: (32 + 6) * 2^25 still fits 31 bits.
   const double units = ((double)num_indices * page_size / pa::kTrTile + 2.0 * batch) *
                        ((double)num_tokens * p.group / pa::kTrBlock + batch) * num_kv_heads;
   p.small = batch <= 32 && units < (double)(1 << 25);
