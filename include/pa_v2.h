@@ -41,6 +41,8 @@
  *    L2: speculative reads, range-checked, never written and never used for
  *    a result, which is computed from what is read after the wait.)  Each
  *    kernel also lets the one after it be scheduled early, at its own start.
+ *    The attention kernel of pa_v2_tree_attention is the exception: it starts
+ *    when the kernel before it has completed.
  *  - Units.  Every LSE is in log2 units (scores run in base 2 with log2(e)
  *    folded into the scale); the natural-log LSE is lse2 * ln 2.
  *  - Layouts are row-major and contiguous:

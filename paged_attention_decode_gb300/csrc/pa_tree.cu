@@ -47,7 +47,7 @@
 // stream, and the other stream fills most of the gap.  Around the tiles stand
 // 6.5 us of start (cold code, barriers, tensor memory, the cut, the page list, Q
 // and the first K tile) and, after a cut block, 2-4 us of epilogue and 5 us of
-// merge.  bf16, 32 query heads on 8 KV heads, D = 128, replayed from a graph: 64
+// merge.  16 bits, 32 query heads on 8 KV heads, D = 128, replayed from a graph: 64
 // tokens over 32K 46.6 us (20 us of HBM reads), 4 x 256 tokens over 32K 400 us
 // (1.37 PFLOP/s of 1.92 measured with cuBLAS), 16 ragged requests 99 us (4.4
 // TB/s), 32 chains of 5 tokens with a 4096-token window 72.4 us (5.2 TB/s), 8
@@ -97,7 +97,7 @@ struct TreeCfg {
   static constexpr int kStages = D == 128 ? 5 : 9;  // all the shared memory that the Q tiles leave
   static constexpr int kOffKv = 2 * kTileBytes;     // Q tiles first
   static constexpr int kOffMisc = kOffKv + kStages * kTileBytes;
-  static constexpr int kMisc = D == 128 ? 2048 : 3072;  // barriers, pieces, small exchanges
+  static constexpr int kMisc = D == 128 ? 2048 : 4096;  // barriers, pieces, small exchanges
   static constexpr int kSmem = kOffMisc + kMisc;
   static constexpr int kSmemAlloc = kSmem + 1024;   // room to align the base
   static constexpr int64_t kSlotFloats = (int64_t)kTrBlock * (D + 1);
