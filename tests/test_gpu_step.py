@@ -869,3 +869,49 @@ def test_tables_feed_the_single_token_decode():
     assert ((o2.cpu().double() - ro).abs() <= to).all() and ((l2.cpu().double() - rl).abs() <= tl).all()
     # the decode reads the unrounded q: one rounding of q apart (2^-11 of scores of size |q||k|/sqrt(D) ~ 12)
     assert (o.cpu().double() - ro).abs().max() <= 2e-2 and (l.cpu().double() - rl).abs().max() <= 2e-2
+
+
+@pytest.mark.parametrize("page_size", [16, 5])
+def test_pools_of_more_elements_than_32_bits_count(page_size):
+    hkv, D = 8, 128
+    pages = ((1 << 32) // (hkv * D) + (1 << 17)) // page_size
+    big_k, big_v = (torch.empty(pages, page_size, hkv, D, dtype=torch.float16, device="cuda") for _ in range(2))
+    assert big_k.numel() > 1 << 32
+
+    # the small case's pages at the end of the large pools: the same results, bit for bit
+    c = _tree_case(71, [(900, 33), (40, 5)], 32, hkv, D, page_size, torch.float16)
+    want = _run_tree(c)
+    shift = pages - c["kp"].shape[0]
+    big_k[shift:], big_v[shift:] = c["kp"].cuda(), c["vp"].cuda()
+    d = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in c.items()}
+    out, lse = pa.pa_v2_tree_attention(d["q"], big_k, big_v, d["idx"] + shift, d["indptr"], d["lpl"], d["fpo"], d["qo"],
+                                       d["scale"], tree_mask=d["mask"])
+    assert torch.equal(out.cpu(), want[0]) and torch.equal(lse.cpu(), want[1])
+
+    q, k, v, pos, slots, freq, w, kp, vp = _qk_case(70, 32, hkv, D, 128, torch.float16, True, page_size, 72)
+    weights = dict(q_weight=w[0].cuda(), k_weight=w[1].cuda())
+    dk, dv = kp.cuda(), vp.cuda()
+    small = pa.pa_v2_qk_rope_append(q, k, v, pos.cuda(), slots.cuda(), freq.cuda(), dk, dv, **weights)
+    shift = pages - kp.shape[0]
+    big_k[shift:], big_v[shift:] = kp.cuda(), vp.cuda()
+    large = pa.pa_v2_qk_rope_append(q, k, v, pos.cuda(), slots.cuda() + shift * page_size, freq.cuda(), big_k, big_v,
+                                    **weights)
+    assert torch.equal(large, small) and torch.equal(big_k[shift:], dk) and torch.equal(big_v[shift:], dv)
+
+
+def test_two_calls_at_once_on_two_streams():
+    cases = [_tree_case(73, [(5000, 40), (300, 8)], 32, 8, 128, 16, torch.bfloat16),
+             _tree_case(74, [(64, 3)] * 40, 8, 2, 64, 16, torch.float16, chain=True)]
+    want = [_run_tree(c) for c in cases]
+    ds = [{k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in c.items()} for c in cases]
+    ws = [pa.tree_attention_workspace(c["q"].shape[0], len(c["lpl"]), c["q"].shape[1], c["kp"].shape[2],
+                                      c["q"].shape[2]) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [pa.pa_v2_tree_attention(d["q"], d["kp"], d["vp"], d["idx"], d["indptr"], d["lpl"], d["fpo"], d["qo"],
+                                       d["scale"], tree_mask=d["mask"], workspace=w, stream=s)
+               for d, w, s in zip(ds, ws, streams)]
+        torch.cuda.synchronize()
+        for (out, lse), (ro, rl) in zip(got, want):
+            assert torch.equal(out.cpu(), ro) and torch.equal(lse.cpu(), rl)
