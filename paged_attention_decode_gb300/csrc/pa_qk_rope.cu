@@ -18,15 +18,17 @@
 // lane every element had to be shuffled across lanes, and the kernel was bound by
 // its instructions: 115 us for 16384 tokens of 48 heads).  A CTA walks
 // tiles of up to four tokens, each lane keeping the same heads and the same places in
-// the row: the next token's pieces are in flight while this one's are worked on, and
-// the next tile's cosines and sines are computed by all threads, one angle each, into
-// the other half of a shared buffer (one barrier per tile; with one per token, behind
-// the two warps that computed its angles, the kernel took 86 us).  A frequency is
-// converted once per CTA.  With all of it, 16384 tokens of 48 heads take 80 us, 5.0
-// TB/s (74 % of the measured copy rate): instructions issue in half of the cycles,
-// and 16 warps per SM (120 registers a thread) hide the rest no better; three or
-// four CTAs per SM with the registers that leaves, or 384 and 768 threads a CTA,
-// were no faster.
+// the row: its pieces of the next two tokens are on their way into a ring in shared
+// memory (its own places there: no barrier), and the next tile's cosines and sines are
+// computed by all threads, one angle each, into the other half of a shared buffer (one
+// barrier per tile; with one per token, behind the two warps that computed its angles,
+// the kernel took 86 us).  A frequency is converted once per CTA.
+//
+// 16384 tokens of 48 heads take 73 us, 5.5 TB/s (81 % of the measured copy rate).  With
+// one token ahead in registers 24 KB per SM were under way, too little for the memory's
+// latency: 80 us, and 74.5 with the ring; norm and rotation two elements an instruction
+// took the rest.  A ring of four tokens is equal, of six slower (78), three CTAs per SM
+// with the registers that leaves slower too (90).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -37,6 +39,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.cuh"
+#include "pa_mma.cuh"
 #include "pa_tc05.cuh"
 #include "pa_v2.h"
 
@@ -46,6 +49,7 @@ namespace {
 constexpr int kQkThreads = 256;
 constexpr int kQkPasses = 3;  // heads a lane holds at once, at most (four do not fit its registers)
 constexpr int kQkTile = 4;    // tokens per tile, at most: one angle per thread
+constexpr int kQkSlots = 3;   // tokens whose pieces a thread has room for in the ring
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
 struct QkParams {
@@ -137,10 +141,8 @@ __device__ __forceinline__ float2 rotation(int32_t pos, uint64_t turn) {
   return make_float2(c, s);
 }
 
-__device__ __forceinline__ uint2 load_stream(const void* a) {
-  uint2 x;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(a));
-  return x;
+__device__ __forceinline__ void copy_piece(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
 }
 
 // NP: heads per lane (blockIdx.y takes the next NP * kRows heads).  PAIRED: the lane's pieces are partners (half
@@ -150,7 +152,8 @@ __global__ void __launch_bounds__(kQkThreads, 2) pa_v2_qk_rope_append_kernel(con
   constexpr int N = Vec<T>::N, P = N / 2;     // elements per lane; per piece, and pairs per lane
   constexpr int kLanes = D / N;               // lanes per head row (8, 16 or 32)
   constexpr int kRows = kQkThreads / kLanes;  // head rows in flight per CTA and pass
-  __shared__ __align__(16) float2 cs[2][kQkTile][D / 2];
+  __shared__ __align__(16) float cs[2][kQkTile][2][D / 2];  // cosines, sines
+  extern __shared__ uint2 ring[];  // [kQkSlots][NP][2][kQkThreads]: each thread's own pieces
 
   pdl_launch_dependents();
   pdl_wait_prerequisites();
@@ -197,52 +200,71 @@ __global__ void __launch_bounds__(kQkThreads, 2) pa_v2_qk_rope_append_kernel(con
   const bool has_angle = angle < half && angle_tok < p.tile;
   const uint64_t turn = has_angle ? turn_of(p.inv_freq[angle]) : 0;
   auto angles = [&](int first, int buf) {  // of the tile whose first token is `first`
-    if (has_angle && first + angle_tok < p.tokens)
-      cs[buf][angle_tok][angle] = rotation(p.positions[first + angle_tok], turn);
+    if (has_angle && first + angle_tok < p.tokens) {
+      const float2 r = rotation(p.positions[first + angle_tok], turn);
+      cs[buf][angle_tok][0][angle] = r.x;
+      cs[buf][angle_tok][1][angle] = r.y;
+    }
   };
   int t = blockIdx.x * p.tile, in_tile = 0;
   const int jump = ((int)gridDim.x - 1) * p.tile + 1;  // from a tile's last token to the next tile's first
-  uint4 next[NP];
-  int32_t next_slot = 0;
-  auto fetch = [&](int at) {  // a token's pieces
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      next[i] = make_uint4(0, 0, 0, 0);
-      if (kind[i] < 3) {
-        const char* from = src[i] + (uint64_t)(uint32_t)at * src_step[i];
-        const uint2 a = load_stream(from), b = load_stream(from + gap * (int)sizeof(T));
-        next[i] = make_uint4(a.x, a.y, b.x, b.y);
-      }
-    }
-    next_slot = p.slots[at];
-  };
   auto skip_of = [&](int place) { return place + 1 == p.tile ? jump : 1; };
+  // the pieces of the next tokens are under way to the ring, kQkSlots - 1 tokens ahead
+  const uint32_t mine = smem_addr(ring + threadIdx.x);
+  constexpr uint32_t kPiece = kQkThreads * sizeof(uint2), kSlot = NP * 2 * kPiece;
+  int ahead = t, ahead_place = 0;
+  uint32_t fill = mine, drain = mine;
+  auto next_slot_of = [&](uint32_t at) { return at + kSlot == mine + kQkSlots * kSlot ? mine : at + kSlot; };
+  auto fetch = [&]() {  // one more token's pieces, if there is one
+    if (ahead < p.tokens) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        if (kind[i] < 3) {
+          const char* from = src[i] + (uint64_t)(uint32_t)ahead * src_step[i];
+          copy_piece(fill + 2 * i * kPiece, from);
+          copy_piece(fill + (2 * i + 1) * kPiece, from + gap * (int)sizeof(T));
+        }
+      }
+      ahead += skip_of(ahead_place);
+      ahead_place = ahead_place + 1 == p.tile ? 0 : ahead_place + 1;
+    }
+    cp_async_commit();
+    fill = next_slot_of(fill);
+  };
+  int32_t next_slot = 0;
   if (t < p.tokens) {
-    fetch(t);
+#pragma unroll
+    for (int i = 0; i < kQkSlots - 1; ++i) fetch();
+    next_slot = p.slots[t];
     angles(t, 0);
   }
   __syncthreads();
   for (int buf = 0; t < p.tokens;) {
+    cp_async_wait<kQkSlots - 2>();
     uint4 raw[NP];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) raw[i] = next[i];
+    for (int i = 0; i < NP; ++i) {
+      uint2 a, b;
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a.x), "=r"(a.y) : "r"(drain + 2 * i * kPiece) : "memory");
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                   : "=r"(b.x), "=r"(b.y)
+                   : "r"(drain + (2 * i + 1) * kPiece)
+                   : "memory");
+      raw[i] = make_uint4(a.x, a.y, b.x, b.y);
+    }
+    drain = next_slot_of(drain);
+    fetch();  // into the slot that was read a token ago
     const int64_t slot = next_slot;
     const int place = in_tile, after = t + skip_of(place);
     in_tile = place + 1 == p.tile ? 0 : place + 1;
-    if (after < p.tokens) fetch(after);
+    if (after < p.tokens) next_slot = p.slots[after];
     if (place == 0) angles(t + (int)gridDim.x * p.tile, buf ^ 1);
     if (slot >= 0 && slot < p.num_rows) {
-      float2 r[P];  // the pairs' cosines and sines
+      float2 co[P / 2], si[P / 2];  // the pairs' cosines and sines
 #pragma unroll
-      for (int i = 0; i < P; ++i) r[i] = make_float2(1.f, 0.f);
-      if (rotated) {
-        const float4* at = reinterpret_cast<const float4*>(&cs[buf][place][lane * P]);
-#pragma unroll
-        for (int i = 0; i < P / 2; ++i) {
-          const float4 v = at[i];
-          r[2 * i] = make_float2(v.x, v.y);
-          r[2 * i + 1] = make_float2(v.z, v.w);
-        }
+      for (int i = 0; i < P / 2; ++i) {
+        co[i] = rotated ? *reinterpret_cast<const float2*>(&cs[buf][place][0][lane * P + 2 * i]) : make_float2(1.f, 1.f);
+        si[i] = rotated ? *reinterpret_cast<const float2*>(&cs[buf][place][1][lane * P + 2 * i]) : make_float2(0.f, 0.f);
       }
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
@@ -261,15 +283,24 @@ __global__ void __launch_bounds__(kQkThreads, 2) pa_v2_qk_rope_append_kernel(con
               float g[N];
               Vec<T>::unpack(weight[k], g);
 #pragma unroll
-              for (int i = 0; i < N; ++i) x[i] = x[i] * inv * g[i];
+              for (int i = 0; i < N; i += 2) {
+                const float2 y = mul2(mul2(make_float2(x[i], x[i + 1]), make_float2(inv, inv)),
+                                      make_float2(g[i], g[i + 1]));
+                x[i] = y.x;
+                x[i + 1] = y.y;
+              }
             }
           }
 #pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const int a = PAIRED ? i : 2 * i, b = PAIRED ? i + P : 2 * i + 1;
-            const float u = x[a], w = x[b];
-            x[a] = fmaf(-w, r[i].y, u * r[i].x);
-            x[b] = fmaf(u, r[i].y, w * r[i].x);
+          for (int i = 0; i < P / 2; ++i) {  // two pairs: their first elements in u, their second ones in w
+            const int a = PAIRED ? 2 * i : 4 * i, b = PAIRED ? a + P : a + 1, next = PAIRED ? 1 : 2;
+            const float2 u = make_float2(x[a], x[a + next]), w = make_float2(x[b], x[b + next]);
+            const float2 nu = fma2(make_float2(-w.x, -w.y), si[i], mul2(u, co[i]));
+            const float2 nw = fma2(u, si[i], mul2(w, co[i]));
+            x[a] = nu.x;
+            x[a + next] = nu.y;
+            x[b] = nw.x;
+            x[b + next] = nw.y;
           }
           if (kind[k] == 0 && sizeof(TQ) != sizeof(T)) {  // f32 from 16 bits: a piece is 16 bytes
             char* to = dst[k] + (uint64_t)(uint32_t)t * dst_step[k];
@@ -386,14 +417,16 @@ extern "C" pa_status pa_v2_qk_rope_append(const void* q, int64_t q_stride, const
   const pa::QkKernel fn = dtype == PA_F32   ? pa::pick<float>(head_dim, true, !interleaved, np)
                           : dtype == PA_F16 ? pa::pick<__half>(head_dim, q32, !interleaved, np)
                                             : pa::pick<__nv_bfloat16>(head_dim, q32, !interleaved, np);
+  const size_t smem = sizeof(uint2) * pa::kQkSlots * np * 2 * pa::kQkThreads;
+  if (!pa::prepare_kernel(reinterpret_cast<const void*>(fn), smem)) return PA_ECUDA;
   int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, pa::kQkThreads, 0) != cudaSuccess || per_sm < 1)
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, pa::kQkThreads, smem) != cudaSuccess || per_sm < 1)
     return PA_ECUDA;
   const int64_t wave = ((int64_t)sms * per_sm + groups - 1) / groups;  // CTAs along the tokens: one wave
   int tile = (int)(num_tokens / wave);  // whole tiles only where every CTA still gets some
   p.tile = tile < 1 ? 1 : tile < pa::kQkTile ? tile : pa::kQkTile;
   const int64_t tiles = ((int64_t)num_tokens + p.tile - 1) / p.tile;
   const cudaError_t rc = pa::launch_dependent(fn, dim3((unsigned)(tiles < wave ? tiles : wave), groups),
-                                              dim3(pa::kQkThreads), 0, static_cast<cudaStream_t>(cuda_stream), p);
+                                              dim3(pa::kQkThreads), smem, static_cast<cudaStream_t>(cuda_stream), p);
   return rc == cudaSuccess && cudaGetLastError() == cudaSuccess ? PA_OK : PA_ECUDA;
 }
