@@ -263,8 +263,11 @@ __global__ void __launch_bounds__(kQkThreads, 2) pa_v2_qk_rope_append_kernel(con
       float2 co[P / 2], si[P / 2];  // the pairs' cosines and sines
 #pragma unroll
       for (int i = 0; i < P / 2; ++i) {
-        co[i] = rotated ? *reinterpret_cast<const float2*>(&cs[buf][place][0][lane * P + 2 * i]) : make_float2(1.f, 1.f);
-        si[i] = rotated ? *reinterpret_cast<const float2*>(&cs[buf][place][1][lane * P + 2 * i]) : make_float2(0.f, 0.f);
+        co[i] = si[i] = make_float2(0.f, 0.f);
+        if (rotated) {
+          co[i] = *reinterpret_cast<const float2*>(&cs[buf][place][0][lane * P + 2 * i]);
+          si[i] = *reinterpret_cast<const float2*>(&cs[buf][place][1][lane * P + 2 * i]);
+        }
       }
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
@@ -291,16 +294,18 @@ __global__ void __launch_bounds__(kQkThreads, 2) pa_v2_qk_rope_append_kernel(con
               }
             }
           }
+          if (rotated) {  // the other elements are left out of it: 0 times an infinity next to them is NaN
 #pragma unroll
-          for (int i = 0; i < P / 2; ++i) {  // two pairs: their first elements in u, their second ones in w
-            const int a = PAIRED ? 2 * i : 4 * i, b = PAIRED ? a + P : a + 1, next = PAIRED ? 1 : 2;
-            const float2 u = make_float2(x[a], x[a + next]), w = make_float2(x[b], x[b + next]);
-            const float2 nu = fma2(make_float2(-w.x, -w.y), si[i], mul2(u, co[i]));
-            const float2 nw = fma2(u, si[i], mul2(w, co[i]));
-            x[a] = nu.x;
-            x[a + next] = nu.y;
-            x[b] = nw.x;
-            x[b + next] = nw.y;
+            for (int i = 0; i < P / 2; ++i) {  // two pairs: their first elements in u, their second ones in w
+              const int a = PAIRED ? 2 * i : 4 * i, b = PAIRED ? a + P : a + 1, next = PAIRED ? 1 : 2;
+              const float2 u = make_float2(x[a], x[a + next]), w = make_float2(x[b], x[b + next]);
+              const float2 nu = fma2(make_float2(-w.x, -w.y), si[i], mul2(u, co[i]));
+              const float2 nw = fma2(u, si[i], mul2(w, co[i]));
+              x[a] = nu.x;
+              x[a + next] = nu.y;
+              x[b] = nw.x;
+              x[b + next] = nw.y;
+            }
           }
           if (kind[k] == 0 && sizeof(TQ) != sizeof(T)) {  // f32 from 16 bits: a piece is 16 bytes
             char* to = dst[k] + (uint64_t)(uint32_t)t * dst_step[k];

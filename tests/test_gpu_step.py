@@ -306,6 +306,23 @@ def test_qk_rows_of_zeros_and_large_values():
     _check_qk(case, False, torch.bfloat16)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rot", [(128, 32), (64, 48), (128, 0)])
+def test_qk_infinities_beside_elements_that_are_not_rotated(D, rot, interleaved, dtype):
+    q, k, v, pos, slots, freq, w, kp, vp = _qk_case(6, 4, 2, D, rot, dtype, False, 16, 13)
+    for x in (q, k):
+        x[0, 0, rot], x[1, 1, rot + 3], x[2, 0, D - 1] = math.inf, math.nan, -math.inf
+    dk, dv = kp.cuda(), vp.cuda()
+    out = pa.pa_v2_qk_rope_append(q, k, v, pos.cuda(), slots.cuda(), freq.cuda() if rot else None, dk, dv,
+                                  interleaved=interleaved)
+    assert torch.equal(out[..., rot:].nan_to_num(nan=-3.0), q[..., rot:].nan_to_num(nan=-3.0))
+    assert out[..., :rot].isfinite().all()
+    got = dk.flatten(0, 1)[slots.long().cuda()]
+    assert torch.equal(got[..., rot:].nan_to_num(nan=-3.0), k[..., rot:].nan_to_num(nan=-3.0))
+    assert got[..., :rot].isfinite().all()
+
+
 def test_qk_empty_call_and_default_output():
     q, k, v, pos, slots, freq, w, kp, vp = _qk_case(4, 4, 2, 64, 64, torch.float16, False, 4, 1)
     e = torch.zeros(0, dtype=I32, device="cuda")
