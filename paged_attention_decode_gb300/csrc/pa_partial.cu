@@ -26,7 +26,7 @@ namespace pa {
 
 bool prepare_kernel(const void* fn, size_t smem) {
   constexpr int kMaxDevices = 64;
-  constexpr int kMaxKernels = 256;
+  constexpr int kMaxKernels = 128;
   static std::mutex mu;
   static const void* done[kMaxDevices][kMaxKernels] = {};
   int dev = 0;

@@ -422,11 +422,8 @@ extern "C" pa_status pa_v2_qk_rope_append(const void* q, int64_t q_stride, const
   const pa::QkKernel fn = dtype == PA_F32   ? pa::pick<float>(head_dim, true, !interleaved, np)
                           : dtype == PA_F16 ? pa::pick<__half>(head_dim, q32, !interleaved, np)
                                             : pa::pick<__nv_bfloat16>(head_dim, q32, !interleaved, np);
-  const size_t smem = sizeof(uint2) * pa::kQkSlots * np * 2 * pa::kQkThreads;
-  if (!pa::prepare_kernel(reinterpret_cast<const void*>(fn), smem)) return PA_ECUDA;
-  int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, pa::kQkThreads, smem) != cudaSuccess || per_sm < 1)
-    return PA_ECUDA;
+  const size_t smem = sizeof(uint2) * pa::kQkSlots * np * 2 * pa::kQkThreads;  // with the angles below 48 KB
+  const int per_sm = np == 1 ? 3 : 2;  // CTAs that registers allow (about 70, 100 and 120 a thread); asking costs time in every call
   const int64_t wave = ((int64_t)sms * per_sm + groups - 1) / groups;  // CTAs along the tokens: one wave
   int tile = (int)(num_tokens / wave);  // whole tiles only where every CTA still gets some
   p.tile = tile < 1 ? 1 : tile < pa::kQkTile ? tile : pa::kQkTile;
