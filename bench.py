@@ -124,7 +124,8 @@ KERNEL_SOURCES = {
     "pa_v2_partial_tc_two_plan_kernel": ["pa_partial_tc_cascade.cu", "pa_partial_tc_body.cuh", "pa_internal.cuh",
                                          "pa_device.cuh", "pa_mma.cuh"],
     "pa_v2_partial_simt_kernel": ["pa_partial_simt.cu", "pa_internal.cuh", "pa_device.cuh"],
-    "pa_v2_partial_extra_tc05_kernel": ["pa_partial_extra_tc05.cu", "pa_internal.cuh", "pa_device.cuh", "pa_mma.cuh"],
+    "pa_v2_partial_extra_tc05_kernel": ["pa_partial_extra_tc05.cu", "pa_internal.cuh", "pa_device.cuh", "pa_mma.cuh",
+                                        "pa_tc05.cuh"],
 }
 
 

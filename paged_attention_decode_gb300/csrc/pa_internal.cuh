@@ -492,11 +492,6 @@ int occupancy_partial_extra_tc05(int kv_dtype, int* blocks_per_sm);
 int launch_partial_extra_tc05(const PartialParams& p, const void* q_extra, const void* k_extra, int64_t k_stride,
                               int64_t e_stride, int kv_dtype, dim3 grid, cudaStream_t stream);
 
-// Tensor map over a pool viewed as [rows = num_pages * page_size, Hkv, D] (innermost first: D, Hkv, rows);
-// a box is one KV head x `box_rows` rows x `box_d` elements of the head dim.
-bool make_pool_map(CUtensorMap* map, const void* base, int dtype, int64_t rows, int hkv, int D, int box_d,
-                   int box_rows, CUtensorMapSwizzle swizzle);
-
 // True when the tensor-core kernel stages this page size with TMA.
 inline bool tc_uses_tma(int page_size) {
   return page_size % 8 == 0 && (page_size <= kStageRows || page_size % kStageRows == 0);

@@ -20,6 +20,7 @@
 #include <mutex>
 
 #include "pa_internal.cuh"
+#include "pa_pool_map.h"
 #include "pa_launch.h"
 
 namespace pa {

@@ -64,6 +64,7 @@
 
 #include "pa_internal.cuh"
 #include "pa_mma.cuh"
+#include "pa_pool_map.h"
 #include "pa_tc05.cuh"
 
 namespace pa {
