@@ -523,7 +523,8 @@ __device__ __forceinline__ float half_of(const __nv_bfloat16* x) { return __bflo
 __device__ __forceinline__ bool nothing_seen(float l) { return l == 0.f; }
 
 // The non-finite values of new tokens that the fix warp took out of V, back into the O of the rows that see them
-// (a converged warp; query token tok of the piece's request on this thread's lane).
+// (a converged warp: called under a condition that is the same for all its lanes; query token tok of the piece's
+// request on this thread's lane).
 template <typename T, int D>
 __device__ __noinline__ void put_back(const TreeParams& p, const TreePiece& d, int tok, uint32_t t_o) {
   const int k0 = max(d.tile * kTrTile, d.ds), k1 = min((d.tile + d.tiles) * kTrTile, d.hi);
@@ -823,7 +824,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const bool nothing = nothing_seen(l);
         const float inv = nothing ? 0.f : fast_rcp(l);
         const float lse = nothing ? -INFINITY : m - kShift + fast_log2(l);
-        if (kind == kPieceTiles && d.tainted != 0 && !nothing_seen(l)) put_back<T, D>(p, ring[at], tok, t_o);
+        // (the whole warp or none of it: tensor memory is read and written by converged warps only, and rows that see
+        // nothing in this piece stand beside rows that do)
+        if (kind == kPieceTiles && d.tainted != 0) put_back<T, D>(p, ring[at], tok, t_o);
         const bool valid = rr < rows, whole = d.slot < 0;
         const int qrow = d.row0 + min(rr, rows - 1);  // row of the request
         const int64_t orow = (int64_t)(d.t0 + tok) * p.hq + (int64_t)d.kvh * p.group + (qrow - tok * p.group);

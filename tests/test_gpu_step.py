@@ -543,6 +543,57 @@ def test_tree_visible_nan_and_infinite_values_do_reach_their_rows(dtype):
         assert torch.isfinite(out[t][:, others]).all()
 
 
+def _check_tree_with_nonfinite_values(c):
+    """As _check_tree, where visible values are NaN or infinite: those of the definition have to come out, in the
+    elements they belong to, and every other element is compared as ever."""
+    st = status_word()
+    out, lse = _run_tree(c, 0, st)
+    assert int(st) == 0
+    finite = dict(c, vp=torch.where(c["vp"].isfinite(), c["vp"], torch.zeros_like(c["vp"])))
+    args = (c["idx"], c["indptr"], c["lpl"], c["fpo"], c["qo"], c["scale"], c["mask"])
+    ro = R.attention_ref(c["q"], c["kp"], c["vp"], *args)[0]
+    rf, rl, to, tl = R.attention_ref(c["q"], c["kp"], finite["vp"], *args)
+    out, lse = out.double(), lse.double()
+    empty = rl == -math.inf
+    assert torch.equal(lse == -math.inf, empty) and out[empty].eq(0).all()
+    assert ((lse - rl).abs()[~empty] <= tl[~empty]).all()
+    assert torch.equal(out.isnan(), ro.isnan())
+    assert torch.equal(out == math.inf, ro == math.inf) and torch.equal(out == -math.inf, ro == -math.inf)
+    fin = ro.isfinite()
+    assert ((out - rf).abs()[fin] <= to[fin]).all()
+    return ro
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("page_size", [16, 5])
+@pytest.mark.parametrize("copies", [1, 16])
+@pytest.mark.parametrize("hq,n", [(8, 12), (2, 100), (8, 48)])   # up to 48, 100 and 192 rows a block: joined streams, two tiles
+def test_tree_rows_that_see_nothing_beside_rows_that_see_infinities(hq, n, copies, page_size, dtype):
+    """No context: a token without a mask bit sees nothing at all, in the same warp as tokens that see a NaN or an
+    infinity; a drafted tree padded with empty rows looks like this."""
+    c = _tree_case(81, [(0, n)] * copies, hq, 2, 64, page_size, dtype, fpos=[min(4, page_size - 1)] * copies)
+    vp = c["vp"].flatten(0, 1)
+    for r in range(copies):
+        ids = c["idx"][int(c["indptr"][r]):int(c["indptr"][r + 1])].long()
+        rows = (ids[:, None] * page_size + torch.arange(page_size)).reshape(-1)[int(c["fpo"][r]):]
+        vp[int(rows[2]), 0, 5] = math.inf
+        vp[int(rows[3]), 1, 63] = math.nan
+        vp[int(rows[n - 1]), 0, 33] = -math.inf
+        c["mask"][r * n + 1:r * n + n:3] = 0
+    ref = _check_tree_with_nonfinite_values(c)
+    assert (ref == math.inf).any() and (ref == -math.inf).any() and ref.isnan().any()
+
+
+def test_tree_chain_cut_behind_its_first_tile_beside_infinities():
+    """One block of 200 tokens of a chain without context: the last tile may stand as a piece of its own, in which the
+    tokens before it see nothing and those behind it, in the same warp, an infinity."""
+    c = _tree_case(82, [(0, 200)], 1, 1, 128, 16, torch.bfloat16, chain=True)
+    rows = (c["idx"].long()[:, None] * 16 + torch.arange(16)).reshape(-1)
+    vp = c["vp"].flatten(0, 1)
+    vp[int(rows[130]), 0, 7], vp[int(rows[199]), 0, 8], vp[int(rows[3]), 0, 9] = math.inf, math.nan, -math.inf
+    _check_tree_with_nonfinite_values(c)
+
+
 @pytest.mark.parametrize("dtype", DT)
 def test_tree_sharp_and_flat_scores(dtype):
     c = _tree_case(36, [(900, 8)], 4, 2, 128, 16, dtype)
