@@ -626,7 +626,8 @@ pa_status pa_v2_decode_noalloc(const pa_v2_plan_t* plan, const float* q, const v
  *    a row of table_width int32.  With a free list, entries from ceil(c/s) on
  *    are taken from it, requests in order (request r's first new page is
  *    free_pages[sum of the pages earlier requests take]), and written into
- *    block_table; with free_pages null every entry is the caller's already.
+ *    block_table; with free_pages null every entry is the caller's already (a
+ *    list that ran out is a non-null pointer, which is not read, and num_free 0).
  *    pages_needed[0] receives the number of pages the step takes.
  *  - Page table.  The visible window is the last min(t, window) tokens (all of
  *    them when window is 0): indices[indptr[r] ..) lists its pages,

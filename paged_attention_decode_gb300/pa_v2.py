@@ -695,7 +695,8 @@ def pa_v2_build_tables(cached_lens, new_lens, block_table, page_size: int, table
                        parents=None, window: int = 0, status=None, stream=None) -> StepTables:
     """Page table, slots, positions and tree masks of one step (pa_v2_build_tables), on the device.
 
-    cached_lens, new_lens [B]; block_table [B, width], extended in place from free_pages when given;
+    cached_lens, new_lens [B]; block_table [B, width], extended in place from free_pages when given (an empty
+    list is one that ran out: its pages are -1; None means that the table holds every page already);
     parents [token capacity] (request-relative, -1 a root) for trees, None for chains.  Fills and returns
     `tables`."""
     if block_table.dim() != 2:
@@ -707,9 +708,13 @@ def pa_v2_build_tables(cached_lens, new_lens, block_table, page_size: int, table
     if mask is not None and mask.dim() != 2:
         raise ValueError("tree_mask must be [token capacity, mask words]")
     words = mask.shape[1] if mask is not None else 0
+    free, num_free = ptr(free_pages, "free_pages", dev, i32), free_pages.numel() if free_pages is not None else 0
+    if free_pages is not None and num_free == 0:
+        # an empty tensor has no address, and null means that there is no list: any device address stands for a list
+        # that ran out (it is not read)
+        free = t.indptr.data_ptr()
     args = (ptr(cached_lens, "cached_lens", dev, i32, B), ptr(new_lens, "new_lens", dev, i32, B), B,
-            ptr(block_table, "block_table", dev, i32), width, ptr(free_pages, "free_pages", dev, i32),
-            free_pages.numel() if free_pages is not None else 0, ptr(parents, "parents", dev, i32, cap_t),
+            ptr(block_table, "block_table", dev, i32), width, free, num_free, ptr(parents, "parents", dev, i32, cap_t),
             page_size, window, ptr(t.indptr, "indptr", dev, i32, B + 1), ptr(t.indices, "indices", dev, i32), cap_i,
             ptr(t.last_page_len, "last_page_len", dev, i32, B),
             ptr(t.first_page_offset, "first_page_offset", dev, i32, B),

@@ -164,6 +164,32 @@ def test_tables_short_free_list_and_capacities():
     assert t.indptr.tolist() == [0, 2, 4] and t.qo_indptr.tolist() == [0, 3, 4]
 
 
+def test_tables_empty_free_list_is_one_that_ran_out():
+    """No page left: the pages are -1 and reported, and what stood in the table's unused entries (here another
+    request's pages) is not taken for them."""
+    stale = torch.tensor([[3, 9, 3, 9], [5, 6, 5, 6]], dtype=I32)
+    pool = torch.arange(12, dtype=I32, device="cuda")
+    for free in (torch.empty(0, dtype=I32, device="cuda"), pool[12:], pool[5:5]):
+        st = status_word()
+        t = _fresh_tables(2, 8, 8, 0)
+        d = stale.cuda()
+        pa.pa_v2_build_tables(i32([3, 4]).cuda(), i32([4, 1]).cuda(), d, 2, t, free_pages=free, status=st)
+        torch.cuda.synchronize()
+        assert int(st) == pa.DEVICE_NO_PAGES
+        assert int(t.pages_needed) == 3
+        assert d.tolist() == [[3, 9, -1, -1], [5, 6, -1, 6]]
+        assert t.indices[:7].tolist() == [3, 9, -1, -1, 5, 6, -1]
+        assert t.slots[:5].tolist() == [9 * 2 + 1, -1, -1, -1, -1]
+    # one page to take (two cached tokens fill the second request's first page), then none: an empty list is enough
+    st = status_word()
+    pa.pa_v2_build_tables(i32([3, 2]).cuda(), i32([1, 2]).cuda(), stale.cuda(), 2, t, free_pages=pool[:0], status=st)
+    assert int(st) == pa.DEVICE_NO_PAGES and int(t.pages_needed) == 1
+    assert t.slots[:3].tolist() == [9 * 2 + 1, -1, -1]
+    st = status_word()
+    pa.pa_v2_build_tables(i32([3, 3]).cuda(), i32([1, 1]).cuda(), stale.cuda(), 2, t, free_pages=pool[:0], status=st)
+    assert int(st) == 0 and int(t.pages_needed) == 0 and t.slots[:2].tolist() == [9 * 2 + 1, 6 * 2 + 1]
+
+
 def test_tables_bad_parents_become_roots():
     st = status_word()
     t = _fresh_tables(1, 4, 5, 1)
