@@ -524,14 +524,27 @@ __device__ __forceinline__ bool nothing_seen(float l) { return l == 0.f; }
 
 // The non-finite values of new tokens that the fix warp took out of V, back into the O of the rows that see them
 // (a converged warp: called under a condition that is the same for all its lanes; query token tok of the piece's
-// request on this thread's lane).
+// request on this thread's lane).  Where two streams were joined, y is stream B's O of this row (D / 4 quads, kTrTile
+// apart), and O becomes o s0 + y s1 first: an infinity added before would meet s0 = 0 in a row whose keys are all
+// stream B's, and 0 times it is NaN.
 template <typename T, int D>
-__device__ __noinline__ void put_back(const TreeParams& p, const TreePiece& d, int tok, uint32_t t_o) {
+__device__ __noinline__ void put_back(const TreeParams& p, const TreePiece& d, int tok, uint32_t t_o, const float4* y,
+                                      float s0, float s1) {
   const int k0 = max(d.tile * kTrTile, d.ds), k1 = min((d.tile + d.tiles) * kTrTile, d.hi);
   for (int c = 0; c < D / 32; ++c) {
     uint32_t o[32];
     __syncwarp();
     tmem_ld32(t_o + 32 * c, o);
+    if (y) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 b = y[(8 * c + i) * kTrTile];
+        o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * s0 + b.x * s1);
+        o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * s0 + b.y * s1);
+        o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * s0 + b.z * s1);
+        o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * s0 + b.w * s1);
+      }
+    }
     for (int k = k0; k < k1; ++k) {
       if (!(visible_bits(p, d.lo, d.ds, d.hi, d.t0 + tok, tok, k) & 1u)) continue;
       const int sl = (int)fast_div((uint32_t)k, p.ps_magic, p.ps_shift);
@@ -541,8 +554,8 @@ __device__ __noinline__ void put_back(const TreeParams& p, const TreePiece& d, i
                      (((int64_t)page * p.page_size + (k - sl * p.page_size)) * p.hkv + d.kvh) * D + 32 * c;
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const float y = half_of(src + i);
-        if (!isfinite(y)) o[i] = __float_as_uint(__uint_as_float(o[i]) + y);
+        const float x = half_of(src + i);
+        if (!isfinite(x)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
       }
     }
     __syncwarp();
@@ -826,7 +839,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const float lse = nothing ? -INFINITY : m - kShift + fast_log2(l);
         // (the whole warp or none of it: tensor memory is read and written by converged warps only, and rows that see
         // nothing in this piece stand beside rows that do)
-        if (kind == kPieceTiles && d.tainted != 0) put_back<T, D>(p, ring[at], tok, t_o);
+        const bool mended = kind == kPieceTiles && d.tainted != 0;
+        if (mended) put_back<T, D>(p, ring[at], tok, t_o, joined ? xo + row : nullptr, s0, s1);
         const bool valid = rr < rows, whole = d.slot < 0;
         const int qrow = d.row0 + min(rr, rows - 1);  // row of the request
         const int64_t orow = (int64_t)(d.t0 + tok) * p.hq + (int64_t)d.kvh * p.group + (qrow - tok * p.group);
@@ -843,7 +857,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = nothing ? 0.f : __uint_as_float(o[i]);
-          if (joined && !nothing) {
+          if (joined && !mended && !nothing) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float4 y = xo[(8 * c + i) * kTrTile + row];

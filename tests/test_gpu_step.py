@@ -610,6 +610,27 @@ def test_tree_rows_that_see_nothing_beside_rows_that_see_infinities(hq, n, copie
     assert (ref == math.inf).any() and (ref == -math.inf).any() and ref.isnan().any()
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("page_size", [16, 5])
+@pytest.mark.parametrize("copies", [1, 12])
+def test_tree_infinities_of_rows_whose_keys_all_lie_in_one_tile(copies, page_size, dtype):
+    """128 rows a block, two or three key tiles in one piece (two streams, joined): tokens that see only themselves, in
+    the first tile or in the second, and an infinity or a NaN there.  12 requests: 192 or 288 units, so that a CTA
+    takes a whole block."""
+    first, n = page_size - 1, 128 - (page_size - 1) % 4
+    c = _tree_case(83, [(0, n)] * copies, 8, 8, 64, page_size, dtype, fpos=[first] * copies)
+    vp = c["vp"].flatten(0, 1)
+    for r in range(copies):
+        ids = c["idx"][int(c["indptr"][r]):int(c["indptr"][r + 1])].long()
+        rows = (ids[:, None] * page_size + torch.arange(page_size)).reshape(-1)[int(c["fpo"][r]):]
+        for token, element, value in ((5, 1, math.inf), (n - 1, 2, math.inf), (n - 2, 62, -math.inf), (9, 3, math.nan)):
+            c["mask"][r * n:(r + 1) * n, token // 32] &= ~(1 << token % 32) if token % 32 < 31 else 2**31 - 1
+            c["mask"][r * n + token] = i32(R.words_of(1 << token, 4))
+            vp[int(rows[token]), 1, element] = value
+    ref = _check_tree_with_nonfinite_values(c)
+    assert ref.isinf().any() and ref.isnan().any()
+
+
 def test_tree_chain_cut_behind_its_first_tile_beside_infinities():
     """One block of 200 tokens of a chain without context: the last tile may stand as a piece of its own, in which the
     tokens before it see nothing and those behind it, in the same warp, an infinity."""
