@@ -732,8 +732,10 @@ def pa_v2_build_tables(cached_lens, new_lens, block_table, page_size: int, table
 
 def _token_rows(t, name: str, tokens: int, head_dim: int, dtype, index: int) -> tuple[int, int, int]:
     """(pointer, token stride in elements, heads) of a [tokens, heads, head_dim] view with contiguous token rows."""
-    if t.get_device() != index or t.dtype is not dtype or t.dim() != 3:
-        _refuse(t, name, index, dtype, None)
+    if t.get_device() != index or t.dtype is not dtype:
+        _refuse(t, name, index, dtype, -1)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [{tokens}, heads, {head_dim}], got {list(t.shape)}")
     n, heads, d = t.shape
     if n != tokens or d != head_dim:
         raise ValueError(f"{name} must be [{tokens}, heads, {head_dim}], got {list(t.shape)}")

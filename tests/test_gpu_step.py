@@ -358,6 +358,27 @@ def test_qk_empty_call_and_default_output():
     assert torch.equal(out, q.float())
 
 
+def test_qk_refuses_what_it_cannot_pass_on():
+    q, k, v, pos, slots, freq, w, kp, vp = _qk_case(4, 4, 2, 64, 64, torch.float16, True, 4, 1)
+    good = dict(q=q, k=k, v=v, positions=pos.cuda(), slots=slots.cuda(), inv_freq=freq.cuda(), k_pool=kp.cuda(),
+                v_pool=vp.cuda(), q_weight=w[0].cuda(), k_weight=w[1].cuda())
+    for change, words in ((dict(k=k.flatten(1)), r"k must be \[4, heads, 64\], got \[4, 128\]"),
+                          (dict(v=v[:, 0]), r"v must be \[4, heads, 64\], got \[4, 64\]"),
+                          (dict(q=q[0]), "q must be"), (dict(q=q[None]), "q must be"), (dict(k=k[None]), "k must be"),
+                          (dict(k=k.float()), "k must be torch.float16"), (dict(v=v.cpu()), "v must be a CUDA tensor"),
+                          (dict(k=k[:3]), "k must be"), (dict(k=k[..., ::2]), "k must be"),
+                          (dict(v=v.transpose(0, 1)), "v must be"), (dict(v=v[:, :1]), "k, v and the pools must agree"),
+                          (dict(k=k.transpose(1, 2).contiguous().transpose(1, 2)), "must be contiguous"),
+                          (dict(slots=slots.cuda().long()), "slots must be torch.int32"),
+                          (dict(positions=pos.cuda()[:2]), "positions must hold 4 elements"),
+                          (dict(inv_freq=freq.cuda().half()), "inv_freq must be torch.float32"),
+                          (dict(q_weight=w[0].cuda()[:32]), "q_weight must hold 64 elements"),
+                          (dict(q_out=torch.zeros(4, 2, 64, dtype=torch.float16, device="cuda")), "q_out must be")):
+        with pytest.raises(ValueError, match=words):
+            pa.pa_v2_qk_rope_append(**{**good, **change})
+    assert pa.pa_v2_qk_rope_append(**good).shape == (4, 4, 64)
+
+
 # ---------------------------------------------------------------------------
 # tree attention
 # ---------------------------------------------------------------------------
