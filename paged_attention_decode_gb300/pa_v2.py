@@ -667,6 +667,16 @@ def _device_index(t, name: str) -> int:
     return index
 
 
+def _mask_words(mask, shape: str) -> int:
+    """Words per row of a tree mask, 0 for none.  A mask without words is refused: its tensor has no address, and null
+    means a chain."""
+    if mask is None:
+        return 0
+    if mask.dim() != 2 or mask.shape[1] < 1:
+        raise ValueError(f"tree_mask must be {shape} with at least one word, got {list(mask.shape)}")
+    return mask.shape[1]
+
+
 @dataclass
 class StepTables:
     """Outputs of pa_v2_build_tables: device int32 buffers a program keeps and reuses from step to step."""
@@ -705,9 +715,7 @@ def pa_v2_build_tables(cached_lens, new_lens, block_table, page_size: int, table
     i32, ptr = torch.int32, _step_ptr
     t, mask = tables, tables.tree_mask
     cap_i, cap_t = t.indices.numel(), t.slots.numel()
-    if mask is not None and mask.dim() != 2:
-        raise ValueError("tree_mask must be [token capacity, mask words]")
-    words = mask.shape[1] if mask is not None else 0
+    words = _mask_words(mask, "[token capacity, mask words]")
     free, num_free = ptr(free_pages, "free_pages", dev, i32), free_pages.numel() if free_pages is not None else 0
     if free_pages is not None and num_free == 0:
         # an empty tensor has no address, and null means that there is no list: any device address stands for a list
@@ -840,9 +848,7 @@ def pa_v2_tree_attention(q, k_pool, v_pool, indices, indptr, last_page_len, firs
     if pool_dim != D:
         raise ValueError(f"pools must be [P, page_size, Hkv, {D}]")
     B, dt, i32, ptr = last_page_len.numel(), k_pool.dtype, torch.int32, _step_ptr
-    if tree_mask is not None and tree_mask.dim() != 2:
-        raise ValueError("tree_mask must be [tokens, mask words]")
-    words = tree_mask.shape[1] if tree_mask is not None else 0
+    words = _mask_words(tree_mask, "[tokens, mask words]")
     head = (ptr(q, "q", dev, dt), k_ptr, v_ptr, KV_DTYPES[dt], P, ps, hq, hkv, D, ptr(indices, "indices", dev, i32),
             indices.numel(), ptr(indptr, "indptr", dev, i32, B + 1),
             ptr(last_page_len, "last_page_len", dev, i32, B),

@@ -535,6 +535,19 @@ def test_tree_general_masks_and_all_bits():
     _check_tree(c)
 
 
+def test_tree_mask_without_words_is_refused():
+    """An empty mask is not a chain: its rows show nothing to anybody, and nothing can hold that."""
+    c = _tree_case(63, [(70, 3)], 4, 2, 64, 16, torch.float16)
+    with pytest.raises(ValueError, match="at least one word"):
+        _run_tree(dict(c, mask=torch.zeros(3, 0, dtype=I32)))
+    with pytest.raises(ValueError, match="at least one word"):
+        _run_tree(dict(c, mask=c["mask"].flatten()))
+    t = _fresh_tables(1, 4, 4, 1)
+    t.tree_mask = t.tree_mask[:, :0]
+    with pytest.raises(ValueError, match="at least one word"):
+        pa.pa_v2_build_tables(i32([3]).cuda(), i32([2]).cuda(), torch.zeros(1, 4, dtype=I32, device="cuda"), 4, t)
+
+
 def test_tree_wider_mask_rows_than_needed():
     _check_tree(_tree_case(62, [(70, 20), (5, 33)], 4, 2, 64, 16, torch.float16, words=32))
 
