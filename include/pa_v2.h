@@ -629,8 +629,8 @@ pa_status pa_v2_decode_noalloc(const pa_v2_plan_t* plan, const float* q, const v
  *    block_table; with free_pages null every entry is the caller's already (a
  *    list that ran out is a non-null pointer, which is not read, and num_free 0).
  *    pages_needed[0] receives the number of pages the step takes.
- *  - Page table.  The visible window is the last min(t, window) tokens (all of
- *    them when window is 0): indices[indptr[r] ..) lists its pages,
+ *  - Page table.  The visible window is the last min(t, max(window, n)) tokens
+ *    (all of them when window is 0; the new tokens are always in it): indices[indptr[r] ..) lists its pages,
  *    first_page_offset[r] is the entry it starts at, last_page_len[r] the
  *    entries used of its last page, as the decode calls read them.  A request
  *    with t = 0 has no page.

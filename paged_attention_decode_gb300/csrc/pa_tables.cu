@@ -3,7 +3,7 @@
 //
 // With c cached and n new tokens, s = page_size, t = c + n (per request):
 //   pages taken    ceil(t/s) - ceil(c/s), handed out from the free list in request order;
-//   window         the last w = min(t, window) tokens, from token t - w on;
+//   window         the last w = min(t, max(window, n)) tokens, from token t - w on;
 //   page list      entries (t-w)/s .. ceil(t/s)-1 of the request's block-table row;
 //   token i        row page((c+i)/s) * s + (c+i) % s, position c + depth(i).
 //
@@ -83,7 +83,8 @@ __device__ __forceinline__ ReqGeom request_geom(const TableParams& p, int r) {
     const int32_t need = pages_of(p, t);
     g.bad = need > p.width;
     if (!g.bad && t > 0) {
-      const int32_t start = p.window > 0 && t > p.window ? t - p.window : 0;
+      const int32_t span = max(p.window, n);  // new tokens are always among the visible ones
+      const int32_t start = p.window > 0 && t > span ? t - span : 0;
       g.have = pages_of(p, c);
       g.need = need;
       g.first = (int32_t)fast_div((uint32_t)start, p.ps_magic, p.ps_shift);

@@ -107,6 +107,30 @@ def test_tables_of_a_long_chain_and_chain_masks():
     _check_tables(t, table.cuda(), ref, 70)
 
 
+def test_tables_window_shorter_than_the_new_tokens():
+    """More new tokens than the window: all of them are listed, so that the attention has a row for each; the request
+    beside them is cut to the window as ever."""
+    ps, cached, fresh, window = 4, [9, 30, 0], [6, 2, 5], 3
+    table = torch.randperm(40, generator=torch.Generator().manual_seed(1))[:30].reshape(3, 10).to(I32)
+    t, st = _fresh_tables(3, 30, 13, 1), status_word()
+    pa.pa_v2_build_tables(i32(cached).cuda(), i32(fresh).cuda(), table.cuda(), ps, t, window=window, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    assert t.first_page_offset.tolist() == [1, 1, 0] and t.last_page_len.tolist() == [3, 4, 1]   # tokens 9, 29 and 0
+    assert t.indptr.tolist() == [0, 2, 3, 5] and t.indices[:5].tolist() == [*table[0, 2:4], table[1, 7], *table[2, :2]]
+    # the attention over these tables: 6, 3 and 5 visible tokens, nothing refused
+    g = torch.Generator().manual_seed(2)
+    kp, vp = (torch.randn(40, ps, 2, 64, generator=g).half() for _ in range(2))
+    q = torch.randn(13, 4, 64, generator=g).half()
+    out, lse = pa.pa_v2_tree_attention(q.cuda(), kp.cuda(), vp.cuda(), t.indices, t.indptr, t.last_page_len,
+                                       t.first_page_offset, t.qo_indptr, 0.125, tree_mask=t.tree_mask, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    ro, rl, to, tl = R.attention_ref(q, kp, vp, t.indices.cpu(), t.indptr.cpu(), t.last_page_len.cpu(),
+                                     t.first_page_offset.cpu(), t.qo_indptr.cpu(), 0.125, t.tree_mask.cpu())
+    assert ((out.cpu().double() - ro).abs() <= to).all() and ((lse.cpu().double() - rl).abs() <= tl).all()
+
+
 def test_tables_same_call_again_and_reuse_for_another_batch():
     case = _tables_case(5, 6, 16, 500, 20, True, 0, True, 4)
     cached, fresh, parents, table, free, cap_i, cap_t, words = case
