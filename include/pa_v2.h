@@ -630,7 +630,9 @@ pa_status pa_v2_decode_noalloc(const pa_v2_plan_t* plan, const float* q, const v
  *    list that ran out is a non-null pointer, which is not read, and num_free 0).
  *    pages_needed[0] receives the number of pages the step takes.
  *  - Page table.  The visible window is the last min(t, max(window, n)) tokens
- *    (all of them when window is 0; the new tokens are always in it): indices[indptr[r] ..) lists its pages,
+ *    (all of them when window is 0; the new tokens are always in it).  It is the
+ *    request's, not a token's: a model's sliding window over several new tokens
+ *    is pa_v2_build_tables_sliding's.  indices[indptr[r] ..) lists its pages,
  *    first_page_offset[r] is the entry it starts at, last_page_len[r] the
  *    entries used of its last page, as the decode calls read them.  A request
  *    with t = 0 has no page.
@@ -667,6 +669,25 @@ pa_status pa_v2_build_tables(const int32_t* cached_lens, const int32_t* new_lens
                              int32_t* first_page_offset, int32_t* qo_indptr, int32_t* slots, int32_t* positions,
                              int64_t token_capacity, int32_t* tree_mask, int32_t mask_words,
                              int32_t* pages_needed, int32_t* status, void* cuda_stream);
+
+/* The same for a model whose tokens see a sliding window of `window` >= 1
+ * positions (PA_EINVAL below): the token at position x sees the keys at
+ * positions x - window + 1 .. x.  pa_v2_build_tables' window is one of the
+ * request, the same last tokens for all its new ones; with one new token per
+ * request the two agree, with several they do not.  Here
+ *  - the page table lists what the request's first new token sees and all new
+ *    tokens: from token max(0, c + 1 - window) on (without a new token, the
+ *    last min(c, window));
+ *  - tree_mask shows a token the nearest window - 1 of its ancestors and itself
+ *    (a chain: of the tokens before it).
+ * pa_v2_tree_attention_sliding reads them. */
+pa_status pa_v2_build_tables_sliding(const int32_t* cached_lens, const int32_t* new_lens, int32_t batch,
+                                     int32_t* block_table, int32_t table_width, const int32_t* free_pages,
+                                     int32_t num_free, const int32_t* parents, int32_t page_size, int32_t window,
+                                     int32_t* indptr, int32_t* indices, int64_t index_capacity,
+                                     int32_t* last_page_len, int32_t* first_page_offset, int32_t* qo_indptr,
+                                     int32_t* slots, int32_t* positions, int64_t token_capacity, int32_t* tree_mask,
+                                     int32_t mask_words, int32_t* pages_needed, int32_t* status, void* cuda_stream);
 
 /* pa_v2_qk_rope_append: what stands between the projections and the attention,
  * in one pass.  For every token t with slots[t] >= 0 and every head:
@@ -742,6 +763,28 @@ pa_status pa_v2_tree_attention(const void* q, const void* k_pool, const void* v_
                                int32_t num_tokens, const int32_t* tree_mask, int32_t mask_words, float sm_scale,
                                void* out, float* lse2_out, void* workspace, int64_t workspace_bytes,
                                int32_t* status, void* cuda_stream);
+
+/* The same under a sliding window of `window` >= 1 positions: of the tokens
+ * before the new ones, those at positions positions[t] - window + 1 and later
+ * are seen by query token t.  positions [num_tokens] int32 as the tables give
+ * them: a request's first new token stands at the number of tokens before it,
+ * and new token i at most i positions behind that.  Of the new tokens a chain
+ * (tree_mask null) shows token i its last `window`, itself included; with a
+ * tree_mask the mask alone decides (pa_v2_build_tables_sliding cuts it).
+ * A request whose page table holds fewer earlier tokens than its first new
+ * token sees, min(positions, window - 1), is refused (PA_DEVICE_BAD_TREE, zeros
+ * and -inf); it may hold more, down to all of them, and pages that lie before
+ * the window are not read.  Every block of query rows meets the request's keys
+ * from its first token's window on.  PA_EINVAL: window below 1, positions null. */
+pa_status pa_v2_tree_attention_sliding(const void* q, const void* k_pool, const void* v_pool, int32_t kv_dtype,
+                                       int64_t num_pages, int32_t page_size, int32_t num_qo_heads,
+                                       int32_t num_kv_heads, int32_t head_dim, const int32_t* indices,
+                                       int64_t num_indices, const int32_t* indptr, const int32_t* last_page_len,
+                                       const int32_t* first_page_offset, int32_t batch, const int32_t* qo_indptr,
+                                       int32_t num_tokens, const int32_t* tree_mask, int32_t mask_words,
+                                       const int32_t* positions, int32_t window, float sm_scale, void* out,
+                                       float* lse2_out, void* workspace, int64_t workspace_bytes, int32_t* status,
+                                       void* cuda_stream);
 
 /* The variable-length merge (issue #898, design piece 3 and Task 3; PR
  * #984, What changed 3).  For output row r and head h, the rows

@@ -3,8 +3,9 @@
 //
 // With c cached and n new tokens, s = page_size, t = c + n (per request):
 //   pages taken    ceil(t/s) - ceil(c/s), handed out from the free list in request order;
-//   window         the last w = min(t, max(window, n)) tokens, from token t - w on;
-//   page list      entries (t-w)/s .. ceil(t/s)-1 of the request's block-table row;
+//   window         the last w = min(t, max(window, n)) tokens, from token t - w on; a sliding window of W: what
+//                  the first new token sees, from token max(0, c + 1 - W) on (c - W without a new token);
+//   page list      entries (that token)/s .. ceil(t/s)-1 of the request's block-table row;
 //   token i        row page((c+i)/s) * s + (c+i) % s, position c + depth(i).
 //
 // Three prefix sums over the requests (pages listed, pages taken, new tokens)
@@ -52,6 +53,7 @@ struct TableParams {
   int32_t* pages_needed;
   int32_t* status;
   int32_t batch, width, num_free, page_size, window, mask_words;
+  int32_t reach;  // sliding window: what a token sees of its line of ancestors, itself included; else 0
   int32_t index_cap, token_cap;
   uint32_t ps_magic, ps_shift;
 };
@@ -84,7 +86,8 @@ __device__ __forceinline__ ReqGeom request_geom(const TableParams& p, int r) {
     g.bad = need > p.width;
     if (!g.bad && t > 0) {
       const int32_t span = max(p.window, n);  // new tokens are always among the visible ones
-      const int32_t start = p.window > 0 && t > span ? t - span : 0;
+      int32_t start = p.window > 0 && t > span ? t - span : 0;
+      if (p.reach > 0) start = max(c + (n > 0 ? 1 : 0) - p.reach, 0);
       g.have = pages_of(p, c);
       g.need = need;
       g.first = (int32_t)fast_div((uint32_t)start, p.ps_magic, p.ps_shift);
@@ -274,13 +277,14 @@ __global__ void __launch_bounds__(kTabThreads) pa_v2_build_tables_kernel(const T
     // ancestors, from the token up: indices fall on the way, so the mask's words come out last to first
     int32_t depth = 0, word = p.mask_words;
     uint32_t bits = 0;
+    const int32_t reach = p.reach > 0 ? p.reach : INT32_MAX;
     int32_t* row = p.tree_mask ? p.tree_mask + t * p.mask_words : nullptr;
     bool bad_tree = row && i >= 32 * p.mask_words;
     if (p.parents || row) {
       int32_t j = i;
       while (true) {
         const int32_t w = j >> 5;
-        if (row && w < p.mask_words) {
+        if (row && w < p.mask_words && depth < reach) {
           while (word > w) {
             if (word < p.mask_words) row[word] = (int32_t)bits;
             bits = 0;
@@ -314,17 +318,13 @@ __global__ void __launch_bounds__(kTabThreads) pa_v2_build_tables_kernel(const T
   }
 }
 
-}  // namespace
-}  // namespace pa
-
-extern "C" pa_status pa_v2_build_tables(const int32_t* cached_lens, const int32_t* new_lens, int32_t batch,
-                                        int32_t* block_table, int32_t table_width, const int32_t* free_pages,
-                                        int32_t num_free, const int32_t* parents, int32_t page_size, int32_t window,
-                                        int32_t* indptr, int32_t* indices, int64_t index_capacity,
-                                        int32_t* last_page_len, int32_t* first_page_offset, int32_t* qo_indptr,
-                                        int32_t* slots, int32_t* positions, int64_t token_capacity,
-                                        int32_t* tree_mask, int32_t mask_words, int32_t* pages_needed,
-                                        int32_t* status, void* cuda_stream) {
+pa_status build_tables(const int32_t* cached_lens, const int32_t* new_lens, int32_t batch, int32_t* block_table,
+                       int32_t table_width, const int32_t* free_pages, int32_t num_free, const int32_t* parents,
+                       int32_t page_size, int32_t window, int32_t reach, int32_t* indptr, int32_t* indices,
+                       int64_t index_capacity, int32_t* last_page_len, int32_t* first_page_offset,
+                       int32_t* qo_indptr, int32_t* slots, int32_t* positions, int64_t token_capacity,
+                       int32_t* tree_mask, int32_t mask_words, int32_t* pages_needed, int32_t* status,
+                       void* cuda_stream) {
   if (batch < 0 || table_width < 0 || num_free < 0 || page_size < 1 || window < 0 || index_capacity < 0 ||
       token_capacity < 0 || mask_words < 0 || !indptr || !qo_indptr || !pages_needed)
     return PA_EINVAL;
@@ -339,7 +339,7 @@ extern "C" pa_status pa_v2_build_tables(const int32_t* cached_lens, const int32_
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return PA_ECUDA;
-  pa::TableParams p;
+  TableParams p;
   p.cached = cached_lens;
   p.fresh = new_lens;
   p.free_pages = free_pages;
@@ -360,19 +360,52 @@ extern "C" pa_status pa_v2_build_tables(const int32_t* cached_lens, const int32_
   p.num_free = num_free;
   p.page_size = page_size;
   p.window = window;
+  p.reach = reach;
   p.mask_words = mask_words;
   p.index_cap = (int32_t)index_capacity;
   p.token_cap = (int32_t)token_capacity;
-  const pa::FastDiv fd = pa::FastDiv::make((uint32_t)page_size);
+  const FastDiv fd = FastDiv::make((uint32_t)page_size);
   p.ps_magic = fd.magic;
   p.ps_shift = fd.shift;
   const size_t smem = 3 * ((size_t)batch + 1) * sizeof(int32_t);
   constexpr size_t kMaxSmem = 3 * (PA_V2_MAX_TABLE_BATCH + 1) * sizeof(int32_t);
-  if (!pa::prepare_kernel(reinterpret_cast<const void*>(pa::pa_v2_build_tables_kernel), kMaxSmem)) return PA_ECUDA;
+  if (!prepare_kernel(reinterpret_cast<const void*>(pa_v2_build_tables_kernel), kMaxSmem)) return PA_ECUDA;
   const int64_t work = index_capacity / 8 > token_capacity ? index_capacity / 8 : token_capacity;
-  const int64_t want = (work + pa::kTabThreads - 1) / pa::kTabThreads;
+  const int64_t want = (work + kTabThreads - 1) / kTabThreads;
   const int blocks = (int)(want < 1 ? 1 : want < sms ? want : sms);
-  const cudaError_t rc = pa::launch_dependent(pa::pa_v2_build_tables_kernel, dim3(blocks), dim3(pa::kTabThreads),
-                                              smem, static_cast<cudaStream_t>(cuda_stream), p);
+  const cudaError_t rc = launch_dependent(pa_v2_build_tables_kernel, dim3(blocks), dim3(kTabThreads), smem,
+                                          static_cast<cudaStream_t>(cuda_stream), p);
   return rc == cudaSuccess && cudaGetLastError() == cudaSuccess ? PA_OK : PA_ECUDA;
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" pa_status pa_v2_build_tables(const int32_t* cached_lens, const int32_t* new_lens, int32_t batch,
+                                        int32_t* block_table, int32_t table_width, const int32_t* free_pages,
+                                        int32_t num_free, const int32_t* parents, int32_t page_size, int32_t window,
+                                        int32_t* indptr, int32_t* indices, int64_t index_capacity,
+                                        int32_t* last_page_len, int32_t* first_page_offset, int32_t* qo_indptr,
+                                        int32_t* slots, int32_t* positions, int64_t token_capacity,
+                                        int32_t* tree_mask, int32_t mask_words, int32_t* pages_needed,
+                                        int32_t* status, void* cuda_stream) {
+  return pa::build_tables(cached_lens, new_lens, batch, block_table, table_width, free_pages, num_free, parents,
+                          page_size, window, 0, indptr, indices, index_capacity, last_page_len, first_page_offset,
+                          qo_indptr, slots, positions, token_capacity, tree_mask, mask_words, pages_needed, status,
+                          cuda_stream);
+}
+
+extern "C" pa_status pa_v2_build_tables_sliding(const int32_t* cached_lens, const int32_t* new_lens, int32_t batch,
+                                                int32_t* block_table, int32_t table_width,
+                                                const int32_t* free_pages, int32_t num_free, const int32_t* parents, int32_t page_size,
+                                                int32_t window, int32_t* indptr, int32_t* indices, int64_t index_capacity,
+                                                int32_t* last_page_len, int32_t* first_page_offset, int32_t* qo_indptr,
+                                                int32_t* slots, int32_t* positions, int64_t token_capacity,
+                                                int32_t* tree_mask, int32_t mask_words, int32_t* pages_needed,
+                                                int32_t* status, void* cuda_stream) {
+  if (window < 1) return PA_EINVAL;
+  return pa::build_tables(cached_lens, new_lens, batch, block_table, table_width, free_pages, num_free, parents,
+                          page_size, 0, window, indptr, indices, index_capacity, last_page_len, first_page_offset,
+                          qo_indptr, slots, positions, token_capacity, tree_mask, mask_words, pages_needed, status,
+                          cuda_stream);
 }

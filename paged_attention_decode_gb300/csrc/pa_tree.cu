@@ -5,7 +5,10 @@
 // Query token i of request r sees the L - n earlier visible tokens and the new
 // tokens its mask row (or the chain rule j <= i) allows:
 //   s = scale log2(e) q . k,  out = sum 2^(s - m) v / sum 2^(s - m),
-// one pass over the keys with a running maximum m and sum in f32.
+// one pass over the keys with a running maximum m and sum in f32.  Under a sliding window
+// of W a token at depth d below its request's first one sees of the earlier tokens the
+// last W - 1 - d: the request's keys begin where its first token's window does, and up to
+// where its last token's can begin each row has an edge of its own.
 //
 // Work.  The query rows of a KV head are its n * G (token, head) pairs; a block
 // of up to 256 of them meets the request's keys in tiles of 128 pool rows (page
@@ -34,10 +37,11 @@
 //    pages takes a thread about 1000 cycles), or cp.async by both for page sizes
 //    whose pages do not start on 8-row boundaries; both walk the CTA's share of
 //    the work, and warp 9 hands its pieces to the other roles;
-//  - warp 11: makes V tiles that hold rows outside the visible range or new
-//    tokens safe: 0 * NaN is NaN, so what a mask hides must not be left in V.
-//    Outside rows become zeros; non-finite elements of new tokens become zeros
-//    and are added back, in the epilogue, to the rows that do see them.
+//  - warp 11: makes V tiles that hold rows outside the visible range, or rows that
+//    not every new token sees, safe: 0 * NaN is NaN, so what a mask or a window hides
+//    must not be left in V.  Outside rows become zeros; non-finite elements of the
+//    others become zeros and are added back, in the epilogue, to the rows that do see
+//    them.
 //
 // What bounds it.  A tile of two streams of 128 rows is 2500 cycles of products
 // (S and PV, D = 128, at the cuBLAS burst rate) and, from HBM, 2900 cycles of K
@@ -124,6 +128,7 @@ struct TreeParams {
   const int32_t* first_page_offset;
   const int32_t* qo_indptr;
   const int32_t* tree_mask;
+  const int32_t* positions;
   void* out;
   float* lse_out;
   float* slots;    // partial results: kTrSlots * ctas
@@ -135,8 +140,16 @@ struct TreeParams {
   float scale_log2;   // |sm_scale| * log2(e), or 1 for a zero scale
   uint32_t q_xor;     // sign flip of both halves of a q word for a negative scale
   uint32_t q_and;     // 0 for a zero scale
+  int32_t window;     // sliding window, 0 for none
   int32_t small;      // the batch's requests fit a warp's lanes and all units 32 bits
 };
+
+// The sliding window, in kernels that know one: the others are compiled without it (its rows' edges cost 8 tokens over
+// 1K 0.8 us of 15.2, and 4 x 256 tokens over 32K 1 %).
+template <bool SLIDING>
+__device__ __forceinline__ int32_t window_of(const TreeParams& p) {
+  return SLIDING ? p.window : 0;
+}
 
 // One request's share of the work.
 struct TreeReq {
@@ -159,8 +172,10 @@ __device__ __forceinline__ int32_t tail_of(const TreeReq& g, int group, int b) {
   return (g.ds + tok + kTrTile - 1) / kTrTile - g.tile0 - g.common;
 }
 
+template <bool SLIDING>
 __device__ __forceinline__ TreeReq tree_req(const TreeParams& p, int r, bool tell) {
   TreeReq g = {};
+  const int32_t window = window_of<SLIDING>(p);
   const int32_t a = p.qo_indptr[r], b = p.qo_indptr[r + 1];
   const int32_t s0 = p.indptr[r], s1 = p.indptr[r + 1];
   const int32_t lpl = p.last_page_len[r], fpo = p.first_page_offset[r];
@@ -183,14 +198,17 @@ __device__ __forceinline__ TreeReq tree_req(const TreeParams& p, int r, bool tel
     return g;
   }
   const int32_t hi = pages > 0 ? ((int32_t)pages - 1) * p.page_size + lpl : 0;
-  const int32_t tile0 = fpo / kTrTile;
+  // a sliding window: the first row its first token sees
+  const int32_t lo = window > 0 ? max(fpo, hi - g.n - window + 1) : fpo;
+  const int32_t tile0 = lo / kTrTile;
   const int32_t all = (hi + kTrTile - 1) / kTrTile - tile0;
   if (pages == 0 || lpl < 1 || lpl > p.page_size || fpo < 0 || fpo >= p.page_size || hi - fpo < g.n ||
-      (p.tree_mask && g.n > 32 * p.mask_words) || (int64_t)g.blocks * (all + kTrCost2) > INT32_MAX) {
+      (p.tree_mask && g.n > 32 * p.mask_words) || (int64_t)g.blocks * (all + kTrCost2) > INT32_MAX ||
+      (window > 0 && hi - fpo - g.n < min(p.positions[a], window - 1))) {
     if (tell) report(p.status, PA_DEVICE_BAD_TREE);
     return g;
   }
-  g.lo = fpo;
+  g.lo = lo;
   g.hi = hi;
   g.ds = hi - g.n;
   g.tile0 = tile0;
@@ -324,14 +342,14 @@ __device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* warp_sum, in
 }
 
 // The same for any batch, by every thread of the block (each a run of consecutive requests).
-template <int THREADS>
+template <int THREADS, bool SLIDING>
 __device__ __forceinline__ void cut_block(const TreeParams& p, int c, bool tell, TreeCut* out,
                                           int64_t* warp_sum) {
   const int per = (p.batch + THREADS - 1) / THREADS;
   const int r0 = (int)min((int64_t)threadIdx.x * per, (int64_t)p.batch), r1 = min(r0 + per, p.batch);
   int64_t tiles = 0, cost = 0;
   for (int r = r0; r < r1; ++r) {
-    const TreeReq g = tree_req(p, r, tell);
+    const TreeReq g = tree_req<SLIDING>(p, r, tell);
     tiles += (int64_t)g.units * p.hkv;
     cost += (int64_t)g.blocks * g.cost * p.hkv;
   }
@@ -342,7 +360,7 @@ __device__ __forceinline__ void cut_block(const TreeParams& p, int c, bool tell,
   t.run = run_of(all_tiles, all_cost, p.ctas);
   int64_t chunks = 0, weight = 0;
   for (int r = r0; r < r1; ++r) {
-    const HeadCut h = head_cut(tree_req(p, r, false), p.group, t.run);
+    const HeadCut h = head_cut(tree_req<SLIDING>(p, r, false), p.group, t.run);
     chunks += (int64_t)h.chunks * p.hkv;
     weight += (int64_t)h.weight * p.hkv;
   }
@@ -359,7 +377,7 @@ __device__ __forceinline__ void cut_block(const TreeParams& p, int c, bool tell,
   t.off = t.r_weight = t.r_chunks = 0;
   if (at >= begin && at < begin + mine) {
     for (t.r = r0; t.r < r1; ++t.r) {
-      const HeadCut h = head_cut(tree_req(p, t.r, false), p.group, t.run);
+      const HeadCut h = head_cut(tree_req<SLIDING>(p, t.r, false), p.group, t.run);
       const int64_t u = (int64_t)(chunk ? h.chunks : h.weight) * p.hkv;
       t.off = at - (chunk ? chunks_at : weight_at);
       if (t.off < u) break;
@@ -435,17 +453,18 @@ struct TreePiece {
   int32_t kind;            // 0: no more, 1: key tiles, 2: nothing visible
   int32_t tile, tiles;     // key tiles [tile, tile + tiles)
   int32_t lo, hi, ds;
-  int32_t t0, n;
+  int32_t all;             // rows [all, ds) are seen by every new token
+  int32_t t0;
   int32_t slot_base;       // the request's first page-table slot
   int32_t row0, rows;      // query rows [row0, row0 + rows) of the request
   int32_t kvh, slot;       // slot < 0: the whole block, written as the result
-  int32_t tainted;         // set by the fix warp: a visible new token has a non-finite value
+  int32_t tainted;         // set by the fix warp: it took non-finite values out of V
 };
 
 constexpr int kPieceEnd = 0, kPieceTiles = 1, kPieceEmpty = 2;
 
 __device__ __forceinline__ bool needs_fix(const TreePiece& d, int tile) {
-  return tile * kTrTile < d.lo || (tile + 1) * kTrTile > d.ds;
+  return tile * kTrTile < d.all || (tile + 1) * kTrTile > d.ds;
 }
 
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
@@ -460,11 +479,22 @@ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
   return (b >= 32 ? 0xffffffffu : ((1u << b) - 1u)) & ~((1u << a) - 1u);
 }
 
-// Which of the keys base .. base+31 (page order) a query token sees: token `token` of the batch, new token i of a
-// request whose visible rows are [lo, hi) and whose new tokens are [ds, hi).
-__device__ __forceinline__ uint32_t visible_bits(const TreeParams& p, int lo, int ds, int hi, int token, int i,
+// The first row that a query token sees: token `token` of the batch, new token i of a request whose visible rows
+// begin at lo and whose new tokens begin at ds.  A sliding window of W ends W - 1 - depth rows before ds, the depth (at
+// most i) being how far the token's position lies behind the request's first new token's.
+template <bool SLIDING>
+__device__ __forceinline__ int first_seen(const TreeParams& p, int lo, int ds, int token, int i) {
+  if (!SLIDING) return lo;
+  const int depth = p.tree_mask ? min(max(__ldg(p.positions + token) - __ldg(p.positions + token - i), 0), i) : i;
+  return max(lo, ds + (depth + 1 - p.window));
+}
+
+// Which of the keys base .. base+31 (page order) it sees, from row `low` on, its request's visible rows ending at hi.
+// (Of the new tokens a tree's mask holds the window's cut itself.)
+template <bool SLIDING>
+__device__ __forceinline__ uint32_t visible_bits(const TreeParams& p, int low, int ds, int hi, int token, int i,
                                                  int base) {
-  uint32_t bits = bit_range(lo - base, ds - base);
+  uint32_t bits = bit_range(low - base, ds - base);
   if (base + 32 > ds && base < hi) {
     if (p.tree_mask) {
       const int32_t* row = p.tree_mask + (int64_t)token * p.mask_words;
@@ -474,7 +504,7 @@ __device__ __forceinline__ uint32_t visible_bits(const TreeParams& p, int lo, in
       const uint32_t x1 = w + 1 >= 0 && w + 1 < p.mask_words ? (uint32_t)__ldg(row + w + 1) : 0u;
       bits |= __funnelshift_r(x0, x1, sh) & bit_range(ds - base, hi - base);
     } else {
-      bits |= bit_range(ds - base, min(ds + i + 1, hi) - base);
+      bits |= bit_range((SLIDING ? max(ds, low) : ds) - base, min(ds + i + 1, hi) - base);
     }
   }
   return bits;
@@ -522,15 +552,17 @@ __device__ __forceinline__ float half_of(const __nv_bfloat16* x) { return __bflo
 // No key was visible to the row (a NaN sum stays NaN).
 __device__ __forceinline__ bool nothing_seen(float l) { return l == 0.f; }
 
-// The non-finite values of new tokens that the fix warp took out of V, back into the O of the rows that see them
-// (a converged warp: called under a condition that is the same for all its lanes; query token tok of the piece's
-// request on this thread's lane).  Where two streams were joined, y is stream B's O of this row (D / 4 quads, kTrTile
-// apart), and O becomes o s0 + y s1 first: an infinity added before would meet s0 = 0 in a row whose keys are all
-// stream B's, and 0 times it is NaN.
-template <typename T, int D>
+// The non-finite values that the fix warp took out of V (of rows that not every new token sees), back into the O of
+// the rows that see them (a converged warp: called under a condition that is the same for all its lanes; query token
+// tok of the piece's request on this thread's lane).  Where two streams were joined, y is stream B's O of this row
+// (D / 4 quads, kTrTile apart), and O becomes o s0 + y s1 first: an infinity added before would meet s0 = 0 in a row
+// whose keys are all stream B's, and 0 times it is NaN.
+template <typename T, int D, bool SLIDING>
 __device__ __noinline__ void put_back(const TreeParams& p, const TreePiece& d, int tok, uint32_t t_o, const float4* y,
                                       float s0, float s1) {
-  const int k0 = max(d.tile * kTrTile, d.ds), k1 = min((d.tile + d.tiles) * kTrTile, d.hi);
+  // of the rows that not every token sees, [lo, all) and [ds, hi)
+  const int k0 = max(d.tile * kTrTile, d.lo), k1 = min((d.tile + d.tiles) * kTrTile, d.hi);
+  const int low = first_seen<SLIDING>(p, d.lo, d.ds, d.t0 + tok, tok);
   for (int c = 0; c < D / 32; ++c) {
     uint32_t o[32];
     __syncwarp();
@@ -546,7 +578,9 @@ __device__ __noinline__ void put_back(const TreeParams& p, const TreePiece& d, i
       }
     }
     for (int k = k0; k < k1; ++k) {
-      if (!(visible_bits(p, d.lo, d.ds, d.hi, d.t0 + tok, tok, k) & 1u)) continue;
+      if (k >= d.all && k < d.ds) k = d.ds;
+      if (k >= k1) break;
+      if (!(visible_bits<SLIDING>(p, low, d.ds, d.hi, d.t0 + tok, tok, k) & 1u)) continue;
       const int sl = (int)fast_div((uint32_t)k, p.ps_magic, p.ps_shift);
       const int32_t page = __ldg(p.indices + d.slot_base + sl);
       if (page < 0 || page >= p.num_pages) continue;
@@ -563,7 +597,7 @@ __device__ __noinline__ void put_back(const TreeParams& p, const TreePiece& d, i
   }
 }
 
-template <typename T, int D, bool TMA>
+template <typename T, int D, bool TMA, bool SLIDING>
 __global__ void __launch_bounds__(kTrThreads, 1)
     pa_v2_tree_attention_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tm_k,
                                 const __grid_constant__ CUtensorMap tm_v) {
@@ -641,7 +675,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   const uint32_t tmem = *tmem_slot;
   // the loader warp finds the CTA's place alone when a request fits a lane, else all threads do
   const bool small = p.small != 0;
-  if (!small) cut_block<kTrThreads>(p, blockIdx.x, blockIdx.x == 0, start, warp_sum);
+  if (!small) cut_block<kTrThreads, SLIDING>(p, blockIdx.x, blockIdx.x == 0, start, warp_sum);
 
   // Registers follow the roles: 208 for the softmax threads, which hold a row of scores, 88 for the others
   // (256 * 208 + 128 * 88 = 384 * 168).  Each warpgroup sets its own count on its own path.
@@ -709,7 +743,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           if (lane == 0) mbar_arrive(b_q);
         }
         // ---- key tiles
-        const int tiles = d.tiles, tile0 = d.tile, clear0 = d.lo, clear1 = d.ds;  // no mask inside [clear0, clear1)
+        const int tiles = d.tiles, tile0 = d.tile, clear0 = d.all, clear1 = d.ds;  // no mask inside [clear0, clear1)
+        const int low = first_seen<SLIDING>(p, d.lo, clear1, d.t0 + tok, tok);
         for (int j = dual ? 0 : w; j < tiles; j += dual ? 1 : 2) {
           if (!wait_phase(&b_s[w], par_s, abort_flag, p.status)) {
             alive = false;
@@ -730,7 +765,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
               const int hi = d.hi, t0 = d.t0;
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                const uint32_t vis = visible_bits(p, clear0, clear1, hi, t0 + tok, tok, c0 + 32 * c);
+                const uint32_t vis = visible_bits<SLIDING>(p, low, clear1, hi, t0 + tok, tok, c0 + 32 * c);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                   x[c >> 1][(c & 1) * 32 + i] = (vis >> i) & 1u ? x[c >> 1][(c & 1) * 32 + i] : 0xff800000u;
@@ -840,7 +875,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         // (the whole warp or none of it: tensor memory is read and written by converged warps only, and rows that see
         // nothing in this piece stand beside rows that do)
         const bool mended = kind == kPieceTiles && d.tainted != 0;
-        if (mended) put_back<T, D>(p, ring[at], tok, t_o, joined ? xo + row : nullptr, s0, s1);
+        if (mended) put_back<T, D, SLIDING>(p, ring[at], tok, t_o, joined ? xo + row : nullptr, s0, s1);
         const bool valid = rr < rows, whole = d.slot < 0;
         const int qrow = d.row0 + min(rr, rows - 1);  // row of the request
         const int64_t orow = (int64_t)(d.t0 + tok) * p.hq + (int64_t)d.kvh * p.group + (qrow - tok * p.group);
@@ -904,7 +939,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       TreeReq mine = {};
       TreeCut cut;
       if (small) {
-        if (lane < p.batch) mine = tree_req(p, lane, leader && blockIdx.x == 0);
+        if (lane < p.batch) mine = tree_req<SLIDING>(p, lane, leader && blockIdx.x == 0);
         cut = cut_warp(p, blockIdx.x, mine, lane);
       } else {
         cut = *start;
@@ -947,11 +982,12 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             const int at = row0 + lane * box_rows;
             const int slot = (int)fast_div((uint32_t)at, p.ps_magic, p.ps_shift);
             const int32_t page = __ldg(p.indices + g.slot_base + slot);
-            if (page >= 0 && page < p.num_pages) {
+            if (page >= 0 && page < p.num_pages && (!SLIDING || at + box_rows > g.lo)) {
               mine_row = page * p.page_size + (at - slot * p.page_size);
             } else {
-              mine_row = (int32_t)(p.num_pages * p.page_size);  // past the pool: the box is zero-filled
-              if (!is_v) report(p.status, PA_DEVICE_BAD_PAGE);
+              // past the pool: the box is zero-filled (as are boxes before a sliding window, whose pages may be gone)
+              mine_row = (int32_t)(p.num_pages * p.page_size);
+              if (!is_v && (!SLIDING || at + box_rows > g.lo)) report(p.status, PA_DEVICE_BAD_PAGE);
             }
           }
           volatile int32_t* box_row = rows_of[u >> 5];
@@ -1035,8 +1071,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         d.lo = g.lo;
         d.hi = g.hi;
         d.ds = g.ds;
+        d.all = SLIDING ? max(g.lo, min(g.ds, g.hi - p.window)) : g.lo;
         d.t0 = g.t0;
-        d.n = g.n;
         d.slot_base = g.slot_base;
         d.row0 = b * kTrBlock;
         d.rows = min(kTrBlock, g.n * p.group - d.row0);
@@ -1090,7 +1126,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 
       int r = cut.r;
       if (r < p.batch && (int)blockIdx.x < cut.chunks) {
-        g = small ? shfl_req(mine, r) : tree_req(p, r, false);
+        g = small ? shfl_req(mine, r) : tree_req<SLIDING>(p, r, false);
         const HeadCut h = head_cut(g, p.group, run);
         const int kvh = (int)div_units(cut.off, h.chunks);
         const BlockAt k = block_at(g, p.group, run, (int32_t)(cut.off - (int64_t)kvh * h.chunks), true);
@@ -1104,7 +1140,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                                     cut.weight - (int64_t)((int)blockIdx.x - cut.chunks) * cut.stretch);
         int chunks_before = cut.r_chunks;
         for (; r < p.batch && left > 0 && alive; ++r, off = 0) {
-          g = small ? shfl_req(mine, r) : tree_req(p, r, false);
+          g = small ? shfl_req(mine, r) : tree_req<SLIDING>(p, r, false);
           const HeadCut h = head_cut(g, p.group, run);
           int kvh = h.weight > 0 ? (int)div_units(off, h.weight) : p.hkv;
           int32_t in_head = (int32_t)(off - (int64_t)kvh * h.weight);
@@ -1334,9 +1370,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 }
               }
             };
-            // rows of the tile: outside, earlier tokens (left alone), new tokens, outside
+            // rows of the tile: outside, earlier tokens that only some see, that all see (left alone), new tokens,
+            // outside
             const int in0 = min(max(d.lo - c0, 0), kTrTile), in1 = min(max(d.hi - c0, in0), kTrTile);
             zero_rows(0, in0);
+            if (SLIDING) check_rows(in0, min(max(d.all - c0, in0), kTrTile));
             check_rows(min(max(d.ds - c0, in0), in1), in1);
             zero_rows(in1, kTrTile);
             if (__any_sync(0xffffffffu, any != 0) && lane == 0)
@@ -1469,10 +1507,14 @@ bool aligned16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) ==
 using TreeKernel = void (*)(const TreeParams, const CUtensorMap, const CUtensorMap);
 using MergeKernel = void (*)(const TreeParams);
 
+template <typename T, int D, bool TMA>
+TreeKernel pick_window(bool sliding) {
+  return sliding ? pa_v2_tree_attention_kernel<T, D, TMA, true> : pa_v2_tree_attention_kernel<T, D, TMA, false>;
+}
 template <typename T>
-TreeKernel pick_tree(int D, bool tma) {
-  if (D == 64) return tma ? pa_v2_tree_attention_kernel<T, 64, true> : pa_v2_tree_attention_kernel<T, 64, false>;
-  return tma ? pa_v2_tree_attention_kernel<T, 128, true> : pa_v2_tree_attention_kernel<T, 128, false>;
+TreeKernel pick_tree(int D, bool tma, bool sliding) {
+  if (D == 64) return tma ? pick_window<T, 64, true>(sliding) : pick_window<T, 64, false>(sliding);
+  return tma ? pick_window<T, 128, true>(sliding) : pick_window<T, 128, false>(sliding);
 }
 
 int64_t slots_bytes(int32_t ctas, int32_t head_dim) {
@@ -1508,14 +1550,17 @@ extern "C" pa_status pa_v2_tree_attention_workspace(int32_t device, int32_t num_
   return PA_OK;
 }
 
-extern "C" pa_status pa_v2_tree_attention(const void* q, const void* k_pool, const void* v_pool, int32_t kv_dtype,
-                                          int64_t num_pages, int32_t page_size, int32_t num_qo_heads,
-                                          int32_t num_kv_heads, int32_t head_dim, const int32_t* indices,
-                                          int64_t num_indices, const int32_t* indptr, const int32_t* last_page_len,
-                                          const int32_t* first_page_offset, int32_t batch, const int32_t* qo_indptr,
-                                          int32_t num_tokens, const int32_t* tree_mask, int32_t mask_words,
-                                          float sm_scale, void* out, float* lse2_out, void* workspace,
-                                          int64_t workspace_bytes, int32_t* status, void* cuda_stream) {
+namespace pa {
+namespace {
+
+// window 0: none, and positions are not read.
+pa_status tree_attention(const void* q, const void* k_pool, const void* v_pool, int32_t kv_dtype, int64_t num_pages,
+                         int32_t page_size, int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+                         const int32_t* indices, int64_t num_indices, const int32_t* indptr,
+                         const int32_t* last_page_len, const int32_t* first_page_offset, int32_t batch,
+                         const int32_t* qo_indptr, int32_t num_tokens, const int32_t* tree_mask, int32_t mask_words,
+                         const int32_t* positions, int32_t window, float sm_scale, void* out, float* lse2_out,
+                         void* workspace, int64_t workspace_bytes, int32_t* status, void* cuda_stream) {
   if (num_tokens < 0 || batch < 0 || num_kv_heads < 1 || num_qo_heads < num_kv_heads ||
       num_qo_heads % num_kv_heads || page_size < 1 || num_pages < 1 || num_indices < 0 || mask_words < 0 ||
       (tree_mask && mask_words < 1) || !std::isfinite(sm_scale))
@@ -1525,13 +1570,13 @@ extern "C" pa_status pa_v2_tree_attention(const void* q, const void* k_pool, con
   if (page_size > 256 || (page_size > 16 && page_size % 16 != 0)) return PA_EUNSUPPORTED;
   if (num_pages >= (1ll << 31) || num_pages * page_size >= (1ll << 31)) return PA_EUNSUPPORTED;
   if (tree_mask && mask_words > PA_V2_MAX_MASK_WORDS) return PA_EUNSUPPORTED;
-  if ((int64_t)num_tokens * (num_qo_heads / num_kv_heads) > INT32_MAX - 2 * pa::kTrBlock) return PA_EUNSUPPORTED;
+  if ((int64_t)num_tokens * (num_qo_heads / num_kv_heads) > INT32_MAX - 2 * kTrBlock) return PA_EUNSUPPORTED;
   if (num_tokens == 0 || batch == 0) return PA_OK;
   if (!q || !k_pool || !v_pool || !indptr || !last_page_len || !first_page_offset || !qo_indptr || !out ||
-      !lse2_out || !workspace || (num_indices > 0 && !indices))
+      !lse2_out || !workspace || (num_indices > 0 && !indices) || (window > 0 && !positions))
     return PA_EINVAL;
   for (const void* x : {q, k_pool, v_pool, static_cast<const void*>(out), static_cast<const void*>(workspace)})
-    if (!pa::aligned16(x)) return PA_EINVAL;
+    if (!aligned16(x)) return PA_EINVAL;
   int dev = 0;
   int64_t need = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PA_ECUDA;
@@ -1542,17 +1587,17 @@ extern "C" pa_status pa_v2_tree_attention(const void* q, const void* k_pool, con
   alignas(64) CUtensorMap tm_k, tm_v;
   std::memset(&tm_k, 0, sizeof(tm_k));
   std::memset(&tm_v, 0, sizeof(tm_v));
-  const bool tma = pa::tc_uses_tma(page_size);
+  const bool tma = tc_uses_tma(page_size);
   int box_rows = 8;  // rows of a TMA box: the largest power of two that divides a page, up to a whole tile
-  while (box_rows < pa::kTrTile && page_size % (2 * box_rows) == 0) box_rows *= 2;
+  while (box_rows < kTrTile && page_size % (2 * box_rows) == 0) box_rows *= 2;
   if (tma) {
-    if (!pa::make_pool_map(&tm_k, k_pool, kv_dtype, num_pages * page_size, num_kv_heads, head_dim, 64, box_rows,
+    if (!make_pool_map(&tm_k, k_pool, kv_dtype, num_pages * page_size, num_kv_heads, head_dim, 64, box_rows,
                            CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !pa::make_pool_map(&tm_v, v_pool, kv_dtype, num_pages * page_size, num_kv_heads, head_dim, 64, box_rows,
+        !make_pool_map(&tm_v, v_pool, kv_dtype, num_pages * page_size, num_kv_heads, head_dim, 64, box_rows,
                            CU_TENSOR_MAP_SWIZZLE_128B))
       return PA_ECUDA;
   }
-  pa::TreeParams p;
+  TreeParams p;
   std::memset(&p, 0, sizeof(p));
   p.q = q;
   p.k_pool = k_pool;
@@ -1571,16 +1616,18 @@ extern "C" pa_status pa_v2_tree_attention(const void* q, const void* k_pool, con
   p.num_indices = num_indices;
   p.batch = batch;
   p.num_tokens = num_tokens;
+  p.positions = positions;
+  p.window = window;
   p.mask_words = mask_words;
   p.page_size = page_size;
   p.box_rows = box_rows;
   p.hq = num_qo_heads;
   p.hkv = num_kv_heads;
   p.group = num_qo_heads / num_kv_heads;
-  const pa_status sm = pa::tree_ctas(dev, &p.ctas);
+  const pa_status sm = tree_ctas(dev, &p.ctas);
   if (sm != PA_OK) return sm;
-  p.folds = reinterpret_cast<pa::TreeFold*>(static_cast<char*>(workspace) + pa::slots_bytes(p.ctas, head_dim));
-  const pa::FastDiv fd = pa::FastDiv::make((uint32_t)page_size), fg = pa::FastDiv::make((uint32_t)p.group);
+  p.folds = reinterpret_cast<TreeFold*>(static_cast<char*>(workspace) + slots_bytes(p.ctas, head_dim));
+  const FastDiv fd = FastDiv::make((uint32_t)page_size), fg = FastDiv::make((uint32_t)p.group);
   p.ps_magic = fd.magic;
   p.ps_shift = fd.shift;
   p.g_magic = fg.magic;
@@ -1588,33 +1635,65 @@ extern "C" pa_status pa_v2_tree_attention(const void* q, const void* k_pool, con
   // the work's units at most, for tables that list every page and token once: every block of the batch against every
   // key tile.  The blocks' starting costs are at most 6 / batch times that, and a broken table can claim all of it
   // again for each of 32 requests: (32 + 6) * 2^25 still fits 31 bits.
-  const double units = ((double)num_indices * page_size / pa::kTrTile + 2.0 * batch) *
-                       ((double)num_tokens * p.group / pa::kTrBlock + batch) * num_kv_heads;
+  const double units = ((double)num_indices * page_size / kTrTile + 2.0 * batch) *
+                       ((double)num_tokens * p.group / kTrBlock + batch) * num_kv_heads;
   p.small = batch <= 32 && units < (double)(1 << 25);
   const bool flat = std::fabs(sm_scale) < 1e-30f;  // every score is zero
   p.scale_log2 = flat ? 1.f : std::fabs(sm_scale) * 1.4426950408889634f;
   p.q_xor = sm_scale < 0.f ? 0x80008000u : 0u;
   p.q_and = flat ? 0u : 0xffffffffu;
   const bool f16 = kv_dtype == PA_F16;
-  const int smem = head_dim == 64 ? pa::TreeCfg<64>::kSmemAlloc : pa::TreeCfg<128>::kSmemAlloc;
-  const pa::TreeKernel fn = f16 ? pa::pick_tree<__half>(head_dim, tma) : pa::pick_tree<__nv_bfloat16>(head_dim, tma);
-  if (!pa::prepare_kernel(reinterpret_cast<const void*>(fn), smem)) return PA_ECUDA;
+  const int smem = head_dim == 64 ? TreeCfg<64>::kSmemAlloc : TreeCfg<128>::kSmemAlloc;
+  const TreeKernel fn = f16 ? pick_tree<__half>(head_dim, tma, window > 0)
+                            : pick_tree<__nv_bfloat16>(head_dim, tma, window > 0);
+  if (!prepare_kernel(reinterpret_cast<const void*>(fn), smem)) return PA_ECUDA;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
   // Not a programmatic dependent: its CTAs want an SM each, and taking the SMs as the kernel before it frees them puts
   // the blocks that share keys far apart (16 ragged requests behind the q/k preparation: a step of 128 us, 150 with
   // the early launch).
-  fn<<<dim3(p.ctas), dim3(pa::kTrThreads), smem, stream>>>(p, tm_k, tm_v);
+  fn<<<dim3(p.ctas), dim3(kTrThreads), smem, stream>>>(p, tm_k, tm_v);
   if (cudaGetLastError() != cudaSuccess) return PA_ECUDA;
-  const pa::MergeKernel merge =
-      f16 ? (head_dim == 64 ? pa::pa_v2_tree_merge_kernel<__half, 64> : pa::pa_v2_tree_merge_kernel<__half, 128>)
-          : (head_dim == 64 ? pa::pa_v2_tree_merge_kernel<__nv_bfloat16, 64>
-                            : pa::pa_v2_tree_merge_kernel<__nv_bfloat16, 128>);
+  const MergeKernel merge =
+      f16 ? (head_dim == 64 ? pa_v2_tree_merge_kernel<__half, 64> : pa_v2_tree_merge_kernel<__half, 128>)
+          : (head_dim == 64 ? pa_v2_tree_merge_kernel<__nv_bfloat16, 64>
+                            : pa_v2_tree_merge_kernel<__nv_bfloat16, 128>);
   if (p.ctas > 1) {
-    const cudaError_t rc = pa::launch_dependent(merge, dim3(p.ctas, 4), dim3(pa::kMergeThreads), 0, stream, p);
+    const cudaError_t rc = launch_dependent(merge, dim3(p.ctas, 4), dim3(kMergeThreads), 0, stream, p);
     if (rc != cudaSuccess) {
       cudaGetLastError();
       return PA_ECUDA;
     }
   }
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ECUDA;
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" pa_status pa_v2_tree_attention(const void* q, const void* k_pool, const void* v_pool, int32_t kv_dtype,
+                                          int64_t num_pages, int32_t page_size, int32_t num_qo_heads,
+                                          int32_t num_kv_heads, int32_t head_dim, const int32_t* indices,
+                                          int64_t num_indices, const int32_t* indptr, const int32_t* last_page_len,
+                                          const int32_t* first_page_offset, int32_t batch, const int32_t* qo_indptr,
+                                          int32_t num_tokens, const int32_t* tree_mask, int32_t mask_words,
+                                          float sm_scale, void* out, float* lse2_out, void* workspace,
+                                          int64_t workspace_bytes, int32_t* status, void* cuda_stream) {
+  return pa::tree_attention(q, k_pool, v_pool, kv_dtype, num_pages, page_size, num_qo_heads, num_kv_heads, head_dim,
+                            indices, num_indices, indptr, last_page_len, first_page_offset, batch, qo_indptr,
+                            num_tokens, tree_mask, mask_words, nullptr, 0, sm_scale, out, lse2_out, workspace,
+                            workspace_bytes, status, cuda_stream);
+}
+
+extern "C" pa_status pa_v2_tree_attention_sliding(
+    const void* q, const void* k_pool, const void* v_pool, int32_t kv_dtype, int64_t num_pages, int32_t page_size,
+    int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, const int32_t* indices, int64_t num_indices,
+    const int32_t* indptr, const int32_t* last_page_len, const int32_t* first_page_offset, int32_t batch,
+    const int32_t* qo_indptr, int32_t num_tokens, const int32_t* tree_mask, int32_t mask_words,
+    const int32_t* positions, int32_t window, float sm_scale, void* out, float* lse2_out, void* workspace,
+    int64_t workspace_bytes, int32_t* status, void* cuda_stream) {
+  if (window < 1) return PA_EINVAL;
+  return pa::tree_attention(q, k_pool, v_pool, kv_dtype, num_pages, page_size, num_qo_heads, num_kv_heads, head_dim,
+                            indices, num_indices, indptr, last_page_len, first_page_offset, batch, qo_indptr,
+                            num_tokens, tree_mask, mask_words, positions, window, sm_scale, out, lse2_out, workspace,
+                            workspace_bytes, status, cuda_stream);
 }

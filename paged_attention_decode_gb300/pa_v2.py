@@ -39,7 +39,8 @@ ABI_SYMBOLS = ("pa_v2_q_heads_per_cta", "pa_v2_default_target_ctas", "pa_v2_plan
                "pa_v2_host_graph_run", "pa_v2_host_graph_destroy", "pa_v2_decode_host_mapped",
                "pa_v2_host_graph_create_mapped", "pa_v2_wave_fit_pages_per_chunk",
                "pa_v2_balanced_pages_per_chunk", "pa_v2_cascade_plan", "pa_v2_cascade_decode", "pa_v2_build_tables",
-               "pa_v2_qk_rope_append", "pa_v2_tree_attention_workspace", "pa_v2_tree_attention",
+               "pa_v2_build_tables_sliding", "pa_v2_qk_rope_append", "pa_v2_tree_attention_workspace",
+               "pa_v2_tree_attention", "pa_v2_tree_attention_sliding",
                "pa_status_from_device", "pa_status_string", "pa_version")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -141,6 +142,8 @@ def lib() -> ctypes.CDLL:
         L.pa_v2_build_tables.argtypes = [P, P, i32, P, i32, P, i32, P, i32, i32, P, P, i64, P, P, P, P, P, i64, P, i32,
                                          P, P, P]
         L.pa_v2_build_tables.restype = i32
+        L.pa_v2_build_tables_sliding.argtypes = L.pa_v2_build_tables.argtypes
+        L.pa_v2_build_tables_sliding.restype = i32
         L.pa_v2_qk_rope_append.argtypes = [P, i64, P, i64, P, i64, i32, i32, i32, i32, i32, P, P, P, i32, i32, P, P, f32,
                                            P, i32, P, P, i64, i32, P, P]
         L.pa_v2_qk_rope_append.restype = i32
@@ -149,6 +152,9 @@ def lib() -> ctypes.CDLL:
         L.pa_v2_tree_attention.argtypes = [P, P, P, i32, i64, i32, i32, i32, i32, P, i64, P, P, P, i32, P, i32, P, i32,
                                            f32, P, P, P, i64, P, P]
         L.pa_v2_tree_attention.restype = i32
+        L.pa_v2_tree_attention_sliding.argtypes = [P, P, P, i32, i64, i32, i32, i32, i32, P, i64, P, P, P, i32, P, i32,
+                                                   P, i32, P, i32, f32, P, P, P, i64, P, P]
+        L.pa_v2_tree_attention_sliding.restype = i32
         L.pa_status_from_device.argtypes = [i32]
         L.pa_status_from_device.restype = i32
         L.pa_status_string.argtypes = [i32]
@@ -702,13 +708,18 @@ class StepTables:
 
 
 def pa_v2_build_tables(cached_lens, new_lens, block_table, page_size: int, tables: StepTables, free_pages=None,
-                       parents=None, window: int = 0, status=None, stream=None) -> StepTables:
+                       parents=None, window: int = 0, status=None, stream=None,
+                       sliding_window: int = 0) -> StepTables:
     """Page table, slots, positions and tree masks of one step (pa_v2_build_tables), on the device.
 
     cached_lens, new_lens [B]; block_table [B, width], extended in place from free_pages when given (an empty
     list is one that ran out: its pages are -1; None means that the table holds every page already);
-    parents [token capacity] (request-relative, -1 a root) for trees, None for chains.  Fills and returns
-    `tables`."""
+    parents [token capacity] (request-relative, -1 a root) for trees, None for chains.  window: list the last tokens
+    of each request only.  sliding_window, instead of it: a model's window, of so many positions up to each token's own
+    (pa_v2_build_tables_sliding; pa_v2_tree_attention takes the same); with one new token per request they agree.
+    Fills and returns `tables`."""
+    if window and sliding_window:
+        raise ValueError("give window (the request's) or sliding_window (each token's), not both")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch, width]")
     dev, (B, width) = _device_index(block_table, "block_table"), block_table.shape
@@ -723,16 +734,18 @@ def pa_v2_build_tables(cached_lens, new_lens, block_table, page_size: int, table
         free = t.indptr.data_ptr()
     args = (ptr(cached_lens, "cached_lens", dev, i32, B), ptr(new_lens, "new_lens", dev, i32, B), B,
             ptr(block_table, "block_table", dev, i32), width, free, num_free, ptr(parents, "parents", dev, i32, cap_t),
-            page_size, window, ptr(t.indptr, "indptr", dev, i32, B + 1), ptr(t.indices, "indices", dev, i32), cap_i,
+            page_size, sliding_window or window, ptr(t.indptr, "indptr", dev, i32, B + 1), ptr(t.indices, "indices", dev, i32), cap_i,
             ptr(t.last_page_len, "last_page_len", dev, i32, B),
             ptr(t.first_page_offset, "first_page_offset", dev, i32, B),
             ptr(t.qo_indptr, "qo_indptr", dev, i32, B + 1), ptr(t.slots, "slots", dev, i32, cap_t),
             ptr(t.positions, "positions", dev, i32, cap_t), cap_t, ptr(mask, "tree_mask", dev, i32, cap_t * words),
             words, ptr(t.pages_needed, "pages_needed", dev, i32, 1), ptr(status, "status", dev, i32))
+    entry = "pa_v2_build_tables_sliding" if sliding_window else "pa_v2_build_tables"
+
     def launch(handle):
-        rc = lib().pa_v2_build_tables(*args, handle)
+        rc = getattr(lib(), entry)(*args, handle)
         if rc != PA_OK:
-            raise PaError(rc, "pa_v2_build_tables")
+            raise PaError(rc, entry)
 
     _run_on(dev, stream, launch)
     return tables
@@ -833,12 +846,13 @@ def tree_attention_workspace(num_tokens: int, batch: int, num_qo_heads: int, num
 
 def pa_v2_tree_attention(q, k_pool, v_pool, indices, indptr, last_page_len, first_page_offset, qo_indptr,
                          sm_scale: float, tree_mask=None, out=None, lse2_out=None, workspace=None, status=None,
-                         stream=None):
+                         stream=None, sliding_window: int = 0, positions=None):
     """Attention of each request's new tokens over its paged cache (pa_v2_tree_attention).
 
     q [T, Hq, D] of the pools' 16-bit dtype, packed request by request (qo_indptr [B + 1]); tree_mask
-    [T, words] int32 ancestor bits, or None for chains.  Returns (out [T, Hq, D], lse2 [T, Hq] float32); rows
-    behind the last token are not written."""
+    [T, words] int32 ancestor bits, or None for chains.  sliding_window: each token sees so many positions up to its own
+    (pa_v2_tree_attention_sliding), with positions [T] int32, both as in the call that made the tables.  Returns
+    (out [T, Hq, D], lse2 [T, Hq] float32); rows behind the last token are not written."""
     dev = _device_index(q, "q")
     k_ptr, v_ptr = _pools(k_pool, v_pool, dev)
     if q.dim() != 3:
@@ -853,8 +867,13 @@ def pa_v2_tree_attention(q, k_pool, v_pool, indices, indptr, last_page_len, firs
             indices.numel(), ptr(indptr, "indptr", dev, i32, B + 1),
             ptr(last_page_len, "last_page_len", dev, i32, B),
             ptr(first_page_offset, "first_page_offset", dev, i32, B), B,
-            ptr(qo_indptr, "qo_indptr", dev, i32, B + 1), T, ptr(tree_mask, "tree_mask", dev, i32, T * words), words,
-            sm_scale)
+            ptr(qo_indptr, "qo_indptr", dev, i32, B + 1), T, ptr(tree_mask, "tree_mask", dev, i32, T * words), words)
+    entry = "pa_v2_tree_attention"
+    if sliding_window:
+        if positions is None:
+            raise ValueError("a sliding window needs the tokens' positions")
+        entry = "pa_v2_tree_attention_sliding"
+        head += ptr(positions, "positions", dev, i32, T), sliding_window
     st = ptr(status, "status", dev, i32)
     for t, name, shape in ((out, "out", (T, hq, D)), (lse2_out, "lse2_out", (T, hq))):
         if t is not None and t.shape != shape:
@@ -868,12 +887,12 @@ def pa_v2_tree_attention(q, k_pool, v_pool, indices, indptr, last_page_len, firs
             out = torch.empty(T, hq, D, dtype=dt, device=q.device)
         if lse2_out is None:
             lse2_out = torch.empty(T, hq, dtype=torch.float32, device=q.device)
-        rc = lib().pa_v2_tree_attention(*head, ptr(out, "out", dev, dt), ptr(lse2_out, "lse2_out", dev, torch.float32),
-                                        ptr(workspace, "workspace", dev),
-                                        workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                                        st, handle)
+        rc = getattr(lib(), entry)(*head, sm_scale, ptr(out, "out", dev, dt),
+                                  ptr(lse2_out, "lse2_out", dev, torch.float32), ptr(workspace, "workspace", dev),
+                                  workspace.numel() * workspace.element_size() if workspace is not None else 0, st,
+                                  handle)
         if rc != PA_OK:
-            raise PaError(rc, "pa_v2_tree_attention")
+            raise PaError(rc, entry)
 
     _run_on(dev, stream, launch)
     return out, lse2_out
@@ -933,10 +952,10 @@ class HostStep:
         if graph_scale is not None:
             g = ctypes.c_void_p()
             name = "pa_v2_host_graph_create_mapped" if mapped else "pa_v2_host_graph_create"
-            rc = getattr(lib(), name)(*self._args, float(graph_scale), self.ws[0].data_ptr(), self.ws[1].data_ptr(),
+            rc = getattr(lib(), entry)(*self._args, float(graph_scale), self.ws[0].data_ptr(), self.ws[1].data_ptr(),
                                       ctypes.byref(g))
             if rc != PA_OK:
-                raise PaError(rc, name)
+                raise PaError(rc, entry)
             self._graph, self._graph_scale = g, float(graph_scale)
             self._lib = lib()
 

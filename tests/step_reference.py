@@ -74,6 +74,22 @@ def tables_ref(cached, new, block_table, free, parents, page_size, window, mask_
     return out
 
 
+def sliding_tables_ref(cached, new, block_table, free, parents, page_size, window, mask_words):
+    """tables_ref for a model whose tokens each see a window of positions up to their own."""
+    out = tables_ref(cached, new, block_table, free, parents, page_size, 0, mask_words)
+    table = out["block_table"]
+    out.update(indptr=[0], indices=[], first_page_offset=[], tree_mask=[])
+    for r, (c, n) in enumerate(zip(cached, new)):
+        first = max(0, c - (window - 1 if n else window))
+        out["indices"] += [int(table[r, col]) for col in range(first // page_size, -(-(c + n) // page_size))]
+        out["indptr"].append(len(out["indices"]))
+        out["first_page_offset"].append(first % page_size if c + n else 0)
+        for i in range(n if mask_words else 0):
+            line = ancestors(parents[r] if parents is not None else None, i)[:window]
+            out["tree_mask"].append(words_of(sum(1 << j for j in line), mask_words))
+    return out
+
+
 def rope_ref(x, weight, eps, positions, inv_freq, interleaved):
     """Norm (when weight is given) and rotation of x [T, H, D] in f64; returns (result, magnitude), the
     magnitude |x| + |partner| before the rotation, which bounds what f32 arithmetic can lose."""
@@ -145,3 +161,11 @@ def attention_ref(q, k_pool, v_pool, indices, indptr, lpl, fpo, qo_indptr, scale
             rel = eps / 2 + 2 * math.log(2.0) * ds + 2.0 ** -18
             tol_o[t0 + i] = (o.abs() * (eps / 2) + rel[..., None] * mean_abs).reshape(hq, D)
     return out, lse, tol_o, tol_l
+
+
+def rows_attention_ref(q, k_pool, v_pool, seen, scale):
+    """attention_ref of every query token alone, over the pool rows seen[t] (its own the last)."""
+    one = lambda x: x.reshape(-1, 1, *x.shape[2:])
+    parts = [attention_ref(q[t:t + 1], one(k_pool), one(v_pool), torch.tensor(rows), [0, len(rows)], [1], [0], [0, 1], scale)
+             for t, rows in enumerate(seen)]
+    return tuple(torch.cat(x) for x in zip(*parts))

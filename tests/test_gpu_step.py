@@ -899,6 +899,166 @@ def test_tree_single_tokens_agree_with_the_decode():
 
 
 # ---------------------------------------------------------------------------
+# sliding windows: every token sees its own
+# ---------------------------------------------------------------------------
+
+def _sliding_case(seed, reqs, window, tree, hq, hkv, D, page_size, dtype, words=None):
+    """reqs [(cached, new)] whose K and V, new tokens' included, lie in the pools at block_table's pages; seen: the pool
+    rows each new token sees."""
+    rng = random.Random(seed)
+    g = torch.Generator().manual_seed(seed)
+    cached, fresh = [c for c, _ in reqs], [n for _, n in reqs]
+    parents = [R.random_tree(rng, n) for n in fresh] if tree == "random" else \
+              [[i - 1 if i % 9 else max(i - 4, -1) for i in range(n)] for n in fresh] if tree == "deep" else None
+    width = max(-(-(c + n) // page_size) for c, n in reqs) + 1
+    P = len(reqs) * width + 2
+    table = torch.randperm(P, generator=g)[:len(reqs) * width].reshape(-1, width).to(I32)
+    kp, vp = (torch.randn(P, page_size, hkv, D, generator=g).to(dtype) for _ in range(2))
+    q = (1.5 * torch.randn(sum(fresh), hq, D, generator=g)).to(dtype)
+    seen = []
+    for r, (c, n) in enumerate(reqs):
+        row = lambda at: int(table[r, at // page_size]) * page_size + at % page_size
+        for i in range(n):
+            line = R.ancestors(parents[r] if parents is not None else None, i)
+            low = c + len(line) - 1 - window + 1          # its position is c + its depth
+            seen.append([row(x) for x in range(max(low, 0), c)] +
+                        [row(c + j) for d, j in reversed(list(enumerate(line))) if d < window])
+    words = words or (-(-max(fresh) // 32) if tree else 0)
+    return dict(cached=cached, fresh=fresh, parents=parents, table=table, kp=kp, vp=vp, q=q, seen=seen, words=words,
+                window=window, page_size=page_size, scale=D ** -0.5)
+
+
+def _sliding_run(c, st, table=None, tables_window=None, kp=None, vp=None):
+    """Tables, then attention: (tables, out, lse2)."""
+    cap_t = sum(c["fresh"]) + 3
+    t = _fresh_tables(len(c["cached"]), c["table"].numel(), cap_t, c["words"])
+    packed = i32([p for ps in c["parents"] for p in ps] + [-1] * 3).cuda() if c["parents"] is not None else None
+    pa.pa_v2_build_tables(i32(c["cached"]).cuda(), i32(c["fresh"]).cuda(), (c["table"] if table is None else table).cuda(),
+                          c["page_size"], t, parents=packed, status=st,
+                          **(tables_window if tables_window is not None else dict(sliding_window=c["window"])))
+    q = torch.cat((c["q"], torch.full((3, *c["q"].shape[1:]), float("nan"), dtype=c["q"].dtype))).cuda()
+    out, lse = torch.full_like(q, 5.0), torch.full(q.shape[:2], 5.0, device="cuda")
+    pa.pa_v2_tree_attention(q, (c["kp"] if kp is None else kp).cuda(), (c["vp"] if vp is None else vp).cuda(), t.indices,
+                            t.indptr, t.last_page_len, t.first_page_offset, t.qo_indptr, c["scale"],
+                            tree_mask=t.tree_mask, out=out, lse2_out=lse, status=st, sliding_window=c["window"],
+                            positions=t.positions)
+    torch.cuda.synchronize()
+    assert out[-3:].eq(5.0).all() and lse[-3:].eq(5.0).all()
+    return t, out[:-3].cpu().double(), lse[:-3].cpu().double()
+
+
+def _check_sliding(c, ref, got):
+    assert ((got[1] - ref[1]).abs() <= ref[3]).all(), (got[1] - ref[1]).abs().max()
+    assert ((got[0] - ref[0]).abs() <= ref[2]).all(), (got[0] - ref[0]).abs().max()
+
+
+SLIDING = [
+    ([(5000, 5), (100, 5), (4094, 3)], 4096, None, 8, 2, 128, 16),     # a verified chain
+    ([(700, 5), (0, 5), (127, 4), (128, 1), (40, 0)], 128, None, 8, 2, 128, 16),
+    ([(700, 64), (126, 64), (3, 64)], 128, "random", 8, 2, 128, 16),
+    ([(700, 64), (30, 50)], 20, "deep", 8, 2, 64, 16),                 # trees deeper than the window
+    ([(300, 9), (50, 33)], 1, "deep", 4, 2, 64, 5),                    # every token sees itself alone
+    ([(300, 9), (0, 30)], 1, None, 4, 2, 64, 16),
+    ([(257, 7), (511, 40)], 33, "random", 4, 4, 128, 5),
+    ([(900, 300), (0, 290)], 64, None, 4, 1, 64, 16),                  # several blocks, more new tokens than the window
+    ([(900, 300), (20, 130)], 500, None, 8, 2, 128, 48),
+    ([(2000, 200)], 300, "deep", 4, 1, 64, 256),
+    ([(200, 3)] * 70, 100, None, 2, 1, 64, 16),                        # more requests than a warp's lanes
+    ([(400, 6)], 100000, "random", 4, 2, 64, 16),                      # a window that never binds
+]
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("reqs,window,tree,hq,hkv,D,page_size", SLIDING)
+def test_sliding_step_equals_each_token_alone(reqs, window, tree, hq, hkv, D, page_size, dtype):
+    c = _sliding_case(len(reqs) + window, reqs, window, tree, hq, hkv, D, page_size, dtype)
+    st = status_word()
+    t, out, lse = _sliding_run(c, st)
+    assert int(st) == 0
+    ref = R.sliding_tables_ref(c["cached"], c["fresh"], c["table"], None, c["parents"], page_size, window, c["words"])
+    _check_tables(t, c["table"], ref, sum(c["fresh"]) + 3)
+    _check_sliding(c, R.rows_attention_ref(c["q"], c["kp"], c["vp"], c["seen"], c["scale"]), (out, lse))
+
+
+@pytest.mark.parametrize("page_size", [16, 5])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("tree", [None, "deep"])
+def test_sliding_window_hides_what_lies_before_it(tree, bad, page_size):
+    """Keys and values before the window of every token, pages that are gone, and rows that only the first tokens of a
+    request still see: none of it reaches a token that does not see it."""
+    c = _sliding_case(7, [(700, 40), (300, 7), (60, 12)], 150, tree, 8, 2, 64, page_size, torch.bfloat16)
+    ref = R.rows_attention_ref(c["q"], c["kp"], c["vp"], c["seen"], c["scale"])
+    used = torch.zeros(c["kp"].shape[0] * page_size, dtype=torch.bool)
+    for rows in c["seen"]:
+        used[rows] = True
+    kp, vp = c["kp"].clone(), c["vp"].clone()
+    kp.flatten(0, 1)[~used], vp.flatten(0, 1)[~used] = bad, bad
+    st = status_word()
+    _check_sliding(c, ref, _sliding_run(c, st, kp=kp, vp=vp)[1:])
+    # tables that list every page, those before the window given back already
+    gone = c["table"].clone()
+    for r, n in enumerate(c["cached"]):
+        gone[r, :max(0, n - 149) // page_size] = -1 if r else 10**6
+    _check_sliding(c, ref, _sliding_run(c, st, table=gone, tables_window={}, kp=kp, vp=vp)[1:])
+    # tables of a window that is wide enough for the longest request
+    _check_sliding(c, ref, _sliding_run(c, st, table=gone, tables_window=dict(window=189))[1:])
+    assert int(st) == 0
+    # what the first token of each request sees last of all: bad for it and for nobody else
+    hidden, t0 = set(), 0
+    for n in c["fresh"]:
+        row = c["seen"][t0][0]
+        kp.flatten(0, 1)[row], vp.flatten(0, 1)[row] = bad, bad
+        hidden |= {t for t, rows in enumerate(c["seen"]) if row in rows}
+        t0 += n
+    keep = [t for t in range(len(c["seen"])) if t not in hidden]
+    assert len(keep) > 40
+    _, out, lse = _sliding_run(c, st, kp=kp, vp=vp)
+    assert int(st) == 0
+    assert ((out - ref[0]).abs()[keep] <= ref[2][keep]).all() and ((lse - ref[1]).abs()[keep] <= ref[3][keep]).all()
+    # a value alone (its key is finite): the tokens that see it get it, in its element
+    kp = c["kp"]
+    vp = c["vp"].clone()
+    vp.flatten(0, 1)[c["seen"][0][0], 1, 9] = bad
+    sees = [c["seen"][0][0] in rows for rows in c["seen"]]
+    _, out, lse = _sliding_run(c, st, vp=vp)
+    assert (~out[:, 4:, 9].isfinite()).all(1).tolist() == sees and (~out[:, 4:, 9].isfinite()).any(1).tolist() == sees
+    out[:, 4:, 9] = ref[0][:, 4:, 9]
+    _check_sliding(c, ref, (out, lse))
+
+
+def test_sliding_step_refuses_tables_that_lack_what_its_tokens_see():
+    """Tables of the request's last 100 tokens hold 95 earlier ones beside 5 new; the first new one sees 99."""
+    c = _sliding_case(9, [(300, 5), (60, 5), (300, 1)], 100, None, 4, 2, 64, 16, torch.float16)
+    ref = R.rows_attention_ref(c["q"], c["kp"], c["vp"], c["seen"], c["scale"])
+    st = status_word()
+    _, out, lse = _sliding_run(c, st, tables_window=dict(window=100))
+    assert int(st) == pa.DEVICE_BAD_TREE
+    assert out[:5].eq(0).all() and (lse[:5] == -math.inf).all()
+    assert ((out - ref[0]).abs()[5:] <= ref[2][5:]).all()            # everything of 60, and a single token's window
+    with pytest.raises(ValueError, match="positions"):
+        pa.pa_v2_tree_attention(*([torch.zeros(1, 2, 64, dtype=torch.float16, device="cuda")] +
+                                  [torch.zeros(1, 1, 2, 64, dtype=torch.float16, device="cuda")] * 2 +
+                                  [torch.zeros(2, dtype=I32, device="cuda")] * 2 +
+                                  [torch.zeros(1, dtype=I32, device="cuda")] * 2 +
+                                  [torch.zeros(2, dtype=I32, device="cuda")]), 0.1, sliding_window=3)
+
+
+def test_sliding_chain_at_once_equals_one_token_at_a_time():
+    """The chain of a step against the same tokens appended one by one, each through tables and attention of its own."""
+    c = _sliding_case(10, [(500, 6), (130, 6)], 128, None, 8, 2, 128, 16, torch.bfloat16)
+    st = status_word()
+    _, out, lse = _sliding_run(c, st)
+    ref = R.rows_attention_ref(c["q"], c["kp"], c["vp"], c["seen"], c["scale"])
+    for i in range(6):
+        one = dict(c, cached=[n + i for n in c["cached"]], fresh=[1, 1], q=c["q"][[i, 6 + i]])
+        for tables_window in (dict(window=128), dict(sliding_window=128)):
+            _, o, l = _sliding_run(one, st, tables_window=tables_window)
+            assert ((o - out[[i, 6 + i]]).abs() <= 2 * ref[2][[i, 6 + i]]).all()      # each within its tolerance
+            assert ((l - lse[[i, 6 + i]]).abs() <= 2 * ref[3][[i, 6 + i]]).all()
+    assert int(st) == 0
+
+
+# ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
 
@@ -1088,3 +1248,71 @@ def test_two_calls_at_once_on_two_streams():
         torch.cuda.synchronize()
         for (out, lse), (ro, rl) in zip(got, want):
             assert torch.equal(out.cpu(), ro) and torch.equal(lse.cpu(), rl)
+
+
+@pytest.mark.parametrize("tree", [True, False])
+@pytest.mark.parametrize("graph", [False, True])
+def test_a_whole_sliding_step(graph, tree):
+    """Tables, q/k preparation and attention under a sliding window, eagerly and from a graph replayed with other
+    lengths: each token's q and k at its own position, and its output over the rows that its own window holds."""
+    dtype, hq, hkv, D, ps, B, window, cap_t, width, P = torch.bfloat16, 8, 2, 64, 16, 3, 50, 60, 30, 120
+    rng, g = random.Random(91), torch.Generator().manual_seed(91)
+    freq = torch.tensor([10000.0 ** (-j / 32) for j in range(32)], dtype=torch.float32)
+    weights = [(1 + 0.2 * torch.randn(D, generator=g)).to(dtype) for _ in range(2)]
+    table = torch.randperm(P, generator=g)[:B * width].reshape(B, width).to(I32)
+    kp, vp = (torch.randn(P, ps, hkv, D, generator=g).to(dtype) for _ in range(2))
+    dtab, dk, dv, dfreq, dw = table.cuda(), kp.cuda(), vp.cuda(), freq.cuda(), [w.cuda() for w in weights]
+    dc, dn, dpar = torch.zeros(B, dtype=I32, device="cuda"), torch.zeros(B, dtype=I32, device="cuda"), i32([-1] * cap_t).cuda()
+    dx = torch.zeros(cap_t, hq + 2 * hkv, D, dtype=dtype, device="cuda")
+    t, st = pa.StepTables.empty(B, B * width, cap_t, 1 if tree else 0), status_word()
+    dq = torch.empty(cap_t, hq, D, dtype=dtype, device="cuda")
+    out, lse = torch.empty_like(dq), torch.empty(cap_t, hq, device="cuda")
+    ws = pa.tree_attention_workspace(cap_t, B, hq, hkv, D)
+
+    def step():
+        pa.pa_v2_build_tables(dc, dn, dtab, ps, t, parents=dpar if tree else None, sliding_window=window, status=st)
+        pa.pa_v2_qk_rope_append(dx[:, :hq], dx[:, hq:hq + hkv], dx[:, hq + hkv:], t.positions, t.slots, dfreq, dk, dv,
+                                q_out=dq, q_weight=dw[0], k_weight=dw[1], eps=1e-6, status=st)
+        pa.pa_v2_tree_attention(dq, dk, dv, t.indices, t.indptr, t.last_page_len, t.first_page_offset, t.qo_indptr,
+                                D ** -0.5, tree_mask=t.tree_mask, out=out, lse2_out=lse, workspace=ws, status=st,
+                                sliding_window=window, positions=t.positions)
+
+    replay = step
+    if graph:
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            step()
+        s.synchronize()
+        cg = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cg, stream=s):
+            step()
+        replay = cg.replay
+    for cached in ([200, 0, 37], [49, 50, 333]):
+        fresh = [rng.randint(1, 19) for _ in range(B)]
+        trees = [R.random_tree(rng, n) for n in fresh] if tree else [None] * B
+        n = sum(fresh)
+        x = torch.randn(n, hq + 2 * hkv, D, generator=g).to(dtype)
+        dc.copy_(i32(cached))
+        dn.copy_(i32(fresh))
+        if tree:
+            dpar[:n] = i32(p for ps_ in trees for p in ps_).cuda()
+        dx[:n] = x.cuda()
+        replay()
+        torch.cuda.synchronize()
+        assert int(st) == 0
+        pos, own, seen = [], [], []
+        for r, (c, m) in enumerate(zip(cached, fresh)):
+            row = lambda at: int(table[r, at // ps]) * ps + at % ps
+            for i in range(m):
+                line = R.ancestors(trees[r], i)
+                pos.append(c + len(line) - 1)
+                own.append(row(c + i))
+                seen.append([row(y) for y in range(max(pos[-1] - window + 1, 0), c)] +
+                            [row(c + j) for j in reversed(line[:window])])
+        q, k, v = dq[:n].cpu(), dk.cpu(), dv.cpu()
+        for got, heads, w in ((q, x[:, :hq], weights[0]), (k.flatten(0, 1)[own], x[:, hq:hq + hkv], weights[1])):
+            ref, mag = R.rope_ref(heads, w, 1e-6, pos, freq, False)
+            assert ((got.double() - ref).abs() <= R.rope_tolerance(ref, mag, dtype)).all()
+        assert torch.equal(v.flatten(0, 1)[own], x[:, hq + hkv:])
+        ro, rl, to, tl = R.rows_attention_ref(q, k, v, seen, D ** -0.5)
+        assert ((out[:n].cpu().double() - ro).abs() <= to).all() and ((lse[:n].cpu().double() - rl).abs() <= tl).all()

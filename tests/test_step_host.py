@@ -95,6 +95,40 @@ def test_tree_attention_without_work_does_nothing():
         assert pa.lib().pa_v2_tree_attention(*{**TREE, **change}.values()) == pa.PA_OK
 
 
+SLIDING = {k: v for key, value in TREE.items() for k, v in
+           ((("positions", FAKE), ("window", 64), (key, value)) if key == "scale" else ((key, value),))}
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(window=0), pa.PA_EINVAL), (dict(window=-1), pa.PA_EINVAL), (dict(positions=None), pa.PA_EINVAL),
+    (dict(q=None), pa.PA_EINVAL), (dict(words=0), pa.PA_EINVAL), (dict(scale=math.nan), pa.PA_EINVAL),
+    (dict(hq=7), pa.PA_EINVAL), (dict(dtype=pa.PA_F32), pa.PA_EUNSUPPORTED), (dict(D=96), pa.PA_EUNSUPPORTED),
+    (dict(words=pa.MAX_MASK_WORDS + 1), pa.PA_EUNSUPPORTED)])
+def test_tree_attention_sliding_refusals(change, want):
+    assert list(SLIDING)[17:22] == ["mask", "words", "positions", "window", "scale"]
+    assert pa.lib().pa_v2_tree_attention_sliding(*{**SLIDING, **change}.values()) == want
+
+
+def test_tree_attention_sliding_without_work_does_nothing():
+    for change in (dict(tokens=0), dict(batch=0)):
+        assert pa.lib().pa_v2_tree_attention_sliding(*{**SLIDING, **change}.values()) == pa.PA_OK
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(window=0), pa.PA_EINVAL), (dict(window=-1), pa.PA_EINVAL), (dict(cached=None), pa.PA_EINVAL),
+    (dict(page_size=0), pa.PA_EINVAL), (dict(mask_words=0), pa.PA_EINVAL),
+    (dict(batch=pa.MAX_TABLE_BATCH + 1), pa.PA_EUNSUPPORTED)])
+def test_build_tables_sliding_refusals(change, want):
+    assert pa.lib().pa_v2_build_tables_sliding(*{**TABLES, "window": 5, **change}.values()) == want
+
+
+def test_binding_refuses_two_windows():
+    z = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="not both"):
+        pa.pa_v2_build_tables(z, z, torch.zeros(4, 4, dtype=torch.int32), 16, pa.StepTables.empty(4, 8, 8, 1, device="cpu"),
+                              window=3, sliding_window=3)
+
+
 def test_tree_attention_workspace_refusals():
     n = ctypes.c_int64()
     f = pa.lib().pa_v2_tree_attention_workspace
@@ -172,3 +206,23 @@ def test_reference_attention_equals_dense_softmax():
         o = torch.nn.functional.scaled_dot_product_attention(q.half().double()[None, :, h], k[None], v[None], attn_mask=allow,
                                                              scale=0.125)[0]
         assert (o - ro[:, h]).abs().max() < 1e-12
+
+
+def test_reference_sliding_tables_of_a_worked_example():
+    # window 3, 4-entry pages: a tree behind 9 cached tokens (its roots see tokens 7 and 8), a chain behind 2, no token
+    table = torch.tensor([[3, 9, 4, 8], [5, 6, 0, 0], [7, 1, 2, 0]], dtype=torch.int32)
+    ref = R.sliding_tables_ref([9, 2, 10], [5, 5, 0], table, None, [[-1, 0, 1, 2, 0], [-1, 0, 1, 2, 3], []], 4, 3, 1)
+    assert ref["first_page_offset"] == [3, 0, 3] and ref["last_page_len"] == [2, 3, 2]
+    assert ref["indices"] == [9, 4, 8, 5, 6, 1, 2] and ref["indptr"] == [0, 3, 5, 7]
+    assert ref["positions"] == [9, 10, 11, 12, 10, 2, 3, 4, 5, 6]
+    assert ref["tree_mask"] == [[1], [3], [7], [14], [17], [1], [3], [7], [14], [28]]
+
+
+def test_reference_rows_attention_equals_the_paged_one():
+    g = torch.Generator().manual_seed(3)
+    q, kp, vp = (torch.randn(*s, generator=g).half() for s in ((2, 4, 64), (5, 4, 2, 64), (5, 4, 2, 64)))
+    idx = torch.tensor([3, 1], dtype=torch.int32)
+    paged = R.attention_ref(q, kp, vp, idx, [0, 2], [3], [1], [0, 2], 0.1)
+    rows = [13, 14, 15, 4, 5, 6]
+    alone = R.rows_attention_ref(q, kp, vp, [rows[:5], rows], 0.1)
+    assert all(torch.allclose(a, b, atol=1e-13) for a, b in zip(paged, alone))
