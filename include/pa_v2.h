@@ -751,7 +751,8 @@ pa_status pa_v2_qk_rope_append(const void* q, int64_t q_stride, const void* k, i
  * one request (PA_DEVICE_BAD_TREE, the request's rows become zeros and -inf).
  * P = exp(s) enters the second product rounded to kv_dtype; scores, statistics
  * and sums are f32.  head_dim 64 or 128, page_size 1..16 or a multiple of 16 up
- * to 256, pools below 2^31 rows (else PA_EUNSUPPORTED).  DEVICE pointers. */
+ * to 256, pools below 2^31 rows, |sm_scale| log2(e) within f32 (else
+ * PA_EUNSUPPORTED).  DEVICE pointers. */
 #define PA_V2_MAX_MASK_WORDS 32
 pa_status pa_v2_tree_attention_workspace(int32_t device, int32_t num_tokens, int32_t batch, int32_t num_qo_heads,
                                          int32_t num_kv_heads, int32_t head_dim, int64_t* bytes);

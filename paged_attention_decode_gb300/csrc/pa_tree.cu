@@ -1570,6 +1570,8 @@ pa_status tree_attention(const void* q, const void* k_pool, const void* v_pool, 
   if (page_size > 256 || (page_size > 16 && page_size % 16 != 0)) return PA_EUNSUPPORTED;
   if (num_pages >= (1ll << 31) || num_pages * page_size >= (1ll << 31)) return PA_EUNSUPPORTED;
   if (tree_mask && mask_words > PA_V2_MAX_MASK_WORDS) return PA_EUNSUPPORTED;
+  const float scale_log2 = std::fabs(sm_scale) * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2)) return PA_EUNSUPPORTED;  // times a score of 0 it would be NaN
   if ((int64_t)num_tokens * (num_qo_heads / num_kv_heads) > INT32_MAX - 2 * kTrBlock) return PA_EUNSUPPORTED;
   if (num_tokens == 0 || batch == 0) return PA_OK;
   if (!q || !k_pool || !v_pool || !indptr || !last_page_len || !first_page_offset || !qo_indptr || !out ||
@@ -1638,8 +1640,8 @@ pa_status tree_attention(const void* q, const void* k_pool, const void* v_pool, 
   const double units = ((double)num_indices * page_size / kTrTile + 2.0 * batch) *
                        ((double)num_tokens * p.group / kTrBlock + batch) * num_kv_heads;
   p.small = batch <= 32 && units < (double)(1 << 25);
-  const bool flat = std::fabs(sm_scale) < 1e-30f;  // every score is zero
-  p.scale_log2 = flat ? 1.f : std::fabs(sm_scale) * 1.4426950408889634f;
+  const bool flat = sm_scale == 0.f;  // every score is zero, behind a mask's -inf too, where 0 times it is NaN
+  p.scale_log2 = flat ? 1.f : scale_log2;
   p.q_xor = sm_scale < 0.f ? 0x80008000u : 0u;
   p.q_and = flat ? 0u : 0xffffffffu;
   const bool f16 = kv_dtype == PA_F16;

@@ -741,6 +741,17 @@ def test_tree_negative_and_zero_scale():
         assert ((lse.double() - rl).abs() <= tol[3]).all()
 
 
+@pytest.mark.parametrize("scale,size", [(1e-31, 2.0 ** 50), (1e-36, 2.0 ** 58)])
+def test_tree_tiny_scales_of_large_scores(scale, size):
+    """Scores of about one out of products of 1e31 and 1e36, which f32 and bf16 hold."""
+    c = _tree_case(39, [(300, 9)], 4, 2, 64, 16, torch.bfloat16)
+    c["scale"] = float(torch.tensor(scale, dtype=torch.float32))
+    c["q"] = (c["q"].float() * size).to(torch.bfloat16)
+    c["kp"] = (c["kp"].float() * (0.3 / scale / size)).to(torch.bfloat16)
+    _, lse = _check_tree(c)
+    assert lse.std() > 0.5
+
+
 def test_tree_bad_tables_are_contained_and_reported():
     base = _tree_case(40, [(100, 6), (50, 4), (30, 5)], 4, 2, 64, 16, torch.float16)
     ref = _check_tree(base)

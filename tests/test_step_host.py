@@ -90,6 +90,11 @@ def test_tree_attention_refusals(change, want):
     assert pa.lib().pa_v2_tree_attention(*{**TREE, **change}.values()) == want
 
 
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38])
+def test_tree_attention_refuses_scales_that_overflow_in_base_2(scale):
+    assert pa.lib().pa_v2_tree_attention(*{**TREE, "scale": scale}.values()) == pa.PA_EUNSUPPORTED
+
+
 def test_tree_attention_without_work_does_nothing():
     for change in (dict(tokens=0), dict(batch=0)):
         assert pa.lib().pa_v2_tree_attention(*{**TREE, **change}.values()) == pa.PA_OK
