@@ -952,10 +952,10 @@ class HostStep:
         if graph_scale is not None:
             g = ctypes.c_void_p()
             name = "pa_v2_host_graph_create_mapped" if mapped else "pa_v2_host_graph_create"
-            rc = getattr(lib(), entry)(*self._args, float(graph_scale), self.ws[0].data_ptr(), self.ws[1].data_ptr(),
+            rc = getattr(lib(), name)(*self._args, float(graph_scale), self.ws[0].data_ptr(), self.ws[1].data_ptr(),
                                       ctypes.byref(g))
             if rc != PA_OK:
-                raise PaError(rc, entry)
+                raise PaError(rc, name)
             self._graph, self._graph_scale = g, float(graph_scale)
             self._lib = lib()
 
