@@ -650,9 +650,9 @@ pa_status pa_v2_decode_noalloc(const pa_v2_plan_t* plan, const float* q, const v
  *    behind the last are left as they were.
  * The lengths are read, not advanced: the same call again gives the same
  * result.  DEVICE pointers; indices [index_capacity], slots and positions (and
- * parents) [token_capacity].  Bad data is recorded in `status` and contained:
- * negative lengths count as 0 and a request that needs more pages than
- * table_width gets no page and slots -1 (PA_DEVICE_BAD_LENGTH); pages or tokens
+ * parents) [token_capacity].  Bad data is recorded in `status` and contained: a
+ * request with a negative length (no token where it is new_lens) or that needs
+ * more pages than table_width gets no page and slots -1 (PA_DEVICE_BAD_LENGTH); pages or tokens
  * past a capacity are not written (the same bit); a page the free list does not
  * have is -1 (PA_DEVICE_NO_PAGES), as are the slots on it; a parent outside
  * [-1, i) makes token i a root, and a tree of more than 32 * mask_words tokens
@@ -732,7 +732,8 @@ pa_status pa_v2_qk_rope_append(const void* q, int64_t q_stride, const void* k, i
  * <= i).  With s the scaled scores over what it sees,
  *   out = sum softmax(s) v,   lse2 = log2(sum exp(s));
  * a token that sees nothing gets zeros and -inf.  Values behind a cleared bit or
- * outside the visible rows never reach a result, NaN and infinities included.
+ * outside the visible rows never reach a result, NaN and infinities included;
+ * those that a token sees do.
  *   q, out [num_tokens, num_qo_heads, head_dim] of kv_dtype (f16 or bf16;
  *     16-byte aligned), lse2_out [num_tokens, num_qo_heads] f32;
  *   tree_mask [num_tokens, mask_words] int32, mask_words <= PA_V2_MAX_MASK_WORDS;

@@ -395,14 +395,12 @@ extern "C" pa_status pa_v2_build_tables(const int32_t* cached_lens, const int32_
                           cuda_stream);
 }
 
-extern "C" pa_status pa_v2_build_tables_sliding(const int32_t* cached_lens, const int32_t* new_lens, int32_t batch,
-                                                int32_t* block_table, int32_t table_width,
-                                                const int32_t* free_pages, int32_t num_free, const int32_t* parents, int32_t page_size,
-                                                int32_t window, int32_t* indptr, int32_t* indices, int64_t index_capacity,
-                                                int32_t* last_page_len, int32_t* first_page_offset, int32_t* qo_indptr,
-                                                int32_t* slots, int32_t* positions, int64_t token_capacity,
-                                                int32_t* tree_mask, int32_t mask_words, int32_t* pages_needed,
-                                                int32_t* status, void* cuda_stream) {
+extern "C" pa_status pa_v2_build_tables_sliding(
+    const int32_t* cached_lens, const int32_t* new_lens, int32_t batch, int32_t* block_table, int32_t table_width,
+    const int32_t* free_pages, int32_t num_free, const int32_t* parents, int32_t page_size, int32_t window,
+    int32_t* indptr, int32_t* indices, int64_t index_capacity, int32_t* last_page_len, int32_t* first_page_offset,
+    int32_t* qo_indptr, int32_t* slots, int32_t* positions, int64_t token_capacity, int32_t* tree_mask,
+    int32_t mask_words, int32_t* pages_needed, int32_t* status, void* cuda_stream) {
   if (window < 1) return PA_EINVAL;
   return pa::build_tables(cached_lens, new_lens, batch, block_table, table_width, free_pages, num_free, parents,
                           page_size, 0, window, indptr, indices, index_capacity, last_page_len, first_page_offset,

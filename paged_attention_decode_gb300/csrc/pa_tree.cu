@@ -48,14 +48,15 @@
 // and V when nothing else reads them; it takes 3100-3250: a row's softmax (1550:
 // reading S, the maximum, 128 exponentials, packing, writing P) and the PV and S
 // products that need it and that it needs (1250) follow one another within a
-// stream, and the other stream fills most of the gap.  Around the tiles stand
-// 6.5 us of start (cold code, barriers, tensor memory, the cut, the page list, Q
-// and the first K tile) and, after a cut block, 2-4 us of epilogue and 5 us of
-// merge.  16 bits, 32 query heads on 8 KV heads, D = 128, replayed from a graph: 64
-// tokens over 32K 46.6 us (20 us of HBM reads), 4 x 256 tokens over 32K 400 us
-// (1.37 PFLOP/s of 1.92 measured with cuBLAS), 16 ragged requests 99 us (4.4
-// TB/s), 32 chains of 5 tokens with a 4096-token window 72.4 us (5.2 TB/s), 8
-// tokens over 1K 15.5 us (nearly all start and merge).
+// stream, and the other stream fills most of the gap.  Around the tiles stand 6 to
+// 8 us of start (cold code, barriers, tensor memory, the cut, the page list, Q
+// and the first K tile) and, after a cut block, 2-4 us of epilogue, 1.4 us between
+// the kernels and 3-6 us of merge.  16 bits, 32 query heads on 8 KV heads, D = 128,
+// replayed from a graph: 64 tokens over 32K 46.6 us (20 us of HBM reads), 4 x 256
+// tokens over 32K 400 us (1.37 PFLOP/s of 1.92 measured with cuBLAS) at 2070 MHz
+// and 440 where the power cap holds the clock at 1800, 16 ragged requests 100 us
+// (4.4 TB/s), 32 chains of 5 tokens with a 4096-token window 73 us (5.2 TB/s), 8
+// tokens over 1K 15.2 us (nearly all start and merge).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -82,7 +83,7 @@ constexpr int kTrSlots = 2;       // partial results per CTA (see rest_slot)
 // piece before written, Q fetched, the first tile's softmax and the edges of the request (5 to 7 us, about 1.5 us a
 // tile), and, with two, keys that no CTA beside reads at the time.  Sweeps over 4 x 256 tokens and 64 tokens over 32K,
 // 16 ragged requests and 32 windowed chains: 2 / 2 gives 493, 44.8, 136 and 92 us, 6 / 6 gives 436, 44.6, 105 and 80,
-// 4 / 12 gives 400, 46.9, 99 and 72.5, 4 / 24 gives 415, 46.9, 104 and 72.6.
+// 4 / 12 gives 400, 46.9, 99 and 72.5, 4 / 24 gives 415, 46.9, 104 and 72.6.  (D = 128; short contexts were not swept.)
 constexpr int kTrCost1 = 4, kTrCost2 = 12;
 constexpr int kTrMmaWarp = 8, kTrLoadWarp = 9, kTrFixWarp = 11;
 constexpr int kTrLoadThreads = 64;  // loader threads without TMA
@@ -99,7 +100,8 @@ template <int D>
 struct TreeCfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kTrTile * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : 9;  // all the shared memory that the Q tiles leave
+  // D = 128: all the shared memory that the Q tiles leave; D = 64: room for two more is left
+  static constexpr int kStages = D == 128 ? 5 : 9;
   static constexpr int kOffKv = 2 * kTileBytes;     // Q tiles first
   static constexpr int kOffMisc = kOffKv + kStages * kTileBytes;
   static constexpr int kMisc = D == 128 ? 2048 : 4096;  // barriers, pieces, small exchanges
@@ -111,7 +113,9 @@ struct TreeCfg {
 // P is rounded to 16 bits relative to 2^kShift at the row's offset, and the offset follows the running maximum
 // with a lag of up to kLazy (log2 units).  bf16 has f32's range and takes a wide lag.  f16 holds nothing below
 // 2^-24: the shift keeps weights down to 2^-35 of the largest (a long context can hold thousands of those), and
-// 2^(kShift + kLazy) stays below its largest value.
+// 2^(kShift + kLazy) stays below its largest value.  One 16-bit term: a second one for what the rounding drops would
+// be a second product of P and V, half as much tensor work again; the outputs' relative error is 1.1 to 1.4 times
+// that of f32 weights (bf16 0.0023 against 0.0017, f16 0.00024 to 0.00028 against 0.00021).
 template <typename T> struct PRange;
 template <> struct PRange<__half> { static constexpr float kShift = 11.f, kLazy = 4.f; };
 template <> struct PRange<__nv_bfloat16> { static constexpr float kShift = 0.f, kLazy = 8.f; };
