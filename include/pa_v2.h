@@ -651,12 +651,13 @@ pa_status pa_v2_decode_noalloc(const pa_v2_plan_t* plan, const float* q, const v
  * The lengths are read, not advanced: the same call again gives the same
  * result.  DEVICE pointers; indices [index_capacity], slots and positions (and
  * parents) [token_capacity].  Bad data is recorded in `status` and contained: a
- * request with a negative length (no token where it is new_lens) or that needs
- * more pages than table_width gets no page and slots -1 (PA_DEVICE_BAD_LENGTH); pages or tokens
- * past a capacity are not written (the same bit); a page the free list does not
- * have is -1 (PA_DEVICE_NO_PAGES), as are the slots on it; a parent outside
- * [-1, i) makes token i a root, and a tree of more than 32 * mask_words tokens
- * loses the bits that do not fit (PA_DEVICE_BAD_TREE).
+ * request with a negative length (a negative new_lens counts as no token) or that
+ * needs more pages than table_width gets no page and slots -1
+ * (PA_DEVICE_BAD_LENGTH); pages or tokens past a capacity are not written (the
+ * same bit); a page the free list does not have is -1 (PA_DEVICE_NO_PAGES), as
+ * are the slots on it; a parent outside [-1, i) makes token i a root, and a tree
+ * of more than 32 * mask_words tokens loses the bits that do not fit
+ * (PA_DEVICE_BAD_TREE).
  * PA_EINVAL: null pointers, negative sizes, page_size < 1, window < 0,
  * mask_words < 1 with a tree_mask.  PA_EUNSUPPORTED: batch above
  * PA_V2_MAX_TABLE_BATCH, batch * table_width or token_capacity * mask_words
