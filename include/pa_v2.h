@@ -72,7 +72,9 @@ typedef enum pa_status {
     PA_EOOB = -6           /* device-side out-of-range data (see pa_status_from_device) */
 } pa_status;
 
-typedef enum pa_dtype { PA_F32 = 0, PA_F16 = 1, PA_BF16 = 2 } pa_dtype;
+/* PA_E4M3: the codes of the 8-bit cache; only pa_v2_qk_rope_append_fp8's and pa_v2_attention_fp8's pools hold
+ * them, and no call takes it as a kv_dtype. */
+typedef enum pa_dtype { PA_F32 = 0, PA_F16 = 1, PA_BF16 = 2, PA_E4M3 = 3 } pa_dtype;
 
 /* Device status bits (OR-ed into the optional status word). */
 #define PA_DEVICE_BAD_REQUEST   0x1  /* request_indices entry outside [0, batch) */
@@ -788,6 +790,80 @@ pa_status pa_v2_tree_attention_sliding(const void* q, const void* k_pool, const 
                                        const int32_t* positions, int32_t window, float sm_scale, void* out,
                                        float* lse2_out, void* workspace, int64_t workspace_bytes, int32_t* status,
                                        void* cuda_stream);
+
+/* ---- the 8-bit cache ----
+ *
+ * Pools of e4m3 codes (4 exponent bits, 3 mantissa bits, no infinity, 0x7f and
+ * 0xff NaN) [num_pages, page_size, num_kv_heads, head_dim], half the bytes of a
+ * 16-bit cache, with one exponent per page and KV head, k_exp and v_exp int8
+ * [num_pages, num_kv_heads]: an element is code * 2^exponent.  Exponents lie in
+ * [PA_V2_FP8_EXP_MIN, PA_V2_FP8_EXP_MAX]: every element is then a binary16
+ * number (2^-24 .. 57344), so that the attention multiplies what is stored
+ * without rounding it again, and a power of two costs a code no bits.  Others
+ * that the arrays hold are taken for the nearer end of the range. */
+#define PA_V2_FP8_EXP_MIN (-15)
+#define PA_V2_FP8_EXP_MAX 7
+
+/* pa_v2_qk_rope_append_fp8: pa_v2_qk_rope_append (its norm, rotation, q_out and
+ * arguments) into such pools.  The tokens of one page must be neighbours in the
+ * call, as pa_v2_build_tables' slots are: they form a run.  For each run, each
+ * KV head and each side, with x the rotated k (f32) or v:
+ *  - need = the least exponent whose largest code, 448 * 2^need, holds the
+ *    finite |x| of the run, within the range above;
+ *  - a run with the page's entry 0 begins the page: exponent = need.  Else the
+ *    entries before the run's least hold earlier tokens and the exponent never
+ *    falls: exponent = max(old, need), and where it grows the earlier entries'
+ *    codes become round(code * 2^(old - exponent)), which only codes that turn
+ *    subnormal lose bits by;
+ *  - code = round(x / 2^exponent) to nearest even, magnitudes above
+ *    448 * 2^PA_V2_FP8_EXP_MAX to that, infinities and NaN to NaN.
+ * The other entries of the page keep their codes: no token lies there.  A token
+ * with a negative slot is padding, one with a slot past the pool is skipped and
+ * recorded (PA_DEVICE_BAD_SLOT); either ends a run, so padding lies behind the
+ * last token.  Slots must be distinct, q_out must not overlap an input.
+ * Arguments, types and refusals as pa_v2_qk_rope_append, dtype that of q, k and
+ * v; page_size up to 256 (PA_EUNSUPPORTED above). */
+pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                   int64_t v_stride, int32_t dtype, int32_t num_tokens, int32_t num_qo_heads,
+                                   int32_t num_kv_heads, int32_t head_dim, const int32_t* positions,
+                                   const int32_t* slots, const float* inv_freq, int32_t rot_dim, int32_t interleaved,
+                                   const void* q_weight, const void* k_weight, float eps, void* q_out,
+                                   int32_t q_dtype, void* k_pool, void* v_pool, int8_t* k_exp, int8_t* v_exp,
+                                   int64_t num_pages, int32_t page_size, int32_t* status, void* cuda_stream);
+
+/* pa_v2_attention_fp8: attention of each request's new tokens (one each is a
+ * decode step) over the 8-bit cache: page table, new tokens, tree_mask, out and
+ * lse2_out as in pa_v2_tree_attention, whose rules on rows that see nothing and
+ * on hidden values hold here too (a NaN code is the only non-finite value), q
+ * and out of q_dtype (f16 or bf16).  window 0: a token sees all earlier ones.
+ * window >= 1: the token at position x sees the positions y <= x with y < sinks
+ * or y > x - window; of the new tokens a tree_mask alone decides
+ * (pa_v2_build_tables_sliding cuts one).  Positions are counted from the first
+ * listed row; positions [num_tokens] int32 (as the tables give them) tell how
+ * deep in its tree a token stands and are needed with a tree_mask and a window
+ * (PA_EINVAL without); a chain does without them (null), and where they are given
+ * a table that lists less than what they and the window ask for is refused
+ * (PA_DEVICE_BAD_TREE, zeros and -inf), as pa_v2_tree_attention_sliding does.
+ * With sinks the table lists the whole request (first_page_offset 0, and
+ * positions, if given, that start at the number of earlier tokens), else it is
+ * refused in the same way; entries of pages that nobody sees are not read and may be
+ * anything, so a program gives back the pages between sinks and window.
+ * P = exp(s) enters the second product rounded to f16; scores, statistics and sums are f32.
+ * PA_EINVAL: sinks without a window.  PA_EUNSUPPORTED: as pa_v2_tree_attention, and batch
+ * above 2^20.  The workspace (pa_v2_attention_fp8_workspace's size, 16-byte
+ * aligned) needs no initialisation; two calls sharing it must not overlap on
+ * the GPU. */
+pa_status pa_v2_attention_fp8_workspace(int32_t device, int32_t num_tokens, int32_t batch, int32_t num_qo_heads,
+                                        int32_t num_kv_heads, int32_t head_dim, int64_t* bytes);
+pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const void* k_pool, const void* v_pool,
+                              const int8_t* k_exp, const int8_t* v_exp, int64_t num_pages, int32_t page_size,
+                              int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, const int32_t* indices,
+                              int64_t num_indices, const int32_t* indptr, const int32_t* last_page_len,
+                              const int32_t* first_page_offset, int32_t batch, const int32_t* qo_indptr,
+                              int32_t num_tokens, const int32_t* tree_mask, int32_t mask_words,
+                              const int32_t* positions, int32_t window, int32_t sinks, float sm_scale, void* out,
+                              float* lse2_out, void* workspace, int64_t workspace_bytes, int32_t* status,
+                              void* cuda_stream);
 
 /* The variable-length merge (issue #898, design piece 3 and Task 3; PR
  * #984, What changed 3).  For output row r and head h, the rows

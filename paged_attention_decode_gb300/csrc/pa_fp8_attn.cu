@@ -1,0 +1,1110 @@
+// pa_fp8_attn.cu -- pa_v2_attention_fp8: attention of each request's new tokens (one,
+// a chain or a tree of them) over a paged cache of e4m3 codes with a power-of-two
+// exponent for each page and KV head.
+//
+//   k_j = 2^ek(page of j) kc_j,   v_j likewise,
+//   s_ij = scale log2(e) 2^ek(j) q_i . kc_j,  out_i = sum 2^(s_ij - m_i) v_j / sum 2^(s_ij - m_i),
+// one pass over the keys with a running maximum m and sum in f32.  The codes become f16
+// in registers (exactly), q is f16 times a power of two of its row (exact but for
+// elements 2^-24 of the row's largest and below), and the exponents, -15 .. 7, keep every
+// 2^ev vc a binary16 number: both products of m16n8k16 have exact operands but for P,
+// which is rounded to f16 once, 2^kF8Shift at the row's offset so that weights down to
+// 2^-35 of the largest survive (2^-11 each, where the f16 or bf16 output rounds by 2^-11 or
+// 2^-8 anyhow); scores, statistics and sums are f32.
+//
+// Work.  The query rows of a KV head (n * G pairs of new token and head) are taken in
+// blocks of 8 NT; one block against one tile of 32 pool rows (page order) is a unit.  The
+// units of the batch in order (request, KV head, block, tile) are cut into equal runs, one
+// for each warp of one CTA per SM: no host plan, no wave tail, whatever the lengths.  A
+// warp that meets a block's tiles alone writes its result; parts of the same block in
+// one CTA are joined in shared memory, and CTAs that share a block leave one partial
+// result each, which pa_v2_fp8_merge_kernel folds.
+//
+// A warp owns a ring of stages (a stage: 32 K rows and 32 V rows of D bytes) and walks
+// its units without a block barrier: TMA boxes, 128- or 64-byte swizzled, or 16-byte
+// cp.async copies for page sizes that do not start on 8-row boundaries.  S^T = K Q^T takes
+// the K rows as the A operand: a lane's fragment is the 16 dims of one LDS.128 per four
+// k-steps, since the order of the dims is free as long as q's is the same.  O^T += V^T P^T
+// takes V through ldmatrix.trans of byte pairs: a register holds two tokens x two dims,
+// one byte permutation apart from the two A registers it becomes.  P^T goes from the
+// accumulator's layout to the B operand's by movmatrix.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "pa_internal.cuh"
+#include "pa_mma.cuh"
+#include "pa_pool_map.h"
+#include "pa_tc05.cuh"
+#include "pa_v2.h"
+
+namespace pa {
+namespace {
+
+constexpr int kF8Warps = 8;
+constexpr int kF8Threads = 32 * kF8Warps;
+constexpr int kF8Tile = 32;       // keys of a unit
+constexpr int kF8Infos = 8;       // requests a warp's ring can have under way, a power of two
+constexpr float kF8Shift = 11.f;  // P is rounded relative to 2^kF8Shift at the row's offset,
+constexpr float kF8Lazy = 4.f;    // which follows the running maximum with a lag of up to kF8Lazy (log2 units)
+constexpr int kF8MaxRows = 32;    // query rows of a block, at most
+constexpr int kMergeWarps = 8;
+constexpr int64_t kF8MaxUnits = 1ll << 40;  // units of one request, at most
+
+template <int D, int NT>
+struct F8Cfg {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kSide = kF8Tile * D;    // bytes of a stage's K, or V
+  static constexpr bool kQSmem = NT > 2;       // q's fragments live in shared memory: 16 NT registers are too many
+  static constexpr int kStages = (D == 128 ? 1 : 2) * (kQSmem ? 2 : 3);
+  static constexpr int kRing = kStages * 2 * kSide;
+  static constexpr int kQ = kQSmem ? kRows * D * 2 : 0;
+  static constexpr int kOffQ = kF8Warps * kRing;
+  static constexpr int kOffMeta = kOffQ + kF8Warps * kQ;
+};
+
+struct F8Header;
+
+struct F8Params {
+  const void* q;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const int8_t* k_exp;
+  const int8_t* v_exp;
+  const int32_t* indices;
+  const int32_t* indptr;
+  const int32_t* last_page_len;
+  const int32_t* first_page_offset;
+  const int32_t* qo_indptr;
+  const int32_t* tree_mask;
+  const int32_t* positions;
+  void* out;
+  float* lse_out;
+  float* warp_parts;   // [ctas * kF8Warps][kF8MaxRows * head_dim]
+  float* cta_parts;    // [ctas][2][kF8MaxRows * (head_dim + 1)]
+  F8Header* headers;   // [ctas]
+  int32_t* status;
+  int64_t num_pages, num_indices;
+  int32_t batch, num_tokens, mask_words, page_size, box_rows, hq, hkv, group, ctas, q_bf16;
+  uint32_t ps_magic, ps_shift, g_magic, g_shift;
+  float scale_log2;
+  int32_t window, sinks;  // 0: no window
+};
+
+// One request: rows are pool rows in page order, counted from its first listed page.
+struct F8Req {
+  int32_t kind;        // 0: no new token, 1: nothing visible or a bad table (zeros and -inf), 2: keys
+  int32_t slot_base, t0, n;
+  int32_t lo, hi, ds;  // listed rows [lo, hi), new tokens [ds, hi)
+  int32_t sink_end;    // rows [lo, sink_end) are seen by all, as far as they come before a token (sink_end <= hi)
+  int32_t win0;        // the first row that the window of the first new token shows
+  int32_t ns, gap;     // the first ns tiles hold sinks, the others lie `gap` further on
+  int32_t tiles, blocks;
+  __device__ __forceinline__ int32_t tile(int32_t v) const { return v < ns ? v : v + gap; }
+  // some new token sees row x
+  __device__ __forceinline__ bool seen(int32_t x) const { return x < hi && (x >= win0 || (x >= lo && x < sink_end)); }
+};
+constexpr int kF8Empty = 1, kF8Keys = 2;
+
+template <int ROWS>
+__device__ __forceinline__ F8Req f8_req(const F8Params& p, int r, bool tell) {
+  F8Req g = {};
+  const int32_t a = p.qo_indptr[r], b = p.qo_indptr[r + 1];
+  const int32_t s0 = p.indptr[r], s1 = p.indptr[r + 1];
+  const int32_t lpl = p.last_page_len[r], fpo = p.first_page_offset[r];
+  if (a < 0 || b < a || b > p.num_tokens) {
+    if (tell) report(p.status, PA_DEVICE_BAD_INDPTR);
+    return g;
+  }
+  if (a == b) return g;
+  g.slot_base = s0;
+  g.t0 = a;
+  g.n = b - a;
+  g.blocks = (int32_t)(((int64_t)g.n * p.group + ROWS - 1) / ROWS);  // num_tokens * group fits 31 bits (checked by the host)
+  g.kind = kF8Empty;
+  g.tiles = 1;
+  const int64_t pages = (int64_t)s1 - s0;
+  if (s0 < 0 || pages < 0 || s1 > p.num_indices || pages * p.page_size > INT32_MAX - 2 * kF8Tile) {
+    if (tell) report(p.status, PA_DEVICE_BAD_SLOT);
+    return g;
+  }
+  const int32_t hi = pages > 0 ? ((int32_t)pages - 1) * p.page_size + lpl : 0;
+  const int32_t ds = hi - g.n;
+  bool bad = pages == 0 || lpl < 1 || lpl > p.page_size || fpo < 0 || fpo >= p.page_size || ds < fpo ||
+             (p.tree_mask && g.n > 32 * p.mask_words);
+  if (!bad && p.window > 0) {
+    // sinks are the request's first tokens, so all of it is listed; else what the first new token's window shows
+    if (p.sinks > 0) bad = fpo != 0 || (p.positions && p.positions[a] != ds);
+    else bad = p.positions && ds - fpo < min(p.positions[a], p.window - 1);
+  }
+  const int32_t win0 = p.window > 0 ? (int32_t)max((int64_t)fpo, (int64_t)ds + 1 - p.window) : fpo;
+  const int32_t sink_end = p.window > 0 && p.sinks > 0 ? min(p.sinks, hi) : fpo;
+  const int32_t last = (hi + kF8Tile - 1) / kF8Tile, near = win0 / kF8Tile;
+  const int32_t ns = sink_end > fpo ? min((sink_end + kF8Tile - 1) / kF8Tile, near) : 0;
+  const int32_t first = ns > 0 ? 0 : near;  // sinks mean fpo = 0
+  const int32_t tiles = ns + last - max(ns, near);
+  if (!bad && (int64_t)g.blocks * tiles > kF8MaxUnits / p.hkv) bad = true;
+  if (bad) {
+    if (tell) report(p.status, PA_DEVICE_BAD_TREE);
+    return g;
+  }
+  g.kind = kF8Keys;
+  g.lo = fpo;
+  g.hi = hi;
+  g.ds = ds;
+  g.sink_end = sink_end;
+  g.win0 = win0;
+  g.ns = ns > 0 ? ns : 0;
+  g.gap = ns > 0 ? max(ns, near) - ns : first;
+  g.tiles = tiles;
+  return g;
+}
+
+__device__ __forceinline__ int64_t units_of(const F8Params& p, const F8Req& g) {
+  return g.kind == 0 ? 0 : (int64_t)g.blocks * g.tiles * p.hkv;
+}
+
+// What the loading side of a warp tells the computing side of a stage.
+struct F8Unit {
+  int32_t info, kvh, blk, v;
+};
+struct alignas(16) F8Meta {
+  float k_scale[kF8Tile];
+  __half v_scale[kF8Tile];
+  F8Unit unit;
+};
+
+// A block's keys that a warp met only part of.
+struct F8Part {
+  int32_t valid, from_prev, to_next, in_ring;
+  int32_t t0, row0, rows, kvh;
+  int64_t end;  // the unit behind the block's last
+};
+
+// A block that begins in a CTA and goes on in the next: what CTA x of the merge kernel folds.
+struct alignas(16) F8Header {
+  int32_t valid, t0, row0, rows, kvh, last_cta, pad[2];
+};
+
+// Bits [a, b) of a word, a and b clamped to [0, 32].
+__device__ __forceinline__ uint32_t bits_between(int a, int b) {
+  a = max(a, 0);
+  b = min(b, 32);
+  if (a >= b) return 0u;
+  return (b >= 32 ? 0xffffffffu : ((1u << b) - 1u)) & ~((1u << a) - 1u);
+}
+
+// The first row that new token i of the request sees through its window: at depth d behind the request's first new
+// token (a chain: d = i) rows up to ds + d - window are hidden.
+__device__ __forceinline__ int32_t window_from(const F8Params& p, const F8Req& g, int32_t i) {
+  if (p.window == 0) return g.lo;
+  const int32_t depth =
+      p.tree_mask ? min(max(__ldg(p.positions + g.t0 + i) - __ldg(p.positions + g.t0), 0), i) : i;
+  return (int32_t)max((int64_t)g.lo, (int64_t)g.ds + depth + 1 - p.window);
+}
+
+// Which of the rows base .. base + 31 new token i sees, its window beginning at `low`.
+__device__ __forceinline__ uint32_t seen_bits(const F8Params& p, const F8Req& g, int32_t i, int32_t low, int32_t base) {
+  uint32_t bits = bits_between(low - base, g.ds - base) | bits_between(g.lo - base, min(g.sink_end, g.ds) - base);
+  if (base + kF8Tile > g.ds && base < g.hi) {
+    if (p.tree_mask) {  // the mask holds the window's cut of the new tokens itself
+      const int32_t* row = p.tree_mask + (int64_t)(g.t0 + i) * p.mask_words;
+      const int at = base - g.ds;  // new-token number of bit 0
+      const int w = at >> 5, sh = at & 31;
+      const uint32_t x0 = w >= 0 && w < p.mask_words ? (uint32_t)__ldg(row + w) : 0u;
+      const uint32_t x1 = w + 1 >= 0 && w + 1 < p.mask_words ? (uint32_t)__ldg(row + w + 1) : 0u;
+      bits |= __funnelshift_r(x0, x1, sh) & bits_between(g.ds - base, g.hi - base);
+    } else {
+      const int32_t end = min(g.ds + i + 1, g.hi);
+      bits |= bits_between(max(g.ds, low) - base, end - base) | bits_between(g.ds - base, min(g.sink_end, end) - base);
+    }
+  }
+  return bits;
+}
+
+// Two e4m3 codes as f16, exactly.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t x) {
+  uint32_t y;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t codes_hi(uint32_t x) {
+  uint32_t y;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {  // once this thread's cp.async copies so far have landed
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// Byte offset of 16-byte chunk `ch` of row `row` of a side.
+template <int D>
+__device__ __forceinline__ uint32_t side_at(int row, int ch) {
+  return D == 128 ? (uint32_t)(row * 128 + ((ch ^ (row & 7)) << 4)) : (uint32_t)(row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ uint32_t pack16(const F8Params& p, float a, float b) {
+  return p.q_bf16 ? TC<__nv_bfloat16>::pack(a, b) : TC<__half>::pack(a, b);
+}
+
+// Row `row` of a request's rows of KV head kvh, as a row of q and out.
+__device__ __forceinline__ int64_t out_row_of(const F8Params& p, int32_t t0, int32_t kvh, int32_t row) {
+  const int32_t tok = (int32_t)fast_div((uint32_t)row, p.g_magic, p.g_shift);
+  return (int64_t)(t0 + tok) * p.hq + (int64_t)kvh * p.group + (row - tok * p.group);
+}
+
+template <int D, int NT, bool TMA>
+__global__ void __launch_bounds__(kF8Threads, 1)
+    pa_v2_attention_fp8_kernel(const F8Params p, const __grid_constant__ CUtensorMap tm_k,
+                               const __grid_constant__ CUtensorMap tm_v) {
+  using C = F8Cfg<D, NT>;
+  constexpr int S = C::kStages, R = C::kRows, KS = D / 16;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t bars[kF8Warps][S];
+  __shared__ F8Req infos[kF8Warps][kF8Infos];
+  __shared__ F8Part parts[kF8Warps][2];
+  __shared__ float stats[kF8Warps][2][2][kF8MaxRows];  // [part][maxima, sums]
+  __shared__ int64_t warp_sum[kF8Warps];
+  __shared__ int64_t start_off[kF8Warps];
+  __shared__ int32_t start_req[kF8Warps];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  unsigned char* ring = smem + warp * C::kRing;
+  F8Meta* meta = reinterpret_cast<F8Meta*>(smem + C::kOffMeta) + warp * S;
+  uint64_t* full = bars[warp];
+
+  pdl_launch_dependents();
+  if (lane == 0) {
+    for (int i = 0; i < S; ++i) mbar_init(&full[i], TMA ? 1 : 32);
+    fence_barrier_init();
+    parts[warp][0].valid = parts[warp][1].valid = 0;
+    start_req[warp] = -1;
+  }
+  pdl_wait_prerequisites();
+
+  // ---- the cut: every warp's first unit
+  int64_t units = 0, mine = 0;
+  const int per_thread = (p.batch + kF8Threads - 1) / kF8Threads;
+  const int r0 = (int)min((int64_t)threadIdx.x * per_thread, (int64_t)p.batch), r1 = min(r0 + per_thread, p.batch);
+  for (int r = r0; r < r1; ++r) mine += units_of(p, f8_req<R>(p, r, blockIdx.x == 0));
+  int64_t upto = mine;
+#pragma unroll
+  for (int w = 1; w < 32; w <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, upto, w);
+    if (lane >= w) upto += x;
+  }
+  if (lane == 31) warp_sum[warp] = upto;
+  __syncthreads();
+  int64_t before = upto - mine;
+  for (int w = 0; w < kF8Warps; ++w) {
+    if (w < warp) before += warp_sum[w];
+    units += warp_sum[w];
+  }
+  const int64_t workers = (int64_t)gridDim.x * kF8Warps;
+  const int64_t run = max((units + workers - 1) / workers, (int64_t)1);
+  if (mine > 0) {
+    const int64_t first = (int64_t)blockIdx.x * kF8Warps * run;
+    if (before + mine > first && before < first + kF8Warps * run) {
+      int64_t at = before;
+      for (int r = r0; r < r1; ++r) {
+        const int64_t u = units_of(p, f8_req<R>(p, r, false));
+        for (int w = 0; w < kF8Warps; ++w) {
+          const int64_t x = first + w * run;
+          if (x >= at && x < at + u) {
+            start_req[w] = r;
+            start_off[w] = x - at;
+          }
+        }
+        at += u;
+      }
+    }
+  }
+  __syncthreads();
+
+  const int64_t u0 = ((int64_t)blockIdx.x * kF8Warps + warp) * run;
+  const int64_t count = start_req[warp] < 0 ? 0 : min(run, units - u0);
+
+  // ---- the loading side: the next unit to load, its pages already on their way
+  F8Req lq = {};
+  int32_t l_r = 0, l_kvh = 0, l_blk = 0, l_v = 0, l_info = 0;
+  int32_t l_page = -2;      // this lane's row's page: -2 nobody sees it
+  uint32_t l_vis = 0;       // rows that somebody sees, whole boxes
+  int32_t pend_k = 0, pend_v = 0, pend_stage = -1;
+  const uint64_t policy = policy_evict_first(), keep = policy_evict_normal();
+
+  auto resolve = [&]() {  // the pages of unit (l_r, l_kvh, l_blk, l_v)
+    l_vis = 0;
+    l_page = -2;
+    if (lq.kind != kF8Keys) return;
+    const int32_t at = lq.tile(l_v) * kF8Tile + lane;
+    l_vis = __ballot_sync(0xffffffffu, lq.seen(at));
+    if (TMA) {  // whole boxes
+      const int b = lane / p.box_rows * p.box_rows;
+      l_vis = __ballot_sync(0xffffffffu, (l_vis & bits_between(b, b + p.box_rows)) != 0);
+    }
+    if (l_vis >> lane & 1u) {
+      const int32_t slot = (int32_t)fast_div((uint32_t)at, p.ps_magic, p.ps_shift);
+      l_page = __ldg(p.indices + lq.slot_base + slot);
+    }
+  };
+  auto enter = [&](int r) {  // the next request with units, from r on
+    for (;; ++r) {
+      lq = f8_req<R>(p, r, false);
+      if (lq.kind != 0) break;
+    }
+    l_r = r;
+    l_info = (l_info + 1) & (kF8Infos - 1);
+    if (lane == 0) infos[warp][l_info] = lq;
+  };
+  auto flush = [&]() {  // the exponents of the unit loaded last
+    if (pend_stage < 0) return;
+    meta[pend_stage].k_scale[lane] = power_of_two(min(max(pend_k, PA_V2_FP8_EXP_MIN), PA_V2_FP8_EXP_MAX));
+    meta[pend_stage].v_scale[lane] = __float2half_rn(power_of_two(min(max(pend_v, PA_V2_FP8_EXP_MIN), PA_V2_FP8_EXP_MAX)));
+    pend_stage = -1;
+  };
+  auto issue = [&](int stage, bool more) {  // load the unit, and go on to the next one if there is one
+    flush();
+    unsigned char* kd = ring + stage * 2 * C::kSide;
+    const bool good = l_page >= 0 && l_page < p.num_pages;
+    const int32_t at = lq.tile(l_v) * kF8Tile + lane;
+    // a bad page: past the pool, where a box is zero-filled
+    int32_t row = TMA ? (int32_t)(p.num_pages * p.page_size) : -1;
+    pend_k = pend_v = 0;
+    if (l_page != -2) {
+      const int32_t slot = (int32_t)fast_div((uint32_t)at, p.ps_magic, p.ps_shift);
+      if (good) {
+        row = l_page * p.page_size + (at - slot * p.page_size);
+        const int64_t e = (int64_t)l_page * p.hkv + l_kvh;
+        pend_k = __ldg(p.k_exp + e);
+        pend_v = __ldg(p.v_exp + e);
+      } else {
+        report(p.status, PA_DEVICE_BAD_PAGE);
+      }
+    }
+    pend_stage = stage;
+    if (lane == 0) meta[stage].unit = F8Unit{l_info, l_kvh, l_blk, l_v};
+    // rows that several blocks read stay in L2 as other data does, the others leave it first
+    const uint64_t pol = lq.blocks > 1 ? keep : policy;
+    if (TMA) {
+      const int step = p.box_rows;
+      if (lane == 0) {
+        const uint32_t bytes = (uint32_t)__popc(l_vis) * D * 2;
+        if (bytes) mbar_arrive_expect_tx(&full[stage], bytes);
+        else arrive(&full[stage]);
+      }
+      for (int b = 0; b < kF8Tile; b += step) {
+        const int32_t y = __shfl_sync(0xffffffffu, row, b);
+        if (lane == 0 && (l_vis >> b & 1u)) {
+          tma_load_3d(kd + b * D, &tm_k, &full[stage], 0, l_kvh, y, pol);
+          tma_load_3d(kd + C::kSide + b * D, &tm_v, &full[stage], 0, l_kvh, y, pol);
+        }
+      }
+    } else {
+      constexpr int kChunks = D / 16, kPass = 32 / kChunks;
+      const int ch = lane % kChunks, sub = lane / kChunks;
+      const int64_t pitch = (int64_t)p.hkv * D;
+      const uint32_t to = smem_addr(kd);
+#pragma unroll
+      for (int i = 0; i < kF8Tile; i += kPass) {
+        const int32_t y = __shfl_sync(0xffffffffu, row, i + sub);
+        const uint32_t d = to + side_at<D>(i + sub, ch);
+        if (y >= 0) {
+          const int64_t from = y * pitch + (int64_t)l_kvh * D + ch * 16;
+          cp_async_16(d, p.k_pool + from, pol);
+          cp_async_16(d + C::kSide, p.v_pool + from, pol);
+        } else {
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(d), "r"(0u) : "memory");
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(d + C::kSide), "r"(0u) : "memory");
+        }
+      }
+      copies_arrive(&full[stage]);
+    }
+    if (more) {
+      if (++l_v == lq.tiles) {
+        l_v = 0;
+        if (++l_blk == lq.blocks) {
+          l_blk = 0;
+          if (++l_kvh == p.hkv) {
+            l_kvh = 0;
+            enter(l_r + 1);
+          }
+        }
+      }
+      resolve();
+    }
+    __syncwarp();
+  };
+
+  int64_t issued = 0;
+  if (count > 0) {
+    enter(start_req[warp]);
+    const int64_t off = start_off[warp], head = (int64_t)lq.blocks * lq.tiles;
+    l_kvh = (int32_t)(off / head);
+    const int64_t in_head = off - l_kvh * head;
+    l_blk = (int32_t)(in_head / lq.tiles);
+    l_v = (int32_t)(in_head - (int64_t)l_blk * lq.tiles);
+    resolve();
+    for (; issued < min(count, (int64_t)S); ++issued) issue((int)issued, issued + 1 < count);
+    if (issued == count) flush();
+    __syncwarp();
+  }
+
+  // ---- the computing side
+  float o[KS][NT][4];           // O^T: dims 16 c + 2 g, + 1 (elements 0, 2 and 1, 3's rows), columns 2 t, 2 t + 1
+  uint32_t qb[C::kQSmem ? 1 : KS][C::kQSmem ? 1 : NT][2];
+  float m[NT][2], l[NT][2];     // of columns 2 t and 2 t + 1; sums over this lane's keys
+  float qf[NT][2];              // scale of the columns' scores
+  uint2* qs = reinterpret_cast<uint2*>(smem + C::kOffQ + warp * C::kQ);  // [KS][NT][32], with kQSmem
+  int32_t low = 0, tok = -1, clear0 = 0;  // of the row on this lane; rows [clear0, ds) are seen by all of the block's
+  F8Req cq = {};
+  int32_t rows = 0, row0 = 0, kvh = 0, v_first = 0;
+  bool alive = true;
+  int stage = 0;
+  uint32_t parity = 0;
+  for (int64_t j = 0; j < count; ++j) {
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[stage], parity, kWaitLimitCycles))) {
+      report(p.status, PA_DEVICE_WAIT_TIMEOUT);
+      alive = false;
+      break;
+    }
+    const F8Unit unit = meta[stage].unit;
+    if (j == 0 || unit.v == 0) {
+      // ---- a block begins (here): its rows, Q and an empty state
+      cq = infos[warp][unit.info];
+      kvh = unit.kvh;
+      row0 = unit.blk * R;
+      rows = (int32_t)min((int64_t)R, (int64_t)cq.n * p.group - row0);
+      v_first = unit.v;
+      const int32_t last_tok = (int32_t)fast_div((uint32_t)(row0 + rows - 1), p.g_magic, p.g_shift);
+      tok = lane < rows ? (int32_t)fast_div((uint32_t)(row0 + lane), p.g_magic, p.g_shift) : -1;
+      if (cq.kind == kF8Keys) {
+        low = tok >= 0 ? window_from(p, cq, tok) : 0;
+        clear0 = p.window > 0 ? (int32_t)max((int64_t)cq.lo, (int64_t)cq.ds + last_tok + 1 - p.window) : cq.lo;
+        constexpr int kMine = D / 4;  // dims of a lane: t D / 4 ..
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int32_t c = nt * 8 + g;
+          float x[kMine];
+          float top = 0.f;
+          if (c < rows) {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                static_cast<const uint16_t*>(p.q) + out_row_of(p, cq.t0, kvh, row0 + c) * D + t * kMine);
+#pragma unroll
+            for (int i = 0; i < kMine / 8; ++i) {
+              const uint4 u = __ldg(src + i);
+              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float2 f;
+                if (p.q_bf16) f = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+                else f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                x[8 * i + 2 * k] = f.x;
+                x[8 * i + 2 * k + 1] = f.y;
+                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) x[i] = 0.f;
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // the row's largest element to [2^13, 2^14)
+          int e = 13;
+          if (top > 0.f && top <= 3.4028234e38f) e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+          const float up = power_of_two(13 - e), down = power_of_two(e - 13) * p.scale_log2;
+          qf[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+          qf[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const uint32_t b0 = TC<__half>::pack(x[4 * k] * up, x[4 * k + 1] * up);
+            const uint32_t b1 = TC<__half>::pack(x[4 * k + 2] * up, x[4 * k + 3] * up);
+            if (C::kQSmem) {
+              qs[(k * NT + nt) * 32 + lane] = make_uint2(b0, b1);
+            } else {
+              qb[k][nt][0] = b0;
+              qb[k][nt][1] = b1;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+        for (int c = 0; c < KS; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[c][nt][i] = 0.f;
+      }
+    }
+
+    const int32_t base = cq.tile(unit.v) * kF8Tile;
+    const bool clear = base + kF8Tile <= cq.ds && (base >= clear0 || (base >= cq.lo && base + kF8Tile <= cq.sink_end));
+    uint32_t mine_bits = 0, some = 0xffffffffu;
+    bool skip = cq.kind != kF8Keys;
+    if (!clear && !skip) {
+      if (tok >= 0) mine_bits = seen_bits(p, cq, tok, low, base);
+      some = __reduce_or_sync(0xffffffffu, mine_bits);
+      skip = some == 0;
+    }
+    if (!skip) {
+      const uint32_t kb = smem_addr(ring + stage * 2 * C::kSide), vb = kb + C::kSide;
+      // ---- S^T
+      float s[2][NT][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t x[2][2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[i][h][0]), "=r"(x[i][h][1]), "=r"(x[i][h][2]), "=r"(x[i][h][3])
+                         : "r"(kb + side_at<D>(16 * i + 8 * h + g, t * (D / 64) + c))
+                         : "memory");
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int k = 4 * c + w;
+          uint32_t b[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (C::kQSmem) {
+              const uint2 u = qs[(k * NT + nt) * 32 + lane];
+              b[nt][0] = u.x;
+              b[nt][1] = u.y;
+            } else {
+              b[nt][0] = qb[k][nt][0];
+              b[nt][1] = qb[k][nt][1];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a[4] = {codes_lo(x[i][0][w]), codes_lo(x[i][1][w]), codes_hi(x[i][0][w]), codes_hi(x[i][1][w])};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) TC<__half>::mma(s[i][nt], a, b[nt][0], b[nt][1]);
+          }
+        }
+      }
+      // ---- scores in log2 units, softmax
+      const float ks[4] = {meta[stage].k_scale[g], meta[stage].k_scale[8 + g], meta[stage].k_scale[16 + g],
+                           meta[stage].k_scale[24 + g]};
+      uint32_t pb[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+        if (!clear) {
+          see[0] = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t);
+          see[1] = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t + 1);
+        }
+        float mt[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // token 16 i + 8 (k >> 1) + g, column 2 t + (k & 1)
+            const int q4 = 2 * i + (k >> 1);
+            float y = s[i][nt][k] * (ks[q4] * qf[nt][k & 1]);
+            if (!clear) y = see[k & 1] >> (8 * q4 + g) & 1u ? y : -INFINITY;
+            s[i][nt][k] = y;
+            mt[k & 1] = fmaxf(mt[k & 1], y);
+          }
+        float scale[2];
+        bool grow = false;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          mt[k] = fmaxf(mt[k], __shfl_xor_sync(0xffffffffu, mt[k], 4));
+          mt[k] = fmaxf(mt[k], __shfl_xor_sync(0xffffffffu, mt[k], 8));
+          mt[k] = fmaxf(mt[k], __shfl_xor_sync(0xffffffffu, mt[k], 16));
+          const bool need = mt[k] > m[nt][k] + kF8Lazy;  // m = -inf at first: any finite maximum
+          scale[k] = 1.f;
+          if (need) {
+            scale[k] = m[nt][k] == -INFINITY ? 0.f : fast_exp2(m[nt][k] - mt[k]);
+            m[nt][k] = mt[k];
+          }
+          l[nt][k] *= scale[k];
+          grow |= need;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int c = 0; c < KS; ++c) {
+            o[c][nt][0] *= scale[0];
+            o[c][nt][1] *= scale[1];
+            o[c][nt][2] *= scale[0];
+            o[c][nt][3] *= scale[1];
+          }
+        }
+        const float off[2] = {(m[nt][0] == -INFINITY ? 0.f : m[nt][0]) - kF8Shift,
+                              (m[nt][1] == -INFINITY ? 0.f : m[nt][1]) - kF8Shift};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float e0 = fast_exp2(s[i][nt][2 * h] - off[0]), e1 = fast_exp2(s[i][nt][2 * h + 1] - off[1]);
+            l[nt][0] += e0;
+            l[nt][1] += e1;
+            pb[nt][2 * i + h] = transposed(TC<__half>::pack(e0, e1));
+          }
+      }
+      // ---- O^T += V^T P^T
+      uint32_t vs[4];  // tokens 8 i + 2 t, + 1
+#pragma unroll
+      for (int i = 0; i < 4; ++i) vs[i] = *reinterpret_cast<const uint32_t*>(&meta[stage].v_scale[8 * i + 2 * t]);
+      if (clear) {
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+          uint32_t x[4];
+          ldsm_x4_trans(x, vb + side_at<D>(lane, c));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t y0 = __byte_perm(x[2 * h], 0, 0x3120), y1 = __byte_perm(x[2 * h + 1], 0, 0x3120);
+            const uint32_t a[4] = {mul_f16(codes_lo(y0), vs[2 * h]), mul_f16(codes_hi(y0), vs[2 * h]),
+                                   mul_f16(codes_lo(y1), vs[2 * h + 1]), mul_f16(codes_hi(y1), vs[2 * h + 1])};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) TC<__half>::mma(o[c][nt], a, pb[nt][2 * h], pb[nt][2 * h + 1]);
+          }
+        }
+      } else {
+        // what a row does not see must not meet its zero weight as a NaN: rows that nobody sees become zeros, and NaN
+        // codes of the others zeros that are put back below for the rows that see them
+        uint32_t vm[4], taint = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t u = some >> (8 * i + 2 * t);
+          vm[i] = (u & 1u ? 0x00ff00ffu : 0u) | (u & 2u ? 0xff00ff00u : 0u);
+        }
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+          uint32_t x[4];
+          ldsm_x4_trans(x, vb + side_at<D>(lane, c));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = __byte_perm(x[i], 0, 0x3120) & vm[i];
+            const uint32_t nan = __vcmpeq4(x[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            taint |= nan;
+            x[i] &= ~nan;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a[4] = {mul_f16(codes_lo(x[2 * h]), vs[2 * h]), mul_f16(codes_hi(x[2 * h]), vs[2 * h]),
+                                   mul_f16(codes_lo(x[2 * h + 1]), vs[2 * h + 1]),
+                                   mul_f16(codes_hi(x[2 * h + 1]), vs[2 * h + 1])};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) TC<__half>::mma(o[c][nt], a, pb[nt][2 * h], pb[nt][2 * h + 1]);
+          }
+        }
+        if (__any_sync(0xffffffffu, taint != 0)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t see0 = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t);
+            const uint32_t see1 = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t + 1);
+#pragma unroll
+            for (int c = 0; c < KS; ++c) {
+#pragma unroll 1
+              for (int k = 0; k < kF8Tile; ++k) {
+                uint16_t pair;  // dims 16 c + 2 g, + 1 of token k
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(pair) : "r"(vb + side_at<D>(k, c) + 2 * g) : "memory");
+                const bool n0 = (pair & 0x7f) == 0x7f, n1 = (pair >> 8 & 0x7f) == 0x7f;
+                if (see0 >> k & 1u) {
+                  if (n0) o[c][nt][0] = NAN;
+                  if (n1) o[c][nt][2] = NAN;
+                }
+                if (see1 >> k & 1u) {
+                  if (n0) o[c][nt][1] = NAN;
+                  if (n1) o[c][nt][3] = NAN;
+                }
+              }
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+
+    // ---- the block's last unit, or this warp's
+    const bool ends = unit.v + 1 == cq.tiles;
+    const bool last = j + 1 == count;
+    if (ends || last) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 4);
+          l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 8);
+          l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 16);
+        }
+      if (ends && v_first == 0) {  // all of it was met here
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int32_t c = 8 * nt + 2 * t + k;
+            if (c >= rows) continue;
+            const int64_t row = out_row_of(p, cq.t0, kvh, row0 + c);
+            const float sum = l[nt][k], inv = sum == 0.f ? 0.f : 1.f / sum;
+            uint32_t* to = static_cast<uint32_t*>(p.out) + row * (D / 2) + g;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) to[8 * i] = pack16(p, o[i][nt][k] * inv, o[i][nt][2 + k] * inv);
+            if (g == 0) p.lse_out[row] = sum == 0.f ? -INFINITY : m[nt][k] - kF8Shift + fast_log2(sum);
+          }
+      } else {
+        // a part: the warp's last in its ring, which nothing loads into any more, else in the workspace
+        const int part = last ? 1 : 0;
+        float* to = last ? reinterpret_cast<float*>(ring)
+                         : p.warp_parts + ((int64_t)blockIdx.x * kF8Warps + warp) * (kF8MaxRows * D);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int32_t c = 8 * nt + 2 * t + k;
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+              *reinterpret_cast<float2*>(to + c * D + 16 * i + 2 * g) = make_float2(o[i][nt][k], o[i][nt][2 + k]);
+            if (g == 0) {
+              stats[warp][part][0][c] = m[nt][k];
+              stats[warp][part][1][c] = l[nt][k];
+            }
+          }
+        if (lane == 0)
+          parts[warp][part] = F8Part{1, v_first != 0, !ends, last, cq.t0, row0, rows, kvh, u0 + j + (cq.tiles - unit.v)};
+      }
+    }
+    if (issued < count) {
+      issue(stage, issued + 1 < count);
+      ++issued;
+    } else {
+      flush();
+      __syncwarp();
+    }
+    if (++stage == S) {
+      stage = 0;
+      parity ^= 1;
+    }
+  }
+  if (!alive) {  // no copy of this warp is left in flight
+    for (int i = 0; i < S; ++i) {
+      mbar_wait_bounded(&full[stage], parity, kWaitLimitCycles);
+      if (++stage == S) {
+        stage = 0;
+        parity ^= 1;
+      }
+    }
+    if (!TMA) cp_async_wait<0>();
+    if (lane == 0) parts[warp][0].valid = parts[warp][1].valid = 0;
+  }
+  __syncthreads();
+
+  // ---- parts of the same block are joined: with those of other CTAs still to come, or as the result
+  if (threadIdx.x == 0) p.headers[blockIdx.x].valid = 0;
+  for (int i = 0; i < 2 * kF8Warps;) {
+    if (!parts[i >> 1][i & 1].valid) {
+      ++i;
+      continue;
+    }
+    const F8Part a = parts[i >> 1][i & 1];
+    uint32_t chain = 1u << i;
+    int end = i;
+    for (int k = i + 1; k < 2 * kF8Warps && parts[end >> 1][end & 1].to_next; ++k) {
+      if (!parts[k >> 1][k & 1].valid) continue;
+      chain |= 1u << k;
+      end = k;
+    }
+    const bool from_prev = a.from_prev != 0, to_next = parts[end >> 1][end & 1].to_next != 0;
+    float* slot = p.cta_parts + ((int64_t)blockIdx.x * 2 + (from_prev ? 0 : 1)) * (kF8MaxRows * (D + 1));
+    for (int e = threadIdx.x; e < a.rows * (D / 2); e += kF8Threads) {
+      const int c = e / (D / 2), d = e % (D / 2);
+      float M = -INFINITY;
+      for (uint32_t b = chain; b; b &= b - 1) {
+        const int k = __ffs(b) - 1;
+        M = fmaxf(M, stats[k >> 1][k & 1][0][c]);
+      }
+      float sum = 0.f;
+      float2 acc = make_float2(0.f, 0.f);
+      for (uint32_t b = chain; b; b &= b - 1) {
+        const int k = __ffs(b) - 1;
+        const float mk = stats[k >> 1][k & 1][0][c];
+        const float w = mk == -INFINITY ? 0.f : fast_exp2(mk - M);
+        float2 x;
+        if (k & 1) {
+          x = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(smem + (k >> 1) * C::kRing) + c * D + 2 * d);
+        } else {
+          x = __ldcg(reinterpret_cast<const float2*>(
+              p.warp_parts + ((int64_t)blockIdx.x * kF8Warps + (k >> 1)) * (kF8MaxRows * D) + c * D + 2 * d));
+        }
+        sum += w * stats[k >> 1][k & 1][1][c];
+        acc.x += w * x.x;
+        acc.y += w * x.y;
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const float lse = sum == 0.f ? -INFINITY : M - kF8Shift + fast_log2(sum);
+      if (from_prev || to_next) {
+        *reinterpret_cast<float2*>(slot + c * D + 2 * d) = make_float2(acc.x * inv, acc.y * inv);
+        if (d == 0) slot[kF8MaxRows * D + c] = lse;
+      } else {
+        const int64_t row = out_row_of(p, a.t0, a.kvh, a.row0 + c);
+        static_cast<uint32_t*>(p.out)[row * (D / 2) + d] = pack16(p, acc.x * inv, acc.y * inv);
+        if (d == 0) p.lse_out[row] = lse;
+      }
+    }
+    if (threadIdx.x == 0 && !from_prev && to_next)
+      p.headers[blockIdx.x] = F8Header{1, a.t0, a.row0, a.rows, a.kvh, (int32_t)((a.end - 1) / (run * kF8Warps)), {0, 0}};
+    i = end + 1;
+  }
+}
+
+// Folds the parts of a block that several CTAs met: weights 2^(lse_i - max) of the normalized parts.  CTA (x, y) takes
+// row y of the block that begins in CTA x of the attention kernel; its warps take every eighth part, joined in a fixed
+// order.
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) pa_v2_fp8_merge_kernel(const F8Params p) {
+  constexpr int V = D / 32;  // dims of a lane
+  __shared__ float sm[kMergeWarps], sl[kMergeWarps], so[kMergeWarps][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  pdl_wait_prerequisites();
+  const F8Header h = p.headers[blockIdx.x];
+  const int c = blockIdx.y;
+  if (!h.valid || c >= h.rows) return;
+  const int n = h.last_cta - (int)blockIdx.x + 1;
+  float M = -INFINITY, L = 0.f, acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  constexpr int kBatch = 4;
+  for (int k0 = warp; k0 < n; k0 += kBatch * kMergeWarps) {
+    float lse[kBatch], x[kBatch][V];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int k = k0 + b * kMergeWarps;
+      lse[b] = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[b][i] = 0.f;
+      if (k < n) {
+        const float* slot = p.cta_parts + ((int64_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * (kF8MaxRows * (D + 1));
+        lse[b] = __ldcg(slot + kF8MaxRows * D + c);
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(slot + c * D + V * lane + i));
+          x[b][i] = y.x;
+          x[b][i + 1] = y.y;
+        }
+      }
+    }
+    float mb = M;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) mb = fmaxf(mb, lse[b]);
+    const float mu = mb == -INFINITY ? 0.f : mb;
+    const float sc = M == -INFINITY ? 0.f : fast_exp2(M - mu);
+    L *= sc;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] *= sc;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (lse[b] == -INFINITY) continue;
+      const float w = fast_exp2(lse[b] - mu);
+      L += w;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = fmaf(w, x[b][i], acc[i]);
+    }
+    M = mb;
+  }
+  if (lane == 0) {
+    sm[warp] = M;
+    sl[warp] = L;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) so[warp][V * lane + i] = acc[i];
+  __syncthreads();
+  if (threadIdx.x >= D / 2) return;
+  float mx = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) mx = fmaxf(mx, sm[w]);
+  float sum = 0.f;
+  float2 out = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    const float f = sm[w] == -INFINITY ? 0.f : fast_exp2(sm[w] - mx);
+    sum += f * sl[w];
+    out.x += f * so[w][2 * threadIdx.x];
+    out.y += f * so[w][2 * threadIdx.x + 1];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t row = out_row_of(p, h.t0, h.kvh, h.row0 + c);
+  static_cast<uint32_t*>(p.out)[row * (D / 2) + threadIdx.x] = pack16(p, out.x * inv, out.y * inv);
+  if (threadIdx.x == 0) p.lse_out[row] = sum == 0.f ? -INFINITY : mx + fast_log2(sum);
+}
+
+using F8Kernel = void (*)(const F8Params, const CUtensorMap, const CUtensorMap);
+
+struct F8Pick {
+  F8Kernel fn;
+  int rows, smem;
+};
+template <int D, int NT>
+F8Pick pick_f8(bool tma) {
+  using C = F8Cfg<D, NT>;
+  return {tma ? pa_v2_attention_fp8_kernel<D, NT, true> : pa_v2_attention_fp8_kernel<D, NT, false>, C::kRows,
+          C::kOffMeta + (int)(kF8Warps * C::kStages * sizeof(F8Meta)) + 1024};
+}
+template <int D>
+F8Pick pick_f8(int64_t rows, bool tma) {
+  return rows <= 8 ? pick_f8<D, 1>(tma) : rows <= 16 ? pick_f8<D, 2>(tma) : pick_f8<D, 4>(tma);
+}
+
+bool f8_aligned(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }
+
+int64_t warp_part_bytes(int32_t ctas, int32_t head_dim) {
+  return (int64_t)ctas * kF8Warps * kF8MaxRows * head_dim * (int64_t)sizeof(float);
+}
+int64_t cta_part_bytes(int32_t ctas, int32_t head_dim) {
+  return (int64_t)ctas * 2 * kF8MaxRows * (head_dim + 1) * (int64_t)sizeof(float);
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" pa_status pa_v2_attention_fp8_workspace(int32_t device, int32_t num_tokens, int32_t batch,
+                                                   int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+                                                   int64_t* bytes) {
+  if (!bytes || device < 0 || num_tokens < 0 || batch < 0 || num_kv_heads < 1 || num_qo_heads < num_kv_heads ||
+      num_qo_heads % num_kv_heads)
+    return PA_EINVAL;
+  if (head_dim != 64 && head_dim != 128) return PA_EUNSUPPORTED;
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms < 1) {
+    cudaGetLastError();
+    return PA_ECUDA;
+  }
+  *bytes = pa::warp_part_bytes(sms, head_dim) + pa::cta_part_bytes(sms, head_dim) + sms * (int64_t)sizeof(pa::F8Header);
+  return PA_OK;
+}
+
+extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const void* k_pool, const void* v_pool,
+                                         const int8_t* k_exp, const int8_t* v_exp, int64_t num_pages,
+                                         int32_t page_size, int32_t num_qo_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, const int32_t* indices, int64_t num_indices,
+                                         const int32_t* indptr, const int32_t* last_page_len,
+                                         const int32_t* first_page_offset, int32_t batch, const int32_t* qo_indptr,
+                                         int32_t num_tokens, const int32_t* tree_mask, int32_t mask_words,
+                                         const int32_t* positions, int32_t window, int32_t sinks, float sm_scale,
+                                         void* out, float* lse2_out, void* workspace, int64_t workspace_bytes,
+                                         int32_t* status, void* cuda_stream) {
+  using namespace pa;
+  if (num_tokens < 0 || batch < 0 || num_kv_heads < 1 || num_qo_heads < num_kv_heads ||
+      num_qo_heads % num_kv_heads || page_size < 1 || num_pages < 1 || num_indices < 0 || mask_words < 0 ||
+      (tree_mask && mask_words < 1) || window < 0 || sinks < 0 || (sinks > 0 && window == 0) || !std::isfinite(sm_scale))
+    return PA_EINVAL;
+  if (q_dtype != PA_F16 && q_dtype != PA_BF16) return PA_EUNSUPPORTED;
+  if (head_dim != 64 && head_dim != 128) return PA_EUNSUPPORTED;
+  if (page_size > 256 || (page_size > 16 && page_size % 16 != 0)) return PA_EUNSUPPORTED;
+  if (num_pages >= (1ll << 31) || num_pages * page_size >= (1ll << 31)) return PA_EUNSUPPORTED;
+  if (tree_mask && mask_words > PA_V2_MAX_MASK_WORDS) return PA_EUNSUPPORTED;
+  if (batch > (1 << 20)) return PA_EUNSUPPORTED;
+  const float scale_log2 = sm_scale * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2)) return PA_EUNSUPPORTED;
+  const int32_t group = num_qo_heads / num_kv_heads;
+  if ((int64_t)num_tokens * group > INT32_MAX - 2 * kF8MaxRows) return PA_EUNSUPPORTED;
+  if (num_tokens == 0 || batch == 0) return PA_OK;
+  if (!q || !k_pool || !v_pool || !k_exp || !v_exp || !indptr || !last_page_len || !first_page_offset || !qo_indptr ||
+      !out || !lse2_out || !workspace || (num_indices > 0 && !indices) || (window > 0 && tree_mask && !positions))
+    return PA_EINVAL;
+  for (const void* x : {q, k_pool, v_pool, static_cast<const void*>(out), static_cast<const void*>(workspace)})
+    if (!f8_aligned(x)) return PA_EINVAL;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+    cudaGetLastError();
+    return PA_ECUDA;
+  }
+  const int64_t a = warp_part_bytes(sms, head_dim), b = cta_part_bytes(sms, head_dim);
+  if (workspace_bytes < a + b + sms * (int64_t)sizeof(F8Header)) return PA_ECAPACITY;
+  alignas(64) CUtensorMap tm_k, tm_v;
+  std::memset(&tm_k, 0, sizeof(tm_k));
+  std::memset(&tm_v, 0, sizeof(tm_v));
+  const bool tma = tc_uses_tma(page_size);
+  int box_rows = 8;  // rows of a TMA box: the largest power of two that divides a page, up to a whole tile
+  while (box_rows < kF8Tile && page_size % (2 * box_rows) == 0) box_rows *= 2;
+  if (tma) {
+    const CUtensorMapSwizzle sw = head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    if (!make_pool_map(&tm_k, k_pool, PA_E4M3, num_pages * page_size, num_kv_heads, head_dim, head_dim, box_rows, sw) ||
+        !make_pool_map(&tm_v, v_pool, PA_E4M3, num_pages * page_size, num_kv_heads, head_dim, head_dim, box_rows, sw))
+      return PA_ECUDA;
+  }
+  F8Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = q;
+  p.k_pool = static_cast<const uint8_t*>(k_pool);
+  p.v_pool = static_cast<const uint8_t*>(v_pool);
+  p.k_exp = k_exp;
+  p.v_exp = v_exp;
+  p.indices = indices;
+  p.indptr = indptr;
+  p.last_page_len = last_page_len;
+  p.first_page_offset = first_page_offset;
+  p.qo_indptr = qo_indptr;
+  p.tree_mask = tree_mask;
+  p.positions = positions;
+  p.out = out;
+  p.lse_out = lse2_out;
+  p.warp_parts = static_cast<float*>(workspace);
+  p.cta_parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + a);
+  p.headers = reinterpret_cast<F8Header*>(static_cast<char*>(workspace) + a + b);
+  p.status = status;
+  p.num_pages = num_pages;
+  p.num_indices = num_indices;
+  p.batch = batch;
+  p.num_tokens = num_tokens;
+  p.mask_words = mask_words;
+  p.page_size = page_size;
+  p.box_rows = box_rows;
+  p.hq = num_qo_heads;
+  p.hkv = num_kv_heads;
+  p.group = group;
+  p.ctas = sms;
+  p.q_bf16 = q_dtype == PA_BF16;
+  const FastDiv fd = FastDiv::make((uint32_t)page_size), fg = FastDiv::make((uint32_t)group);
+  p.ps_magic = fd.magic;
+  p.ps_shift = fd.shift;
+  p.g_magic = fg.magic;
+  p.g_shift = fg.shift;
+  p.scale_log2 = scale_log2;
+  p.window = window;
+  p.sinks = sinks;
+  // Rows of a block: a request's query rows per KV head, were the tokens spread evenly (the lengths are on the device).
+  const int64_t rows = ((int64_t)num_tokens + batch - 1) / batch * group;
+  const F8Pick pick = head_dim == 64 ? pick_f8<64>(rows, tma) : pick_f8<128>(rows, tma);
+  if (!prepare_kernel(reinterpret_cast<const void*>(pick.fn), pick.smem)) return PA_ECUDA;
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  cudaError_t rc = launch_dependent(pick.fn, dim3(sms), dim3(kF8Threads), pick.smem, stream, p, tm_k, tm_v);
+  if (rc == cudaSuccess && sms > 1)
+    rc = launch_dependent(head_dim == 64 ? pa_v2_fp8_merge_kernel<64> : pa_v2_fp8_merge_kernel<128>,
+                          dim3(sms, pick.rows), dim3(32 * kMergeWarps), 0, stream, p);
+  if (rc != cudaSuccess) {
+    cudaGetLastError();
+    return PA_ECUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ECUDA;
+}

@@ -72,8 +72,9 @@ bool make_pool_map(CUtensorMap* map, const void* base, int dtype, int64_t rows, 
   if (!fn) return false;
   const CUtensorMapDataType dt = dtype == PA_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                  : dtype == PA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const int esize = dtype == PA_F32 ? 4 : 2;
+                                 : dtype == PA_E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int esize = dtype == PA_F32 ? 4 : dtype == PA_E4M3 ? 1 : 2;
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)hkv, (cuuint64_t)rows};
   cuuint64_t strides[2] = {(cuuint64_t)D * esize, (cuuint64_t)hkv * D * esize};
   cuuint32_t box[3] = {(cuuint32_t)box_d, 1u, (cuuint32_t)box_rows};

@@ -40,6 +40,7 @@
 #include "pa_device.cuh"
 #include "pa_internal.cuh"
 #include "pa_mma.cuh"
+#include "pa_rope.cuh"
 #include "pa_tc05.cuh"
 #include "pa_v2.h"
 
@@ -50,7 +51,6 @@ constexpr int kQkThreads = 256;
 constexpr int kQkPasses = 3;  // heads a lane holds at once, at most (four do not fit its registers)
 constexpr int kQkTile = 4;    // tokens per tile, at most: one angle per thread
 constexpr int kQkSlots = 3;   // tokens whose pieces a thread has room for in the ring
-constexpr double kInvTwoPi = 0.15915494309189533577;
 
 struct QkParams {
   const void* q;
@@ -70,76 +70,6 @@ struct QkParams {
   float eps;
   int32_t tokens, hq, hkv, rot, tile;
 };
-
-// Two 8-byte pieces of T as floats, and back (one rounding).
-template <typename T> struct Vec;
-template <> struct Vec<float> {
-  static constexpr int N = 4;
-  __device__ __forceinline__ static void unpack(const uint4& u, float (&x)[4]) {
-    x[0] = __uint_as_float(u.x);
-    x[1] = __uint_as_float(u.y);
-    x[2] = __uint_as_float(u.z);
-    x[3] = __uint_as_float(u.w);
-  }
-  __device__ __forceinline__ static uint4 pack(const float (&x)[4]) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-  }
-};
-template <> struct Vec<__half> {
-  static constexpr int N = 8;
-  __device__ __forceinline__ static void unpack(const uint4& u, float (&x)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-  }
-  __device__ __forceinline__ static uint4 pack(const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <> struct Vec<__nv_bfloat16> {
-  static constexpr int N = 8;
-  __device__ __forceinline__ static void unpack(const uint4& u, float (&x)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-  __device__ __forceinline__ static uint4 pack(const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-
-// The part of a turn that one position adds, times 2^64.
-__device__ __forceinline__ uint64_t turn_of(float inv_freq) {
-  const double f = (double)inv_freq * kInvTwoPi;
-  return __double2ull_rd((f - floor(f)) * 18446744073709551616.0);
-}
-
-// Cosine and sine after pos positions.
-__device__ __forceinline__ float2 rotation(int32_t pos, uint64_t turn) {
-  const int32_t part = (int32_t)(uint32_t)(((uint64_t)(int64_t)pos * turn) >> 32);  // [-1/2, 1/2) turns, times 2^32
-  float s, c;
-  sincospif((float)part * 4.656612873077393e-10f, &s, &c);  // 2^-31: sincospif takes half turns
-  return make_float2(c, s);
-}
 
 __device__ __forceinline__ void copy_piece(uint32_t to, const void* from) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");

@@ -21,12 +21,13 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpa_v2.so")
 
 PA_OK, PA_EINVAL, PA_EGEOMETRY, PA_ECAPACITY, PA_EUNSUPPORTED, PA_ECUDA, PA_EOOB = 0, -1, -2, -3, -4, -5, -6
-PA_F32, PA_F16, PA_BF16 = 0, 1, 2
+PA_F32, PA_F16, PA_BF16, PA_E4M3 = 0, 1, 2, 3
 PA_V2_MAX_CHUNKS = 65535
 DEVICE_BAD_REQUEST, DEVICE_BAD_SLOT, DEVICE_BAD_PAGE, DEVICE_BAD_INDPTR, DEVICE_WAIT_TIMEOUT = 1, 2, 4, 8, 16
 DEVICE_BAD_BLOCK = 32
 DEVICE_BAD_LENGTH, DEVICE_NO_PAGES, DEVICE_BAD_TREE = 64, 128, 256
 MAX_TABLE_BATCH, MAX_MASK_WORDS = 16384, 32
+FP8_EXP_MIN, FP8_EXP_MAX = -15, 7
 
 KV_DTYPES = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
 
@@ -40,7 +41,8 @@ ABI_SYMBOLS = ("pa_v2_q_heads_per_cta", "pa_v2_default_target_ctas", "pa_v2_plan
                "pa_v2_host_graph_create_mapped", "pa_v2_wave_fit_pages_per_chunk",
                "pa_v2_balanced_pages_per_chunk", "pa_v2_cascade_plan", "pa_v2_cascade_decode", "pa_v2_build_tables",
                "pa_v2_build_tables_sliding", "pa_v2_qk_rope_append", "pa_v2_tree_attention_workspace",
-               "pa_v2_tree_attention", "pa_v2_tree_attention_sliding",
+               "pa_v2_tree_attention", "pa_v2_tree_attention_sliding", "pa_v2_qk_rope_append_fp8",
+               "pa_v2_attention_fp8_workspace", "pa_v2_attention_fp8",
                "pa_status_from_device", "pa_status_string", "pa_version")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -155,6 +157,14 @@ def lib() -> ctypes.CDLL:
         L.pa_v2_tree_attention_sliding.argtypes = [P, P, P, i32, i64, i32, i32, i32, i32, P, i64, P, P, P, i32, P, i32,
                                                    P, i32, P, i32, f32, P, P, P, i64, P, P]
         L.pa_v2_tree_attention_sliding.restype = i32
+        L.pa_v2_qk_rope_append_fp8.argtypes = [P, i64, P, i64, P, i64, i32, i32, i32, i32, i32, P, P, P, i32, i32, P, P,
+                                               f32, P, i32, P, P, P, P, i64, i32, P, P]
+        L.pa_v2_qk_rope_append_fp8.restype = i32
+        L.pa_v2_attention_fp8_workspace.argtypes = L.pa_v2_tree_attention_workspace.argtypes
+        L.pa_v2_attention_fp8_workspace.restype = i32
+        L.pa_v2_attention_fp8.argtypes = [P, i32, P, P, P, P, i64, i32, i32, i32, i32, P, i64, P, P, P, i32, P, i32, P,
+                                          i32, P, i32, i32, f32, P, P, P, i64, P, P]
+        L.pa_v2_attention_fp8.restype = i32
         L.pa_status_from_device.argtypes = [i32]
         L.pa_status_from_device.restype = i32
         L.pa_status_string.argtypes = [i32]
@@ -893,6 +903,151 @@ def pa_v2_tree_attention(q, k_pool, v_pool, indices, indptr, last_page_len, firs
                                   handle)
         if rc != PA_OK:
             raise PaError(rc, entry)
+
+    _run_on(dev, stream, launch)
+    return out, lse2_out
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit cache
+# ---------------------------------------------------------------------------
+
+def _pools_fp8(k_pool, v_pool, k_exp, v_exp, index: int) -> tuple[int, int, int, int]:
+    """(k, v, k exponents, v exponents) pointers of an 8-bit cache."""
+    if k_pool.dtype != torch.float8_e4m3fn or v_pool.dtype != torch.float8_e4m3fn or k_pool.shape != v_pool.shape:
+        raise ValueError("k_pool and v_pool must be float8_e4m3fn and share a shape")
+    if k_pool.dim() != 4:
+        raise ValueError("pools must be [num_pages, page_size, num_kv_heads, head_dim]")
+    shape = (k_pool.shape[0], k_pool.shape[2])
+    for t, name in ((k_exp, "k_exp"), (v_exp, "v_exp")):
+        if t.shape != shape:
+            raise ValueError(f"{name} must be [num_pages, num_kv_heads] = {list(shape)}, got {list(t.shape)}")
+    ptr = _step_ptr
+    return (ptr(k_pool, "k_pool", index), ptr(v_pool, "v_pool", index), ptr(k_exp, "k_exp", index, torch.int8),
+            ptr(v_exp, "v_exp", index, torch.int8))
+
+
+def pa_v2_qk_rope_append_fp8(q, k, v, positions, slots, inv_freq, k_pool, v_pool, k_exp, v_exp, q_out=None,
+                             q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False, q_dtype=None,
+                             status=None, stream=None):
+    """Per-head norm and rotation of q and k, k and v appended to an 8-bit cache (pa_v2_qk_rope_append_fp8).
+
+    As pa_v2_qk_rope_append, with k_pool and v_pool [P, page_size, Hkv, D] float8_e4m3fn and k_exp and v_exp [P, Hkv]
+    int8, the exponents of each page and KV head (an element is code * 2^exponent); the tokens of one page must be
+    neighbours in the call.  Returns q_out [T, Hq, D] in q_dtype (q's dtype by default, or float32)."""
+    dev = _device_index(q, "q")
+    pools = _pools_fp8(k_pool, v_pool, k_exp, v_exp, dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    if q.dtype not in KV_DTYPES:
+        raise ValueError(f"q, k and v must be one of {list(KV_DTYPES)}")
+    T, _, D = q.shape
+    dt, i32, ptr = q.dtype, torch.int32, _step_ptr
+    qp, qs, hq = _token_rows(q, "q", T, D, dt, dev)
+    kp, ks, hkv = _token_rows(k, "k", T, D, dt, dev)
+    vp, vs, hv = _token_rows(v, "v", T, D, dt, dev)
+    pages, page_size, pool_heads, pool_dim = k_pool.shape
+    if hv != hkv or pool_heads != hkv or pool_dim != D:
+        raise ValueError(f"k, v and the pools must agree on heads and head_dim: {hkv}, {hv}, {list(k_pool.shape)}")
+    rot = 2 * inv_freq.numel() if inv_freq is not None else 0
+    if q_out is not None:
+        q_dtype = q_out.dtype
+    elif q_dtype is None:
+        q_dtype = dt
+    if q_dtype not in KV_DTYPES:
+        raise ValueError(f"q_dtype must be one of {list(KV_DTYPES)}")
+    head = (qp, qs, kp, ks, vp, vs, KV_DTYPES[dt], T, hq, hkv, D, ptr(positions, "positions", dev, i32, T),
+            ptr(slots, "slots", dev, i32, T), ptr(inv_freq, "inv_freq", dev, torch.float32), rot,
+            1 if interleaved else 0, ptr(q_weight, "q_weight", dev, dt, D), ptr(k_weight, "k_weight", dev, dt, D),
+            eps)
+    st = ptr(status, "status", dev, i32)
+    if q_out is not None and tuple(q_out.shape) != (T, hq, D):
+        raise ValueError(f"q_out must be [{T}, {hq}, {D}], got {list(q_out.shape)}")
+
+    def launch(handle):
+        nonlocal q_out
+        if q_out is None:
+            q_out = torch.empty(T, hq, D, dtype=q_dtype, device=q.device)
+        rc = lib().pa_v2_qk_rope_append_fp8(*head, ptr(q_out, "q_out", dev), KV_DTYPES[q_dtype], *pools, pages,
+                                            page_size, st, handle)
+        if rc != PA_OK:
+            raise PaError(rc, "pa_v2_qk_rope_append_fp8")
+
+    _run_on(dev, stream, launch)
+    return q_out
+
+
+def pa_v2_attention_fp8_workspace(num_tokens: int, batch: int, num_qo_heads: int, num_kv_heads: int, head_dim: int,
+                                  device: int | None = None) -> int:
+    """Bytes of device scratch pa_v2_attention_fp8 needs for these sizes."""
+    dev = torch.cuda.current_device() if device is None else device
+    out = ctypes.c_int64()
+    rc = lib().pa_v2_attention_fp8_workspace(dev, num_tokens, batch, num_qo_heads, num_kv_heads, head_dim,
+                                             ctypes.byref(out))
+    if rc != PA_OK:
+        raise PaError(rc, "pa_v2_attention_fp8_workspace")
+    return int(out.value)
+
+
+def attention_fp8_workspace(num_tokens: int, batch: int, num_qo_heads: int, num_kv_heads: int, head_dim: int,
+                            device="cuda") -> torch.Tensor:
+    """A workspace tensor for pa_v2_attention_fp8 calls of up to these sizes."""
+    dev = torch.device(device)
+    index = dev.index if dev.index is not None else torch.cuda.current_device()
+    n = pa_v2_attention_fp8_workspace(num_tokens, batch, num_qo_heads, num_kv_heads, head_dim, index)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+
+
+def pa_v2_attention_fp8(q, k_pool, v_pool, k_exp, v_exp, indices, indptr, last_page_len, first_page_offset, qo_indptr,
+                        sm_scale: float, tree_mask=None, positions=None, sliding_window: int = 0, sinks: int = 0,
+                        out=None, lse2_out=None, workspace=None, status=None, stream=None):
+    """Attention of each request's new tokens over an 8-bit cache (pa_v2_attention_fp8).
+
+    q [T, Hq, D] float16 or bfloat16, packed request by request (qo_indptr [B + 1]; one token each is a decode step);
+    pools and exponents as pa_v2_qk_rope_append_fp8 fills them; tree_mask [T, words] int32 ancestor bits, or None for
+    chains.  sliding_window: each token sees so many positions up to its own, and with sinks the request's first
+    `sinks` ones too (the page table then lists the whole request; pages that nobody sees may be gone); positions [T]
+    int32, as in the tables, are needed with a tree_mask and a window.  Returns (out [T, Hq, D] of q's dtype, lse2
+    [T, Hq] float32); rows behind the last token are not written."""
+    dev = _device_index(q, "q")
+    pools = _pools_fp8(k_pool, v_pool, k_exp, v_exp, dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("q must be float16 or bfloat16")
+    T, hq, D = q.shape
+    P, ps, hkv, pool_dim = k_pool.shape
+    if pool_dim != D:
+        raise ValueError(f"pools must be [P, page_size, Hkv, {D}]")
+    B, dt, i32, ptr = last_page_len.numel(), q.dtype, torch.int32, _step_ptr
+    words = _mask_words(tree_mask, "[tokens, mask words]")
+    if sliding_window and tree_mask is not None and positions is None:
+        raise ValueError("a sliding window over trees needs the tokens' positions")
+    head = (ptr(q, "q", dev), KV_DTYPES[dt], *pools, P, ps, hq, hkv, D, ptr(indices, "indices", dev, i32),
+            indices.numel(), ptr(indptr, "indptr", dev, i32, B + 1),
+            ptr(last_page_len, "last_page_len", dev, i32, B),
+            ptr(first_page_offset, "first_page_offset", dev, i32, B), B,
+            ptr(qo_indptr, "qo_indptr", dev, i32, B + 1), T, ptr(tree_mask, "tree_mask", dev, i32, T * words), words,
+            ptr(positions, "positions", dev, i32, T), sliding_window, sinks)
+    st = ptr(status, "status", dev, i32)
+    for t, name, shape in ((out, "out", (T, hq, D)), (lse2_out, "lse2_out", (T, hq))):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+    def launch(handle):
+        nonlocal workspace, out, lse2_out
+        if workspace is None and hkv > 0 and hq % hkv == 0 and D in (64, 128):
+            workspace = attention_fp8_workspace(T, B, hq, hkv, D, q.device)
+        if out is None:
+            out = torch.empty(T, hq, D, dtype=dt, device=q.device)
+        if lse2_out is None:
+            lse2_out = torch.empty(T, hq, dtype=torch.float32, device=q.device)
+        rc = lib().pa_v2_attention_fp8(*head, sm_scale, ptr(out, "out", dev, dt),
+                                       ptr(lse2_out, "lse2_out", dev, torch.float32), ptr(workspace, "workspace", dev),
+                                       workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                       st, handle)
+        if rc != PA_OK:
+            raise PaError(rc, "pa_v2_attention_fp8")
 
     _run_on(dev, stream, launch)
     return out, lse2_out
