@@ -791,6 +791,25 @@ pa_status pa_v2_tree_attention_sliding(const void* q, const void* k_pool, const 
                                        float* lse2_out, void* workspace, int64_t workspace_bytes, int32_t* status,
                                        void* cuda_stream);
 
+/* The sliding window with sinks: the request's first `sinks` >= 1 tokens stay
+ * visible beside the window, so the token at position x sees the positions y <= x
+ * with y < sinks or y > x - window.  Of the new tokens a chain shows token i those
+ * as well; with a tree_mask the mask alone decides.  The page table lists the
+ * whole request (first_page_offset 0, positions that start at the number of
+ * tokens before the new ones; else the request is refused: PA_DEVICE_BAD_TREE,
+ * zeros and -inf), as pa_v2_build_tables without a window makes it; entries of
+ * pages that lie between the sinks and the first new token's window are not read
+ * and may be anything.  PA_EINVAL: window or sinks below 1, positions null. */
+pa_status pa_v2_tree_attention_sinks(const void* q, const void* k_pool, const void* v_pool, int32_t kv_dtype,
+                                     int64_t num_pages, int32_t page_size, int32_t num_qo_heads, int32_t num_kv_heads,
+                                     int32_t head_dim, const int32_t* indices, int64_t num_indices,
+                                     const int32_t* indptr, const int32_t* last_page_len,
+                                     const int32_t* first_page_offset, int32_t batch, const int32_t* qo_indptr,
+                                     int32_t num_tokens, const int32_t* tree_mask, int32_t mask_words,
+                                     const int32_t* positions, int32_t window, int32_t sinks, float sm_scale,
+                                     void* out, float* lse2_out, void* workspace, int64_t workspace_bytes,
+                                     int32_t* status, void* cuda_stream);
+
 /* ---- the 8-bit cache ----
  *
  * Pools of e4m3 codes (4 exponent bits, 3 mantissa bits, no infinity, 0x7f and

@@ -41,7 +41,8 @@ ABI_SYMBOLS = ("pa_v2_q_heads_per_cta", "pa_v2_default_target_ctas", "pa_v2_plan
                "pa_v2_host_graph_create_mapped", "pa_v2_wave_fit_pages_per_chunk",
                "pa_v2_balanced_pages_per_chunk", "pa_v2_cascade_plan", "pa_v2_cascade_decode", "pa_v2_build_tables",
                "pa_v2_build_tables_sliding", "pa_v2_qk_rope_append", "pa_v2_tree_attention_workspace",
-               "pa_v2_tree_attention", "pa_v2_tree_attention_sliding", "pa_v2_qk_rope_append_fp8",
+               "pa_v2_tree_attention", "pa_v2_tree_attention_sliding", "pa_v2_tree_attention_sinks",
+               "pa_v2_qk_rope_append_fp8",
                "pa_v2_attention_fp8_workspace", "pa_v2_attention_fp8",
                "pa_status_from_device", "pa_status_string", "pa_version")
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -157,6 +158,9 @@ def lib() -> ctypes.CDLL:
         L.pa_v2_tree_attention_sliding.argtypes = [P, P, P, i32, i64, i32, i32, i32, i32, P, i64, P, P, P, i32, P, i32,
                                                    P, i32, P, i32, f32, P, P, P, i64, P, P]
         L.pa_v2_tree_attention_sliding.restype = i32
+        L.pa_v2_tree_attention_sinks.argtypes = [P, P, P, i32, i64, i32, i32, i32, i32, P, i64, P, P, P, i32, P, i32, P,
+                                                 i32, P, i32, i32, f32, P, P, P, i64, P, P]
+        L.pa_v2_tree_attention_sinks.restype = i32
         L.pa_v2_qk_rope_append_fp8.argtypes = [P, i64, P, i64, P, i64, i32, i32, i32, i32, i32, P, P, P, i32, i32, P, P,
                                                f32, P, i32, P, P, P, P, i64, i32, P, P]
         L.pa_v2_qk_rope_append_fp8.restype = i32
@@ -856,12 +860,13 @@ def tree_attention_workspace(num_tokens: int, batch: int, num_qo_heads: int, num
 
 def pa_v2_tree_attention(q, k_pool, v_pool, indices, indptr, last_page_len, first_page_offset, qo_indptr,
                          sm_scale: float, tree_mask=None, out=None, lse2_out=None, workspace=None, status=None,
-                         stream=None, sliding_window: int = 0, positions=None):
+                         stream=None, sliding_window: int = 0, positions=None, sinks: int = 0):
     """Attention of each request's new tokens over its paged cache (pa_v2_tree_attention).
 
     q [T, Hq, D] of the pools' 16-bit dtype, packed request by request (qo_indptr [B + 1]); tree_mask
     [T, words] int32 ancestor bits, or None for chains.  sliding_window: each token sees so many positions up to its own
-    (pa_v2_tree_attention_sliding), with positions [T] int32, both as in the call that made the tables.  Returns
+    (pa_v2_tree_attention_sliding), with positions [T] int32, both as in the call that made the tables.  sinks: and the
+    request's first so many positions (pa_v2_tree_attention_sinks), over tables that list the whole request.  Returns
     (out [T, Hq, D], lse2 [T, Hq] float32); rows behind the last token are not written."""
     dev = _device_index(q, "q")
     k_ptr, v_ptr = _pools(k_pool, v_pool, dev)
@@ -884,6 +889,11 @@ def pa_v2_tree_attention(q, k_pool, v_pool, indices, indptr, last_page_len, firs
             raise ValueError("a sliding window needs the tokens' positions")
         entry = "pa_v2_tree_attention_sliding"
         head += ptr(positions, "positions", dev, i32, T), sliding_window
+    if sinks:
+        if not sliding_window:
+            raise ValueError("sinks stand beside a sliding window: without one every token is seen")
+        entry = "pa_v2_tree_attention_sinks"
+        head += (sinks,)
     st = ptr(status, "status", dev, i32)
     for t, name, shape in ((out, "out", (T, hq, D)), (lse2_out, "lse2_out", (T, hq))):
         if t is not None and t.shape != shape:
