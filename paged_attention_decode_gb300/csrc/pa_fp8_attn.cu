@@ -61,6 +61,7 @@ struct F8Cfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kSide = kF8Tile * D;    // bytes of a stage's K, or V
   static constexpr bool kQSmem = NT > 2;       // q's fragments live in shared memory: 16 NT registers are too many
+  static constexpr int kMt = NT > 3 ? 1 : 2;   // 16-key halves of a tile that go through the softmax at once
   static constexpr int kStages = (D == 128 ? 1 : 2) * (kQSmem ? 2 : 3);
   static constexpr int kRing = kStages * 2 * kSide;
   static constexpr int kQ = kQSmem ? kRows * D * 2 : 0;
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const int64_t count = start_req[warp] < 0 ? 0 : min(run, units - u0);
 
   // ---- the loading side: the next unit to load, its pages already on their way
-  F8Req lq = {};
+  // (requests are read from shared memory where they are needed: in registers, twice, they crowd out the accumulators)
   int32_t l_r = 0, l_kvh = 0, l_blk = 0, l_v = 0, l_info = 0;
   int32_t l_page = -2;      // this lane's row's page: -2 nobody sees it
   uint32_t l_vis = 0;       // rows that somebody sees, whole boxes
@@ -356,26 +357,29 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   auto resolve = [&]() {  // the pages of unit (l_r, l_kvh, l_blk, l_v)
     l_vis = 0;
     l_page = -2;
-    if (lq.kind != kF8Keys) return;
-    const int32_t at = lq.tile(l_v) * kF8Tile + lane;
-    l_vis = __ballot_sync(0xffffffffu, lq.seen(at));
+    if (infos[warp][l_info].kind != kF8Keys) return;
+    const int32_t at = infos[warp][l_info].tile(l_v) * kF8Tile + lane;
+    l_vis = __ballot_sync(0xffffffffu, infos[warp][l_info].seen(at));
     if (TMA) {  // whole boxes
       const int b = lane / p.box_rows * p.box_rows;
       l_vis = __ballot_sync(0xffffffffu, (l_vis & bits_between(b, b + p.box_rows)) != 0);
     }
     if (l_vis >> lane & 1u) {
       const int32_t slot = (int32_t)fast_div((uint32_t)at, p.ps_magic, p.ps_shift);
-      l_page = __ldg(p.indices + lq.slot_base + slot);
+      l_page = __ldg(p.indices + infos[warp][l_info].slot_base + slot);
     }
   };
   auto enter = [&](int r) {  // the next request with units, from r on
+    F8Req q;
     for (;; ++r) {
-      lq = f8_req<R>(p, r, false);
-      if (lq.kind != 0) break;
+      q = f8_req<R>(p, r, false);
+      if (q.kind != 0) break;
     }
     l_r = r;
     l_info = (l_info + 1) & (kF8Infos - 1);
-    if (lane == 0) infos[warp][l_info] = lq;
+    __syncwarp();
+    if (lane == 0) infos[warp][l_info] = q;
+    __syncwarp();
   };
   auto flush = [&]() {  // the exponents of the unit loaded last
     if (pend_stage < 0) return;
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     flush();
     unsigned char* kd = ring + stage * 2 * C::kSide;
     const bool good = l_page >= 0 && l_page < p.num_pages;
-    const int32_t at = lq.tile(l_v) * kF8Tile + lane;
+    const int32_t at = infos[warp][l_info].tile(l_v) * kF8Tile + lane;
     // a bad page: past the pool, where a box is zero-filled
     int32_t row = TMA ? (int32_t)(p.num_pages * p.page_size) : -1;
     pend_k = pend_v = 0;
@@ -405,7 +409,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     pend_stage = stage;
     if (lane == 0) meta[stage].unit = F8Unit{l_info, l_kvh, l_blk, l_v};
     // rows that several blocks read stay in L2 as other data does, the others leave it first
-    const uint64_t pol = lq.blocks > 1 ? keep : policy;
+    const uint64_t pol = infos[warp][l_info].blocks > 1 ? keep : policy;
     if (TMA) {
       const int step = p.box_rows;
       if (lane == 0) {
@@ -441,9 +445,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       copies_arrive(&full[stage]);
     }
     if (more) {
-      if (++l_v == lq.tiles) {
+      if (++l_v == infos[warp][l_info].tiles) {
         l_v = 0;
-        if (++l_blk == lq.blocks) {
+        if (++l_blk == infos[warp][l_info].blocks) {
           l_blk = 0;
           if (++l_kvh == p.hkv) {
             l_kvh = 0;
@@ -459,11 +463,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   int64_t issued = 0;
   if (count > 0) {
     enter(start_req[warp]);
-    const int64_t off = start_off[warp], head = (int64_t)lq.blocks * lq.tiles;
+    const int64_t off = start_off[warp], head = (int64_t)infos[warp][l_info].blocks * infos[warp][l_info].tiles;
     l_kvh = (int32_t)(off / head);
     const int64_t in_head = off - l_kvh * head;
-    l_blk = (int32_t)(in_head / lq.tiles);
-    l_v = (int32_t)(in_head - (int64_t)l_blk * lq.tiles);
+    l_blk = (int32_t)(in_head / infos[warp][l_info].tiles);
+    l_v = (int32_t)(in_head - (int64_t)l_blk * infos[warp][l_info].tiles);
     resolve();
     for (; issued < min(count, (int64_t)S); ++issued) issue((int)issued, issued + 1 < count);
     if (issued == count) flush();
@@ -477,30 +481,24 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   float qf[NT][2];              // scale of the columns' scores
   uint2* qs = reinterpret_cast<uint2*>(smem + C::kOffQ + warp * C::kQ);  // [KS][NT][32], with kQSmem
   int32_t low = 0, tok = -1, clear0 = 0;  // of the row on this lane; rows [clear0, ds) are seen by all of the block's
-  F8Req cq = {};
-  int32_t rows = 0, row0 = 0, kvh = 0, v_first = 0;
+  int32_t c_info = 0, rows = 0, row0 = 0, kvh = 0, v_first = 0;
   bool alive = true;
   int stage = 0;
   uint32_t parity = 0;
   for (int64_t j = 0; j < count; ++j) {
-    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[stage], parity, kWaitLimitCycles))) {
-      report(p.status, PA_DEVICE_WAIT_TIMEOUT);
-      alive = false;
-      break;
-    }
     const F8Unit unit = meta[stage].unit;
     if (j == 0 || unit.v == 0) {
       // ---- a block begins (here): its rows, Q and an empty state
-      cq = infos[warp][unit.info];
+      c_info = unit.info;
       kvh = unit.kvh;
       row0 = unit.blk * R;
-      rows = (int32_t)min((int64_t)R, (int64_t)cq.n * p.group - row0);
+      rows = (int32_t)min((int64_t)R, (int64_t)infos[warp][c_info].n * p.group - row0);
       v_first = unit.v;
       const int32_t last_tok = (int32_t)fast_div((uint32_t)(row0 + rows - 1), p.g_magic, p.g_shift);
       tok = lane < rows ? (int32_t)fast_div((uint32_t)(row0 + lane), p.g_magic, p.g_shift) : -1;
-      if (cq.kind == kF8Keys) {
-        low = tok >= 0 ? window_from(p, cq, tok) : 0;
-        clear0 = p.window > 0 ? (int32_t)max((int64_t)cq.lo, (int64_t)cq.ds + last_tok + 1 - p.window) : cq.lo;
+      if (infos[warp][c_info].kind == kF8Keys) {
+        low = tok >= 0 ? window_from(p, infos[warp][c_info], tok) : 0;
+        clear0 = p.window > 0 ? (int32_t)max((int64_t)infos[warp][c_info].lo, (int64_t)infos[warp][c_info].ds + last_tok + 1 - p.window) : infos[warp][c_info].lo;
         constexpr int kMine = D / 4;  // dims of a lane: t D / 4 ..
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -509,7 +507,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           float top = 0.f;
           if (c < rows) {
             const uint4* src = reinterpret_cast<const uint4*>(
-                static_cast<const uint16_t*>(p.q) + out_row_of(p, cq.t0, kvh, row0 + c) * D + t * kMine);
+                static_cast<const uint16_t*>(p.q) + out_row_of(p, infos[warp][c_info].t0, kvh, row0 + c) * D + t * kMine);
 #pragma unroll
             for (int i = 0; i < kMine / 8; ++i) {
               const uint4 u = __ldg(src + i);
@@ -560,182 +558,191 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       }
     }
 
-    const int32_t base = cq.tile(unit.v) * kF8Tile;
-    const bool clear = base + kF8Tile <= cq.ds && (base >= clear0 || (base >= cq.lo && base + kF8Tile <= cq.sink_end));
+    const int32_t base = infos[warp][c_info].tile(unit.v) * kF8Tile;
+    const bool clear = base + kF8Tile <= infos[warp][c_info].ds && (base >= clear0 || (base >= infos[warp][c_info].lo && base + kF8Tile <= infos[warp][c_info].sink_end));
     uint32_t mine_bits = 0, some = 0xffffffffu;
-    bool skip = cq.kind != kF8Keys;
+    bool skip = infos[warp][c_info].kind != kF8Keys;
     if (!clear && !skip) {
-      if (tok >= 0) mine_bits = seen_bits(p, cq, tok, low, base);
+      if (tok >= 0) mine_bits = seen_bits(p, infos[warp][c_info], tok, low, base);
       some = __reduce_or_sync(0xffffffffu, mine_bits);
       skip = some == 0;
     }
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[stage], parity, kWaitLimitCycles))) {
+      report(p.status, PA_DEVICE_WAIT_TIMEOUT);
+      alive = false;
+      break;
+    }
     if (!skip) {
       const uint32_t kb = smem_addr(ring + stage * 2 * C::kSide), vb = kb + C::kSide;
-      // ---- S^T
-      float s[2][NT][4];
+      constexpr int MT = C::kMt;
+#pragma unroll 1
+      for (int pass = 0; pass < 2 / MT; ++pass) {
+        const int key0 = 16 * MT * pass;  // of the tile
+        // ---- S^T
+        float s[MT][NT][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.f;
+          for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.f;
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t x[2][2][4];
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t x[MT][2][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x[i][h][0]), "=r"(x[i][h][1]), "=r"(x[i][h][2]), "=r"(x[i][h][3])
-                         : "r"(kb + side_at<D>(16 * i + 8 * h + g, t * (D / 64) + c))
-                         : "memory");
+            for (int h = 0; h < 2; ++h)
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(x[i][h][0]), "=r"(x[i][h][1]), "=r"(x[i][h][2]), "=r"(x[i][h][3])
+                           : "r"(kb + side_at<D>(key0 + 16 * i + 8 * h + g, t * (D / 64) + c))
+                           : "memory");
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int k = 4 * c + w;
-          uint32_t b[NT][2];
+          for (int w = 0; w < 4; ++w) {
+            const int k = 4 * c + w;
+            uint32_t b[NT][2];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (C::kQSmem) {
-              const uint2 u = qs[(k * NT + nt) * 32 + lane];
-              b[nt][0] = u.x;
-              b[nt][1] = u.y;
-            } else {
-              b[nt][0] = qb[k][nt][0];
-              b[nt][1] = qb[k][nt][1];
+            for (int nt = 0; nt < NT; ++nt) {
+              if (C::kQSmem) {
+                const uint2 u = qs[(k * NT + nt) * 32 + lane];
+                b[nt][0] = u.x;
+                b[nt][1] = u.y;
+              } else {
+                b[nt][0] = qb[k][nt][0];
+                b[nt][1] = qb[k][nt][1];
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              const uint32_t a[4] = {codes_lo(x[i][0][w]), codes_lo(x[i][1][w]), codes_hi(x[i][0][w]),
+                                     codes_hi(x[i][1][w])};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) TC<__half>::mma(s[i][nt], a, b[nt][0], b[nt][1]);
             }
           }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t a[4] = {codes_lo(x[i][0][w]), codes_lo(x[i][1][w]), codes_hi(x[i][0][w]), codes_hi(x[i][1][w])};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) TC<__half>::mma(s[i][nt], a, b[nt][0], b[nt][1]);
-          }
         }
-      }
-      // ---- scores in log2 units, softmax
-      const float ks[4] = {meta[stage].k_scale[g], meta[stage].k_scale[8 + g], meta[stage].k_scale[16 + g],
-                           meta[stage].k_scale[24 + g]};
-      uint32_t pb[NT][4];
+        // ---- scores in log2 units, softmax
+        float ks[2 * MT];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-        if (!clear) {
-          see[0] = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t);
-          see[1] = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t + 1);
-        }
-        float mt[2] = {-INFINITY, -INFINITY};
+        for (int i = 0; i < 2 * MT; ++i) ks[i] = meta[stage].k_scale[key0 + 8 * i + g];
+        uint32_t pb[NT][2 * MT];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // token 16 i + 8 (k >> 1) + g, column 2 t + (k & 1)
-            const int q4 = 2 * i + (k >> 1);
-            float y = s[i][nt][k] * (ks[q4] * qf[nt][k & 1]);
-            if (!clear) y = see[k & 1] >> (8 * q4 + g) & 1u ? y : -INFINITY;
-            s[i][nt][k] = y;
-            mt[k & 1] = fmaxf(mt[k & 1], y);
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+          if (!clear) {
+            see[0] = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t) >> key0;
+            see[1] = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t + 1) >> key0;
           }
-        float scale[2];
-        bool grow = false;
+          float mt[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          mt[k] = fmaxf(mt[k], __shfl_xor_sync(0xffffffffu, mt[k], 4));
-          mt[k] = fmaxf(mt[k], __shfl_xor_sync(0xffffffffu, mt[k], 8));
-          mt[k] = fmaxf(mt[k], __shfl_xor_sync(0xffffffffu, mt[k], 16));
-          const bool need = mt[k] > m[nt][k] + kF8Lazy;  // m = -inf at first: any finite maximum
-          scale[k] = 1.f;
-          if (need) {
-            scale[k] = m[nt][k] == -INFINITY ? 0.f : fast_exp2(m[nt][k] - mt[k]);
-            m[nt][k] = mt[k];
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // token key0 + 16 i + 8 (k >> 1) + g, column 2 t + (k & 1)
+              const int q4 = 2 * i + (k >> 1);
+              float y = s[i][nt][k] * (ks[q4] * qf[nt][k & 1]);
+              if (!clear) y = see[k & 1] >> (8 * q4 + g) & 1u ? y : -INFINITY;
+              s[i][nt][k] = y;
+              mt[k & 1] = fmaxf(mt[k & 1], y);
+            }
+          float scale[2];
+          bool grow = false;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            mt[k] = fmaxf(mt[k], __shfl_xor_sync(0xffffffffu, mt[k], 4));
+            mt[k] = fmaxf(mt[k], __shfl_xor_sync(0xffffffffu, mt[k], 8));
+            mt[k] = fmaxf(mt[k], __shfl_xor_sync(0xffffffffu, mt[k], 16));
+            const bool need = mt[k] > m[nt][k] + kF8Lazy;  // m = -inf at first: any finite maximum
+            scale[k] = 1.f;
+            if (need) {
+              scale[k] = m[nt][k] == -INFINITY ? 0.f : fast_exp2(m[nt][k] - mt[k]);
+              m[nt][k] = mt[k];
+            }
+            l[nt][k] *= scale[k];
+            grow |= need;
           }
-          l[nt][k] *= scale[k];
-          grow |= need;
-        }
-        if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-          for (int c = 0; c < KS; ++c) {
-            o[c][nt][0] *= scale[0];
-            o[c][nt][1] *= scale[1];
-            o[c][nt][2] *= scale[0];
-            o[c][nt][3] *= scale[1];
-          }
-        }
-        const float off[2] = {(m[nt][0] == -INFINITY ? 0.f : m[nt][0]) - kF8Shift,
-                              (m[nt][1] == -INFINITY ? 0.f : m[nt][1]) - kF8Shift};
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float e0 = fast_exp2(s[i][nt][2 * h] - off[0]), e1 = fast_exp2(s[i][nt][2 * h + 1] - off[1]);
-            l[nt][0] += e0;
-            l[nt][1] += e1;
-            pb[nt][2 * i + h] = transposed(TC<__half>::pack(e0, e1));
-          }
-      }
-      // ---- O^T += V^T P^T
-      uint32_t vs[4];  // tokens 8 i + 2 t, + 1
-#pragma unroll
-      for (int i = 0; i < 4; ++i) vs[i] = *reinterpret_cast<const uint32_t*>(&meta[stage].v_scale[8 * i + 2 * t]);
-      if (clear) {
-#pragma unroll
-        for (int c = 0; c < KS; ++c) {
-          uint32_t x[4];
-          ldsm_x4_trans(x, vb + side_at<D>(lane, c));
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t y0 = __byte_perm(x[2 * h], 0, 0x3120), y1 = __byte_perm(x[2 * h + 1], 0, 0x3120);
-            const uint32_t a[4] = {mul_f16(codes_lo(y0), vs[2 * h]), mul_f16(codes_hi(y0), vs[2 * h]),
-                                   mul_f16(codes_lo(y1), vs[2 * h + 1]), mul_f16(codes_hi(y1), vs[2 * h + 1])};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) TC<__half>::mma(o[c][nt], a, pb[nt][2 * h], pb[nt][2 * h + 1]);
-          }
-        }
-      } else {
-        // what a row does not see must not meet its zero weight as a NaN: rows that nobody sees become zeros, and NaN
-        // codes of the others zeros that are put back below for the rows that see them
-        uint32_t vm[4], taint = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t u = some >> (8 * i + 2 * t);
-          vm[i] = (u & 1u ? 0x00ff00ffu : 0u) | (u & 2u ? 0xff00ff00u : 0u);
-        }
-#pragma unroll
-        for (int c = 0; c < KS; ++c) {
-          uint32_t x[4];
-          ldsm_x4_trans(x, vb + side_at<D>(lane, c));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = __byte_perm(x[i], 0, 0x3120) & vm[i];
-            const uint32_t nan = __vcmpeq4(x[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-            taint |= nan;
-            x[i] &= ~nan;
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t a[4] = {mul_f16(codes_lo(x[2 * h]), vs[2 * h]), mul_f16(codes_hi(x[2 * h]), vs[2 * h]),
-                                   mul_f16(codes_lo(x[2 * h + 1]), vs[2 * h + 1]),
-                                   mul_f16(codes_hi(x[2 * h + 1]), vs[2 * h + 1])};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) TC<__half>::mma(o[c][nt], a, pb[nt][2 * h], pb[nt][2 * h + 1]);
-          }
-        }
-        if (__any_sync(0xffffffffu, taint != 0)) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t see0 = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t);
-            const uint32_t see1 = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t + 1);
+          if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int c = 0; c < KS; ++c) {
+              o[c][nt][0] *= scale[0];
+              o[c][nt][1] *= scale[1];
+              o[c][nt][2] *= scale[0];
+              o[c][nt][3] *= scale[1];
+            }
+          }
+          const float off[2] = {(m[nt][0] == -INFINITY ? 0.f : m[nt][0]) - kF8Shift,
+                                (m[nt][1] == -INFINITY ? 0.f : m[nt][1]) - kF8Shift};
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float e0 = fast_exp2(s[i][nt][2 * h] - off[0]), e1 = fast_exp2(s[i][nt][2 * h + 1] - off[1]);
+              l[nt][0] += e0;
+              l[nt][1] += e1;
+              pb[nt][2 * i + h] = transposed(TC<__half>::pack(e0, e1));
+            }
+        }
+        // ---- O^T += V^T P^T, 32 / MT dims at a time
+        uint32_t vs[2 * MT];  // tokens key0 + 8 i + 2 t, + 1
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i)
+          vs[i] = *reinterpret_cast<const uint32_t*>(&meta[stage].v_scale[key0 + 8 * i + 2 * t]);
+        // what a row does not see must not meet its zero weight as a NaN: rows that nobody sees become zeros, and NaN
+        // codes of the others zeros that are put back below for the rows that see them
+        uint32_t vm[2 * MT], taint = 0;
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+          const uint32_t u = some >> (key0 + 8 * i + 2 * t);
+          vm[i] = (u & 1u ? 0x00ff00ffu : 0u) | (u & 2u ? 0xff00ff00u : 0u);
+        }
+        auto values = [&](bool safe) {
+#pragma unroll
+          for (int cc = 0; cc < KS * MT / 2; ++cc) {
+            uint32_t x[4];  // 16 dims of 32 keys, or 32 dims of 16 keys
+            if (MT == 2) ldsm_x4_trans(x, vb + side_at<D>(lane, cc));
+            else ldsm_x4_trans(x, vb + side_at<D>(key0 + (lane & 15), 2 * cc + (lane >> 4)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[i] = __byte_perm(x[i], 0, 0x3120);
+              if (safe) {
+                x[i] &= vm[i % (2 * MT)];
+                const uint32_t nan = __vcmpeq4(x[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                taint |= nan;
+                x[i] &= ~nan;
+              }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int c = MT == 2 ? cc : 2 * cc + h, k = MT == 2 ? 2 * h : 0;
+              const uint32_t a[4] = {mul_f16(codes_lo(x[2 * h]), vs[k]), mul_f16(codes_hi(x[2 * h]), vs[k]),
+                                     mul_f16(codes_lo(x[2 * h + 1]), vs[k + 1]),
+                                     mul_f16(codes_hi(x[2 * h + 1]), vs[k + 1])};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) TC<__half>::mma(o[c][nt], a, pb[nt][k], pb[nt][k + 1]);
+            }
+          }
+        };
+        if (clear) {
+          values(false);
+        } else {
+          values(true);
+          if (__any_sync(0xffffffffu, taint != 0)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint32_t see0 = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t);
+              const uint32_t see1 = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t + 1);
+#pragma unroll
+              for (int c = 0; c < KS; ++c) {
 #pragma unroll 1
-              for (int k = 0; k < kF8Tile; ++k) {
-                uint16_t pair;  // dims 16 c + 2 g, + 1 of token k
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(pair) : "r"(vb + side_at<D>(k, c) + 2 * g) : "memory");
-                const bool n0 = (pair & 0x7f) == 0x7f, n1 = (pair >> 8 & 0x7f) == 0x7f;
-                if (see0 >> k & 1u) {
-                  if (n0) o[c][nt][0] = NAN;
-                  if (n1) o[c][nt][2] = NAN;
-                }
-                if (see1 >> k & 1u) {
-                  if (n0) o[c][nt][1] = NAN;
-                  if (n1) o[c][nt][3] = NAN;
+                for (int k = key0; k < key0 + 16 * MT; ++k) {
+                  uint16_t pair;  // dims 16 c + 2 g, + 1 of token k
+                  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(pair) : "r"(vb + side_at<D>(k, c) + 2 * g) : "memory");
+                  const bool n0 = (pair & 0x7f) == 0x7f, n1 = (pair >> 8 & 0x7f) == 0x7f;
+                  if (see0 >> k & 1u) {
+                    if (n0) o[c][nt][0] = NAN;
+                    if (n1) o[c][nt][2] = NAN;
+                  }
+                  if (see1 >> k & 1u) {
+                    if (n0) o[c][nt][1] = NAN;
+                    if (n1) o[c][nt][3] = NAN;
+                  }
                 }
               }
             }
@@ -746,7 +753,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     __syncwarp();
 
     // ---- the block's last unit, or this warp's
-    const bool ends = unit.v + 1 == cq.tiles;
+    const bool ends = unit.v + 1 == infos[warp][c_info].tiles;
     const bool last = j + 1 == count;
     if (ends || last) {
 #pragma unroll
@@ -764,7 +771,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           for (int k = 0; k < 2; ++k) {
             const int32_t c = 8 * nt + 2 * t + k;
             if (c >= rows) continue;
-            const int64_t row = out_row_of(p, cq.t0, kvh, row0 + c);
+            const int64_t row = out_row_of(p, infos[warp][c_info].t0, kvh, row0 + c);
             const float sum = l[nt][k], inv = sum == 0.f ? 0.f : 1.f / sum;
             uint32_t* to = static_cast<uint32_t*>(p.out) + row * (D / 2) + g;
 #pragma unroll
@@ -790,7 +797,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             }
           }
         if (lane == 0)
-          parts[warp][part] = F8Part{1, v_first != 0, !ends, last, cq.t0, row0, rows, kvh, u0 + j + (cq.tiles - unit.v)};
+          parts[warp][part] = F8Part{1, v_first != 0, !ends, last, infos[warp][c_info].t0, row0, rows, kvh, u0 + j + (infos[warp][c_info].tiles - unit.v)};
       }
     }
     if (issued < count) {
@@ -971,7 +978,10 @@ F8Pick pick_f8(bool tma) {
 }
 template <int D>
 F8Pick pick_f8(int64_t rows, bool tma) {
-  return rows <= 8 ? pick_f8<D, 1>(tma) : rows <= 16 ? pick_f8<D, 2>(tma) : pick_f8<D, 4>(tma);
+  return rows <= 8    ? pick_f8<D, 1>(tma)
+         : rows <= 16 ? pick_f8<D, 2>(tma)
+         : rows <= 24 ? pick_f8<D, 3>(tma)
+                      : pick_f8<D, 4>(tma);
 }
 
 bool f8_aligned(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }

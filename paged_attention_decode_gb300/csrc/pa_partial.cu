@@ -79,8 +79,13 @@ bool make_pool_map(CUtensorMap* map, const void* base, int dtype, int64_t rows, 
   cuuint64_t strides[2] = {(cuuint64_t)D * esize, (cuuint64_t)hkv * D * esize};
   cuuint32_t box[3] = {(cuuint32_t)box_d, 1u, (cuuint32_t)box_rows};
   cuuint32_t estr[3] = {1u, 1u, 1u};
+  // L2 lines as long as a row of the box, where that is shorter than 256 bytes: the 8-bit attention's neighbouring row
+  // belongs to another head, met at another time (256 bytes made it read 1.89 GB from HBM for 1.33).
+  const CUtensorMapL2promotion promotion = dtype != PA_E4M3 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                           : D == 128       ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                            : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
   CUresult rc = fn(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   swizzle, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return rc == CUDA_SUCCESS;
 }
 
