@@ -65,6 +65,8 @@ struct F8Cfg {
   static constexpr int kStages = (D == 128 ? 1 : 2) * (kQSmem ? 2 : 3);
   static constexpr int kRing = kStages * 2 * kSide;
   static constexpr int kQ = kQSmem ? kRows * D * 2 : 0;
+  // floats of a row of a partial result in the ring: shifted by 4 banks a row where there is room
+  static constexpr int kPartRow = kRows * (D + 4) * 4 <= kRing ? D + 4 : D;
   static constexpr int kOffQ = kF8Warps * kRing;
   static constexpr int kOffMeta = kOffQ + kF8Warps * kQ;
 };
@@ -86,7 +88,7 @@ struct F8Params {
   const int32_t* positions;
   void* out;
   float* lse_out;
-  float* warp_parts;   // [ctas * kF8Warps][kF8MaxRows * head_dim]
+  float* warp_parts;   // [ctas * kF8Warps][kF8MaxRows * (head_dim + 4)]
   float* cta_parts;    // [ctas][2][kF8MaxRows * (head_dim + 1)]
   F8Header* headers;   // [ctas]
   int32_t* status;
@@ -164,6 +166,12 @@ __device__ __forceinline__ F8Req f8_req(const F8Params& p, int r, bool tell) {
   g.gap = ns > 0 ? max(ns, near) - ns : first;
   g.tiles = tiles;
   return g;
+}
+
+// a / b for 0 <= a, 0 < b; in 32 bits where they allow.
+__device__ __forceinline__ int64_t div_units(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
 }
 
 __device__ __forceinline__ int64_t units_of(const F8Params& p, const F8Req& g) {
@@ -308,7 +316,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   int64_t units = 0, mine = 0;
   const int per_thread = (p.batch + kF8Threads - 1) / kF8Threads;
   const int r0 = (int)min((int64_t)threadIdx.x * per_thread, (int64_t)p.batch), r1 = min(r0 + per_thread, p.batch);
-  for (int r = r0; r < r1; ++r) mine += units_of(p, f8_req<R>(p, r, blockIdx.x == 0));
+  F8Req own = {};
+  for (int r = r0; r < r1; ++r) {
+    own = f8_req<R>(p, r, blockIdx.x == 0);
+    mine += units_of(p, own);
+  }
   int64_t upto = mine;
 #pragma unroll
   for (int w = 1; w < 32; w <<= 1) {
@@ -323,18 +335,20 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     units += warp_sum[w];
   }
   const int64_t workers = (int64_t)gridDim.x * kF8Warps;
-  const int64_t run = max((units + workers - 1) / workers, (int64_t)1);
+  const int64_t run = max(div_units(units + workers - 1, workers), (int64_t)1);
   if (mine > 0) {
     const int64_t first = (int64_t)blockIdx.x * kF8Warps * run;
     if (before + mine > first && before < first + kF8Warps * run) {
       int64_t at = before;
       for (int r = r0; r < r1; ++r) {
-        const int64_t u = units_of(p, f8_req<R>(p, r, false));
+        if (per_thread > 1) own = f8_req<R>(p, r, false);
+        const int64_t u = units_of(p, own);
         for (int w = 0; w < kF8Warps; ++w) {
           const int64_t x = first + w * run;
           if (x >= at && x < at + u) {
             start_req[w] = r;
             start_off[w] = x - at;
+            infos[w][0] = own;
           }
         }
         at += u;
@@ -346,82 +360,78 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const int64_t u0 = ((int64_t)blockIdx.x * kF8Warps + warp) * run;
   const int64_t count = start_req[warp] < 0 ? 0 : min(run, units - u0);
 
-  // ---- the loading side: the next unit to load, its pages already on their way
+  // ---- the loading side: units are taken (their pages asked for) and then loaded
   // (requests are read from shared memory where they are needed: in registers, twice, they crowd out the accumulators)
-  int32_t l_r = 0, l_kvh = 0, l_blk = 0, l_v = 0, l_info = 0;
-  int32_t l_page = -2;      // this lane's row's page: -2 nobody sees it
-  uint32_t l_vis = 0;       // rows that somebody sees, whole boxes
+  int32_t l_r = 0, l_kvh = 0, l_blk = 0, l_v = -1, l_info = 0;
   int32_t pend_k = 0, pend_v = 0, pend_stage = -1;
   const uint64_t policy = policy_evict_first(), keep = policy_evict_normal();
-
-  auto resolve = [&]() {  // the pages of unit (l_r, l_kvh, l_blk, l_v)
-    l_vis = 0;
-    l_page = -2;
-    if (infos[warp][l_info].kind != kF8Keys) return;
-    const int32_t at = infos[warp][l_info].tile(l_v) * kF8Tile + lane;
-    l_vis = __ballot_sync(0xffffffffu, infos[warp][l_info].seen(at));
-    if (TMA) {  // whole boxes
-      const int b = lane / p.box_rows * p.box_rows;
-      l_vis = __ballot_sync(0xffffffffu, (l_vis & bits_between(b, b + p.box_rows)) != 0);
-    }
-    if (l_vis >> lane & 1u) {
-      const int32_t slot = (int32_t)fast_div((uint32_t)at, p.ps_magic, p.ps_shift);
-      l_page = __ldg(p.indices + infos[warp][l_info].slot_base + slot);
-    }
+  struct Taken {
+    int32_t page, entry;  // of this lane's row; page -2: nobody sees it
+    uint32_t vis;         // rows that somebody sees, whole boxes
+    F8Unit unit;
   };
-  auto enter = [&](int r) {  // the next request with units, from r on
-    F8Req q;
-    for (;; ++r) {
-      q = f8_req<R>(p, r, false);
-      if (q.kind != 0) break;
-    }
-    l_r = r;
-    l_info = (l_info + 1) & (kF8Infos - 1);
-    __syncwarp();
-    if (lane == 0) infos[warp][l_info] = q;
-    __syncwarp();
-  };
-  auto flush = [&]() {  // the exponents of the unit loaded last
-    if (pend_stage < 0) return;
-    meta[pend_stage].k_scale[lane] = power_of_two(min(max(pend_k, PA_V2_FP8_EXP_MIN), PA_V2_FP8_EXP_MAX));
-    meta[pend_stage].v_scale[lane] = __float2half_rn(power_of_two(min(max(pend_v, PA_V2_FP8_EXP_MIN), PA_V2_FP8_EXP_MAX)));
-    pend_stage = -1;
-  };
-  auto issue = [&](int stage, bool more) {  // load the unit, and go on to the next one if there is one
-    flush();
-    unsigned char* kd = ring + stage * 2 * C::kSide;
-    const bool good = l_page >= 0 && l_page < p.num_pages;
-    const int32_t at = infos[warp][l_info].tile(l_v) * kF8Tile + lane;
-    // a bad page: past the pool, where a box is zero-filled
-    int32_t row = TMA ? (int32_t)(p.num_pages * p.page_size) : -1;
-    pend_k = pend_v = 0;
-    if (l_page != -2) {
-      const int32_t slot = (int32_t)fast_div((uint32_t)at, p.ps_magic, p.ps_shift);
-      if (good) {
-        row = l_page * p.page_size + (at - slot * p.page_size);
-        const int64_t e = (int64_t)l_page * p.hkv + l_kvh;
-        pend_k = __ldg(p.k_exp + e);
-        pend_v = __ldg(p.v_exp + e);
-      } else {
-        report(p.status, PA_DEVICE_BAD_PAGE);
+  auto take = [&](Taken& n) {  // the unit behind the one taken last
+    if (++l_v == infos[warp][l_info].tiles) {
+      l_v = 0;
+      if (++l_blk == infos[warp][l_info].blocks) {
+        l_blk = 0;
+        if (++l_kvh == p.hkv) {
+          l_kvh = 0;
+          F8Req q;
+          do q = f8_req<R>(p, ++l_r, false);  // (there is one with units: this one is in it)
+          while (q.kind == 0);
+          l_info = (l_info + 1) & (kF8Infos - 1);
+          __syncwarp();
+          if (lane == 0) infos[warp][l_info] = q;
+          __syncwarp();
+        }
       }
     }
-    pend_stage = stage;
-    if (lane == 0) meta[stage].unit = F8Unit{l_info, l_kvh, l_blk, l_v};
+    const F8Req& q = infos[warp][l_info];
+    n.unit = F8Unit{l_info, l_kvh, l_blk, l_v};
+    n.vis = 0;
+    n.page = -2;
+    n.entry = 0;
+    if (q.kind != kF8Keys) return;
+    const int32_t at = q.tile(l_v) * kF8Tile + lane;
+    n.vis = __ballot_sync(0xffffffffu, q.seen(at));
+    if (TMA) {  // whole boxes
+      const int b = lane & -p.box_rows;
+      n.vis = __ballot_sync(0xffffffffu, (n.vis & bits_between(b, b + p.box_rows)) != 0);
+    }
+    if (n.vis >> lane & 1u) {
+      const int32_t slot = (int32_t)fast_div((uint32_t)at, p.ps_magic, p.ps_shift);
+      n.entry = at - slot * p.page_size;
+      n.page = __ldg(p.indices + q.slot_base + slot);
+    }
+  };
+  auto load = [&](const Taken& n, int stage, int32_t& ek, int32_t& ev) {  // and ask for its rows' exponents
+    unsigned char* kd = ring + stage * 2 * C::kSide;
+    // a bad page: past the pool, where a box is zero-filled
+    int32_t row = TMA ? (int32_t)(p.num_pages * p.page_size) : -1;
+    ek = ev = 0;
+    if (n.page >= 0 && n.page < p.num_pages) {
+      row = n.page * p.page_size + n.entry;
+      const int64_t e = (int64_t)n.page * p.hkv + n.unit.kvh;
+      ek = __ldg(p.k_exp + e);
+      ev = __ldg(p.v_exp + e);
+    } else if (n.page != -2) {
+      report(p.status, PA_DEVICE_BAD_PAGE);
+    }
+    if (lane == 0) meta[stage].unit = n.unit;
     // rows that several blocks read stay in L2 as other data does, the others leave it first
-    const uint64_t pol = infos[warp][l_info].blocks > 1 ? keep : policy;
+    const uint64_t pol = infos[warp][n.unit.info].blocks > 1 ? keep : policy;
     if (TMA) {
-      const int step = p.box_rows;
       if (lane == 0) {
-        const uint32_t bytes = (uint32_t)__popc(l_vis) * D * 2;
+        const uint32_t bytes = (uint32_t)__popc(n.vis) * D * 2;
         if (bytes) mbar_arrive_expect_tx(&full[stage], bytes);
         else arrive(&full[stage]);
       }
-      for (int b = 0; b < kF8Tile; b += step) {
+      for (int b = 0; b < kF8Tile; b += p.box_rows) {
         const int32_t y = __shfl_sync(0xffffffffu, row, b);
-        if (lane == 0 && (l_vis >> b & 1u)) {
-          tma_load_3d(kd + b * D, &tm_k, &full[stage], 0, l_kvh, y, pol);
-          tma_load_3d(kd + C::kSide + b * D, &tm_v, &full[stage], 0, l_kvh, y, pol);
+        if (lane == 0 && (n.vis >> b & 1u)) {
+          tma_load_3d(kd + b * D, &tm_k, &full[stage], 0, n.unit.kvh, y, pol);
+          tma_load_3d(kd + C::kSide + b * D, &tm_v, &full[stage], 0, n.unit.kvh, y, pol);
         }
       }
     } else {
@@ -434,7 +444,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         const int32_t y = __shfl_sync(0xffffffffu, row, i + sub);
         const uint32_t d = to + side_at<D>(i + sub, ch);
         if (y >= 0) {
-          const int64_t from = y * pitch + (int64_t)l_kvh * D + ch * 16;
+          const int64_t from = y * pitch + (int64_t)n.unit.kvh * D + ch * 16;
           cp_async_16(d, p.k_pool + from, pol);
           cp_async_16(d + C::kSide, p.v_pool + from, pol);
         } else {
@@ -444,33 +454,41 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       }
       copies_arrive(&full[stage]);
     }
-    if (more) {
-      if (++l_v == infos[warp][l_info].tiles) {
-        l_v = 0;
-        if (++l_blk == infos[warp][l_info].blocks) {
-          l_blk = 0;
-          if (++l_kvh == p.hkv) {
-            l_kvh = 0;
-            enter(l_r + 1);
-          }
-        }
-      }
-      resolve();
-    }
+    __syncwarp();
+  };
+  auto store_exponents = [&](int stage, int32_t ek, int32_t ev) {
+    meta[stage].k_scale[lane] = power_of_two(min(max(ek, PA_V2_FP8_EXP_MIN), PA_V2_FP8_EXP_MAX));
+    meta[stage].v_scale[lane] = __float2half_rn(power_of_two(min(max(ev, PA_V2_FP8_EXP_MIN), PA_V2_FP8_EXP_MAX)));
+  };
+  auto flush = [&]() {  // the exponents of the unit loaded last
+    if (pend_stage >= 0) store_exponents(pend_stage, pend_k, pend_v);
+    pend_stage = -1;
     __syncwarp();
   };
 
-  int64_t issued = 0;
+  int64_t issued = min(count, (int64_t)S);
+  Taken next;
   if (count > 0) {
-    enter(start_req[warp]);
-    const int64_t off = start_off[warp], head = (int64_t)infos[warp][l_info].blocks * infos[warp][l_info].tiles;
-    l_kvh = (int32_t)(off / head);
+    l_r = start_req[warp];
+    const int32_t tiles = infos[warp][0].tiles;
+    const int64_t off = start_off[warp], head = (int64_t)infos[warp][0].blocks * tiles;
+    l_kvh = (int32_t)div_units(off, head);
     const int64_t in_head = off - l_kvh * head;
-    l_blk = (int32_t)(in_head / infos[warp][l_info].tiles);
-    l_v = (int32_t)(in_head - (int64_t)l_blk * infos[warp][l_info].tiles);
-    resolve();
-    for (; issued < min(count, (int64_t)S); ++issued) issue((int)issued, issued + 1 < count);
-    if (issued == count) flush();
+    l_blk = (int32_t)div_units(in_head, tiles);
+    l_v = (int32_t)(in_head - (int64_t)l_blk * tiles) - 1;
+    // each step for all stages before the next: their loads' latencies pass together
+    Taken n[S];
+    int32_t ek[S], ev[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+      if (i < issued) take(n[i]);
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+      if (i < issued) load(n[i], i, ek[i], ev[i]);
+    if (issued < count) take(next);
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+      if (i < issued) store_exponents(i, ek[i], ev[i]);
     __syncwarp();
   }
 
@@ -623,7 +641,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         float ks[2 * MT];
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) ks[i] = meta[stage].k_scale[key0 + 8 * i + g];
-        uint32_t pb[NT][2 * MT];
+        // (each step for all columns before the next: 2 warps a scheduler do not hide one column's chain of shuffles)
+        float mt[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           uint32_t see[2] = {0xffffffffu, 0xffffffffu};
@@ -631,7 +650,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             see[0] = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t) >> key0;
             see[1] = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t + 1) >> key0;
           }
-          float mt[2] = {-INFINITY, -INFINITY};
+          mt[nt][0] = mt[nt][1] = -INFINITY;
 #pragma unroll
           for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -640,25 +659,31 @@ __global__ void __launch_bounds__(kF8Threads, 1)
               float y = s[i][nt][k] * (ks[q4] * qf[nt][k & 1]);
               if (!clear) y = see[k & 1] >> (8 * q4 + g) & 1u ? y : -INFINITY;
               s[i][nt][k] = y;
-              mt[k & 1] = fmaxf(mt[k & 1], y);
+              mt[nt][k & 1] = fmaxf(mt[nt][k & 1], y);
             }
-          float scale[2];
-          bool grow = false;
+        }
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            mt[k] = fmaxf(mt[k], __shfl_xor_sync(0xffffffffu, mt[k], 4));
-            mt[k] = fmaxf(mt[k], __shfl_xor_sync(0xffffffffu, mt[k], 8));
-            mt[k] = fmaxf(mt[k], __shfl_xor_sync(0xffffffffu, mt[k], 16));
-            const bool need = mt[k] > m[nt][k] + kF8Lazy;  // m = -inf at first: any finite maximum
-            scale[k] = 1.f;
-            if (need) {
-              scale[k] = m[nt][k] == -INFINITY ? 0.f : fast_exp2(m[nt][k] - mt[k]);
-              m[nt][k] = mt[k];
-            }
-            l[nt][k] *= scale[k];
-            grow |= need;
+        for (int x = 4; x <= 16; x <<= 1)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mt[nt][0] = fmaxf(mt[nt][0], __shfl_xor_sync(0xffffffffu, mt[nt][0], x));
+            mt[nt][1] = fmaxf(mt[nt][1], __shfl_xor_sync(0xffffffffu, mt[nt][1], x));
           }
-          if (__any_sync(0xffffffffu, grow)) {
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          grow |= mt[nt][0] > m[nt][0] + kF8Lazy || mt[nt][1] > m[nt][1] + kF8Lazy;
+        if (__any_sync(0xffffffffu, grow)) {  // m = -inf at first: any finite maximum
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float scale[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const bool need = mt[nt][k] > m[nt][k] + kF8Lazy;
+              scale[k] = !need ? 1.f : m[nt][k] == -INFINITY ? 0.f : fast_exp2(m[nt][k] - mt[nt][k]);
+              if (need) m[nt][k] = mt[nt][k];
+              l[nt][k] *= scale[k];
+            }
 #pragma unroll
             for (int c = 0; c < KS; ++c) {
               o[c][nt][0] *= scale[0];
@@ -667,6 +692,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
               o[c][nt][3] *= scale[1];
             }
           }
+        }
+        uint32_t pb[NT][2 * MT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
           const float off[2] = {(m[nt][0] == -INFINITY ? 0.f : m[nt][0]) - kF8Shift,
                                 (m[nt][1] == -INFINITY ? 0.f : m[nt][1]) - kF8Shift};
 #pragma unroll
@@ -676,9 +705,13 @@ __global__ void __launch_bounds__(kF8Threads, 1)
               const float e0 = fast_exp2(s[i][nt][2 * h] - off[0]), e1 = fast_exp2(s[i][nt][2 * h + 1] - off[1]);
               l[nt][0] += e0;
               l[nt][1] += e1;
-              pb[nt][2 * i + h] = transposed(TC<__half>::pack(e0, e1));
+              pb[nt][2 * i + h] = TC<__half>::pack(e0, e1);
             }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2 * MT; ++i) pb[nt][i] = transposed(pb[nt][i]);
         // ---- O^T += V^T P^T, 32 / MT dims at a time
         uint32_t vs[2 * MT];  // tokens key0 + 8 i + 2 t, + 1
 #pragma unroll
@@ -782,7 +815,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         // a part: the warp's last in its ring, which nothing loads into any more, else in the workspace
         const int part = last ? 1 : 0;
         float* to = last ? reinterpret_cast<float*>(ring)
-                         : p.warp_parts + ((int64_t)blockIdx.x * kF8Warps + warp) * (kF8MaxRows * D);
+                         : p.warp_parts + ((int64_t)blockIdx.x * kF8Warps + warp) * (kF8MaxRows * (D + 4));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -790,7 +823,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             const int32_t c = 8 * nt + 2 * t + k;
 #pragma unroll
             for (int i = 0; i < KS; ++i)
-              *reinterpret_cast<float2*>(to + c * D + 16 * i + 2 * g) = make_float2(o[i][nt][k], o[i][nt][2 + k]);
+              *reinterpret_cast<float2*>(to + c * C::kPartRow + 16 * i + 2 * g) = make_float2(o[i][nt][k], o[i][nt][2 + k]);
             if (g == 0) {
               stats[warp][part][0][c] = m[nt][k];
               stats[warp][part][1][c] = l[nt][k];
@@ -800,12 +833,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           parts[warp][part] = F8Part{1, v_first != 0, !ends, last, infos[warp][c_info].t0, row0, rows, kvh, u0 + j + (infos[warp][c_info].tiles - unit.v)};
       }
     }
+    flush();
     if (issued < count) {
-      issue(stage, issued + 1 < count);
-      ++issued;
-    } else {
-      flush();
-      __syncwarp();
+      load(next, stage, pend_k, pend_v);
+      pend_stage = stage;
+      if (++issued < count) take(next);
     }
     if (++stage == S) {
       stage = 0;
@@ -823,63 +855,92 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     if (!TMA) cp_async_wait<0>();
     if (lane == 0) parts[warp][0].valid = parts[warp][1].valid = 0;
   }
+  if (threadIdx.x == 0) p.headers[blockIdx.x].valid = 0;
   __syncthreads();
 
-  // ---- parts of the same block are joined: with those of other CTAs still to come, or as the result
-  if (threadIdx.x == 0) p.headers[blockIdx.x].valid = 0;
-  for (int i = 0; i < 2 * kF8Warps;) {
-    if (!parts[i >> 1][i & 1].valid) {
-      ++i;
-      continue;
+  // ---- parts of the same block are joined: with those of other CTAs still to come, or as the result.  Part 2 w + k is
+  // warp w's; parts whose block goes on in the next one form a chain.
+  const F8Part& mine_part = parts[(lane & 15) >> 1][lane & 1];
+  const uint32_t valid = __ballot_sync(0xffffffffu, lane < 16 && mine_part.valid);
+  const uint32_t goes_on = __ballot_sync(0xffffffffu, lane < 16 && mine_part.valid && mine_part.to_next);
+  auto next_chain = [&](uint32_t& left) {
+    uint32_t chain = left & -left;
+    left &= left - 1;
+    while (left && (goes_on & (1u << (31 - __clz(chain))))) {
+      chain |= left & -left;
+      left &= left - 1;
     }
-    const F8Part a = parts[i >> 1][i & 1];
-    uint32_t chain = 1u << i;
-    int end = i;
-    for (int k = i + 1; k < 2 * kF8Warps && parts[end >> 1][end & 1].to_next; ++k) {
-      if (!parts[k >> 1][k & 1].valid) continue;
-      chain |= 1u << k;
-      end = k;
-    }
-    const bool from_prev = a.from_prev != 0, to_next = parts[end >> 1][end & 1].to_next != 0;
-    float* slot = p.cta_parts + ((int64_t)blockIdx.x * 2 + (from_prev ? 0 : 1)) * (kF8MaxRows * (D + 1));
-    for (int e = threadIdx.x; e < a.rows * (D / 2); e += kF8Threads) {
-      const int c = e / (D / 2), d = e % (D / 2);
-      float M = -INFINITY;
+    return chain;
+  };
+  auto slot_of = [&](const F8Part& a) {
+    return p.cta_parts + ((int64_t)blockIdx.x * 2 + (a.from_prev ? 0 : 1)) * (kF8MaxRows * (D + 1));
+  };
+  // the parts' weights, normalized: a warp a chain, a lane a row
+  int number = 0;
+  for (uint32_t left = valid; left; ++number) {
+    const uint32_t chain = next_chain(left);
+    if (number % kF8Warps != warp) continue;
+    const F8Part& a = parts[(__ffs(chain) - 1) >> 1][(__ffs(chain) - 1) & 1];
+    const bool cut = a.from_prev || (goes_on >> (31 - __clz(chain)) & 1u);
+    if (lane < a.rows) {
+      float M = -INFINITY, sum = 0.f;
       for (uint32_t b = chain; b; b &= b - 1) {
         const int k = __ffs(b) - 1;
-        M = fmaxf(M, stats[k >> 1][k & 1][0][c]);
+        M = fmaxf(M, stats[k >> 1][k & 1][0][lane]);
       }
-      float sum = 0.f;
-      float2 acc = make_float2(0.f, 0.f);
       for (uint32_t b = chain; b; b &= b - 1) {
         const int k = __ffs(b) - 1;
-        const float mk = stats[k >> 1][k & 1][0][c];
+        const float mk = stats[k >> 1][k & 1][0][lane];
         const float w = mk == -INFINITY ? 0.f : fast_exp2(mk - M);
-        float2 x;
-        if (k & 1) {
-          x = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(smem + (k >> 1) * C::kRing) + c * D + 2 * d);
-        } else {
-          x = __ldcg(reinterpret_cast<const float2*>(
-              p.warp_parts + ((int64_t)blockIdx.x * kF8Warps + (k >> 1)) * (kF8MaxRows * D) + c * D + 2 * d));
-        }
-        sum += w * stats[k >> 1][k & 1][1][c];
-        acc.x += w * x.x;
-        acc.y += w * x.y;
+        sum += w * stats[k >> 1][k & 1][1][lane];
+        stats[k >> 1][k & 1][0][lane] = w;
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      for (uint32_t b = chain; b; b &= b - 1) {
+        const int k = __ffs(b) - 1;
+        stats[k >> 1][k & 1][0][lane] *= inv;
+      }
       const float lse = sum == 0.f ? -INFINITY : M - kF8Shift + fast_log2(sum);
-      if (from_prev || to_next) {
-        *reinterpret_cast<float2*>(slot + c * D + 2 * d) = make_float2(acc.x * inv, acc.y * inv);
-        if (d == 0) slot[kF8MaxRows * D + c] = lse;
+      if (cut) slot_of(a)[kF8MaxRows * D + lane] = lse;
+      else p.lse_out[out_row_of(p, a.t0, a.kvh, a.row0 + lane)] = lse;
+    }
+    if (lane == 0 && !a.from_prev && cut)
+      p.headers[blockIdx.x] = F8Header{1, a.t0, a.row0, a.rows, a.kvh,
+                                       (int32_t)div_units(a.end - 1, run * kF8Warps), {0, 0}};
+  }
+  __syncthreads();
+  // the values: 32 / (D / 4) rows a warp
+  constexpr int kQuads = D / 4;
+  const int d = lane % kQuads * 4;
+  for (uint32_t left = valid; left;) {
+    const uint32_t chain = next_chain(left);
+    const F8Part& a = parts[(__ffs(chain) - 1) >> 1][(__ffs(chain) - 1) & 1];
+    const bool cut = a.from_prev || (goes_on >> (31 - __clz(chain)) & 1u);
+    for (int c = warp * (32 / kQuads) + lane / kQuads; c < a.rows; c += kF8Warps * (32 / kQuads)) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int k = 0; k < 2 * kF8Warps; ++k) {
+        if (!(chain >> k & 1u)) continue;
+        const float w = stats[k >> 1][k & 1][0][c];
+        const float4 x =
+            k & 1 ? *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + (k >> 1) * C::kRing) +
+                                                     c * C::kPartRow + d)
+                  : __ldcg(reinterpret_cast<const float4*>(
+                        p.warp_parts + ((int64_t)blockIdx.x * kF8Warps + (k >> 1)) * (kF8MaxRows * (D + 4)) +
+                        c * C::kPartRow + d));
+        acc.x += w * x.x;
+        acc.y += w * x.y;
+        acc.z += w * x.z;
+        acc.w += w * x.w;
+      }
+      if (cut) {
+        *reinterpret_cast<float4*>(slot_of(a) + c * D + d) = acc;
       } else {
         const int64_t row = out_row_of(p, a.t0, a.kvh, a.row0 + c);
-        static_cast<uint32_t*>(p.out)[row * (D / 2) + d] = pack16(p, acc.x * inv, acc.y * inv);
-        if (d == 0) p.lse_out[row] = lse;
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + d) =
+            make_uint2(pack16(p, acc.x, acc.y), pack16(p, acc.z, acc.w));
       }
     }
-    if (threadIdx.x == 0 && !from_prev && to_next)
-      p.headers[blockIdx.x] = F8Header{1, a.t0, a.row0, a.rows, a.kvh, (int32_t)((a.end - 1) / (run * kF8Warps)), {0, 0}};
-    i = end + 1;
   }
 }
 
@@ -987,7 +1048,7 @@ F8Pick pick_f8(int64_t rows, bool tma) {
 bool f8_aligned(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }
 
 int64_t warp_part_bytes(int32_t ctas, int32_t head_dim) {
-  return (int64_t)ctas * kF8Warps * kF8MaxRows * head_dim * (int64_t)sizeof(float);
+  return (int64_t)ctas * kF8Warps * kF8MaxRows * (head_dim + 4) * (int64_t)sizeof(float);
 }
 int64_t cta_part_bytes(int32_t ctas, int32_t head_dim) {
   return (int64_t)ctas * 2 * kF8MaxRows * (head_dim + 1) * (int64_t)sizeof(float);
