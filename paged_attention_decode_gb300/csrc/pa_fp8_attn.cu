@@ -46,8 +46,7 @@
 namespace pa {
 namespace {
 
-constexpr int kF8Warps = 8;
-constexpr int kF8Threads = 32 * kF8Warps;
+constexpr int kF8MaxWarps = 12;
 constexpr int kF8Tile = 32;       // keys of a unit
 constexpr int kF8Infos = 8;       // requests a warp's ring can have under way, a power of two
 constexpr float kF8Shift = 11.f;  // P is rounded relative to 2^kF8Shift at the row's offset,
@@ -62,13 +61,15 @@ struct F8Cfg {
   static constexpr int kSide = kF8Tile * D;    // bytes of a stage's K, or V
   static constexpr bool kQSmem = NT > 2;       // q's fragments live in shared memory: 16 NT registers are too many
   static constexpr int kMt = NT > 3 ? 1 : 2;   // 16-key halves of a tile that go through the softmax at once
-  static constexpr int kStages = (D == 128 ? 1 : 2) * (kQSmem ? 2 : 3);
+  // 64 K registers: 168 a thread for 12 warps, 255 for 8
+  static constexpr int kWarps = NT == 1 ? 12 : 8;
+  static constexpr int kStages = (D == 128 ? 1 : 2) * (kQSmem || kWarps == 12 ? 2 : 3);
   static constexpr int kRing = kStages * 2 * kSide;
   static constexpr int kQ = kQSmem ? kRows * D * 2 : 0;
   // floats of a row of a partial result in the ring: shifted by 4 banks a row where there is room
   static constexpr int kPartRow = kRows * (D + 4) * 4 <= kRing ? D + 4 : D;
-  static constexpr int kOffQ = kF8Warps * kRing;
-  static constexpr int kOffMeta = kOffQ + kF8Warps * kQ;
+  static constexpr int kOffQ = kWarps * kRing;
+  static constexpr int kOffMeta = kOffQ + kWarps * kQ;
 };
 
 struct F8Header;
@@ -88,7 +89,7 @@ struct F8Params {
   const int32_t* positions;
   void* out;
   float* lse_out;
-  float* warp_parts;   // [ctas * kF8Warps][kF8MaxRows * (head_dim + 4)]
+  float* warp_parts;   // [ctas * kF8MaxWarps][kF8MaxRows * (head_dim + 4)]
   float* cta_parts;    // [ctas][2][kF8MaxRows * (head_dim + 1)]
   F8Header* headers;   // [ctas]
   int32_t* status;
@@ -180,8 +181,11 @@ __device__ __forceinline__ int64_t units_of(const F8Params& p, const F8Req& g) {
 
 // What the loading side of a warp tells the computing side of a stage.
 struct F8Unit {
-  int32_t info, kvh, blk, v;
+  int32_t base;   // its first row
+  int32_t flags;  // kUnit* and, above them, its request's place in the warp's infos
+  int32_t kvh, blk;
 };
+constexpr int kUnitBegins = 1, kUnitEnds = 2, kUnitShift = 2;  // the first, the last unit of its block
 struct alignas(16) F8Meta {
   float k_scale[kF8Tile];
   __half v_scale[kF8Tile];
@@ -281,21 +285,21 @@ __device__ __forceinline__ int64_t out_row_of(const F8Params& p, int32_t t0, int
 }
 
 template <int D, int NT, bool TMA>
-__global__ void __launch_bounds__(kF8Threads, 1)
+__global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
     pa_v2_attention_fp8_kernel(const F8Params p, const __grid_constant__ CUtensorMap tm_k,
                                const __grid_constant__ CUtensorMap tm_v) {
   using C = F8Cfg<D, NT>;
-  constexpr int S = C::kStages, R = C::kRows, KS = D / 16;
+  constexpr int S = C::kStages, R = C::kRows, KS = D / 16, W = C::kWarps;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ uint64_t bars[kF8Warps][S];
-  __shared__ F8Req infos[kF8Warps][kF8Infos];
-  __shared__ F8Part parts[kF8Warps][2];
-  __shared__ float stats[kF8Warps][2][2][kF8MaxRows];  // [part][maxima, sums]
-  __shared__ int64_t warp_sum[kF8Warps];
-  __shared__ int64_t start_off[kF8Warps];
-  __shared__ int32_t start_req[kF8Warps];
+  __shared__ uint64_t bars[W][S];
+  __shared__ F8Req infos[W][kF8Infos];
+  __shared__ F8Part parts[W][2];
+  __shared__ float stats[W][2][2][kF8MaxRows];  // [part][maxima, sums]
+  __shared__ int64_t warp_sum[W];
+  __shared__ int64_t start_off[W];
+  __shared__ int32_t start_req[W];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -314,7 +318,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 
   // ---- the cut: every warp's first unit
   int64_t units = 0, mine = 0;
-  const int per_thread = (p.batch + kF8Threads - 1) / kF8Threads;
+  const int per_thread = (p.batch + (32 * W) - 1) / (32 * W);
   const int r0 = (int)min((int64_t)threadIdx.x * per_thread, (int64_t)p.batch), r1 = min(r0 + per_thread, p.batch);
   F8Req own = {};
   for (int r = r0; r < r1; ++r) {
@@ -330,20 +334,20 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   if (lane == 31) warp_sum[warp] = upto;
   __syncthreads();
   int64_t before = upto - mine;
-  for (int w = 0; w < kF8Warps; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w < warp) before += warp_sum[w];
     units += warp_sum[w];
   }
-  const int64_t workers = (int64_t)gridDim.x * kF8Warps;
+  const int64_t workers = (int64_t)gridDim.x * W;
   const int64_t run = max(div_units(units + workers - 1, workers), (int64_t)1);
   if (mine > 0) {
-    const int64_t first = (int64_t)blockIdx.x * kF8Warps * run;
-    if (before + mine > first && before < first + kF8Warps * run) {
+    const int64_t first = (int64_t)blockIdx.x * W * run;
+    if (before + mine > first && before < first + W * run) {
       int64_t at = before;
       for (int r = r0; r < r1; ++r) {
         if (per_thread > 1) own = f8_req<R>(p, r, false);
         const int64_t u = units_of(p, own);
-        for (int w = 0; w < kF8Warps; ++w) {
+        for (int w = 0; w < W; ++w) {
           const int64_t x = first + w * run;
           if (x >= at && x < at + u) {
             start_req[w] = r;
@@ -357,12 +361,14 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   }
   __syncthreads();
 
-  const int64_t u0 = ((int64_t)blockIdx.x * kF8Warps + warp) * run;
+  const int64_t u0 = ((int64_t)blockIdx.x * W + warp) * run;
   const int64_t count = start_req[warp] < 0 ? 0 : min(run, units - u0);
 
   // ---- the loading side: units are taken (their pages asked for) and then loaded
   // (requests are read from shared memory where they are needed: in registers, twice, they crowd out the accumulators)
-  int32_t l_r = 0, l_kvh = 0, l_blk = 0, l_v = -1, l_info = 0;
+  int32_t l_r = 0, l_kvh = 0, l_blk = 0, l_v = 0, l_info = 0;  // the unit taken last
+  int32_t l_tiles = 0, l_base = 0, l_sinks = 0, l_win = 0, l_hi = 0;  // of its block: units left behind it, its first
+                                                                      // row, tiles of sinks left, rows [l_win, l_hi)
   int32_t pend_k = 0, pend_v = 0, pend_stage = -1;
   const uint64_t policy = policy_evict_first(), keep = policy_evict_normal();
   struct Taken {
@@ -370,39 +376,59 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     uint32_t vis;         // rows that somebody sees, whole boxes
     F8Unit unit;
   };
-  auto take = [&](Taken& n) {  // the unit behind the one taken last
-    if (++l_v == infos[warp][l_info].tiles) {
-      l_v = 0;
-      if (++l_blk == infos[warp][l_info].blocks) {
-        l_blk = 0;
-        if (++l_kvh == p.hkv) {
-          l_kvh = 0;
-          F8Req q;
-          do q = f8_req<R>(p, ++l_r, false);  // (there is one with units: this one is in it)
-          while (q.kind == 0);
-          l_info = (l_info + 1) & (kF8Infos - 1);
-          __syncwarp();
-          if (lane == 0) infos[warp][l_info] = q;
-          __syncwarp();
-        }
-      }
-    }
+  auto enter_block = [&](int v) {
     const F8Req& q = infos[warp][l_info];
-    n.unit = F8Unit{l_info, l_kvh, l_blk, l_v};
-    n.vis = 0;
+    l_tiles = q.tiles - 1 - v;
+    l_base = q.tile(v) * kF8Tile;
+    l_sinks = q.ns - v;
+    l_win = q.kind == kF8Keys ? q.win0 : INT_MAX;
+    l_hi = q.hi;
+  };
+  auto take = [&](Taken& n, bool first) {  // the unit behind the one taken last (first: that one)
+    int flags = 0;
+    if (!first) {
+      if (l_tiles > 0) {
+        --l_tiles;
+        l_base += kF8Tile;
+        if (--l_sinks == 0) l_base += infos[warp][l_info].gap * kF8Tile;
+      } else {
+        if (++l_blk == infos[warp][l_info].blocks) {
+          l_blk = 0;
+          if (++l_kvh == p.hkv) {
+            l_kvh = 0;
+            F8Req q;
+            do q = f8_req<R>(p, ++l_r, false);  // (there is one with units: this one is in it)
+            while (q.kind == 0);
+            l_info = (l_info + 1) & (kF8Infos - 1);
+            __syncwarp();
+            if (lane == 0) infos[warp][l_info] = q;
+            __syncwarp();
+          }
+        }
+        enter_block(0);
+        flags = kUnitBegins;
+      }
+    } else if (l_v == 0) {
+      flags = kUnitBegins;
+    }
+    if (l_tiles == 0) flags |= kUnitEnds;
+    n.unit = F8Unit{l_base, flags | l_info << kUnitShift, l_kvh, l_blk};
+    const int32_t at = l_base + lane;
     n.page = -2;
     n.entry = 0;
-    if (q.kind != kF8Keys) return;
-    const int32_t at = q.tile(l_v) * kF8Tile + lane;
-    n.vis = __ballot_sync(0xffffffffu, q.seen(at));
-    if (TMA) {  // whole boxes
-      const int b = lane & -p.box_rows;
-      n.vis = __ballot_sync(0xffffffffu, (n.vis & bits_between(b, b + p.box_rows)) != 0);
+    n.vis = 0xffffffffu;
+    if (l_base < l_win || l_base + kF8Tile > l_hi) {  // some rows nobody sees
+      const F8Req& q = infos[warp][l_info];
+      n.vis = __ballot_sync(0xffffffffu, q.kind == kF8Keys && q.seen(at));
+      if (TMA) {  // whole boxes
+        const int b = lane & -p.box_rows;
+        n.vis = __ballot_sync(0xffffffffu, (n.vis & bits_between(b, b + p.box_rows)) != 0);
+      }
     }
     if (n.vis >> lane & 1u) {
       const int32_t slot = (int32_t)fast_div((uint32_t)at, p.ps_magic, p.ps_shift);
       n.entry = at - slot * p.page_size;
-      n.page = __ldg(p.indices + q.slot_base + slot);
+      n.page = __ldg(p.indices + infos[warp][l_info].slot_base + slot);
     }
   };
   auto load = [&](const Taken& n, int stage, int32_t& ek, int32_t& ev) {  // and ask for its rows' exponents
@@ -420,7 +446,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     }
     if (lane == 0) meta[stage].unit = n.unit;
     // rows that several blocks read stay in L2 as other data does, the others leave it first
-    const uint64_t pol = infos[warp][n.unit.info].blocks > 1 ? keep : policy;
+    const uint64_t pol = infos[warp][n.unit.flags >> kUnitShift].blocks > 1 ? keep : policy;
     if (TMA) {
       if (lane == 0) {
         const uint32_t bytes = (uint32_t)__popc(n.vis) * D * 2;
@@ -454,16 +480,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       }
       copies_arrive(&full[stage]);
     }
-    __syncwarp();
   };
   auto store_exponents = [&](int stage, int32_t ek, int32_t ev) {
     meta[stage].k_scale[lane] = power_of_two(min(max(ek, PA_V2_FP8_EXP_MIN), PA_V2_FP8_EXP_MAX));
     meta[stage].v_scale[lane] = __float2half_rn(power_of_two(min(max(ev, PA_V2_FP8_EXP_MIN), PA_V2_FP8_EXP_MAX)));
-  };
-  auto flush = [&]() {  // the exponents of the unit loaded last
-    if (pend_stage >= 0) store_exponents(pend_stage, pend_k, pend_v);
-    pend_stage = -1;
-    __syncwarp();
   };
 
   int64_t issued = min(count, (int64_t)S);
@@ -475,17 +495,18 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     l_kvh = (int32_t)div_units(off, head);
     const int64_t in_head = off - l_kvh * head;
     l_blk = (int32_t)div_units(in_head, tiles);
-    l_v = (int32_t)(in_head - (int64_t)l_blk * tiles) - 1;
+    l_v = (int32_t)(in_head - (int64_t)l_blk * tiles);
+    enter_block(l_v);
     // each step for all stages before the next: their loads' latencies pass together
     Taken n[S];
     int32_t ek[S], ev[S];
 #pragma unroll
     for (int i = 0; i < S; ++i)
-      if (i < issued) take(n[i]);
+      if (i < issued) take(n[i], i == 0);
 #pragma unroll
     for (int i = 0; i < S; ++i)
       if (i < issued) load(n[i], i, ek[i], ev[i]);
-    if (issued < count) take(next);
+    if (issued < count) take(next, false);
 #pragma unroll
     for (int i = 0; i < S; ++i)
       if (i < issued) store_exponents(i, ek[i], ev[i]);
@@ -499,22 +520,28 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   float qf[NT][2];              // scale of the columns' scores
   uint2* qs = reinterpret_cast<uint2*>(smem + C::kOffQ + warp * C::kQ);  // [KS][NT][32], with kQSmem
   int32_t low = 0, tok = -1, clear0 = 0;  // of the row on this lane; rows [clear0, ds) are seen by all of the block's
-  int32_t c_info = 0, rows = 0, row0 = 0, kvh = 0, v_first = 0;
+  int32_t c_info = 0, c_ds = 0, c_sinks = 0, rows = 0, row0 = 0, kvh = 0, v_first = l_v;
+  bool c_keys = false;
+  int64_t block_end = 0;        // the unit behind the block's last
   bool alive = true;
   int stage = 0;
   uint32_t parity = 0;
   for (int64_t j = 0; j < count; ++j) {
     const F8Unit unit = meta[stage].unit;
-    if (j == 0 || unit.v == 0) {
+    if (j == 0 || (unit.flags & kUnitBegins)) {
       // ---- a block begins (here): its rows, Q and an empty state
-      c_info = unit.info;
+      c_info = unit.flags >> kUnitShift;
       kvh = unit.kvh;
+      if (j > 0) v_first = 0;
+      block_end = u0 + j + infos[warp][c_info].tiles - v_first;
+      c_keys = infos[warp][c_info].kind == kF8Keys;
+      c_ds = infos[warp][c_info].ds;
+      c_sinks = min(infos[warp][c_info].sink_end, c_ds);
       row0 = unit.blk * R;
       rows = (int32_t)min((int64_t)R, (int64_t)infos[warp][c_info].n * p.group - row0);
-      v_first = unit.v;
       const int32_t last_tok = (int32_t)fast_div((uint32_t)(row0 + rows - 1), p.g_magic, p.g_shift);
       tok = lane < rows ? (int32_t)fast_div((uint32_t)(row0 + lane), p.g_magic, p.g_shift) : -1;
-      if (infos[warp][c_info].kind == kF8Keys) {
+      if (c_keys) {
         low = tok >= 0 ? window_from(p, infos[warp][c_info], tok) : 0;
         clear0 = p.window > 0 ? (int32_t)max((int64_t)infos[warp][c_info].lo, (int64_t)infos[warp][c_info].ds + last_tok + 1 - p.window) : infos[warp][c_info].lo;
         constexpr int kMine = D / 4;  // dims of a lane: t D / 4 ..
@@ -576,10 +603,12 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       }
     }
 
-    const int32_t base = infos[warp][c_info].tile(unit.v) * kF8Tile;
-    const bool clear = base + kF8Tile <= infos[warp][c_info].ds && (base >= clear0 || (base >= infos[warp][c_info].lo && base + kF8Tile <= infos[warp][c_info].sink_end));
+    // every row of the block sees every row of the tile: behind the last one's window's begin, or among the sinks (which
+    // begin at row 0; without them sink_end is the first listed row, in the first tile)
+    const int32_t base = unit.base;
+    const bool clear = base + kF8Tile <= c_ds && (base >= clear0 || base + kF8Tile <= c_sinks);
     uint32_t mine_bits = 0, some = 0xffffffffu;
-    bool skip = infos[warp][c_info].kind != kF8Keys;
+    bool skip = !c_keys;
     if (!clear && !skip) {
       if (tok >= 0) mine_bits = seen_bits(p, infos[warp][c_info], tok, low, base);
       some = __reduce_or_sync(0xffffffffu, mine_bits);
@@ -719,11 +748,13 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           vs[i] = *reinterpret_cast<const uint32_t*>(&meta[stage].v_scale[key0 + 8 * i + 2 * t]);
         // what a row does not see must not meet its zero weight as a NaN: rows that nobody sees become zeros, and NaN
         // codes of the others zeros that are put back below for the rows that see them
-        uint32_t vm[2 * MT], taint = 0;
+        uint32_t vm[2 * MT] = {}, taint = 0;
+        if (!clear) {
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-          const uint32_t u = some >> (key0 + 8 * i + 2 * t);
-          vm[i] = (u & 1u ? 0x00ff00ffu : 0u) | (u & 2u ? 0xff00ff00u : 0u);
+          for (int i = 0; i < 2 * MT; ++i) {
+            const uint32_t u = some >> (key0 + 8 * i + 2 * t);
+            vm[i] = (u & 1u ? 0x00ff00ffu : 0u) | (u & 2u ? 0xff00ff00u : 0u);
+          }
         }
         auto values = [&](bool safe) {
 #pragma unroll
@@ -786,7 +817,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     __syncwarp();
 
     // ---- the block's last unit, or this warp's
-    const bool ends = unit.v + 1 == infos[warp][c_info].tiles;
+    const bool ends = (unit.flags & kUnitEnds) != 0;
     const bool last = j + 1 == count;
     if (ends || last) {
 #pragma unroll
@@ -815,7 +846,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         // a part: the warp's last in its ring, which nothing loads into any more, else in the workspace
         const int part = last ? 1 : 0;
         float* to = last ? reinterpret_cast<float*>(ring)
-                         : p.warp_parts + ((int64_t)blockIdx.x * kF8Warps + warp) * (kF8MaxRows * (D + 4));
+                         : p.warp_parts + ((int64_t)blockIdx.x * W + warp) * (kF8MaxRows * (D + 4));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -830,15 +861,18 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             }
           }
         if (lane == 0)
-          parts[warp][part] = F8Part{1, v_first != 0, !ends, last, infos[warp][c_info].t0, row0, rows, kvh, u0 + j + (infos[warp][c_info].tiles - unit.v)};
+          parts[warp][part] = F8Part{1, v_first != 0, !ends, last, infos[warp][c_info].t0, row0, rows, kvh,
+                                      block_end};
       }
     }
-    flush();
+    if (pend_stage >= 0) store_exponents(pend_stage, pend_k, pend_v);  // of the unit loaded last
+    pend_stage = -1;
     if (issued < count) {
       load(next, stage, pend_k, pend_v);
       pend_stage = stage;
-      if (++issued < count) take(next);
+      if (++issued < count) take(next, false);
     }
+    __syncwarp();
     if (++stage == S) {
       stage = 0;
       parity ^= 1;
@@ -860,9 +894,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 
   // ---- parts of the same block are joined: with those of other CTAs still to come, or as the result.  Part 2 w + k is
   // warp w's; parts whose block goes on in the next one form a chain.
-  const F8Part& mine_part = parts[(lane & 15) >> 1][lane & 1];
-  const uint32_t valid = __ballot_sync(0xffffffffu, lane < 16 && mine_part.valid);
-  const uint32_t goes_on = __ballot_sync(0xffffffffu, lane < 16 && mine_part.valid && mine_part.to_next);
+  const F8Part& mine_part = parts[min(lane >> 1, W - 1)][lane & 1];
+  const uint32_t valid = __ballot_sync(0xffffffffu, lane < 2 * W && mine_part.valid);
+  const uint32_t goes_on = __ballot_sync(0xffffffffu, lane < 2 * W && mine_part.valid && mine_part.to_next);
   auto next_chain = [&](uint32_t& left) {
     uint32_t chain = left & -left;
     left &= left - 1;
@@ -879,34 +913,34 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   int number = 0;
   for (uint32_t left = valid; left; ++number) {
     const uint32_t chain = next_chain(left);
-    if (number % kF8Warps != warp) continue;
+    if (number % W != warp) continue;
     const F8Part& a = parts[(__ffs(chain) - 1) >> 1][(__ffs(chain) - 1) & 1];
     const bool cut = a.from_prev || (goes_on >> (31 - __clz(chain)) & 1u);
     if (lane < a.rows) {
-      float M = -INFINITY, sum = 0.f;
-      for (uint32_t b = chain; b; b &= b - 1) {
-        const int k = __ffs(b) - 1;
-        M = fmaxf(M, stats[k >> 1][k & 1][0][lane]);
+      float mk[2 * W], lk[2 * W], M = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2 * W; ++k) {
+        const bool in = chain >> k & 1u;
+        mk[k] = in ? stats[k >> 1][k & 1][0][lane] : -INFINITY;
+        lk[k] = in ? stats[k >> 1][k & 1][1][lane] : 0.f;
+        M = fmaxf(M, mk[k]);
       }
-      for (uint32_t b = chain; b; b &= b - 1) {
-        const int k = __ffs(b) - 1;
-        const float mk = stats[k >> 1][k & 1][0][lane];
-        const float w = mk == -INFINITY ? 0.f : fast_exp2(mk - M);
-        sum += w * stats[k >> 1][k & 1][1][lane];
-        stats[k >> 1][k & 1][0][lane] = w;
+#pragma unroll
+      for (int k = 0; k < 2 * W; ++k) {
+        mk[k] = mk[k] == -INFINITY ? 0.f : fast_exp2(mk[k] - M);
+        sum += mk[k] * lk[k];
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      for (uint32_t b = chain; b; b &= b - 1) {
-        const int k = __ffs(b) - 1;
-        stats[k >> 1][k & 1][0][lane] *= inv;
-      }
+#pragma unroll
+      for (int k = 0; k < 2 * W; ++k)
+        if (chain >> k & 1u) stats[k >> 1][k & 1][0][lane] = mk[k] * inv;
       const float lse = sum == 0.f ? -INFINITY : M - kF8Shift + fast_log2(sum);
       if (cut) slot_of(a)[kF8MaxRows * D + lane] = lse;
       else p.lse_out[out_row_of(p, a.t0, a.kvh, a.row0 + lane)] = lse;
     }
     if (lane == 0 && !a.from_prev && cut)
       p.headers[blockIdx.x] = F8Header{1, a.t0, a.row0, a.rows, a.kvh,
-                                       (int32_t)div_units(a.end - 1, run * kF8Warps), {0, 0}};
+                                       (int32_t)div_units(a.end - 1, run * W), {0, 0}};
   }
   __syncthreads();
   // the values: 32 / (D / 4) rows a warp
@@ -916,22 +950,33 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     const uint32_t chain = next_chain(left);
     const F8Part& a = parts[(__ffs(chain) - 1) >> 1][(__ffs(chain) - 1) & 1];
     const bool cut = a.from_prev || (goes_on >> (31 - __clz(chain)) & 1u);
-    for (int c = warp * (32 / kQuads) + lane / kQuads; c < a.rows; c += kF8Warps * (32 / kQuads)) {
+    for (int c = warp * (32 / kQuads) + lane / kQuads; c < a.rows; c += W * (32 / kQuads)) {
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int k = 0; k < 2 * kF8Warps; ++k) {
-        if (!(chain >> k & 1u)) continue;
-        const float w = stats[k >> 1][k & 1][0][c];
-        const float4 x =
-            k & 1 ? *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + (k >> 1) * C::kRing) +
-                                                     c * C::kPartRow + d)
-                  : __ldcg(reinterpret_cast<const float4*>(
-                        p.warp_parts + ((int64_t)blockIdx.x * kF8Warps + (k >> 1)) * (kF8MaxRows * (D + 4)) +
-                        c * C::kPartRow + d));
-        acc.x += w * x.x;
-        acc.y += w * x.y;
-        acc.z += w * x.z;
-        acc.w += w * x.w;
+      for (uint32_t b = chain; b;) {  // four parts' loads at once
+        float w[4];
+        float4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[i] = 0.f;
+          x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (b) {
+            const int k = __ffs(b) - 1;
+            b &= b - 1;
+            w[i] = stats[k >> 1][k & 1][0][c];
+            x[i] = k & 1 ? *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + (k >> 1) * C::kRing) +
+                                                            c * C::kPartRow + d)
+                         : __ldcg(reinterpret_cast<const float4*>(
+                               p.warp_parts + ((int64_t)blockIdx.x * W + (k >> 1)) * (kF8MaxRows * (D + 4)) +
+                               c * C::kPartRow + d));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc.x += w[i] * x[i].x;
+          acc.y += w[i] * x[i].y;
+          acc.z += w[i] * x[i].z;
+          acc.w += w[i] * x[i].w;
+        }
       }
       if (cut) {
         *reinterpret_cast<float4*>(slot_of(a) + c * D + d) = acc;
@@ -1029,13 +1074,13 @@ using F8Kernel = void (*)(const F8Params, const CUtensorMap, const CUtensorMap);
 
 struct F8Pick {
   F8Kernel fn;
-  int rows, smem;
+  int rows, smem, threads;
 };
 template <int D, int NT>
 F8Pick pick_f8(bool tma) {
   using C = F8Cfg<D, NT>;
   return {tma ? pa_v2_attention_fp8_kernel<D, NT, true> : pa_v2_attention_fp8_kernel<D, NT, false>, C::kRows,
-          C::kOffMeta + (int)(kF8Warps * C::kStages * sizeof(F8Meta)) + 1024};
+          C::kOffMeta + (int)(C::kWarps * C::kStages * sizeof(F8Meta)) + 1024, 32 * C::kWarps};
 }
 template <int D>
 F8Pick pick_f8(int64_t rows, bool tma) {
@@ -1048,7 +1093,7 @@ F8Pick pick_f8(int64_t rows, bool tma) {
 bool f8_aligned(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }
 
 int64_t warp_part_bytes(int32_t ctas, int32_t head_dim) {
-  return (int64_t)ctas * kF8Warps * kF8MaxRows * (head_dim + 4) * (int64_t)sizeof(float);
+  return (int64_t)ctas * kF8MaxWarps * kF8MaxRows * (head_dim + 4) * (int64_t)sizeof(float);
 }
 int64_t cta_part_bytes(int32_t ctas, int32_t head_dim) {
   return (int64_t)ctas * 2 * kF8MaxRows * (head_dim + 1) * (int64_t)sizeof(float);
@@ -1169,7 +1214,7 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
   const F8Pick pick = head_dim == 64 ? pick_f8<64>(rows, tma) : pick_f8<128>(rows, tma);
   if (!prepare_kernel(reinterpret_cast<const void*>(pick.fn), pick.smem)) return PA_ECUDA;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-  cudaError_t rc = launch_dependent(pick.fn, dim3(sms), dim3(kF8Threads), pick.smem, stream, p, tm_k, tm_v);
+  cudaError_t rc = launch_dependent(pick.fn, dim3(sms), dim3(pick.threads), pick.smem, stream, p, tm_k, tm_v);
   if (rc == cudaSuccess && sms > 1)
     rc = launch_dependent(head_dim == 64 ? pa_v2_fp8_merge_kernel<64> : pa_v2_fp8_merge_kernel<128>,
                           dim3(sms, pick.rows), dim3(32 * kMergeWarps), 0, stream, p);
