@@ -53,6 +53,10 @@ constexpr float kF8Shift = 11.f;  // P is rounded relative to 2^kF8Shift at the 
 constexpr float kF8Lazy = 4.f;    // which follows the running maximum with a lag of up to kF8Lazy (log2 units)
 constexpr int kF8MaxRows = 32;    // query rows of a block, at most
 constexpr int kMergeWarps = 8;
+constexpr int kMergeFew = 16;     // parts that one warp folds alone
+constexpr int kMergeCtas = 2;     // per SM
+constexpr int kF8PartRows = 256;  // rows of a CTA's runs, at most: 12 warps of 8, 8 of 32
+constexpr int64_t kF8Spread = 16;  // units of a run from which on heads are taken side by side
 constexpr int64_t kF8MaxUnits = 1ll << 40;  // units of one request, at most
 
 template <int D, int NT>
@@ -72,7 +76,12 @@ struct F8Cfg {
   static constexpr int kOffMeta = kOffQ + kWarps * kQ;
 };
 
-struct F8Header;
+// A block that several runs (or CTAs) met, for the merge kernel: `parts` partial results, the first in place `first` of
+// F8Params::parts, the others in next, next + step, ...
+struct alignas(16) F8Header {
+  int32_t t0, row0, kvh, rows;
+  int32_t parts, first, next, step;
+};
 
 struct F8Params {
   const void* q;
@@ -89,12 +98,14 @@ struct F8Params {
   const int32_t* positions;
   void* out;
   float* lse_out;
-  float* warp_parts;   // [ctas * kF8MaxWarps][kF8MaxRows * (head_dim + 4)]
-  float* cta_parts;    // [ctas][2][kF8MaxRows * (head_dim + 1)]
-  F8Header* headers;   // [ctas]
+  float* parts;        // [workers * 2][part_rows * (head_dim + 1)]: values, then lse (log2)
+  int32_t* counts;     // [workers]: what the merge kernel has to do for the header, in CTA's turns; [workers]: 1 where
+                       // only every CTA's first warp has one
+  F8Header* headers;   // [workers]
   int32_t* status;
   int64_t num_pages, num_indices;
-  int32_t batch, num_tokens, mask_words, page_size, box_rows, hq, hkv, group, ctas, q_bf16;
+  int32_t part_rows;  // rows of a part
+  int32_t batch, num_tokens, mask_words, page_size, box_rows, hq, hkv, group, team, workers, q_bf16;
   uint32_t ps_magic, ps_shift, g_magic, g_shift;
   float scale_log2;
   int32_t window, sinks;  // 0: no window
@@ -175,9 +186,8 @@ __device__ __forceinline__ int64_t div_units(int64_t a, int64_t b) {
   return a / b;
 }
 
-__device__ __forceinline__ int64_t units_of(const F8Params& p, const F8Req& g) {
-  return g.kind == 0 ? 0 : (int64_t)g.blocks * g.tiles * p.hkv;
-}
+// Units of a KV head.
+__device__ __forceinline__ int64_t units_of(const F8Req& g) { return g.kind == 0 ? 0 : (int64_t)g.blocks * g.tiles; }
 
 // What the loading side of a warp tells the computing side of a stage.
 struct F8Unit {
@@ -192,17 +202,17 @@ struct alignas(16) F8Meta {
   F8Unit unit;
 };
 
-// A block's keys that a warp met only part of.
+// A block's keys that a warp met only part of, where a CTA joins its warps' parts.
 struct F8Part {
-  int32_t valid, from_prev, to_next, in_ring;
+  int32_t valid, from_prev, to_next;
   int32_t t0, row0, rows, kvh;
   int64_t end;  // the unit behind the block's last
 };
 
-// A block that begins in a CTA and goes on in the next: what CTA x of the merge kernel folds.
-struct alignas(16) F8Header {
-  int32_t valid, t0, row0, rows, kvh, last_cta, pad[2];
-};
+// Turns of a merge CTA for a block: one per row, or, with few parts, one per kMergeWarps rows.
+__device__ __forceinline__ int32_t merge_turns(int32_t rows, int32_t parts) {
+  return parts > kMergeFew ? rows : (rows + kMergeWarps - 1) / kMergeWarps;
+}
 
 // Bits [a, b) of a word, a and b clamped to [0, 32].
 __device__ __forceinline__ uint32_t bits_between(int a, int b) {
@@ -296,7 +306,7 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
   __shared__ uint64_t bars[W][S];
   __shared__ F8Req infos[W][kF8Infos];
   __shared__ F8Part parts[W][2];
-  __shared__ float stats[W][2][2][kF8MaxRows];  // [part][maxima, sums]
+  __shared__ float stats[W][2][2][R];  // [part][maxima, sums]
   __shared__ int64_t warp_sum[W];
   __shared__ int64_t start_off[W];
   __shared__ int32_t start_req[W];
@@ -323,7 +333,7 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
   F8Req own = {};
   for (int r = r0; r < r1; ++r) {
     own = f8_req<R>(p, r, blockIdx.x == 0);
-    mine += units_of(p, own);
+    mine += units_of(own);
   }
   int64_t upto = mine;
 #pragma unroll
@@ -338,17 +348,31 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
     if (w < warp) before += warp_sum[w];
     units += warp_sum[w];
   }
-  const int64_t workers = (int64_t)gridDim.x * W;
-  const int64_t run = max(div_units(units + workers - 1, workers), (int64_t)1);
+  // Warps of a team take the same run of units of neighbouring heads, side by side: their rows lie side by side too, and
+  // HBM serves them so (64 ragged requests of 8 KV heads 255 -> 218 us, 5.2 -> 6.1 TB/s).  Then every warp leaves its own
+  // partial results.  Where runs are short those cost more than that gains (a request of 32K tokens: 205 parts a head, 30
+  // against 22 us): there each team is one warp, the warps of a CTA take neighbouring runs and join their parts.
+  const int32_t worker0 = (int)blockIdx.x * W;
+  int32_t size = p.team, teams = p.workers / size;
+  if (div_units(units * (p.hkv / size), teams) < kF8Spread) {
+    size = 1;
+    teams = p.workers;
+  }
+  const int32_t groups = p.hkv / size;
+  units *= groups;
+  before *= groups;
+  mine *= groups;
+  const bool join = size == 1;
+  const int64_t run = max(div_units(units + teams - 1, teams), (int64_t)1);
   if (mine > 0) {
-    const int64_t first = (int64_t)blockIdx.x * W * run;
-    if (before + mine > first && before < first + W * run) {
+    const int64_t first = worker0 / size * run, behind = (int64_t)((worker0 + W - 1) / size + 1) * run;
+    if (before + mine > first && before < behind) {
       int64_t at = before;
       for (int r = r0; r < r1; ++r) {
         if (per_thread > 1) own = f8_req<R>(p, r, false);
-        const int64_t u = units_of(p, own);
+        const int64_t u = units_of(own) * groups;
         for (int w = 0; w < W; ++w) {
-          const int64_t x = first + w * run;
+          const int64_t x = (worker0 + w) / size * run;
           if (x >= at && x < at + u) {
             start_req[w] = r;
             start_off[w] = x - at;
@@ -361,7 +385,10 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
   }
   __syncthreads();
 
-  const int64_t u0 = ((int64_t)blockIdx.x * W + warp) * run;
+  const int32_t worker = worker0 + warp, team = worker / size, in_team = worker - team * size;
+  const int64_t u0 = team * run;
+  if (lane == 0) p.counts[worker] = 0;
+  if (worker0 == 0 && threadIdx.x == 0) p.counts[p.workers] = join;
   const int64_t count = start_req[warp] < 0 ? 0 : min(run, units - u0);
 
   // ---- the loading side: units are taken (their pages asked for) and then loaded
@@ -394,8 +421,8 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
       } else {
         if (++l_blk == infos[warp][l_info].blocks) {
           l_blk = 0;
-          if (++l_kvh == p.hkv) {
-            l_kvh = 0;
+          if ((l_kvh += size) >= p.hkv) {
+            l_kvh = in_team;
             F8Req q;
             do q = f8_req<R>(p, ++l_r, false);  // (there is one with units: this one is in it)
             while (q.kind == 0);
@@ -492,8 +519,9 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
     l_r = start_req[warp];
     const int32_t tiles = infos[warp][0].tiles;
     const int64_t off = start_off[warp], head = (int64_t)infos[warp][0].blocks * tiles;
-    l_kvh = (int32_t)div_units(off, head);
-    const int64_t in_head = off - l_kvh * head;
+    const int32_t heads = (int32_t)div_units(off, head);  // groups of heads before
+    const int64_t in_head = off - heads * head;
+    l_kvh = heads * size + in_team;
     l_blk = (int32_t)div_units(in_head, tiles);
     l_v = (int32_t)(in_head - (int64_t)l_blk * tiles);
     enter_block(l_v);
@@ -843,26 +871,35 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
             if (g == 0) p.lse_out[row] = sum == 0.f ? -INFINITY : m[nt][k] - kF8Shift + fast_log2(sum);
           }
       } else {
-        // a part: the warp's last in its ring, which nothing loads into any more, else in the workspace
-        const int part = last ? 1 : 0;
-        float* to = last ? reinterpret_cast<float*>(ring)
-                         : p.warp_parts + ((int64_t)blockIdx.x * W + warp) * (kF8MaxRows * (D + 4));
+        // a part: of a block that began in the run before, or of one that goes on in the next
+        const int part = last ? 1 : 0;  // to be joined: the warp's last in its ring, which nothing loads into any more
+        float* to = join && last ? reinterpret_cast<float*>(ring)
+                                 : p.parts + ((int64_t)worker * 2 + (join || v_first == 0 ? 1 : 0)) * (p.part_rows * (D + 1));
+        const int pitch = join && last ? C::kPartRow : D;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int32_t c = 8 * nt + 2 * t + k;
+            if (c >= rows) continue;
+            const float sum = l[nt][k], by = join ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
             for (int i = 0; i < KS; ++i)
-              *reinterpret_cast<float2*>(to + c * C::kPartRow + 16 * i + 2 * g) = make_float2(o[i][nt][k], o[i][nt][2 + k]);
-            if (g == 0) {
+              *reinterpret_cast<float2*>(to + c * pitch + 16 * i + 2 * g) = make_float2(o[i][nt][k] * by, o[i][nt][2 + k] * by);
+            if (g == 0 && join) {
               stats[warp][part][0][c] = m[nt][k];
-              stats[warp][part][1][c] = l[nt][k];
+              stats[warp][part][1][c] = sum;
+            } else if (g == 0) {
+              to[p.part_rows * D + c] = sum == 0.f ? -INFINITY : m[nt][k] - kF8Shift + fast_log2(sum);
             }
           }
-        if (lane == 0)
-          parts[warp][part] = F8Part{1, v_first != 0, !ends, last, infos[warp][c_info].t0, row0, rows, kvh,
-                                      block_end};
+        if (lane == 0 && join) {
+          parts[warp][part] = F8Part{1, v_first != 0, !ends, infos[warp][c_info].t0, row0, rows, kvh, block_end};
+        } else if (lane == 0 && v_first == 0) {
+          const int32_t n = (int32_t)(div_units(block_end - 1, run) - team) + 1;
+          p.counts[worker] = merge_turns(rows, n);
+          p.headers[worker] = F8Header{infos[warp][c_info].t0, row0, kvh, rows, n, worker * 2 + 1, (worker + size) * 2, size * 2};
+        }
       }
     }
     if (pend_stage >= 0) store_exponents(pend_stage, pend_k, pend_v);  // of the unit loaded last
@@ -887,11 +924,13 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
       }
     }
     if (!TMA) cp_async_wait<0>();
-    if (lane == 0) parts[warp][0].valid = parts[warp][1].valid = 0;
+    if (lane == 0) {
+      p.counts[worker] = 0;
+      parts[warp][0].valid = parts[warp][1].valid = 0;
+    }
   }
-  if (threadIdx.x == 0) p.headers[blockIdx.x].valid = 0;
+  if (!join) return;
   __syncthreads();
-
   // ---- parts of the same block are joined: with those of other CTAs still to come, or as the result.  Part 2 w + k is
   // warp w's; parts whose block goes on in the next one form a chain.
   const F8Part& mine_part = parts[min(lane >> 1, W - 1)][lane & 1];
@@ -907,7 +946,7 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
     return chain;
   };
   auto slot_of = [&](const F8Part& a) {
-    return p.cta_parts + ((int64_t)blockIdx.x * 2 + (a.from_prev ? 0 : 1)) * (kF8MaxRows * (D + 1));
+    return p.parts + (int64_t)(worker0 + (a.from_prev ? 0 : 1)) * 2 * (p.part_rows * (D + 1));
   };
   // the parts' weights, normalized: a warp a chain, a lane a row
   int number = 0;
@@ -935,12 +974,14 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
       for (int k = 0; k < 2 * W; ++k)
         if (chain >> k & 1u) stats[k >> 1][k & 1][0][lane] = mk[k] * inv;
       const float lse = sum == 0.f ? -INFINITY : M - kF8Shift + fast_log2(sum);
-      if (cut) slot_of(a)[kF8MaxRows * D + lane] = lse;
+      if (cut) slot_of(a)[p.part_rows * D + lane] = lse;
       else p.lse_out[out_row_of(p, a.t0, a.kvh, a.row0 + lane)] = lse;
     }
-    if (lane == 0 && !a.from_prev && cut)
-      p.headers[blockIdx.x] = F8Header{1, a.t0, a.row0, a.rows, a.kvh,
-                                       (int32_t)div_units(a.end - 1, run * W), {0, 0}};
+    if (lane == 0 && !a.from_prev && cut) {
+      const int32_t n = (int32_t)div_units(a.end - 1, run * W) - (int)blockIdx.x + 1;
+      p.counts[worker0] = merge_turns(a.rows, n);
+      p.headers[worker0] = F8Header{a.t0, a.row0, a.kvh, a.rows, n, (worker0 + 1) * 2, (worker0 + W) * 2, W * 2};
+    }
   }
   __syncthreads();
   // the values: 32 / (D / 4) rows a warp
@@ -966,8 +1007,7 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
             x[i] = k & 1 ? *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + (k >> 1) * C::kRing) +
                                                             c * C::kPartRow + d)
                          : __ldcg(reinterpret_cast<const float4*>(
-                               p.warp_parts + ((int64_t)blockIdx.x * W + (k >> 1)) * (kF8MaxRows * (D + 4)) +
-                               c * C::kPartRow + d));
+                               p.parts + ((int64_t)(worker0 + (k >> 1)) * 2 + 1) * (p.part_rows * (D + 1)) + c * D + d));
           }
         }
 #pragma unroll
@@ -989,85 +1029,136 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
   }
 }
 
-// Folds the parts of a block that several CTAs met: weights 2^(lse_i - max) of the normalized parts.  CTA (x, y) takes
-// row y of the block that begins in CTA x of the attention kernel; its warps take every eighth part, joined in a fixed
-// order.
+// Folds the parts of the blocks that several runs met: weights 2^(lse_i - max) of the normalized parts.  A turn of a CTA
+// is a row whose parts its warps share, joined in a fixed order, or, where the parts are few, a row for each warp.
+// Where CTAs have joined their warps' parts, kMergeCtas CTAs share each one's header; else every CTA adds up all turns
+// and takes every gridDim.x-th (4 us that the first case does not need).
 template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) pa_v2_fp8_merge_kernel(const F8Params p) {
+__global__ void __launch_bounds__(32 * kMergeWarps, kMergeCtas) pa_v2_fp8_merge_kernel(const F8Params p) {
   constexpr int V = D / 32;  // dims of a lane
+  constexpr int kThreads = 32 * kMergeWarps;
+  extern __shared__ uint8_t counts[];  // [workers]: at most kF8MaxRows each
+  __shared__ int32_t turns_to[kThreads], warp_turns[kMergeWarps];
   __shared__ float sm[kMergeWarps], sl[kMergeWarps], so[kMergeWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait_prerequisites();
-  const F8Header h = p.headers[blockIdx.x];
-  const int c = blockIdx.y;
-  if (!h.valid || c >= h.rows) return;
-  const int n = h.last_cta - (int)blockIdx.x + 1;
-  float M = -INFINITY, L = 0.f, acc[V];
+
+  auto fold = [&](const F8Header& h, int turn) {
+    const bool few = h.parts <= kMergeFew;
+    const int c = few ? turn * kMergeWarps + warp : turn;
+    float M = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  constexpr int kBatch = 4;
-  for (int k0 = warp; k0 < n; k0 += kBatch * kMergeWarps) {
-    float lse[kBatch], x[kBatch][V];
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    constexpr int kBatch = 8;
+    const int stride = few ? 1 : kMergeWarps;
+    for (int k0 = few ? 0 : warp; k0 < h.parts && c < h.rows; k0 += kBatch * stride) {
+      float lse[kBatch], x[kBatch][V];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int k = k0 + b * kMergeWarps;
-      lse[b] = -INFINITY;
+      for (int b = 0; b < kBatch; ++b) {
+        const int k = k0 + b * stride;
+        lse[b] = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < V; ++i) x[b][i] = 0.f;
-      if (k < n) {
-        const float* slot = p.cta_parts + ((int64_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * (kF8MaxRows * (D + 1));
-        lse[b] = __ldcg(slot + kF8MaxRows * D + c);
+        for (int i = 0; i < V; ++i) x[b][i] = 0.f;
+        if (k < h.parts) {
+          const float* part = p.parts + (int64_t)(k == 0 ? h.first : h.next + (k - 1) * h.step) * (p.part_rows * (D + 1));
+          lse[b] = __ldcg(part + p.part_rows * D + c);
 #pragma unroll
-        for (int i = 0; i < V; i += 2) {
-          const float2 y = __ldcg(reinterpret_cast<const float2*>(slot + c * D + V * lane + i));
-          x[b][i] = y.x;
-          x[b][i + 1] = y.y;
+          for (int i = 0; i < V; i += 2) {
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(part + c * D + V * lane + i));
+            x[b][i] = y.x;
+            x[b][i + 1] = y.y;
+          }
         }
       }
+      float mb = M;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) mb = fmaxf(mb, lse[b]);
+      const float mu = mb == -INFINITY ? 0.f : mb;
+      const float sc = M == -INFINITY ? 0.f : fast_exp2(M - mu);
+      L *= sc;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] *= sc;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (lse[b] == -INFINITY) continue;
+        const float w = fast_exp2(lse[b] - mu);
+        L += w;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(w, x[b][i], acc[i]);
+      }
+      M = mb;
     }
-    float mb = M;
+    if (few) {
+      if (c >= h.rows) return;
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const int64_t row = out_row_of(p, h.t0, h.kvh, h.row0 + c);
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) mb = fmaxf(mb, lse[b]);
-    const float mu = mb == -INFINITY ? 0.f : mb;
-    const float sc = M == -INFINITY ? 0.f : fast_exp2(M - mu);
-    L *= sc;
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] *= sc;
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (lse[b] == -INFINITY) continue;
-      const float w = fast_exp2(lse[b] - mu);
-      L += w;
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = fmaf(w, x[b][i], acc[i]);
+      for (int i = 0; i < V; i += 2)
+        static_cast<uint32_t*>(p.out)[row * (D / 2) + (V * lane + i) / 2] = pack16(p, acc[i] * inv, acc[i + 1] * inv);
+      if (lane == 0) p.lse_out[row] = L == 0.f ? -INFINITY : M + fast_log2(L);
+      return;
     }
-    M = mb;
-  }
-  if (lane == 0) {
-    sm[warp] = M;
-    sl[warp] = L;
-  }
+    if (lane == 0) {
+      sm[warp] = M;
+      sl[warp] = L;
+    }
 #pragma unroll
-  for (int i = 0; i < V; ++i) so[warp][V * lane + i] = acc[i];
+    for (int i = 0; i < V; ++i) so[warp][V * lane + i] = acc[i];
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) mx = fmaxf(mx, sm[w]);
+      float sum = 0.f;
+      float2 out = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) {
+        const float f = sm[w] == -INFINITY ? 0.f : fast_exp2(sm[w] - mx);
+        sum += f * sl[w];
+        out.x += f * so[w][2 * threadIdx.x];
+        out.y += f * so[w][2 * threadIdx.x + 1];
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const int64_t row = out_row_of(p, h.t0, h.kvh, h.row0 + c);
+      static_cast<uint32_t*>(p.out)[row * (D / 2) + threadIdx.x] = pack16(p, out.x * inv, out.y * inv);
+      if (threadIdx.x == 0) p.lse_out[row] = sum == 0.f ? -INFINITY : mx + fast_log2(sum);
+    }
+    __syncthreads();
+  };
+
+  const int ctas = gridDim.x / kMergeCtas, mine = (int)blockIdx.x % ctas * (p.workers / ctas);
+  const int joined = __ldcg(p.counts + p.workers), turns = __ldcg(p.counts + mine);
+  const F8Header h = p.headers[mine];  // (asked for with the counts: whether it holds anything they tell)
+  if (joined) {
+    for (int turn = (int)blockIdx.x / ctas; turn < turns; turn += kMergeCtas) fold(h, turn);
+    return;
+  }
+  for (int i = threadIdx.x; i < p.workers; i += kThreads) counts[i] = (uint8_t)__ldcg(p.counts + i);
   __syncthreads();
-  if (threadIdx.x >= D / 2) return;
-  float mx = -INFINITY;
+  // turns up to each thread's stretch of workers
+  const int per = (p.workers + kThreads - 1) / kThreads;
+  int32_t upto = 0;
+  for (int i = threadIdx.x * per; i < min((int)(threadIdx.x + 1) * per, p.workers); ++i) upto += counts[i];
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) mx = fmaxf(mx, sm[w]);
-  float sum = 0.f;
-  float2 out = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    const float f = sm[w] == -INFINITY ? 0.f : fast_exp2(sm[w] - mx);
-    sum += f * sl[w];
-    out.x += f * so[w][2 * threadIdx.x];
-    out.y += f * so[w][2 * threadIdx.x + 1];
+  for (int w = 1; w < 32; w <<= 1) {
+    const int32_t x = __shfl_up_sync(0xffffffffu, upto, w);
+    if (lane >= w) upto += x;
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t row = out_row_of(p, h.t0, h.kvh, h.row0 + c);
-  static_cast<uint32_t*>(p.out)[row * (D / 2) + threadIdx.x] = pack16(p, out.x * inv, out.y * inv);
-  if (threadIdx.x == 0) p.lse_out[row] = sum == 0.f ? -INFINITY : mx + fast_log2(sum);
+  if (lane == 31) warp_turns[warp] = upto;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) upto += warp_turns[w];
+  turns_to[threadIdx.x] = upto;
+  __syncthreads();
+  const int total = turns_to[kThreads - 1];
+  for (int turn = blockIdx.x; turn < total; turn += gridDim.x) {
+    int lo = 0;  // the first stretch that ends behind the turn
+    for (int step = kThreads / 2; step >= 1; step >>= 1)
+      if (turns_to[lo + step - 1] <= turn) lo += step;
+    int worker = lo * per, c = turn - (lo ? turns_to[lo - 1] : 0);
+    while (c >= counts[worker]) c -= counts[worker++];
+    fold(p.headers[worker], c);
+  }
 }
 
 using F8Kernel = void (*)(const F8Params, const CUtensorMap, const CUtensorMap);
@@ -1092,11 +1183,19 @@ F8Pick pick_f8(int64_t rows, bool tma) {
 
 bool f8_aligned(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }
 
-int64_t warp_part_bytes(int32_t ctas, int32_t head_dim) {
-  return (int64_t)ctas * kF8MaxWarps * kF8MaxRows * (head_dim + 4) * (int64_t)sizeof(float);
+// The workspace: partial results, headers and counts.
+int64_t parts_bytes(int32_t ctas, int32_t head_dim) {
+  return (int64_t)ctas * kF8PartRows * 2 * (head_dim + 1) * (int64_t)sizeof(float);
 }
-int64_t cta_part_bytes(int32_t ctas, int32_t head_dim) {
-  return (int64_t)ctas * 2 * kF8MaxRows * (head_dim + 1) * (int64_t)sizeof(float);
+int64_t all_bytes(int32_t ctas, int32_t head_dim) {
+  return parts_bytes(ctas, head_dim) + (int64_t)ctas * kF8MaxWarps * (sizeof(F8Header) + sizeof(int32_t)) + 16;
+}
+
+// Heads that a team of warps takes side by side: the largest divisor of the KV heads up to 64.
+int32_t team_of(int32_t hkv) {
+  int32_t n = hkv < 64 ? hkv : 64;
+  while (hkv % n) --n;
+  return n;
 }
 
 }  // namespace
@@ -1114,7 +1213,7 @@ extern "C" pa_status pa_v2_attention_fp8_workspace(int32_t device, int32_t num_t
     cudaGetLastError();
     return PA_ECUDA;
   }
-  *bytes = pa::warp_part_bytes(sms, head_dim) + pa::cta_part_bytes(sms, head_dim) + sms * (int64_t)sizeof(pa::F8Header);
+  *bytes = pa::all_bytes(sms, head_dim);
   return PA_OK;
 }
 
@@ -1155,8 +1254,7 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
     cudaGetLastError();
     return PA_ECUDA;
   }
-  const int64_t a = warp_part_bytes(sms, head_dim), b = cta_part_bytes(sms, head_dim);
-  if (workspace_bytes < a + b + sms * (int64_t)sizeof(F8Header)) return PA_ECAPACITY;
+  if (workspace_bytes < all_bytes(sms, head_dim)) return PA_ECAPACITY;
   alignas(64) CUtensorMap tm_k, tm_v;
   std::memset(&tm_k, 0, sizeof(tm_k));
   std::memset(&tm_v, 0, sizeof(tm_v));
@@ -1185,9 +1283,9 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
   p.positions = positions;
   p.out = out;
   p.lse_out = lse2_out;
-  p.warp_parts = static_cast<float*>(workspace);
-  p.cta_parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + a);
-  p.headers = reinterpret_cast<F8Header*>(static_cast<char*>(workspace) + a + b);
+  p.parts = static_cast<float*>(workspace);
+  p.headers = reinterpret_cast<F8Header*>(static_cast<char*>(workspace) + parts_bytes(sms, head_dim));
+  p.counts = reinterpret_cast<int32_t*>(p.headers + sms * kF8MaxWarps);
   p.status = status;
   p.num_pages = num_pages;
   p.num_indices = num_indices;
@@ -1199,7 +1297,7 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
   p.hq = num_qo_heads;
   p.hkv = num_kv_heads;
   p.group = group;
-  p.ctas = sms;
+  p.team = team_of(num_kv_heads);
   p.q_bf16 = q_dtype == PA_BF16;
   const FastDiv fd = FastDiv::make((uint32_t)page_size), fg = FastDiv::make((uint32_t)group);
   p.ps_magic = fd.magic;
@@ -1213,11 +1311,13 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
   const int64_t rows = ((int64_t)num_tokens + batch - 1) / batch * group;
   const F8Pick pick = head_dim == 64 ? pick_f8<64>(rows, tma) : pick_f8<128>(rows, tma);
   if (!prepare_kernel(reinterpret_cast<const void*>(pick.fn), pick.smem)) return PA_ECUDA;
+  p.workers = sms * (pick.threads / 32);
+  p.part_rows = pick.rows;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t rc = launch_dependent(pick.fn, dim3(sms), dim3(pick.threads), pick.smem, stream, p, tm_k, tm_v);
-  if (rc == cudaSuccess && sms > 1)
+  if (rc == cudaSuccess)
     rc = launch_dependent(head_dim == 64 ? pa_v2_fp8_merge_kernel<64> : pa_v2_fp8_merge_kernel<128>,
-                          dim3(sms, pick.rows), dim3(32 * kMergeWarps), 0, stream, p);
+                          dim3(sms * kMergeCtas), dim3(32 * kMergeWarps), p.workers, stream, p);
   if (rc != cudaSuccess) {
     cudaGetLastError();
     return PA_ECUDA;
