@@ -105,8 +105,9 @@ struct F8Params {
   int32_t* status;
   int64_t num_pages, num_indices;
   int32_t part_rows;  // rows of a part
-  int32_t batch, num_tokens, mask_words, page_size, box_rows, hq, hkv, group, team, workers, q_bf16;
-  uint32_t ps_magic, ps_shift, g_magic, g_shift;
+  int32_t batch, num_tokens, mask_words, page_size, box_rows, hq, hkv, group, workers, q_bf16;
+  int32_t team, teams, groups;  // heads side by side, the teams of so many warps, and teams that share a request's heads
+  uint32_t ps_magic, ps_shift, g_magic, g_shift, team_magic, team_shift;
   float scale_log2;
   int32_t window, sinks;  // 0: no window
 };
@@ -308,8 +309,7 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
   __shared__ F8Part parts[W][2];
   __shared__ float stats[W][2][2][R];  // [part][maxima, sums]
   __shared__ int64_t warp_sum[W];
-  __shared__ int64_t start_off[W];
-  __shared__ int32_t start_req[W];
+  __shared__ int64_t ends[32 * W];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -322,7 +322,6 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
     for (int i = 0; i < S; ++i) mbar_init(&full[i], TMA ? 1 : 32);
     fence_barrier_init();
     parts[warp][0].valid = parts[warp][1].valid = 0;
-    start_req[warp] = -1;
   }
   pdl_wait_prerequisites();
 
@@ -330,11 +329,7 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
   int64_t units = 0, mine = 0;
   const int per_thread = (p.batch + (32 * W) - 1) / (32 * W);
   const int r0 = (int)min((int64_t)threadIdx.x * per_thread, (int64_t)p.batch), r1 = min(r0 + per_thread, p.batch);
-  F8Req own = {};
-  for (int r = r0; r < r1; ++r) {
-    own = f8_req<R>(p, r, blockIdx.x == 0);
-    mine += units_of(own);
-  }
+  for (int r = r0; r < r1; ++r) mine += units_of(f8_req<R>(p, r, blockIdx.x == 0));
   int64_t upto = mine;
 #pragma unroll
   for (int w = 1; w < 32; w <<= 1) {
@@ -343,53 +338,29 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
   }
   if (lane == 31) warp_sum[warp] = upto;
   __syncthreads();
-  int64_t before = upto - mine;
   for (int w = 0; w < W; ++w) {
-    if (w < warp) before += warp_sum[w];
+    if (w < warp) upto += warp_sum[w];
     units += warp_sum[w];
   }
-  // Warps of a team take the same run of units of neighbouring heads, side by side: their rows lie side by side too, and
-  // HBM serves them so (64 ragged requests of 8 KV heads 255 -> 218 us, 5.2 -> 6.1 TB/s).  Then every warp leaves its own
-  // partial results.  Where runs are short those cost more than that gains (a request of 32K tokens: 205 parts a head, 30
-  // against 22 us): there each team is one warp, the warps of a CTA take neighbouring runs and join their parts.
-  const int32_t worker0 = (int)blockIdx.x * W;
-  int32_t size = p.team, teams = p.workers / size;
-  if (div_units(units * (p.hkv / size), teams) < kF8Spread) {
-    size = 1;
-    teams = p.workers;
-  }
-  const int32_t groups = p.hkv / size;
-  units *= groups;
-  before *= groups;
-  mine *= groups;
-  const bool join = size == 1;
-  const int64_t run = max(div_units(units + teams - 1, teams), (int64_t)1);
-  if (mine > 0) {
-    const int64_t first = worker0 / size * run, behind = (int64_t)((worker0 + W - 1) / size + 1) * run;
-    if (before + mine > first && before < behind) {
-      int64_t at = before;
-      for (int r = r0; r < r1; ++r) {
-        if (per_thread > 1) own = f8_req<R>(p, r, false);
-        const int64_t u = units_of(own) * groups;
-        for (int w = 0; w < W; ++w) {
-          const int64_t x = (worker0 + w) / size * run;
-          if (x >= at && x < at + u) {
-            start_req[w] = r;
-            start_off[w] = x - at;
-            infos[w][0] = own;
-          }
-        }
-        at += u;
-      }
-    }
-  }
+  ends[threadIdx.x] = upto;  // units of a KV head up to this thread's last request
   __syncthreads();
-
-  const int32_t worker = worker0 + warp, team = worker / size, in_team = worker - team * size;
+  // Warps of a team take the same run of units of neighbouring heads, side by side: their rows lie side by side too, and
+  // HBM serves them so (64 ragged requests of 8 KV heads 255 -> 214 us, 5.2 -> 6.2 TB/s).  Then every warp leaves its own
+  // partial results.  Where runs are short those cost more than that gains (a request of 32K tokens: 205 parts a head, 30
+  // against 22 us): there each team is one warp, the warps of a CTA take neighbouring runs and join their parts.  (Runs
+  // of 16 and more units side by side against joined: 4 x 32K tokens 55 and 65 us, 64 x 1-4K 63 and 74, a request of
+  // 128K 58 and 65; of 9, a request of 64K, 45 and 37.)
+  const int32_t worker0 = (int)blockIdx.x * W, worker = worker0 + warp;
+  const bool join = units * p.groups < (int64_t)kF8Spread * p.teams;
+  const int32_t size = join ? 1 : p.team, teams = join ? p.workers : p.teams, groups = join ? p.hkv : p.groups;
+  const int32_t team = join ? worker : (int32_t)fast_div((uint32_t)worker, p.team_magic, p.team_shift);
+  const int32_t in_team = worker - team * size;
+  units *= groups;
+  const int64_t run = max(div_units(units + teams - 1, teams), (int64_t)1);
   const int64_t u0 = team * run;
+  const int64_t count = max(min(run, units - u0), (int64_t)0);
   if (lane == 0) p.counts[worker] = 0;
   if (worker0 == 0 && threadIdx.x == 0) p.counts[p.workers] = join;
-  const int64_t count = start_req[warp] < 0 ? 0 : min(run, units - u0);
 
   // ---- the loading side: units are taken (their pages asked for) and then loaded
   // (requests are read from shared memory where they are needed: in registers, twice, they crowd out the accumulators)
@@ -513,12 +484,98 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
     meta[stage].v_scale[lane] = __float2half_rn(power_of_two(min(max(ev, PA_V2_FP8_EXP_MIN), PA_V2_FP8_EXP_MAX)));
   };
 
+  // ---- the computing side's view of its block, and Q
+  uint32_t qb[C::kQSmem ? 1 : KS][C::kQSmem ? 1 : NT][2];
+  float qf[NT][2];              // scale of the columns' scores
+  uint2* qs = reinterpret_cast<uint2*>(smem + C::kOffQ + warp * C::kQ);  // [KS][NT][32], with kQSmem
+  int32_t low = 0, tok = -1, clear0 = 0;  // of the row on this lane; rows [clear0, ds) are seen by all of the block's
+  int32_t c_info = 0, c_ds = 0, c_sinks = 0, rows = 0, row0 = 0, kvh = 0, v_first = 0;
+  bool c_keys = false;
+  int64_t block_end = 0;        // the unit behind the block's last
+  auto begin = [&](const F8Unit& unit, int64_t j) {  // a block, at the warp's unit j
+    c_info = unit.flags >> kUnitShift;
+    const F8Req& q = infos[warp][c_info];
+    kvh = unit.kvh;
+    block_end = u0 + j + q.tiles - v_first;
+    c_keys = q.kind == kF8Keys;
+    c_ds = q.ds;
+    c_sinks = min(q.sink_end, c_ds);
+    row0 = unit.blk * R;
+    rows = (int32_t)min((int64_t)R, (int64_t)q.n * p.group - row0);
+    const int32_t last_tok = (int32_t)fast_div((uint32_t)(row0 + rows - 1), p.g_magic, p.g_shift);
+    tok = lane < rows ? (int32_t)fast_div((uint32_t)(row0 + lane), p.g_magic, p.g_shift) : -1;
+    low = c_keys && tok >= 0 ? window_from(p, q, tok) : 0;
+    clear0 = p.window > 0 ? (int32_t)max((int64_t)q.lo, (int64_t)q.ds + last_tok + 1 - p.window) : q.lo;
+  };
+  constexpr int kMine = D / 4;  // dims of a lane: t D / 4 ..
+  auto fetch_q = [&](uint4 (&raw)[NT][D / 32]) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int32_t c = nt * 8 + g;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const uint16_t*>(p.q) + out_row_of(p, infos[warp][c_info].t0, kvh, row0 + c) * D + t * kMine);
+#pragma unroll
+      for (int i = 0; i < kMine / 8; ++i) raw[nt][i] = c_keys && c < rows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto take_q = [&](const uint4 (&raw)[NT][D / 32]) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float x[kMine];
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < kMine / 8; ++i) {
+        const uint32_t w[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float2 f;
+          if (p.q_bf16) f = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+          else f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+          x[8 * i + 2 * k] = f.x;
+          x[8 * i + 2 * k + 1] = f.y;
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // the row's largest element to [2^13, 2^14)
+      int e = 13;
+      if (top > 0.f && top <= 3.4028234e38f) e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+      const float up = power_of_two(13 - e), down = power_of_two(e - 13) * p.scale_log2;
+      qf[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+      qf[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const uint32_t b0 = TC<__half>::pack(x[4 * k] * up, x[4 * k + 1] * up);
+        const uint32_t b1 = TC<__half>::pack(x[4 * k + 2] * up, x[4 * k + 3] * up);
+        if (C::kQSmem) {
+          qs[(k * NT + nt) * 32 + lane] = make_uint2(b0, b1);
+        } else {
+          qb[k][nt][0] = b0;
+          qb[k][nt][1] = b1;
+        }
+      }
+    }
+  };
+
   int64_t issued = min(count, (int64_t)S);
   Taken next;
   if (count > 0) {
-    l_r = start_req[warp];
-    const int32_t tiles = infos[warp][0].tiles;
-    const int64_t off = start_off[warp], head = (int64_t)infos[warp][0].blocks * tiles;
+    // the request that holds unit u0, searched by the warp's lanes: its thread, then, where a thread has several, it
+    int first = 0;
+    while (!__any_sync(0xffffffffu, ends[first + lane] * groups > u0)) first += 32;
+    first += __ffs(__ballot_sync(0xffffffffu, ends[first + lane] * groups > u0)) - 1;
+    l_r = min(first * per_thread, p.batch - 1);
+    int64_t off = u0 - (first > 0 ? ends[first - 1] * groups : 0);
+    F8Req q = f8_req<R>(p, l_r, false);
+    while (off >= units_of(q) * groups) {
+      off -= units_of(q) * groups;
+      q = f8_req<R>(p, ++l_r, false);
+    }
+    if (lane == 0) infos[warp][0] = q;
+    __syncwarp();
+    const int32_t tiles = q.tiles;
+    const int64_t head = (int64_t)q.blocks * tiles;
     const int32_t heads = (int32_t)div_units(off, head);  // groups of heads before
     const int64_t in_head = off - heads * head;
     l_kvh = heads * size + in_team;
@@ -534,101 +591,45 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
 #pragma unroll
     for (int i = 0; i < S; ++i)
       if (i < issued) load(n[i], i, ek[i], ev[i]);
+    v_first = l_v;
+    begin(n[0].unit, 0);
+    uint4 raw[NT][D / 32];
+    fetch_q(raw);
     if (issued < count) take(next, false);
 #pragma unroll
     for (int i = 0; i < S; ++i)
       if (i < issued) store_exponents(i, ek[i], ev[i]);
+    take_q(raw);
     __syncwarp();
   }
 
   // ---- the computing side
   float o[KS][NT][4];           // O^T: dims 16 c + 2 g, + 1 (elements 0, 2 and 1, 3's rows), columns 2 t, 2 t + 1
-  uint32_t qb[C::kQSmem ? 1 : KS][C::kQSmem ? 1 : NT][2];
   float m[NT][2], l[NT][2];     // of columns 2 t and 2 t + 1; sums over this lane's keys
-  float qf[NT][2];              // scale of the columns' scores
-  uint2* qs = reinterpret_cast<uint2*>(smem + C::kOffQ + warp * C::kQ);  // [KS][NT][32], with kQSmem
-  int32_t low = 0, tok = -1, clear0 = 0;  // of the row on this lane; rows [clear0, ds) are seen by all of the block's
-  int32_t c_info = 0, c_ds = 0, c_sinks = 0, rows = 0, row0 = 0, kvh = 0, v_first = l_v;
-  bool c_keys = false;
-  int64_t block_end = 0;        // the unit behind the block's last
+  auto reset = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int c = 0; c < KS; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[c][nt][i] = 0.f;
+    }
+  };
+  reset();
   bool alive = true;
   int stage = 0;
   uint32_t parity = 0;
   for (int64_t j = 0; j < count; ++j) {
     const F8Unit unit = meta[stage].unit;
-    if (j == 0 || (unit.flags & kUnitBegins)) {
-      // ---- a block begins (here): its rows, Q and an empty state
-      c_info = unit.flags >> kUnitShift;
-      kvh = unit.kvh;
-      if (j > 0) v_first = 0;
-      block_end = u0 + j + infos[warp][c_info].tiles - v_first;
-      c_keys = infos[warp][c_info].kind == kF8Keys;
-      c_ds = infos[warp][c_info].ds;
-      c_sinks = min(infos[warp][c_info].sink_end, c_ds);
-      row0 = unit.blk * R;
-      rows = (int32_t)min((int64_t)R, (int64_t)infos[warp][c_info].n * p.group - row0);
-      const int32_t last_tok = (int32_t)fast_div((uint32_t)(row0 + rows - 1), p.g_magic, p.g_shift);
-      tok = lane < rows ? (int32_t)fast_div((uint32_t)(row0 + lane), p.g_magic, p.g_shift) : -1;
-      if (c_keys) {
-        low = tok >= 0 ? window_from(p, infos[warp][c_info], tok) : 0;
-        clear0 = p.window > 0 ? (int32_t)max((int64_t)infos[warp][c_info].lo, (int64_t)infos[warp][c_info].ds + last_tok + 1 - p.window) : infos[warp][c_info].lo;
-        constexpr int kMine = D / 4;  // dims of a lane: t D / 4 ..
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int32_t c = nt * 8 + g;
-          float x[kMine];
-          float top = 0.f;
-          if (c < rows) {
-            const uint4* src = reinterpret_cast<const uint4*>(
-                static_cast<const uint16_t*>(p.q) + out_row_of(p, infos[warp][c_info].t0, kvh, row0 + c) * D + t * kMine);
-#pragma unroll
-            for (int i = 0; i < kMine / 8; ++i) {
-              const uint4 u = __ldg(src + i);
-              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float2 f;
-                if (p.q_bf16) f = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
-                else f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                x[8 * i + 2 * k] = f.x;
-                x[8 * i + 2 * k + 1] = f.y;
-                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-              }
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) x[i] = 0.f;
-          }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          // the row's largest element to [2^13, 2^14)
-          int e = 13;
-          if (top > 0.f && top <= 3.4028234e38f) e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
-          const float up = power_of_two(13 - e), down = power_of_two(e - 13) * p.scale_log2;
-          qf[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
-          qf[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            const uint32_t b0 = TC<__half>::pack(x[4 * k] * up, x[4 * k + 1] * up);
-            const uint32_t b1 = TC<__half>::pack(x[4 * k + 2] * up, x[4 * k + 3] * up);
-            if (C::kQSmem) {
-              qs[(k * NT + nt) * 32 + lane] = make_uint2(b0, b1);
-            } else {
-              qb[k][nt][0] = b0;
-              qb[k][nt][1] = b1;
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        m[nt][0] = m[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-        for (int c = 0; c < KS; ++c)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[c][nt][i] = 0.f;
-      }
+    if (j > 0 && (unit.flags & kUnitBegins)) {
+      v_first = 0;
+      begin(unit, j);
+      uint4 raw[NT][D / 32];
+      fetch_q(raw);
+      take_q(raw);
+      reset();
     }
 
     // every row of the block sees every row of the tile: behind the last one's window's begin, or among the sinks (which
@@ -956,23 +957,44 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
     const F8Part& a = parts[(__ffs(chain) - 1) >> 1][(__ffs(chain) - 1) & 1];
     const bool cut = a.from_prev || (goes_on >> (31 - __clz(chain)) & 1u);
     if (lane < a.rows) {
-      float mk[2 * W], lk[2 * W], M = -INFINITY, sum = 0.f;
+      float M = -INFINITY, sum = 0.f;
+      for (uint32_t b = chain; b;) {  // four parts' loads at once
+        float mk[4];
 #pragma unroll
-      for (int k = 0; k < 2 * W; ++k) {
-        const bool in = chain >> k & 1u;
-        mk[k] = in ? stats[k >> 1][k & 1][0][lane] : -INFINITY;
-        lk[k] = in ? stats[k >> 1][k & 1][1][lane] : 0.f;
-        M = fmaxf(M, mk[k]);
+        for (int i = 0; i < 4; ++i) {
+          mk[i] = -INFINITY;
+          if (b) {
+            const int k = __ffs(b) - 1;
+            b &= b - 1;
+            mk[i] = stats[k >> 1][k & 1][0][lane];
+          }
+        }
+        M = fmaxf(M, fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])));
       }
+      for (uint32_t b = chain; b;) {
+        float mk[4], lk[4];
+        float* at[4];
 #pragma unroll
-      for (int k = 0; k < 2 * W; ++k) {
-        mk[k] = mk[k] == -INFINITY ? 0.f : fast_exp2(mk[k] - M);
-        sum += mk[k] * lk[k];
+        for (int i = 0; i < 4; ++i) {
+          mk[i] = -INFINITY;
+          lk[i] = 0.f;
+          at[i] = nullptr;
+          if (b) {
+            const int k = __ffs(b) - 1;
+            b &= b - 1;
+            at[i] = &stats[k >> 1][k & 1][0][lane];
+            mk[i] = *at[i];
+            lk[i] = stats[k >> 1][k & 1][1][lane];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float w = mk[i] == -INFINITY ? 0.f : fast_exp2(mk[i] - M);
+          if (at[i]) *at[i] = w;
+          sum += w * lk[i];
+        }
       }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-      for (int k = 0; k < 2 * W; ++k)
-        if (chain >> k & 1u) stats[k >> 1][k & 1][0][lane] = mk[k] * inv;
+      stats[(__ffs(chain) - 1) >> 1][(__ffs(chain) - 1) & 1][1][lane] = sum == 0.f ? 0.f : 1.f / sum;
       const float lse = sum == 0.f ? -INFINITY : M - kF8Shift + fast_log2(sum);
       if (cut) slot_of(a)[p.part_rows * D + lane] = lse;
       else p.lse_out[out_row_of(p, a.t0, a.kvh, a.row0 + lane)] = lse;
@@ -1018,6 +1040,8 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
           acc.w += w[i] * x[i].w;
         }
       }
+      const float inv = stats[(__ffs(chain) - 1) >> 1][(__ffs(chain) - 1) & 1][1][c];
+      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       if (cut) {
         *reinterpret_cast<float4*>(slot_of(a) + c * D + d) = acc;
       } else {
@@ -1192,8 +1216,9 @@ int64_t all_bytes(int32_t ctas, int32_t head_dim) {
 }
 
 // Heads that a team of warps takes side by side: the largest divisor of the KV heads up to 64.
-int32_t team_of(int32_t hkv) {
+int32_t team_of(int32_t hkv, int32_t workers) {
   int32_t n = hkv < 64 ? hkv : 64;
+  if (n > workers) n = workers;
   while (hkv % n) --n;
   return n;
 }
@@ -1297,7 +1322,6 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
   p.hq = num_qo_heads;
   p.hkv = num_kv_heads;
   p.group = group;
-  p.team = team_of(num_kv_heads);
   p.q_bf16 = q_dtype == PA_BF16;
   const FastDiv fd = FastDiv::make((uint32_t)page_size), fg = FastDiv::make((uint32_t)group);
   p.ps_magic = fd.magic;
@@ -1312,6 +1336,12 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
   const F8Pick pick = head_dim == 64 ? pick_f8<64>(rows, tma) : pick_f8<128>(rows, tma);
   if (!prepare_kernel(reinterpret_cast<const void*>(pick.fn), pick.smem)) return PA_ECUDA;
   p.workers = sms * (pick.threads / 32);
+  p.team = team_of(num_kv_heads, p.workers);
+  p.teams = p.workers / p.team;
+  p.groups = num_kv_heads / p.team;
+  const FastDiv ft = FastDiv::make((uint32_t)p.team);
+  p.team_magic = ft.magic;
+  p.team_shift = ft.shift;
   p.part_rows = pick.rows;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t rc = launch_dependent(pick.fn, dim3(sms), dim3(pick.threads), pick.smem, stream, p, tm_k, tm_v);
