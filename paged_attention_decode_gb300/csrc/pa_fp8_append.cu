@@ -24,6 +24,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -32,6 +33,7 @@
 #include "pa_internal.cuh"
 #include "pa_mma.cuh"
 #include "pa_rope.cuh"
+#include "pa_tc05.cuh"
 #include "pa_v2.h"
 
 namespace pa {
@@ -41,7 +43,7 @@ constexpr int kApThreads = 256;
 constexpr int kApWarps = kApThreads / 32;
 constexpr int kApMaxPage = 256;
 constexpr int kApStretch = 16;  // tokens of a CTA's stretch, at most
-constexpr int kApQTile = 8;     // tokens of a q CTA, at most
+constexpr int kApCtas = 3;      // per SM
 
 struct AppendParams {
   const void* q;
@@ -62,9 +64,9 @@ struct AppendParams {
   int64_t num_rows;  // pool rows
   float eps;
   int32_t tokens, hq, hkv, rot, page_size;
-  uint32_t ps_magic, ps_shift;
+  uint32_t ps_magic, ps_shift, half_magic, half_shift;
   int32_t stretch, kv_ctas, kv_splits;  // tokens per KV CTA, CTAs with runs, and CTAs that share a stretch's heads
-  int32_t q_tile;
+  int32_t q_warps, q_splits, q_share;  // warps with q rows, and warps that share a token's heads, so many each
 };
 
 __device__ __forceinline__ uint32_t codes_of(float a, float b) {  // a in the lower byte
@@ -112,119 +114,189 @@ struct Row {
     const uint2 a = __ldg(reinterpret_cast<const uint2*>(row + e0)), b = __ldg(reinterpret_cast<const uint2*>(row + e1));
     return make_uint4(a.x, a.y, b.x, b.y);
   }
-  // Norm (w non-null: weights as loaded) over the row's lanes, all of which call it.
-  __device__ __forceinline__ static void norm(float (&x)[N], const uint4& w, float eps) {
-    float ss = 0.f;
+  // Norm with weights g, over the row's lanes, all of which call it.
+  __device__ __forceinline__ static void norm(float (&x)[N], const float (&g)[N], float eps) {
+    float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
+    for (int i = 0; i < N; i += 2) s2 = fma2(make_float2(x[i], x[i + 1]), make_float2(x[i], x[i + 1]), s2);
+    float ss = s2.x + s2.y;
 #pragma unroll
     for (int s = kLanes / 2; s >= 1; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
     const float inv = rsqrtf(ss * (1.0f / D) + eps);
-    float g[N];
-    Vec<T>::unpack(w, g);
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = x[i] * inv * g[i];
+    for (int i = 0; i < N; i += 2) {
+      const float2 y = mul2(mul2(make_float2(x[i], x[i + 1]), make_float2(inv, inv)), make_float2(g[i], g[i + 1]));
+      x[i] = y.x;
+      x[i + 1] = y.y;
+    }
   }
   // cs: cosines, then sines `half` floats behind (elements that are not rotated are left out of it: 0 times an
   // infinity next to them is NaN)
   __device__ __forceinline__ void rotate(float (&x)[N], const float* cs, int half) const {
     if (!rotated) return;
+    float2 co[P / 2], si[P / 2];  // half is a multiple of 8, and a lane's pairs of 4 or 2
+    angles_at(cs, half, co, si);
+    turn(x, co, si);
+  }
+  __device__ __forceinline__ void angles_at(const float* cs, int half, float2 (&co)[P / 2], float2 (&si)[P / 2]) const {
+    if (P == 4) {
+      const float4 c = *reinterpret_cast<const float4*>(cs + pair0), s = *reinterpret_cast<const float4*>(cs + half + pair0);
+      co[0] = make_float2(c.x, c.y);
+      si[0] = make_float2(s.x, s.y);
+      co[P / 2 - 1] = make_float2(c.z, c.w);
+      si[P / 2 - 1] = make_float2(s.z, s.w);
+    } else {
+      co[0] = *reinterpret_cast<const float2*>(cs + pair0);
+      si[0] = *reinterpret_cast<const float2*>(cs + half + pair0);
+    }
+  }
+  __device__ __forceinline__ static void turn(float (&x)[N], const float2 (&co)[P / 2], const float2 (&si)[P / 2]) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int a = PAIRED ? i : 2 * i, b = PAIRED ? i + P : 2 * i + 1;
-      const float c = cs[pair0 + i], s = cs[half + pair0 + i];
-      const float u = x[a], w = x[b];
-      x[a] = fmaf(-w, s, u * c);
-      x[b] = fmaf(u, s, w * c);
+    for (int i = 0; i < P / 2; ++i) {  // two pairs: their first elements in u, their second ones in w
+      const int a = PAIRED ? 2 * i : 4 * i, b = PAIRED ? a + P : a + 1, next = PAIRED ? 1 : 2;
+      const float2 u = make_float2(x[a], x[a + next]), w = make_float2(x[b], x[b + next]);
+      const float2 nu = fma2(make_float2(-w.x, -w.y), si[i], mul2(u, co[i]));
+      const float2 nw = fma2(u, si[i], mul2(w, co[i]));
+      x[a] = nu.x;
+      x[a + next] = nu.y;
+      x[b] = nw.x;
+      x[b + next] = nw.y;
     }
   }
 };
 
+// The largest magnitude of a row's lane, infinities with it (NaN is left out); for V straight from the loaded bits.
+template <int N>
+__device__ __forceinline__ float largest(const float (&x)[N], float top) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(x[i]));
+  return top;
+}
+template <int N>
+__device__ __forceinline__ float largest_finite(const float (&x)[N], float top) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (fabsf(x[i]) <= 3.402823466e38f) top = fmaxf(top, fabsf(x[i]));
+  return top;
+}
+
 template <typename T, typename TQ, int D, bool PAIRED>
-__global__ void __launch_bounds__(kApThreads, 2) pa_v2_qk_rope_append_fp8_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kApThreads, kApCtas) pa_v2_qk_rope_append_fp8_kernel(const AppendParams p) {
   using R = Row<T, D, PAIRED>;
   constexpr int N = R::N, P = R::P, kLanes = R::kLanes, kAtOnce = R::kAtOnce;
-  constexpr int kHeld = 64 / N;  // passes of a run that registers hold
-  extern __shared__ float cs[];  // [tokens][2][rot / 2]: cosines, sines
+  constexpr int kHeld = 8;  // passes of a run that registers hold
+  extern __shared__ __align__(16) float cs[];  // [tokens][2][rot / 2]: cosines, sines
   __shared__ uint64_t turns[D / 2];
   __shared__ int32_t slot_of[1 + kApStretch + kApMaxPage];  // from the token before the stretch on
+  __shared__ int32_t pos_of[1 + kApStretch + kApMaxPage];
 
   pdl_launch_dependents();
   pdl_wait_prerequisites();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = p.rot / 2, sub = lane / kLanes;
   const R row(p.rot);
-  for (int i = threadIdx.x; i < half; i += kApThreads) turns[i] = turn_of(p.inv_freq[i]);
-  // cosines and sines of tokens [t0, t0 + n)
-  auto angles = [&](int t0, int n) {
-    for (int i = threadIdx.x; i < n * half; i += kApThreads) {
-      const int tok = i / half, j = i - tok * half;
-      const float2 r = rotation(p.positions[t0 + tok], turns[j]);
-      cs[2 * half * tok + j] = r.x;
-      cs[2 * half * tok + half + j] = r.y;
-    }
-  };
+  const bool is_q = (int)blockIdx.x >= p.kv_ctas;
+  const T* norm_weight = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
+  float weight[N];
+  if (norm_weight) Vec<T>::unpack(row.load(norm_weight), weight);
 
-  if ((int)blockIdx.x >= p.kv_ctas) {
-    // ------------------------------------------------------------------ q
-    const int t0 = ((int)blockIdx.x - p.kv_ctas) * p.q_tile, n = min(p.q_tile, p.tokens - t0);
-    const T* w = static_cast<const T*>(p.q_weight);
-    const uint4 weight = w ? row.load(w) : make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    angles(t0, n);
-    __syncthreads();
-    const int rows = n * p.hq;
-    constexpr int kBatch = 4;  // rows under way per lane
-    for (int base = warp * kAtOnce; base < rows; base += kBatch * kApWarps * kAtOnce) {
-      uint4 raw[kBatch];
-      int32_t tok[kBatch], head[kBatch];
-      bool live[kBatch];
+  if (is_q) {
+    // ------------------------------------------------------------------ q: a warp walks tokens, all their heads with one
+    // computation of a lane's cosines and sines, the next rows on their way
+    const int first = ((int)blockIdx.x - p.kv_ctas) * kApWarps + warp;
+    constexpr int kBatch = 4;  // passes of rows under way per lane, and as many ahead
+    const int h0 = first % p.q_splits * p.q_share, heads = min(p.q_share, p.hq - h0);
+    const int batches = (heads + kBatch * kAtOnce - 1) / (kBatch * kAtOnce);
+    uint64_t lane_turns[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) lane_turns[i] = row.rotated ? turn_of(p.inv_freq[row.pair0 + i]) : 0;
+    int tok = first / p.q_splits;
+    const int step = p.q_warps / p.q_splits;
+    if (tok >= step) return;  // (a last warp of no whole group)
+    auto fetch = [&](int t, int batch, uint4 (&raw)[kBatch]) {
+      const T* q = static_cast<const T*>(p.q) + (int64_t)t * p.q_stride + (h0 + batch * kBatch * kAtOnce + sub) * D;
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int i = min(base + b * kApWarps * kAtOnce + sub, rows - 1);
-        tok[b] = i / p.hq;
-        head[b] = i - tok[b] * p.hq;
-        const int32_t slot = __ldg(p.slots + t0 + tok[b]);
-        live[b] = base + b * kApWarps * kAtOnce + sub < rows && slot >= 0 && slot < p.num_rows;
-        raw[b] = row.load(static_cast<const T*>(p.q) + (int64_t)(t0 + tok[b]) * p.q_stride + head[b] * D);
+        raw[b] = make_uint4(0, 0, 0, 0);
+        if (batch * kBatch * kAtOnce + b * kAtOnce + sub < heads) raw[b] = row.load(q + b * kAtOnce * D);
       }
+    };
+    uint4 raw[kBatch], ahead[kBatch];
+    int32_t slot = -1, pos = 0;
+    if (tok < p.tokens) {
+      slot = __ldg(p.slots + tok);
+      pos = __ldg(p.positions + tok);
+      fetch(tok, 0, ahead);
+    }
+    while (tok < p.tokens) {
+      float2 co[P / 2], si[P / 2];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        float x[N];
-        Vec<T>::unpack(raw[b], x);
-        if (w) R::norm(x, weight, p.eps);
-        row.rotate(x, cs + 2 * half * tok[b], half);
-        if (!live[b]) continue;
-        TQ* to = static_cast<TQ*>(p.q_out) + ((int64_t)(t0 + tok[b]) * p.hq + head[b]) * D;
-        if (sizeof(TQ) != sizeof(T)) {  // f32 from 16 bits: a piece is 16 bytes
-          *reinterpret_cast<float4*>(to + row.e0) = make_float4(x[0], x[1], x[2], x[3]);
-          *reinterpret_cast<float4*>(to + row.e1) = make_float4(x[P], x[P + 1], x[N - 2], x[N - 1]);
-        } else {
-          const uint4 y = Vec<T>::pack(x);
-          *reinterpret_cast<uint2*>(to + row.e0) = make_uint2(y.x, y.y);
-          *reinterpret_cast<uint2*>(to + row.e1) = make_uint2(y.z, y.w);
+      for (int i = 0; i < P / 2; ++i) {
+        const float2 a = rotation(pos, lane_turns[2 * i]), b = rotation(pos, lane_turns[2 * i + 1]);
+        co[i] = make_float2(a.x, b.x);
+        si[i] = make_float2(a.y, b.y);
+      }
+      const bool live = slot >= 0 && slot < p.num_rows;
+      TQ* out = static_cast<TQ*>(p.q_out) + ((int64_t)tok * p.hq + h0 + sub) * D;
+      const int next = tok + step;
+      if (next < p.tokens) {
+        slot = __ldg(p.slots + next);
+        pos = __ldg(p.positions + next);
+      }
+      for (int batch = 0; batch < batches; ++batch) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) raw[b] = ahead[b];
+        if (batch + 1 < batches) fetch(tok, batch + 1, ahead);
+        else if (next < p.tokens) fetch(next, 0, ahead);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int h = (batch * kBatch + b) * kAtOnce;
+          if (h >= heads) break;
+          float x[N];
+          Vec<T>::unpack(raw[b], x);
+          if (norm_weight) R::norm(x, weight, p.eps);
+          if (row.rotated) R::turn(x, co, si);
+          if (!live || h + sub >= heads) continue;
+          TQ* to = out + h * D;
+          if (sizeof(TQ) != sizeof(T)) {  // f32 from 16 bits: a piece is 16 bytes
+            *reinterpret_cast<float4*>(to + row.e0) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(to + row.e1) = make_float4(x[P], x[P + 1], x[N - 2], x[N - 1]);
+          } else {
+            const uint4 y = Vec<T>::pack(x);
+            *reinterpret_cast<uint2*>(to + row.e0) = make_uint2(y.x, y.y);
+            *reinterpret_cast<uint2*>(to + row.e1) = make_uint2(y.z, y.w);
+          }
         }
       }
+      tok = next;
     }
     return;
   }
 
-  // -------------------------------------------------------------------- k and v
-  const int part = (int)blockIdx.x % p.kv_splits;
+  // -------------------------------------------------------------------- k and v: a warp takes a head of a side through the
+  // runs that begin in the CTA's stretch of tokens
+  const int task0 = (int)blockIdx.x % p.kv_splits * kApWarps, task = task0 + warp;
+  const bool is_v = task >= p.hkv, has_k = task0 < p.hkv && half > 0;  // has_k: of the CTA, whose warps then share angles
+  const int head = is_v ? task - p.hkv : task;
   const int w0 = (int)blockIdx.x / p.kv_splits * p.stretch, w1 = min(w0 + p.stretch, p.tokens);
   const int ahead = min(p.stretch + p.page_size, p.tokens - w0);
   for (int i = threadIdx.x; i < ahead + 1; i += kApThreads) {
     int32_t s = -1;
     if (w0 + i > 0) s = __ldg(p.slots + w0 - 1 + i);
+    if (has_k && i > 0) pos_of[i] = __ldg(p.positions + w0 - 1 + i);
     if (s >= p.num_rows) {
-      if (i > 0 && i <= w1 - w0 && part == 0) report(p.status, PA_DEVICE_BAD_SLOT);
+      if (i > 0 && i <= w1 - w0 && task0 == 0) report(p.status, PA_DEVICE_BAD_SLOT);
       s = -1;
     }
     slot_of[i] = s;
   }
-  const T* kw = static_cast<const T*>(p.k_weight);
-  const uint4 weight = kw ? row.load(kw) : make_uint4(0, 0, 0, 0);
+  if (has_k)
+    for (int i = threadIdx.x; i < half; i += kApThreads) turns[i] = turn_of(p.inv_freq[i]);
   __syncthreads();
+  const int64_t stride = is_v ? p.v_stride : p.k_stride, pitch = (int64_t)p.hkv * D;
+  const T* in = static_cast<const T*>(is_v ? p.v : p.k) + head * D;
+  uint8_t* pool = (is_v ? p.v_pool : p.k_pool) + head * D;
+  int8_t* exps = (is_v ? p.v_exp : p.k_exp) + head;
   auto page_of = [&](int i) -> int32_t {  // of slot_of[i], -1 for none
     const int32_t s = slot_of[i];
     return s < 0 ? -1 : (int32_t)fast_div((uint32_t)s, p.ps_magic, p.ps_shift);
@@ -234,98 +306,118 @@ __global__ void __launch_bounds__(kApThreads, 2) pa_v2_qk_rope_append_fp8_kernel
     const int32_t page = page_of(at);
     if (page < 0 || page_of(at - 1) == page) continue;
     // the run: how many tokens, and the least entry
-    int len = 1;
-    while (len < p.page_size && at + len <= ahead && page_of(at + len) == page) ++len;
-    int least = INT_MAX;
-    for (int i = lane; i < len; i += 32) least = min(least, slot_of[at + i] - page * p.page_size);
+    int len = 1, least = INT_MAX;
+    for (int i = 0;; i += 32) {
+      const bool in_run = i + lane < p.page_size && at + i + lane <= ahead && page_of(at + i + lane) == page;
+      const uint32_t run = __ballot_sync(0xffffffffu, in_run);
+      len = i + (run == 0xffffffffu ? 32 : __ffs(~run) - 1);
+      if (i + lane < len) least = min(least, slot_of[at + i + lane] - page * p.page_size);
+      if (run != 0xffffffffu) break;
+    }
     least = __reduce_min_sync(0xffffffffu, least);
-    __syncthreads();  // the run before is done with its angles
-    angles(t, len);
-    __syncthreads();
-    for (int task = part * kApWarps + warp; task < 2 * p.hkv; task += p.kv_splits * kApWarps) {
-      const bool is_v = task >= p.hkv;
-      const int head = is_v ? task - p.hkv : task;
-      const T* src = static_cast<const T*>(is_v ? p.v : p.k) + (int64_t)t * (is_v ? p.v_stride : p.k_stride) + head * D;
-      const int64_t stride = is_v ? p.v_stride : p.k_stride;
-      int8_t* exps = (is_v ? p.v_exp : p.k_exp) + (int64_t)page * p.hkv + head;
-      uint8_t* pool = (is_v ? p.v_pool : p.k_pool) + head * D;
-      const int64_t pitch = (int64_t)p.hkv * D;
-      const int old = least > 0 ? min(max((int)*exps, PA_V2_FP8_EXP_MIN), PA_V2_FP8_EXP_MAX) : 0;
-      float x[kHeld][N];
-      auto fetch = [&](int first) {  // tokens first .. of the run, normed and rotated
-        uint4 raw[kHeld];
+    const bool busy = task < 2 * p.hkv;
+    const T* src = in + (int64_t)t * stride;
+    uint4 raw[kHeld];
+    auto fetch = [&](int first) {  // rows first .. of the run
 #pragma unroll
-        for (int b = 0; b < kHeld; ++b) {
-          raw[b] = make_uint4(0, 0, 0, 0);
-          if (first + b * kAtOnce < len) raw[b] = row.load(src + (int64_t)min(first + b * kAtOnce + sub, len - 1) * stride);
-        }
+      for (int b = 0; b < kHeld; ++b)
+        if (first + b * kAtOnce < len) raw[b] = row.load(src + min(first + b * kAtOnce + sub, len - 1) * stride);
+    };
+    if (busy) fetch(0);
+    if (has_k) {
+      __syncthreads();  // the run before is done with its angles
+      for (int i = threadIdx.x; i < len * half; i += kApThreads) {
+        const int tok = (int)fast_div((uint32_t)i, p.half_magic, p.half_shift), j = i - tok * half;
+        const float2 r = rotation(pos_of[at + tok], turns[j]);
+        cs[2 * half * tok + j] = r.x;
+        cs[2 * half * tok + half + j] = r.y;
+      }
+      __syncthreads();
+    }
+    if (!busy) continue;
+    int8_t* exp = exps + (int64_t)page * p.hkv;
+    const int before = least > 0 ? min(max((int)*exp, PA_V2_FP8_EXP_MIN), PA_V2_FP8_EXP_MAX) : 0;
+    // Row b of those fetched, normed and rotated: computed twice, for the maximum and for the codes, where holding it
+    // would take twice the registers (and leave two CTAs an SM instead of three).
+    auto make = [&](int first, int b, float (&x)[N]) {
+      Vec<T>::unpack(raw[b], x);
+      if (!is_v) {
+        if (norm_weight) R::norm(x, weight, p.eps);
+        row.rotate(x, cs + 2 * half * min(first + b * kAtOnce + sub, len - 1), half);
+      }
+    };
+    const bool again = len > kHeld * kAtOnce;
+    float top = 0.f;
+    for (int first = 0; first < len; first += kHeld * kAtOnce) {
+      if (first > 0) fetch(first);
 #pragma unroll
-        for (int b = 0; b < kHeld; ++b) {
-          if (first + b * kAtOnce >= len) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[b][i] = 0.f;
-            continue;
-          }
-          Vec<T>::unpack(raw[b], x[b]);
-          if (!is_v) {
-            if (kw) R::norm(x[b], weight, p.eps);
-            row.rotate(x[b], cs + 2 * half * min(first + b * kAtOnce + sub, len - 1), half);
-          }
-        }
-      };
-      float top = 0.f;
-      for (int first = 0; first < len; first += kHeld * kAtOnce) {
-        fetch(first);
-#pragma unroll
-        for (int b = 0; b < kHeld; ++b)
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float a = fabsf(x[b][i]);
-            if (a <= 3.402823466e38f) top = fmaxf(top, a);
-          }
+      for (int b = 0; b < kHeld; ++b) {
+        if (first + b * kAtOnce >= len) break;
+        float x[N];
+        make(first, b, x);
+        top = largest(x, top);
+      }
+    }
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    const bool infinite = top > 3.402823466e38f;
+    if (infinite) {  // infinities become NaN and do not count
+      top = 0.f;
+#pragma unroll 1
+      for (int first = 0; first < len; first += kAtOnce) {
+        raw[0] = row.load(src + min(first + sub, len - 1) * stride);
+        float x[N];
+        make(first, 0, x);
+        top = largest_finite(x, top);
       }
       top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-      int e = top > 0.f ? exponent_for(top) : PA_V2_FP8_EXP_MIN;
-      if (least > 0) {
-        e = max(e, old);
-        if (e > old) {  // the page's earlier tokens
-          const __half2 f = __float2half2_rn(power2(old - e));
-          constexpr int kChunks = D / 16;
-          for (int i = lane; i < least * kChunks; i += 32) {
-            uint4* at16 = reinterpret_cast<uint4*>(pool + ((int64_t)page * p.page_size + i / kChunks) * pitch) + i % kChunks;
-            uint4 u = *at16;
-            uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+    }
+    int e = top > 0.f ? exponent_for(top) : PA_V2_FP8_EXP_MIN;
+    if (least > 0) {
+      e = max(e, before);
+      if (e > before) {  // the page's earlier tokens
+        const __half2 f = __float2half2_rn(power2(before - e));
+        constexpr int kChunks = D / 16;
+        for (int i = lane; i < least * kChunks; i += 32) {
+          uint4* at16 = reinterpret_cast<uint4*>(pool + ((int64_t)page * p.page_size + i / kChunks) * pitch) + i % kChunks;
+          uint4 u = *at16;
+          uint32_t* w = reinterpret_cast<uint32_t*>(&u);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = rescaled((uint16_t)w[k], f) | rescaled((uint16_t)(w[k] >> 16), f) << 16;
-            *at16 = u;
-          }
+          for (int j = 0; j < 4; ++j)
+            w[j] = rescaled((uint16_t)w[j], f) | rescaled((uint16_t)(w[j] >> 16), f) << 16;
+          *at16 = u;
         }
       }
-      if (lane == 0) *exps = (int8_t)e;
-      const float down = power2(-e);
-      for (int first = 0; first < len; first += kHeld * kAtOnce) {
-        if (len > kHeld * kAtOnce) fetch(first);
+    }
+    if (lane == 0) *exp = (int8_t)e;
+    const float down = power2(-e);
+    for (int first = 0; first < len; first += kHeld * kAtOnce) {
+      if (again || infinite) fetch(first);
 #pragma unroll
-        for (int b = 0; b < kHeld; ++b) {
-          const int i = first + b * kAtOnce + sub;
-          if (i >= len) continue;
-          uint8_t* to = pool + (int64_t)slot_of[at + i] * pitch;
-          uint32_t y[N / 4];
+      for (int b = 0; b < kHeld; ++b) {
+        const int i = first + b * kAtOnce + sub;
+        if (i - sub >= len) break;
+        float x[N];
+        make(first, b, x);
+        if (infinite) {
 #pragma unroll
-          for (int k = 0; k < N; k += 4) {
-            float z[4];
+          for (int j = 0; j < N; ++j)
+            if (!(fabsf(x[j]) <= 3.402823466e38f)) x[j] = NAN;
+        }
+        uint32_t y[N / 4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) z[j] = fabsf(x[b][k + j]) <= 3.402823466e38f ? x[b][k + j] * down : NAN;
-            y[k / 4] = codes_of(z[0], z[1]) | codes_of(z[2], z[3]) << 16;
-          }
-          if (N == 8) {
-            *reinterpret_cast<uint32_t*>(to + row.e0) = y[0];
-            *reinterpret_cast<uint32_t*>(to + row.e1) = y[N / 4 - 1];
-          } else {  // f32: two elements per piece
-            *reinterpret_cast<uint16_t*>(to + row.e0) = (uint16_t)y[0];
-            *reinterpret_cast<uint16_t*>(to + row.e1) = (uint16_t)(y[0] >> 16);
-          }
+        for (int j = 0; j < N; j += 4) {
+          const float2 z0 = mul2(make_float2(x[j], x[j + 1]), make_float2(down, down));
+          const float2 z1 = mul2(make_float2(x[j + 2], x[j + 3]), make_float2(down, down));
+          y[j / 4] = codes_of(z0.x, z0.y) | codes_of(z1.x, z1.y) << 16;
+        }
+        if (i >= len) continue;
+        uint8_t* to = pool + (int64_t)slot_of[at + i] * pitch;
+        if (N == 8) {
+          *reinterpret_cast<uint32_t*>(to + row.e0) = y[0];
+          *reinterpret_cast<uint32_t*>(to + row.e1) = y[N / 4 - 1];
+        } else {  // f32: two elements per piece
+          *reinterpret_cast<uint16_t*>(to + row.e0) = (uint16_t)y[0];
+          *reinterpret_cast<uint16_t*>(to + row.e1) = (uint16_t)(y[0] >> 16);
         }
       }
     }
@@ -406,6 +498,9 @@ extern "C" pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, c
   const FastDiv fd = FastDiv::make((uint32_t)page_size);
   p.ps_magic = fd.magic;
   p.ps_shift = fd.shift;
+  const FastDiv fr = FastDiv::make((uint32_t)(rot_dim > 0 ? rot_dim / 2 : 1));
+  p.half_magic = fr.magic;
+  p.half_shift = fr.shift;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
@@ -414,14 +509,20 @@ extern "C" pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, c
   }
   // Stretches and q tiles: short enough that the CTAs fill the GPU, and, while the stretches alone do not, the heads of
   // one are shared out.
-  const int per = num_tokens / (2 * sms);
+  // Stretches short enough that the CTAs fill the GPU, and, while the stretches alone do not, the heads of one shared out.
+  // For q as many warps as are resident, or, while the tokens alone do not give them work, several to a token.
+  const int per = num_tokens / (kApCtas * sms);
   p.stretch = per < 1 ? 1 : per < kApStretch ? per : kApStretch;
-  p.q_tile = per < 1 ? 1 : per < kApQTile ? per : kApQTile;
   const int stretches = (num_tokens + p.stretch - 1) / p.stretch;
-  p.kv_splits = stretches < sms ? (2 * num_kv_heads + kApWarps - 1) / kApWarps : 1;
-  if ((int64_t)stretches * p.kv_splits > INT32_MAX / 2) p.kv_splits = 1;
+  p.kv_splits = (2 * num_kv_heads + kApWarps - 1) / kApWarps;
+  if ((int64_t)stretches * p.kv_splits > INT32_MAX / 2) return PA_EUNSUPPORTED;
   p.kv_ctas = stretches * p.kv_splits;
-  const int q_ctas = (num_tokens + p.q_tile - 1) / p.q_tile;
+  const int resident = kApCtas * sms * kApWarps, share = 4;  // heads that are worth a warp
+  p.q_splits = num_tokens < resident ? std::min(resident / num_tokens, (num_qo_heads + share - 1) / share) : 1;
+  p.q_share = (num_qo_heads + p.q_splits - 1) / p.q_splits;
+  p.q_splits = (num_qo_heads + p.q_share - 1) / p.q_share;
+  const int q_ctas = (int)std::min<int64_t>(kApCtas * sms, ((int64_t)num_tokens * p.q_splits + kApWarps - 1) / kApWarps);
+  p.q_warps = q_ctas * kApWarps;
   const bool paired = !interleaved, q32 = q_dtype == PA_F32;
   const AppendKernel fn =
       dtype == PA_F32   ? pick_append<float, float>(head_dim, paired)
@@ -430,7 +531,7 @@ extern "C" pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, c
                                : pick_append<__nv_bfloat16, __nv_bfloat16>(head_dim, paired));
   const size_t most = (size_t)kApMaxPage * 2 * (head_dim / 2) * sizeof(float);
   if (!prepare_kernel(reinterpret_cast<const void*>(fn), most)) return PA_ECUDA;
-  const size_t smem = (size_t)(page_size > kApQTile ? page_size : kApQTile) * rot_dim * sizeof(float);
+  const size_t smem = (size_t)page_size * rot_dim * sizeof(float);
   const cudaError_t rc = launch_dependent(fn, dim3((unsigned)(p.kv_ctas + q_ctas)), dim3(kApThreads), smem,
                                           static_cast<cudaStream_t>(cuda_stream), p);
   if (rc != cudaSuccess) {
