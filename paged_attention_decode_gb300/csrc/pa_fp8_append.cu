@@ -28,6 +28,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_internal.cuh"
@@ -248,15 +249,17 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) pa_v2_qk_rope_append_fp8_
         for (int b = 0; b < kBatch; ++b) raw[b] = ahead[b];
         if (batch + 1 < batches) fetch(tok, batch + 1, ahead);
         else if (next < p.tokens) fetch(next, 0, ahead);
+        // (a whole batch without a test between its passes: they run side by side)
+        auto passes = [&](auto whole) {
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
           const int h = (batch * kBatch + b) * kAtOnce;
-          if (h >= heads) break;
+          if (!decltype(whole)::value && h >= heads) break;
           float x[N];
           Vec<T>::unpack(raw[b], x);
           if (norm_weight) R::norm(x, weight, p.eps);
           if (row.rotated) R::turn(x, co, si);
-          if (!live || h + sub >= heads) continue;
+          if (!live || (!decltype(whole)::value && h + sub >= heads)) continue;
           TQ* to = out + h * D;
           if (sizeof(TQ) != sizeof(T)) {  // f32 from 16 bits: a piece is 16 bytes
             *reinterpret_cast<float4*>(to + row.e0) = make_float4(x[0], x[1], x[2], x[3]);
@@ -267,6 +270,9 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) pa_v2_qk_rope_append_fp8_
             *reinterpret_cast<uint2*>(to + row.e1) = make_uint2(y.z, y.w);
           }
         }
+        };
+        if ((batch + 1) * kBatch * kAtOnce <= heads) passes(std::true_type());
+        else passes(std::false_type());
       }
       tok = next;
     }
@@ -350,13 +356,17 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) pa_v2_qk_rope_append_fp8_
     float top = 0.f;
     for (int first = 0; first < len; first += kHeld * kAtOnce) {
       if (first > 0) fetch(first);
+      auto passes = [&](auto whole) {
 #pragma unroll
-      for (int b = 0; b < kHeld; ++b) {
-        if (first + b * kAtOnce >= len) break;
-        float x[N];
-        make(first, b, x);
-        top = largest(x, top);
-      }
+        for (int b = 0; b < kHeld; ++b) {
+          if (!decltype(whole)::value && first + b * kAtOnce >= len) break;
+          float x[N];
+          make(first, b, x);
+          top = largest(x, top);
+        }
+      };
+      if (first + kHeld * kAtOnce <= len) passes(std::true_type());
+      else passes(std::false_type());
     }
     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
     const bool infinite = top > 3.402823466e38f;
@@ -392,10 +402,11 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) pa_v2_qk_rope_append_fp8_
     const float down = power2(-e);
     for (int first = 0; first < len; first += kHeld * kAtOnce) {
       if (again || infinite) fetch(first);
+      auto passes = [&](auto whole) {
 #pragma unroll
       for (int b = 0; b < kHeld; ++b) {
         const int i = first + b * kAtOnce + sub;
-        if (i - sub >= len) break;
+        if (!decltype(whole)::value && i - sub >= len) break;
         float x[N];
         make(first, b, x);
         if (infinite) {
@@ -410,7 +421,7 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) pa_v2_qk_rope_append_fp8_
           const float2 z1 = mul2(make_float2(x[j + 2], x[j + 3]), make_float2(down, down));
           y[j / 4] = codes_of(z0.x, z0.y) | codes_of(z1.x, z1.y) << 16;
         }
-        if (i >= len) continue;
+        if (!decltype(whole)::value && i >= len) continue;
         uint8_t* to = pool + (int64_t)slot_of[at + i] * pitch;
         if (N == 8) {
           *reinterpret_cast<uint32_t*>(to + row.e0) = y[0];
@@ -420,6 +431,9 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) pa_v2_qk_rope_append_fp8_
           *reinterpret_cast<uint16_t*>(to + row.e1) = (uint16_t)(y[0] >> 16);
         }
       }
+      };
+      if (first + kHeld * kAtOnce <= len) passes(std::true_type());
+      else passes(std::false_type());
     }
   }
 }
