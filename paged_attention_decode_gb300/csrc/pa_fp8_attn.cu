@@ -36,8 +36,10 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "pa_internal.cuh"
+#include "pa_launch.h"
 #include "pa_mma.cuh"
 #include "pa_pool_map.h"
 #include "pa_tc05.cuh"
@@ -1185,6 +1187,162 @@ __global__ void __launch_bounds__(32 * kMergeWarps, kMergeCtas) pa_v2_fp8_merge_
   }
 }
 
+// ---- many query rows per request
+//
+// A prompt's chunk meets each key with hundreds of query rows, in blocks of kRows: the tensor cores bound it, and the warp's
+// ones at that.  So the pages that some token sees are written out once in q's 16-bit type (exactly: an element is a
+// binary16 number of 4 significant bits, and a bfloat16 one) and the tree attention runs over them, tcgen05 products and
+// all.  4 x 256 tokens over 8K: 815 us in blocks of 32 rows.
+struct F8Wide {
+  int32_t* qo_wide;     // qo_indptr for the tree attention, all zero when the pages do not fit
+  int32_t* qo_narrow;   // and for the blocks of few rows, all zero when they do
+  int32_t* indptr;      // the page tables of the requests one behind the other, a refused one's empty
+  int32_t* table;       // pages of k and v
+  void* k;
+  void* v;
+  int64_t max_slots, max_pages;
+  uint32_t hkv_magic, hkv_shift;
+};
+constexpr int kWideThreads = 256;
+constexpr int64_t kWideElements = 1ll << 26;  // of k, and of v
+constexpr int64_t kWideSlots = 1ll << 20;
+constexpr int64_t kWideRows = 64;             // query rows of a KV head from which on
+
+// Pages [0, a) and [b, pages) of the request are seen by some token.
+struct F8Pages {
+  int32_t pages, a, b;
+  __device__ __forceinline__ int32_t seen() const { return a + pages - max(a, b); }
+};
+__device__ __forceinline__ F8Pages f8_pages(const F8Params& p, const F8Req& g, int r) {
+  if (g.kind != kF8Keys) return {0, 0, 0};
+  return {p.indptr[r + 1] - p.indptr[r], g.sink_end > g.lo ? (g.sink_end + p.page_size - 1) / p.page_size : 0,
+          g.win0 / p.page_size};
+}
+
+// 16 codes times 2^e as T.
+template <typename T>
+__device__ __forceinline__ void widen(const uint4& c, int e, uint4 (&out)[2]) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t y[8];
+  const float f = power_of_two(min(max(e, PA_V2_FP8_EXP_MIN), PA_V2_FP8_EXP_MAX));
+  const __half2 h = __float2half2_rn(f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[2 * i] = mul_f16(codes_lo(w[i]), *reinterpret_cast<const uint32_t*>(&h));
+    y[2 * i + 1] = mul_f16(codes_hi(w[i]), *reinterpret_cast<const uint32_t*>(&h));
+  }
+  if (std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
+      y[i] = TC<__nv_bfloat16>::pack(x.x, x.y);
+    }
+  }
+  out[0] = make_uint4(y[0], y[1], y[2], y[3]);
+  out[1] = make_uint4(y[4], y[5], y[6], y[7]);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWideThreads) pa_v2_fp8_expand_kernel(const F8Params p, const F8Wide w) {
+  constexpr int W = kWideThreads / 32;
+  __shared__ int64_t warp_sum[2][W], ends[2][kWideThreads];  // slots, seen pages
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  pdl_wait_prerequisites();
+  const int per_thread = (p.batch + kWideThreads - 1) / kWideThreads;
+  const int r0 = (int)min((int64_t)threadIdx.x * per_thread, (int64_t)p.batch), r1 = min(r0 + per_thread, p.batch);
+  int64_t mine[2] = {0, 0}, total[2] = {0, 0}, upto[2];
+  for (int r = r0; r < r1; ++r) {
+    const F8Pages n = f8_pages(p, f8_req<kF8MaxRows>(p, r, blockIdx.x == 0), r);
+    mine[0] += n.pages;
+    mine[1] += n.seen();
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    upto[k] = mine[k];
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto[k], i);
+      if (lane >= i) upto[k] += x;
+    }
+    if (lane == 31) warp_sum[k][warp] = upto[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    for (int i = 0; i < W; ++i) {
+      if (i < warp) upto[k] += warp_sum[k][i];
+      total[k] += warp_sum[k][i];
+    }
+    ends[k][threadIdx.x] = upto[k];
+  }
+  __syncthreads();
+  const bool fits = total[0] <= w.max_slots && total[1] <= w.max_pages;
+  if (blockIdx.x == 0) {
+    int64_t at = upto[0] - mine[0];
+    for (int r = r0; r < r1; ++r) {
+      const int32_t qo = p.qo_indptr[r];
+      w.qo_wide[r] = fits ? qo : 0;
+      w.qo_narrow[r] = fits ? 0 : qo;
+      w.indptr[r] = fits ? (int32_t)at : 0;
+      at += f8_pages(p, f8_req<kF8MaxRows>(p, r, false), r).pages;
+    }
+    if (threadIdx.x == 0) {
+      const int32_t qo = p.qo_indptr[p.batch];
+      w.qo_wide[p.batch] = fits ? qo : 0;
+      w.qo_narrow[p.batch] = fits ? 0 : qo;
+      w.indptr[p.batch] = fits ? (int32_t)total[0] : 0;
+    }
+  }
+  if (!fits) return;
+  // a run of slots for every warp
+  const int64_t workers = (int64_t)gridDim.x * W, run = div_units(total[0] + workers - 1, workers);
+  int64_t u = ((int64_t)blockIdx.x * W + warp) * run;
+  const int64_t behind = min(u + run, total[0]);
+  if (u >= behind) return;
+  int first = 0;  // the thread of the request that holds slot u
+  while (!__any_sync(0xffffffffu, ends[0][first + lane] > u)) first += 32;
+  first += __ffs(__ballot_sync(0xffffffffu, ends[0][first + lane] > u)) - 1;
+  int r = first * per_thread;
+  int64_t slot0 = first > 0 ? ends[0][first - 1] : 0, page0 = first > 0 ? ends[1][first - 1] : 0;
+  F8Pages n = f8_pages(p, f8_req<kF8MaxRows>(p, r, false), r);
+  const int64_t page_elements = (int64_t)p.page_size * p.hkv * D;
+  const int chunks = (int)(page_elements / 16);
+  for (; u < behind; ++u) {
+    while (u - slot0 >= n.pages) {
+      slot0 += n.pages;
+      page0 += n.seen();
+      ++r;
+      n = f8_pages(p, f8_req<kF8MaxRows>(p, r, false), r);
+    }
+    const int32_t s = (int32_t)(u - slot0);
+    const int32_t page = __ldg(p.indices + p.indptr[r] + s);
+    const bool copied = (s < n.a || s >= n.b) && page >= 0 && page < p.num_pages;  // (the attention reports bad pages)
+    const int64_t id = page0 + (s < n.a ? s : s - max(n.a, n.b) + n.a);
+    if (lane == 0) w.table[u] = copied ? (int32_t)id : -1;
+    if (!copied) continue;
+    const uint4* k = reinterpret_cast<const uint4*>(p.k_pool + page * page_elements);
+    const uint4* v = reinterpret_cast<const uint4*>(p.v_pool + page * page_elements);
+    uint4* ko = reinterpret_cast<uint4*>(static_cast<T*>(w.k) + id * page_elements);
+    uint4* vo = reinterpret_cast<uint4*>(static_cast<T*>(w.v) + id * page_elements);
+    const int8_t* ke = p.k_exp + (int64_t)page * p.hkv;
+    const int8_t* ve = p.v_exp + (int64_t)page * p.hkv;
+#pragma unroll 2
+    for (int c = lane; c < chunks; c += 32) {
+      const uint32_t row = (uint32_t)c / (D / 16);  // of the page's rows and heads
+      const uint32_t head = row - fast_div(row, w.hkv_magic, w.hkv_shift) * p.hkv;
+      const uint4 x = __ldg(k + c), y = __ldg(v + c);
+      uint4 a[2], b[2];
+      widen<T>(x, __ldg(ke + head), a);
+      widen<T>(y, __ldg(ve + head), b);
+      ko[2 * c] = a[0];
+      ko[2 * c + 1] = a[1];
+      vo[2 * c] = b[0];
+      vo[2 * c + 1] = b[1];
+    }
+  }
+}
+
 using F8Kernel = void (*)(const F8Params, const CUtensorMap, const CUtensorMap);
 
 struct F8Pick {
@@ -1215,6 +1373,35 @@ int64_t all_bytes(int32_t ctas, int32_t head_dim) {
   return parts_bytes(ctas, head_dim) + (int64_t)ctas * kF8MaxWarps * (sizeof(F8Header) + sizeof(int32_t)) + 16;
 }
 
+// For many query rows per request: the tables, and k and v.
+struct WideLayout {
+  int64_t qo_wide, qo_narrow, indptr, table, k, v, tree, bytes;  // byte offsets behind the workspace of few rows
+};
+WideLayout wide_layout(int32_t batch, int64_t tree_bytes) {
+  WideLayout l;
+  int64_t at = 0;
+  auto part = [&](int64_t bytes) {
+    const int64_t from = at;
+    at += (bytes + 255) / 256 * 256;
+    return from;
+  };
+  const int64_t ints = ((int64_t)batch + 1) * 4;
+  l.qo_wide = part(ints);
+  l.qo_narrow = part(ints);
+  l.indptr = part(ints);
+  l.table = part(kWideSlots * 4);
+  l.k = part(kWideElements * 2);
+  l.v = part(kWideElements * 2);
+  l.tree = part(tree_bytes);
+  l.bytes = at;
+  return l;
+}
+int64_t few_rows_bytes(int32_t ctas, int32_t head_dim) { return (all_bytes(ctas, head_dim) + 255) / 256 * 256; }
+// Query rows of a KV head and request, were the tokens spread evenly (the lengths are on the device).
+int64_t rows_of(int32_t num_tokens, int32_t batch, int32_t group) {
+  return batch > 0 ? ((int64_t)num_tokens + batch - 1) / batch * group : 0;
+}
+
 // Heads that a team of warps takes side by side: the largest divisor of the KV heads up to 64.
 int32_t team_of(int32_t hkv, int32_t workers) {
   int32_t n = hkv < 64 ? hkv : 64;
@@ -1238,7 +1425,14 @@ extern "C" pa_status pa_v2_attention_fp8_workspace(int32_t device, int32_t num_t
     cudaGetLastError();
     return PA_ECUDA;
   }
-  *bytes = pa::all_bytes(sms, head_dim);
+  *bytes = pa::few_rows_bytes(sms, head_dim);
+  if (pa::rows_of(num_tokens, batch, num_qo_heads / num_kv_heads) > pa::kWideRows) {
+    int64_t tree = 0;
+    const pa_status rc =
+        pa_v2_tree_attention_workspace(device, num_tokens, batch, num_qo_heads, num_kv_heads, head_dim, &tree);
+    if (rc != PA_OK) return rc;
+    *bytes += pa::wide_layout(batch, tree).bytes;
+  }
   return PA_OK;
 }
 
@@ -1279,7 +1473,11 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
     cudaGetLastError();
     return PA_ECUDA;
   }
-  if (workspace_bytes < all_bytes(sms, head_dim)) return PA_ECAPACITY;
+  const int64_t rows = rows_of(num_tokens, batch, group);
+  int64_t need = 0, tree_bytes = 0;
+  pa_status ws = pa_v2_attention_fp8_workspace(dev, num_tokens, batch, num_qo_heads, num_kv_heads, head_dim, &need);
+  if (ws != PA_OK) return ws;
+  if (workspace_bytes < need) return PA_ECAPACITY;
   alignas(64) CUtensorMap tm_k, tm_v;
   std::memset(&tm_k, 0, sizeof(tm_k));
   std::memset(&tm_v, 0, sizeof(tm_v));
@@ -1331,10 +1529,44 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
   p.scale_log2 = scale_log2;
   p.window = window;
   p.sinks = sinks;
-  // Rows of a block: a request's query rows per KV head, were the tokens spread evenly (the lengths are on the device).
-  const int64_t rows = ((int64_t)num_tokens + batch - 1) / batch * group;
   const F8Pick pick = head_dim == 64 ? pick_f8<64>(rows, tma) : pick_f8<128>(rows, tma);
   if (!prepare_kernel(reinterpret_cast<const void*>(pick.fn), pick.smem)) return PA_ECUDA;
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  cudaError_t rc = cudaSuccess;
+  const int64_t page_elements = (int64_t)page_size * num_kv_heads * head_dim;
+  // many rows: (a window's depths come from the positions there, for chains too)
+  if (rows > kWideRows && (window == 0 || positions) && page_elements <= kWideElements) {
+    ws = pa_v2_tree_attention_workspace(dev, num_tokens, batch, num_qo_heads, num_kv_heads, head_dim, &tree_bytes);
+    if (ws != PA_OK) return ws;
+    const WideLayout l = wide_layout(batch, tree_bytes);
+    char* base = static_cast<char*>(workspace) + few_rows_bytes(sms, head_dim);
+    F8Wide w;
+    w.qo_wide = reinterpret_cast<int32_t*>(base + l.qo_wide);
+    w.qo_narrow = reinterpret_cast<int32_t*>(base + l.qo_narrow);
+    w.indptr = reinterpret_cast<int32_t*>(base + l.indptr);
+    w.table = reinterpret_cast<int32_t*>(base + l.table);
+    w.k = base + l.k;
+    w.v = base + l.v;
+    w.max_slots = kWideSlots;
+    w.max_pages = kWideElements / page_elements;
+    const FastDiv fk = FastDiv::make((uint32_t)num_kv_heads);
+    w.hkv_magic = fk.magic;
+    w.hkv_shift = fk.shift;
+    auto expand = p.q_bf16 ? (head_dim == 64 ? pa_v2_fp8_expand_kernel<__nv_bfloat16, 64> : pa_v2_fp8_expand_kernel<__nv_bfloat16, 128>)
+                           : (head_dim == 64 ? pa_v2_fp8_expand_kernel<__half, 64> : pa_v2_fp8_expand_kernel<__half, 128>);
+    rc = launch_dependent(expand, dim3(sms * 6), dim3(kWideThreads), 0, stream, p, w);
+    if (rc != cudaSuccess) {
+      cudaGetLastError();
+      return PA_ECUDA;
+    }
+    ws = tree_attention(q, w.k, w.v, q_dtype, w.max_pages, page_size, num_qo_heads, num_kv_heads, head_dim, w.table,
+                        kWideSlots, w.indptr, last_page_len, first_page_offset, batch, w.qo_wide, num_tokens, tree_mask,
+                        mask_words, positions, window, sinks, sm_scale, out, lse2_out, base + l.tree, tree_bytes, status,
+                        cuda_stream);
+    // the pages fit for sure: nothing is left for the blocks of few rows
+    if (ws != PA_OK || (num_indices <= kWideSlots && num_indices <= w.max_pages)) return ws;
+    p.qo_indptr = w.qo_narrow;
+  }
   p.workers = sms * (pick.threads / 32);
   p.team = team_of(num_kv_heads, p.workers);
   p.teams = p.workers / p.team;
@@ -1343,8 +1575,7 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
   p.team_magic = ft.magic;
   p.team_shift = ft.shift;
   p.part_rows = pick.rows;
-  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-  cudaError_t rc = launch_dependent(pick.fn, dim3(sms), dim3(pick.threads), pick.smem, stream, p, tm_k, tm_v);
+  rc = launch_dependent(pick.fn, dim3(sms), dim3(pick.threads), pick.smem, stream, p, tm_k, tm_v);
   if (rc == cudaSuccess)
     rc = launch_dependent(head_dim == 64 ? pa_v2_fp8_merge_kernel<64> : pa_v2_fp8_merge_kernel<128>,
                           dim3(sms * kMergeCtas), dim3(32 * kMergeWarps), p.workers, stream, p);

@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "pa_launch.h"
 #include "pa_pool_map.h"
 #include "pa_tree_body.cuh"
 
@@ -52,9 +53,7 @@ extern "C" pa_status pa_v2_tree_attention_workspace(int32_t device, int32_t num_
 }
 
 namespace pa {
-namespace {
 
-// window 0: none, and positions are not read.  sinks 0: none.
 pa_status tree_attention(const void* q, const void* k_pool, const void* v_pool, int32_t kv_dtype, int64_t num_pages,
                          int32_t page_size, int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
                          const int32_t* indices, int64_t num_indices, const int32_t* indptr,
@@ -175,7 +174,6 @@ pa_status tree_attention(const void* q, const void* k_pool, const void* v_pool, 
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ECUDA;
 }
 
-}  // namespace
 }  // namespace pa
 
 extern "C" pa_status pa_v2_tree_attention(const void* q, const void* k_pool, const void* v_pool, int32_t kv_dtype,
