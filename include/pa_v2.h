@@ -867,7 +867,11 @@ pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, const void* 
  * positions, if given, that start at the number of earlier tokens), else it is
  * refused in the same way; entries of pages that nobody sees are not read and may be
  * anything, so a program gives back the pages between sinks and window.
- * P = exp(s) enters the second product rounded to f16; scores, statistics and sums are f32.
+ * P = exp(s) enters the second product rounded to f16 (to q_dtype where a request has many query rows); scores,
+ * statistics and sums are f32.  Calls of more than 96 query rows per KV head and request on average (a prompt's
+ * chunk) write the pages that some token sees out in q_dtype first, exactly, and run pa_v2_tree_attention's kernels
+ * over them, where they fit the workspace: 2^26 elements of K, 2^20 listed pages.  Their workspace is larger by 270 MB and
+ * the tree attention's; with a window they need the positions (chains without them take the other way).
  * PA_EINVAL: sinks without a window.  PA_EUNSUPPORTED: as pa_v2_tree_attention, and batch
  * above 2^20.  The workspace (pa_v2_attention_fp8_workspace's size, 16-byte
  * aligned) needs no initialisation; two calls sharing it must not overlap on

@@ -66,8 +66,8 @@ struct AppendParams {
   float eps;
   int32_t tokens, hq, hkv, rot, page_size;
   uint32_t ps_magic, ps_shift, half_magic, half_shift;
-  int32_t stretch, kv_ctas, kv_splits;  // tokens per KV CTA, CTAs with runs, and CTAs that share a stretch's heads
-  int32_t q_warps, q_splits, q_share;  // warps with q rows, and warps that share a token's heads, so many each
+  int32_t stretch, kv_splits;           // tokens per KV CTA, and CTAs that share a stretch's heads
+  int32_t q_from, q_ctas, q_warps, q_splits, q_share;  // warps with q rows, and warps that share a token's heads, so many each
 };
 
 __device__ __forceinline__ uint32_t codes_of(float a, float b) {  // a in the lower byte
@@ -196,7 +196,8 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) pa_v2_qk_rope_append_fp8_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = p.rot / 2, sub = lane / kLanes;
   const R row(p.rot);
-  const bool is_q = (int)blockIdx.x >= p.kv_ctas;
+  const bool is_q = (int)blockIdx.x >= p.q_from && (int)blockIdx.x < p.q_from + p.q_ctas;
+  const int kv_block = (int)blockIdx.x - (p.q_from == 0 ? p.q_ctas : 0);
   const T* norm_weight = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
   float weight[N];
   if (norm_weight) Vec<T>::unpack(row.load(norm_weight), weight);
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) pa_v2_qk_rope_append_fp8_
   if (is_q) {
     // ------------------------------------------------------------------ q: a warp walks tokens, all their heads with one
     // computation of a lane's cosines and sines, the next rows on their way
-    const int first = ((int)blockIdx.x - p.kv_ctas) * kApWarps + warp;
+    const int first = ((int)blockIdx.x - p.q_from) * kApWarps + warp;
     constexpr int kBatch = 4;  // passes of rows under way per lane, and as many ahead
     const int h0 = first % p.q_splits * p.q_share, heads = min(p.q_share, p.hq - h0);
     const int batches = (heads + kBatch * kAtOnce - 1) / (kBatch * kAtOnce);
@@ -281,10 +282,10 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) pa_v2_qk_rope_append_fp8_
 
   // -------------------------------------------------------------------- k and v: a warp takes a head of a side through the
   // runs that begin in the CTA's stretch of tokens
-  const int task0 = (int)blockIdx.x % p.kv_splits * kApWarps, task = task0 + warp;
+  const int task0 = kv_block % p.kv_splits * kApWarps, task = task0 + warp;
   const bool is_v = task >= p.hkv, has_k = task0 < p.hkv && half > 0;  // has_k: of the CTA, whose warps then share angles
   const int head = is_v ? task - p.hkv : task;
-  const int w0 = (int)blockIdx.x / p.kv_splits * p.stretch, w1 = min(w0 + p.stretch, p.tokens);
+  const int w0 = kv_block / p.kv_splits * p.stretch, w1 = min(w0 + p.stretch, p.tokens);
   const int ahead = min(p.stretch + p.page_size, p.tokens - w0);
   for (int i = threadIdx.x; i < ahead + 1; i += kApThreads) {
     int32_t s = -1;
@@ -307,10 +308,12 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) pa_v2_qk_rope_append_fp8_
     const int32_t s = slot_of[i];
     return s < 0 ? -1 : (int32_t)fast_div((uint32_t)s, p.ps_magic, p.ps_shift);
   };
-  for (int t = w0; t < w1; ++t) {
-    const int at = t - w0 + 1;
+  // (a lane a token of the stretch: kApStretch <= 32)
+  const int32_t lane_page = lane < w1 - w0 ? page_of(lane + 1) : -1;
+  uint32_t starts = __ballot_sync(0xffffffffu, lane_page >= 0 && page_of(lane) != lane_page);
+  for (; starts; starts &= starts - 1) {
+    const int at = __ffs(starts), t = w0 + at - 1;
     const int32_t page = page_of(at);
-    if (page < 0 || page_of(at - 1) == page) continue;
     // the run: how many tokens, and the least entry
     int len = 1, least = INT_MAX;
     for (int i = 0;; i += 32) {
@@ -530,13 +533,19 @@ extern "C" pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, c
   const int stretches = (num_tokens + p.stretch - 1) / p.stretch;
   p.kv_splits = (2 * num_kv_heads + kApWarps - 1) / kApWarps;
   if ((int64_t)stretches * p.kv_splits > INT32_MAX / 2) return PA_EUNSUPPORTED;
-  p.kv_ctas = stretches * p.kv_splits;
-  const int resident = kApCtas * sms * kApWarps, share = 4;  // heads that are worth a warp
+  const int kv_ctas = stretches * p.kv_splits;
+  // With many tokens q's CTAs come first and leave a third of each SM to the stretches', which wait for their data most of
+  // the time, so that the two run side by side (16384 tokens 78 us; q last and on all of the SM 84); with few the
+  // stretches, which take longest, come first (777 tokens 7.1 us, last 8.5).
+  const bool q_first = per >= kApStretch;
+  const int q_most = (q_first ? kApCtas - 1 : kApCtas) * sms;
+  const int resident = q_most * kApWarps, share = 4;  // heads that are worth a warp
   p.q_splits = num_tokens < resident ? std::min(resident / num_tokens, (num_qo_heads + share - 1) / share) : 1;
   p.q_share = (num_qo_heads + p.q_splits - 1) / p.q_splits;
   p.q_splits = (num_qo_heads + p.q_share - 1) / p.q_share;
-  const int q_ctas = (int)std::min<int64_t>(kApCtas * sms, ((int64_t)num_tokens * p.q_splits + kApWarps - 1) / kApWarps);
-  p.q_warps = q_ctas * kApWarps;
+  p.q_ctas = (int)std::min<int64_t>(q_most, ((int64_t)num_tokens * p.q_splits + kApWarps - 1) / kApWarps);
+  p.q_warps = p.q_ctas * kApWarps;
+  p.q_from = q_first ? 0 : kv_ctas;
   const bool paired = !interleaved, q32 = q_dtype == PA_F32;
   const AppendKernel fn =
       dtype == PA_F32   ? pick_append<float, float>(head_dim, paired)
@@ -546,7 +555,7 @@ extern "C" pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, c
   const size_t most = (size_t)kApMaxPage * 2 * (head_dim / 2) * sizeof(float);
   if (!prepare_kernel(reinterpret_cast<const void*>(fn), most)) return PA_ECUDA;
   const size_t smem = (size_t)page_size * rot_dim * sizeof(float);
-  const cudaError_t rc = launch_dependent(fn, dim3((unsigned)(p.kv_ctas + q_ctas)), dim3(kApThreads), smem,
+  const cudaError_t rc = launch_dependent(fn, dim3((unsigned)(kv_ctas + p.q_ctas)), dim3(kApThreads), smem,
                                           static_cast<cudaStream_t>(cuda_stream), p);
   if (rc != cudaSuccess) {
     cudaGetLastError();

@@ -1192,7 +1192,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps, kMergeCtas) pa_v2_fp8_merge_
 // A prompt's chunk meets each key with hundreds of query rows, in blocks of kRows: the tensor cores bound it, and the warp's
 // ones at that.  So the pages that some token sees are written out once in q's 16-bit type (exactly: an element is a
 // binary16 number of 4 significant bits, and a bfloat16 one) and the tree attention runs over them, tcgen05 products and
-// all.  4 x 256 tokens over 8K: 815 us in blocks of 32 rows.
+// all: 4 x 256 tokens over 8K take 209 us (expansion 50, attention 153) where blocks of 32 rows took 815.  Around the
+// border, 128 rows over 1K and 8K tokens: one request 26 and 43 us (blocks: 23 and 49), eight 50 and 164 (51 and 222);
+// 68 rows: 25 and 41 (21 and 41), 48 and 160 (44 and 171).
 struct F8Wide {
   int32_t* qo_wide;     // qo_indptr for the tree attention, all zero when the pages do not fit
   int32_t* qo_narrow;   // and for the blocks of few rows, all zero when they do
@@ -1204,9 +1206,10 @@ struct F8Wide {
   uint32_t hkv_magic, hkv_shift;
 };
 constexpr int kWideThreads = 256;
+constexpr int kWideChunks = 256;              // 16-byte pieces of a side that a warp takes at once
 constexpr int64_t kWideElements = 1ll << 26;  // of k, and of v
 constexpr int64_t kWideSlots = 1ll << 20;
-constexpr int64_t kWideRows = 64;             // query rows of a KV head from which on
+constexpr int64_t kWideRows = 96;             // query rows of a KV head: more of them take this way
 
 // Pages [0, a) and [b, pages) of the request are seen by some token.
 struct F8Pages {
@@ -1295,20 +1298,21 @@ __global__ void __launch_bounds__(kWideThreads) pa_v2_fp8_expand_kernel(const F8
     }
   }
   if (!fits) return;
-  // a run of slots for every warp
-  const int64_t workers = (int64_t)gridDim.x * W, run = div_units(total[0] + workers - 1, workers);
-  int64_t u = ((int64_t)blockIdx.x * W + warp) * run;
-  const int64_t behind = min(u + run, total[0]);
-  if (u >= behind) return;
+  // a run of slots' parts of 4096 elements for every warp (whole slots left most warps of 2K slots without one: 85 us)
+  const int64_t page_elements = (int64_t)p.page_size * p.hkv * D;
+  const int chunks = (int)(page_elements / 16), parts = (chunks + kWideChunks - 1) / kWideChunks;
+  const int64_t workers = (int64_t)gridDim.x * W, run = div_units(total[0] * parts + workers - 1, workers);
+  const int64_t begin = ((int64_t)blockIdx.x * W + warp) * run, behind = min(begin + run, total[0] * parts);
+  if (begin >= behind) return;
+  int64_t u = div_units(begin, parts);
+  int part = (int)(begin - u * parts);
   int first = 0;  // the thread of the request that holds slot u
   while (!__any_sync(0xffffffffu, ends[0][first + lane] > u)) first += 32;
   first += __ffs(__ballot_sync(0xffffffffu, ends[0][first + lane] > u)) - 1;
   int r = first * per_thread;
   int64_t slot0 = first > 0 ? ends[0][first - 1] : 0, page0 = first > 0 ? ends[1][first - 1] : 0;
   F8Pages n = f8_pages(p, f8_req<kF8MaxRows>(p, r, false), r);
-  const int64_t page_elements = (int64_t)p.page_size * p.hkv * D;
-  const int chunks = (int)(page_elements / 16);
-  for (; u < behind; ++u) {
+  for (int64_t i = begin; i < behind; ++i) {
     while (u - slot0 >= n.pages) {
       slot0 += n.pages;
       page0 += n.seen();
@@ -1316,10 +1320,16 @@ __global__ void __launch_bounds__(kWideThreads) pa_v2_fp8_expand_kernel(const F8
       n = f8_pages(p, f8_req<kF8MaxRows>(p, r, false), r);
     }
     const int32_t s = (int32_t)(u - slot0);
+    const int64_t slot = u;
+    const int c0 = part * kWideChunks, c1 = min(c0 + kWideChunks, chunks);
+    if (++part == parts) {
+      part = 0;
+      ++u;
+    }
     const int32_t page = __ldg(p.indices + p.indptr[r] + s);
     const bool copied = (s < n.a || s >= n.b) && page >= 0 && page < p.num_pages;  // (the attention reports bad pages)
     const int64_t id = page0 + (s < n.a ? s : s - max(n.a, n.b) + n.a);
-    if (lane == 0) w.table[u] = copied ? (int32_t)id : -1;
+    if (lane == 0 && c0 == 0) w.table[slot] = copied ? (int32_t)id : -1;
     if (!copied) continue;
     const uint4* k = reinterpret_cast<const uint4*>(p.k_pool + page * page_elements);
     const uint4* v = reinterpret_cast<const uint4*>(p.v_pool + page * page_elements);
@@ -1327,8 +1337,8 @@ __global__ void __launch_bounds__(kWideThreads) pa_v2_fp8_expand_kernel(const F8
     uint4* vo = reinterpret_cast<uint4*>(static_cast<T*>(w.v) + id * page_elements);
     const int8_t* ke = p.k_exp + (int64_t)page * p.hkv;
     const int8_t* ve = p.v_exp + (int64_t)page * p.hkv;
-#pragma unroll 2
-    for (int c = lane; c < chunks; c += 32) {
+#pragma unroll 4
+    for (int c = c0 + lane; c < c1; c += 32) {
       const uint32_t row = (uint32_t)c / (D / 16);  // of the page's rows and heads
       const uint32_t head = row - fast_div(row, w.hkv_magic, w.hkv_shift) * p.hkv;
       const uint4 x = __ldg(k + c), y = __ldg(v + c);

@@ -520,6 +520,117 @@ def test_attention_nan_reaches_the_rows_that_see_it_and_no_other(page_size, hq, 
         assert lse[t, :hq // 2].isnan().all() == (hit[0] in rows)
 
 
+# -- more than 96 query rows per KV head: pages written out in q's type, the tree attention over them
+
+MANY = [([(300, 60)], 8, 2, 0, 0), ([(0, 130)], 4, 2, 0, 0), ([(500, 70), (33, 50), (7, 0), (0, 61)], 8, 2, 0, 0),
+        ([(900, 60), (20, 60)], 8, 2, 100, 5), ([(900, 60), (3, 60)], 8, 2, 30, 0), ([(400, 200)], 4, 4, 16, 40)]
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("reqs,hq,hkv,window,sinks", MANY)
+@pytest.mark.parametrize("page_size,D,tree", [(16, 128, False), (5, 64, False), (16, 64, True), (256, 128, True), (1, 128, False)])
+def test_attention_many_rows(reqs, hq, hkv, window, sinks, page_size, D, tree, dtype):
+    rng = random.Random(window)
+    trees = [R.random_tree(rng, n) for _, n in reqs] if tree else None
+    _check_attn(_attn_case(61 + window, reqs, hq, hkv, D, page_size, dtype, window, sinks, trees=trees, give_back=True))
+
+
+@pytest.mark.parametrize("page_size", [16, 5])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3)])
+def test_attention_many_rows_nothing_hidden_and_nan_where_it_is_seen(page_size, window, sinks):
+    rng = random.Random(5)
+    reqs = [(300, 70), (40, 60)]
+    c = _attn_case(71, reqs, 8, 2, 128, page_size, torch.bfloat16, window, sinks,
+                   trees=[R.random_tree(rng, n, 0.3) for _, n in reqs])
+    seen = torch.zeros(c["kp"].shape[0] * page_size, dtype=torch.bool)
+    for rows in c["seen"]:
+        seen[rows] = True
+    for n in ("kp", "vp"):
+        c[n].view(torch.uint8).flatten(0, 1)[~seen] = 0x7f
+    clean = dict(c, vp=c["vp"].float().nan_to_num(0.0).to(E4M3), kp=c["kp"].float().nan_to_num(0.0).to(E4M3))
+    ro, rl, to, tl = ref = _attn_ref(clean)
+    st = status_word()
+    _close(_run_attn(c, status=st), ref)
+    assert int(st) == 0
+    hit = [rows[k] for rows in c["seen"][::9] for k in (0, -1)]
+    for j, row in enumerate(hit):
+        c["vp"].view(torch.uint8).flatten(0, 1)[row, j % 2, (7 * j) % 128] = 0x7f
+    out = _run_attn(c)[0].cpu().double()
+    flat, nan = c["vp"].float().isnan().flatten(0, 1), torch.zeros(ro.shape, dtype=torch.bool)
+    for t, rows in enumerate(c["seen"]):
+        nan[t] = flat[rows].any(0).repeat_interleave(4, 0)
+    clean["vp"] = c["vp"].float().nan_to_num(0.0).to(E4M3)
+    ro, _, to, _ = _attn_ref(clean)
+    assert nan.any() and torch.equal(out.isnan(), nan) and ((out - ro).abs() <= to)[~nan].all()
+
+
+@pytest.mark.parametrize("ctx", [7000, 8300])
+def test_attention_many_rows_of_more_pages_than_fit(ctx):
+    """64 KV heads: 512 pages of 16 tokens fit the workspace; a table with room for more leaves it to the device."""
+    c = _attn_case(81, [(ctx, 100)], 64, 64, 128, 16, torch.float16)
+    c["ids"] = torch.cat((c["ids"], torch.zeros(600, dtype=I32)))
+    _check_attn(c)
+
+
+def test_attention_many_rows_bad_tables_and_graphs():
+    def case():
+        return _attn_case(91, [(50, 60), (20, 60), (33, 60)], 8, 2, 64, 16, torch.float16)
+
+    ref = _attn_ref(case())
+    good = torch.tensor([True] * 60 + [False] * 60 + [True] * 60)
+    for page in (-1, 10 ** 6, 2 ** 31 - 1):
+        c = case()
+        c["ids"][int(c["indptr"][1])] = page
+        st = status_word()
+        out, lse = _run_attn(c, status=st)
+        assert int(st) == pa.DEVICE_BAD_PAGE and out.isfinite().all() and lse.isfinite().all()
+        assert ((out.cpu().double() - ref[0]).abs() <= ref[2])[good].all()
+    for change in (dict(lpl=0), dict(lpl=17), dict(fpo=-1), dict(fpo=16)):
+        c = case()
+        for k, v in change.items():
+            c[k][1] = v
+        st = status_word()
+        out, lse = _run_attn(c, status=st)
+        assert int(st) == pa.DEVICE_BAD_TREE and out[60:120].eq(0).all() and lse[60:120].eq(-math.inf).all()
+        assert ((out.cpu().double() - ref[0]).abs() <= ref[2])[good].all()
+    c = case()
+    c["indptr"][2] = 10 ** 6
+    st = status_word()
+    out, lse = _run_attn(c, status=st)
+    assert int(st) & pa.DEVICE_BAD_SLOT and out[60:].eq(0).all()
+    c = case()
+    c["qo"] = i32([0, 60, 50, 180])
+    st = status_word()
+    _run_attn(c, status=st)
+    assert int(st) & pa.DEVICE_BAD_INDPTR
+    # rows behind the last token, and a captured call replayed over other lengths
+    c = case()
+    args = [c[n].cuda() for n in ("q", "kp", "vp", "ke", "ve", "ids", "indptr", "lpl", "fpo", "qo")]
+    q = torch.cat((args[0], args[0][:7]))
+    out, lse = torch.full_like(q, 5.0), torch.full(q.shape[:2], 6.0, device="cuda")
+    ws = pa.attention_fp8_workspace(187, 3, 8, 2, 64)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.pa_v2_attention_fp8(q, *args[1:], c["scale"], out=out, lse2_out=lse, workspace=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    _close((out, lse), ref)
+    assert out[180:].eq(5.0).all() and lse[180:].eq(6.0).all()
+    d = _attn_case(92, [(70, 10), (10, 150), (3, 20)], 8, 2, 64, 16, torch.float16)
+    n = d["kp"].shape[0]
+    assert n <= args[1].shape[0] and len(d["ids"]) <= len(args[5])
+    for x, k in zip(args[1:5], ("kp", "vp", "ke", "ve")):
+        x[:n] = d[k].cuda()
+    q[:180] = d["q"].cuda()
+    args[5][:len(d["ids"])] = d["ids"].cuda()
+    for x, k in zip(args[6:], ("indptr", "lpl", "fpo", "qo")):
+        x.copy_(d[k])
+    graph.replay()
+    torch.cuda.synchronize()
+    _close((out, lse), _attn_ref(d))
+
+
 @pytest.mark.parametrize("scale", [-0.09, 0.0, 1e-30, 3.0])
 def test_attention_other_scales(scale):
     c = _attn_case(21, [(300, 2), (31, 1)], 8, 2, 128, 16, torch.float16)
