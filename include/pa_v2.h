@@ -841,7 +841,7 @@ pa_status pa_v2_tree_attention_sinks(const void* q, const void* k_pool, const vo
  * recorded (PA_DEVICE_BAD_SLOT); either ends a run, so padding lies behind the
  * last token.  Slots must be distinct, q_out must not overlap an input.
  * Arguments, types and refusals as pa_v2_qk_rope_append, dtype that of q, k and
- * v; page_size up to 256 (PA_EUNSUPPORTED above). */
+ * v; page_size up to 256, num_tokens * num_kv_heads below 2^31 (PA_EUNSUPPORTED above). */
 pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                                    int64_t v_stride, int32_t dtype, int32_t num_tokens, int32_t num_qo_heads,
                                    int32_t num_kv_heads, int32_t head_dim, const int32_t* positions,
@@ -870,8 +870,9 @@ pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, const void* 
  * P = exp(s) enters the second product rounded to f16 (to q_dtype where a request has many query rows); scores,
  * statistics and sums are f32.  Calls of more than 96 query rows per KV head and request on average (a prompt's
  * chunk) write the pages that some token sees out in q_dtype first, exactly, and run pa_v2_tree_attention's kernels
- * over them, where they fit the workspace: 2^26 elements of K, 2^20 listed pages.  Their workspace is larger by 270 MB and
- * the tree attention's; with a window they need the positions (chains without them take the other way).
+ * over them, where the pages fit: 2^26 elements of K, 2^20 listed pages.  The workspace for such sizes is larger by
+ * 270 MB and the tree attention's; calls with a workspace for other sizes, of at least its smaller part, and chains
+ * in a window without positions take the other way.
  * PA_EINVAL: sinks without a window.  PA_EUNSUPPORTED: as pa_v2_tree_attention, and batch
  * above 2^20.  The workspace (pa_v2_attention_fp8_workspace's size, 16-byte
  * aligned) needs no initialisation; two calls sharing it must not overlap on

@@ -14,12 +14,21 @@
 // warp also rescales the page's earlier codes.  A code is a 4-bit number times a power of
 // two, so that step is exact except for codes that turn subnormal.
 //
-// HBM bound: q, k and v are read once and q_out and the codes written once.  The first CTAs
-// take stretches of tokens and handle the runs that begin in theirs (a run's cosines
-// and sines are computed once, for all heads); the others take q's rows.  Rows are held
-// as in pa_qk_rope.cu: 16 bytes per lane in two pieces that hold both elements of each
-// of the lane's pairs.  A run that fits a warp's registers (kHeld passes) is read once;
-// a longer one is read again, out of L2, after its maximum is known.
+// HBM bound: q, k and v are read once and q_out and the codes written once.  Some CTAs walk
+// q's tokens, a warp a token and all its heads with one computation of a lane's cosines
+// and sines, the next rows on their way.  The others take stretches of tokens and handle
+// the runs that begin in theirs, a warp a head of a side (a run's angles are computed once,
+// by the CTA, while its K rows are on their way).  Rows are held as in pa_qk_rope.cu: 16
+// bytes per lane in two pieces that hold both elements of each of the lane's pairs.  A run
+// that fits a warp's registers as loaded (16 tokens of 128 elements) is read once and normed
+// and rotated twice, for the maximum and for the codes; a longer one is read again, out of L2.
+//
+// 16384 tokens of 48 heads take 78 us of 54 (4.7 TB/s of 6.8): alone q takes 52 (5.2 TB/s)
+// and the runs 45, which wait for their data, a run's steps one after the other (8 us a
+// CTA, three CTAs an SM).  2048 tokens 20 us of 7, the same steps twice over.  Kept in shared
+// memory between maximum and codes K costs q more than it saves (93 us); held in registers it
+// leaves two CTAs an SM (106); angles by every warp for itself spill (146); 64 registers for
+// four CTAs spill (118).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -472,6 +481,7 @@ extern "C" pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, c
   if (head_dim != 64 && head_dim != 128) return PA_EUNSUPPORTED;
   if (rot_dim > head_dim || rot_dim % 16 != 0) return PA_EUNSUPPORTED;
   if (num_qo_heads > 16384 || num_kv_heads > 16384 || page_size > kApMaxPage) return PA_EUNSUPPORTED;
+  if ((int64_t)num_tokens * num_kv_heads > INT32_MAX) return PA_EUNSUPPORTED;
   if (num_pages >= (1ll << 31) || num_pages * page_size >= (1ll << 31)) return PA_EUNSUPPORTED;
   if (num_tokens == 0) return PA_OK;
   if (!q || !k || !v || !positions || !slots || !q_out || !k_pool || !v_pool || !k_exp || !v_exp ||
@@ -532,7 +542,6 @@ extern "C" pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, c
   p.stretch = per < 1 ? 1 : per < kApStretch ? per : kApStretch;
   const int stretches = (num_tokens + p.stretch - 1) / p.stretch;
   p.kv_splits = (2 * num_kv_heads + kApWarps - 1) / kApWarps;
-  if ((int64_t)stretches * p.kv_splits > INT32_MAX / 2) return PA_EUNSUPPORTED;
   const int kv_ctas = stretches * p.kv_splits;
   // With many tokens q's CTAs come first and leave a third of each SM to the stretches', which wait for their data most of
   // the time, so that the two run side by side (16384 tokens 78 us; q last and on all of the SM 84); with few the

@@ -14,11 +14,14 @@
 //
 // Work.  The query rows of a KV head (n * G pairs of new token and head) are taken in
 // blocks of 8 NT; one block against one tile of 32 pool rows (page order) is a unit.  The
-// units of the batch in order (request, KV head, block, tile) are cut into equal runs, one
-// for each warp of one CTA per SM: no host plan, no wave tail, whatever the lengths.  A
-// warp that meets a block's tiles alone writes its result; parts of the same block in
-// one CTA are joined in shared memory, and CTAs that share a block leave one partial
-// result each, which pa_v2_fp8_merge_kernel folds.
+// units of the batch in order (request, KV head, block, tile) are cut into equal runs over
+// the warps of one CTA per SM: no host plan, no wave tail, whatever the lengths.  A warp
+// that meets a block's tiles alone writes its result; the others leave partial results,
+// which pa_v2_fp8_merge_kernel folds.  Where runs are long, a run belongs to a team of
+// warps, one for each KV head: a page's rows of all heads lie side by side, and asked for
+// at the same time HBM serves them at 6.2 TB/s, one head after the other at 5.2.  Where
+// runs are short, partial results cost more than that gains: there neighbouring runs of a
+// head go to the warps of a CTA, which joins their parts in shared memory first.
 //
 // A warp owns a ring of stages (a stage: 32 K rows and 32 V rows of D bytes) and walks
 // its units without a block barrier: TMA boxes, 128- or 64-byte swizzled, or 16-byte
@@ -28,6 +31,18 @@
 // takes V through ldmatrix.trans of byte pairs: a register holds two tokens x two dims,
 // one byte permutation apart from the two A registers it becomes.  P^T goes from the
 // accumulator's layout to the B operand's by movmatrix.
+//
+// What bounds it (GB300, 32 query heads on 8 KV heads, D = 128, page size 16, replayed):
+// 64 ragged requests of 1K-32K, one token each, 214-229 us, 5.9-6.2 TB/s of 6.8 measured:
+// HBM; 33 % of the issue slots.  32 chains of 5 tokens in a window of 4096 with 4 sinks
+// 77 us of 29: 20 of 24 columns of products, two warps a scheduler that wait for one
+// another's shuffles and conversions half of the time.  One token over 32K 26 us (10 of
+// HBM), over 1K 13 us: starts (8 us: cold code, tables, pages, tiles, one after the other),
+// joining 2-3, the merge kernel 4.  More warps help while registers allow them (12 at 168
+// for one block of 8 rows: 26 -> 23 us over 32K; the wider blocks need 255); q in registers
+// up to 16 rows, 16 keys at a time for 32 rows (spills made 32 chains 161 us).  Measured and
+// not kept: the same code for a request's geometry called, not inlined (+2 us everywhere);
+// lanes as parts in the joining (equal).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -1484,10 +1499,7 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
     return PA_ECUDA;
   }
   const int64_t rows = rows_of(num_tokens, batch, group);
-  int64_t need = 0, tree_bytes = 0;
-  pa_status ws = pa_v2_attention_fp8_workspace(dev, num_tokens, batch, num_qo_heads, num_kv_heads, head_dim, &need);
-  if (ws != PA_OK) return ws;
-  if (workspace_bytes < need) return PA_ECAPACITY;
+  if (workspace_bytes < few_rows_bytes(sms, head_dim)) return PA_ECAPACITY;
   alignas(64) CUtensorMap tm_k, tm_v;
   std::memset(&tm_k, 0, sizeof(tm_k));
   std::memset(&tm_v, 0, sizeof(tm_v));
@@ -1544,11 +1556,16 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t rc = cudaSuccess;
   const int64_t page_elements = (int64_t)page_size * num_kv_heads * head_dim;
-  // many rows: (a window's depths come from the positions there, for chains too)
+  // many rows, where the workspace has room for their pages (it may be one for other sizes); a window's depths come from
+  // the positions there, for chains too
+  int64_t tree_bytes = 0;
+  pa_status ws = PA_OK;
   if (rows > kWideRows && (window == 0 || positions) && page_elements <= kWideElements) {
     ws = pa_v2_tree_attention_workspace(dev, num_tokens, batch, num_qo_heads, num_kv_heads, head_dim, &tree_bytes);
     if (ws != PA_OK) return ws;
-    const WideLayout l = wide_layout(batch, tree_bytes);
+  }
+  const WideLayout l = wide_layout(batch, tree_bytes);
+  if (tree_bytes > 0 && workspace_bytes - few_rows_bytes(sms, head_dim) >= l.bytes) {
     char* base = static_cast<char*>(workspace) + few_rows_bytes(sms, head_dim);
     F8Wide w;
     w.qo_wide = reinterpret_cast<int32_t*>(base + l.qo_wide);

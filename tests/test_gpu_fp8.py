@@ -782,6 +782,32 @@ def test_attention_repeats_itself_and_takes_any_workspace():
     assert e.value.status == pa.PA_ECAPACITY
 
 
+def test_attention_workspace_for_other_sizes():
+    """A workspace made for the most tokens and requests serves every smaller call, also one whose tokens all belong to
+    one request (which would like a larger one)."""
+    ws = pa.attention_fp8_workspace(128, 128, 8, 2, 128)
+    for reqs in ([(300, 128)], [(300, 100), (7, 28)], [(20, 1)] * 128):
+        _check_attn(_attn_case(36, reqs, 8, 2, 128, 16, torch.bfloat16), workspace=ws)
+    large = pa.attention_fp8_workspace(256, 2, 8, 2, 128)
+    assert large.numel() > ws.numel()
+    for reqs in ([(300, 128), (7, 128)], [(300, 128)], [(20, 1)] * 2):
+        _check_attn(_attn_case(37, reqs, 8, 2, 128, 16, torch.bfloat16), workspace=large)
+
+
+def test_attention_without_a_new_token():
+    c = _attn_case(38, [(30, 0), (0, 0), (5, 0)], 4, 2, 64, 16, torch.float16)
+    out, lse = torch.full((5, 4, 64), 5.0, dtype=torch.float16, device="cuda"), torch.full((5, 4), 6.0, device="cuda")
+    st = status_word()
+    _run_attn(c, pad=5, out=out, lse2_out=lse, status=st)
+    assert int(st) == 0 and out.eq(5.0).all() and lse.eq(6.0).all()
+
+
+@pytest.mark.parametrize("hkv", [67, 96, 130])
+@pytest.mark.parametrize("ctx", [40, 700])
+def test_attention_many_kv_heads(hkv, ctx):
+    _check_attn(_attn_case(hkv, [(ctx, 1), (3, 2), (2 * ctx, 1)], hkv, hkv, 64, 16, torch.float16))
+
+
 def test_attention_two_calls_at_once_and_two_graphs_side_by_side():
     cases = [_attn_case(40 + k, [(3000, 2), (50 + k, 1)], 8, 2, 128, 16, DT[k]) for k in range(2)]
     alone = [[x.clone() for x in _run_attn(c)] for c in cases]
@@ -853,6 +879,41 @@ def test_pools_of_more_elements_than_32_bits_count(page_size):
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("window", [5, 40, 300])
+def test_sliding_tables_feed_the_attention(window, tree):
+    """pa_v2_build_tables_sliding's trimmed tables, cut masks and positions, as the 16-bit attention takes them."""
+    rng = random.Random(window)
+    cached, new, ps, hq, hkv, D = [700, 33, 0, 90], [9, 40, 12, 0], 16, 4, 2, 64
+    g = torch.Generator().manual_seed(window)
+    width = 48
+    table = torch.randperm(4 * width + 3, generator=g)[:4 * width].reshape(4, width).to(I32)
+    parents = [R.random_tree(rng, n) for n in new] if tree else None
+    P, T = 4 * width + 3, sum(new)
+    pools, exps = [], []
+    for _ in range(2):
+        pools.append((torch.randn(P, ps, hkv, D, generator=g) * 64).clamp(-448, 448).to(E4M3))
+        exps.append(torch.randint(-8, -3, (P, hkv), generator=g).to(torch.int8))
+    q = torch.randn(T, hq, D, generator=g).bfloat16()
+    t = pa.StepTables.empty(4, 4 * width, T, 2 if tree else 0)
+    st = status_word()
+    pa.pa_v2_build_tables(i32(cached).cuda(), i32(new).cuda(), table.cuda(), ps, t, sliding_window=window, status=st,
+                          parents=i32(p for ps_ in parents for p in ps_).cuda() if tree else None)
+    got = pa.pa_v2_attention_fp8(q.cuda(), *[x.cuda() for x in pools + exps], t.indices, t.indptr, t.last_page_len,
+                                 t.first_page_offset, t.qo_indptr, D ** -0.5, tree_mask=t.tree_mask,
+                                 positions=t.positions, sliding_window=window, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    seen = []
+    for r in range(4):
+        for i in range(new[r]):
+            line = R.ancestors(parents[r], i)[:window] if tree else None
+            depth = len(R.ancestors(parents[r], i)) - 1 if tree else i
+            seen.append(F.seen_rows(table[r], ps, 0, cached[r] + new[r], new[r], i, window, 0,
+                                    set(line) if tree else None, depth))
+    _close(got, F.attention_ref(q, F.values(pools[0], exps[0]), F.values(pools[1], exps[1]), seen, D ** -0.5))
+
 
 @pytest.mark.parametrize("window,sinks", [(0, 0), (24, 4)])
 @pytest.mark.parametrize("graph", [False, True])
