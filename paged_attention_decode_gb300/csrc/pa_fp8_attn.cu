@@ -342,25 +342,37 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
   }
   pdl_wait_prerequisites();
 
-  // ---- the cut: every warp's first unit
-  int64_t units = 0, mine = 0;
+  // ---- the cut: every warp's first unit.  A warp finds it alone where a lane holds a request, else all threads do
+  // (their barriers and second look at the request cost one token over 1K 0.6 us).
+  const bool alone = p.batch <= 32;
+  int64_t units = 0, upto;
+  F8Req own = {};
   const int per_thread = (p.batch + (32 * W) - 1) / (32 * W);
-  const int r0 = (int)min((int64_t)threadIdx.x * per_thread, (int64_t)p.batch), r1 = min(r0 + per_thread, p.batch);
-  for (int r = r0; r < r1; ++r) mine += units_of(f8_req<R>(p, r, blockIdx.x == 0));
-  int64_t upto = mine;
+  if (alone) {
+    if (lane < p.batch) own = f8_req<R>(p, lane, blockIdx.x == 0 && warp == 0);
+    upto = units_of(own);
+  } else {
+    const int r0 = (int)min((int64_t)threadIdx.x * per_thread, (int64_t)p.batch), r1 = min(r0 + per_thread, p.batch);
+    upto = 0;
+    for (int r = r0; r < r1; ++r) upto += units_of(f8_req<R>(p, r, blockIdx.x == 0));
+  }
 #pragma unroll
   for (int w = 1; w < 32; w <<= 1) {
     const int64_t x = __shfl_up_sync(0xffffffffu, upto, w);
     if (lane >= w) upto += x;
   }
-  if (lane == 31) warp_sum[warp] = upto;
-  __syncthreads();
-  for (int w = 0; w < W; ++w) {
-    if (w < warp) upto += warp_sum[w];
-    units += warp_sum[w];
+  if (alone) {
+    units = __shfl_sync(0xffffffffu, upto, 31);
+  } else {
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) upto += warp_sum[w];
+      units += warp_sum[w];
+    }
+    ends[threadIdx.x] = upto;  // units of a KV head up to this thread's last request
+    __syncthreads();
   }
-  ends[threadIdx.x] = upto;  // units of a KV head up to this thread's last request
-  __syncthreads();
   // Warps of a team take the same run of units of neighbouring heads, side by side: their rows lie side by side too, and
   // HBM serves them so (64 ragged requests of 8 KV heads 255 -> 214 us, 5.2 -> 6.2 TB/s).  Then every warp leaves its own
   // partial results.  Where runs are short those cost more than that gains (a request of 32K tokens: 205 parts a head, 30
@@ -578,19 +590,29 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
   int64_t issued = min(count, (int64_t)S);
   Taken next;
   if (count > 0) {
-    // the request that holds unit u0, searched by the warp's lanes: its thread, then, where a thread has several, it
-    int first = 0;
-    while (!__any_sync(0xffffffffu, ends[first + lane] * groups > u0)) first += 32;
-    first += __ffs(__ballot_sync(0xffffffffu, ends[first + lane] * groups > u0)) - 1;
-    l_r = min(first * per_thread, p.batch - 1);
-    int64_t off = u0 - (first > 0 ? ends[first - 1] * groups : 0);
-    F8Req q = f8_req<R>(p, l_r, false);
-    while (off >= units_of(q) * groups) {
-      off -= units_of(q) * groups;
-      q = f8_req<R>(p, ++l_r, false);
+    // the request that holds unit u0, searched by the warp's lanes: its lane, or its thread and, where a thread has
+    // several, it
+    int64_t off;
+    if (alone) {
+      l_r = __ffs(__ballot_sync(0xffffffffu, upto * groups > u0)) - 1;
+      const int64_t before = __shfl_sync(0xffffffffu, upto, max(l_r - 1, 0));
+      off = u0 - (l_r > 0 ? before * groups : 0);
+      if (lane == l_r) infos[warp][0] = own;
+    } else {
+      int first = 0;
+      while (!__any_sync(0xffffffffu, ends[first + lane] * groups > u0)) first += 32;
+      first += __ffs(__ballot_sync(0xffffffffu, ends[first + lane] * groups > u0)) - 1;
+      l_r = min(first * per_thread, p.batch - 1);
+      off = u0 - (first > 0 ? ends[first - 1] * groups : 0);
+      F8Req q = f8_req<R>(p, l_r, false);
+      while (off >= units_of(q) * groups) {
+        off -= units_of(q) * groups;
+        q = f8_req<R>(p, ++l_r, false);
+      }
+      if (lane == 0) infos[warp][0] = q;
     }
-    if (lane == 0) infos[warp][0] = q;
     __syncwarp();
+    const F8Req& q = infos[warp][0];
     const int32_t tiles = q.tiles;
     const int64_t head = (int64_t)q.blocks * tiles;
     const int32_t heads = (int32_t)div_units(off, head);  // groups of heads before

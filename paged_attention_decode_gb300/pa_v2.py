@@ -922,19 +922,20 @@ def pa_v2_tree_attention(q, k_pool, v_pool, indices, indptr, last_page_len, firs
 # the 8-bit cache
 # ---------------------------------------------------------------------------
 
-def _pools_fp8(k_pool, v_pool, k_exp, v_exp, index: int) -> tuple[int, int, int, int]:
-    """(k, v, k exponents, v exponents) pointers of an 8-bit cache."""
-    if k_pool.dtype != torch.float8_e4m3fn or v_pool.dtype != torch.float8_e4m3fn or k_pool.shape != v_pool.shape:
+def _pools_fp8(k_pool, v_pool, k_exp, v_exp, index: int):
+    """(pointers of k, v, k exponents, v exponents), and the pools' shape, of an 8-bit cache."""
+    e4m3, i8, shape = torch.float8_e4m3fn, torch.int8, k_pool.shape
+    if k_pool.dtype is not e4m3 or v_pool.dtype is not e4m3 or shape != v_pool.shape:
         raise ValueError("k_pool and v_pool must be float8_e4m3fn and share a shape")
-    if k_pool.dim() != 4:
+    if len(shape) != 4:
         raise ValueError("pools must be [num_pages, page_size, num_kv_heads, head_dim]")
-    shape = (k_pool.shape[0], k_pool.shape[2])
-    for t, name in ((k_exp, "k_exp"), (v_exp, "v_exp")):
-        if t.shape != shape:
-            raise ValueError(f"{name} must be [num_pages, num_kv_heads] = {list(shape)}, got {list(t.shape)}")
+    each = (shape[0], shape[2])
+    if k_exp.shape != each or v_exp.shape != each:
+        bad, name = (k_exp, "k_exp") if k_exp.shape != each else (v_exp, "v_exp")
+        raise ValueError(f"{name} must be [num_pages, num_kv_heads] = {list(each)}, got {list(bad.shape)}")
     ptr = _step_ptr
-    return (ptr(k_pool, "k_pool", index), ptr(v_pool, "v_pool", index), ptr(k_exp, "k_exp", index, torch.int8),
-            ptr(v_exp, "v_exp", index, torch.int8))
+    return (ptr(k_pool, "k_pool", index), ptr(v_pool, "v_pool", index), ptr(k_exp, "k_exp", index, i8),
+            ptr(v_exp, "v_exp", index, i8)), shape
 
 
 def pa_v2_qk_rope_append_fp8(q, k, v, positions, slots, inv_freq, k_pool, v_pool, k_exp, v_exp, q_out=None,
@@ -946,39 +947,37 @@ def pa_v2_qk_rope_append_fp8(q, k, v, positions, slots, inv_freq, k_pool, v_pool
     int8, the exponents of each page and KV head (an element is code * 2^exponent); the tokens of one page must be
     neighbours in the call.  Returns q_out [T, Hq, D] in q_dtype (q's dtype by default, or float32)."""
     dev = _device_index(q, "q")
-    pools = _pools_fp8(k_pool, v_pool, k_exp, v_exp, dev)
+    pools, (pages, page_size, pool_heads, pool_dim) = _pools_fp8(k_pool, v_pool, k_exp, v_exp, dev)
+    dt, i32, f32, ptr = q.dtype, torch.int32, torch.float32, _step_ptr
+    code = KV_DTYPES.get(dt)
+    if code is None:
+        raise ValueError(f"q, k and v must be one of {list(KV_DTYPES)}")
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, head_dim]")
-    if q.dtype not in KV_DTYPES:
-        raise ValueError(f"q, k and v must be one of {list(KV_DTYPES)}")
     T, _, D = q.shape
-    dt, i32, ptr = q.dtype, torch.int32, _step_ptr
     qp, qs, hq = _token_rows(q, "q", T, D, dt, dev)
     kp, ks, hkv = _token_rows(k, "k", T, D, dt, dev)
     vp, vs, hv = _token_rows(v, "v", T, D, dt, dev)
-    pages, page_size, pool_heads, pool_dim = k_pool.shape
     if hv != hkv or pool_heads != hkv or pool_dim != D:
         raise ValueError(f"k, v and the pools must agree on heads and head_dim: {hkv}, {hv}, {list(k_pool.shape)}")
     rot = 2 * inv_freq.numel() if inv_freq is not None else 0
-    if q_out is not None:
-        q_dtype = q_out.dtype
-    elif q_dtype is None:
-        q_dtype = dt
-    if q_dtype not in KV_DTYPES:
+    q_dtype = q_out.dtype if q_out is not None else q_dtype or dt
+    q_code = KV_DTYPES.get(q_dtype)
+    if q_code is None:
         raise ValueError(f"q_dtype must be one of {list(KV_DTYPES)}")
-    head = (qp, qs, kp, ks, vp, vs, KV_DTYPES[dt], T, hq, hkv, D, ptr(positions, "positions", dev, i32, T),
-            ptr(slots, "slots", dev, i32, T), ptr(inv_freq, "inv_freq", dev, torch.float32), rot,
+    head = (qp, qs, kp, ks, vp, vs, code, T, hq, hkv, D, ptr(positions, "positions", dev, i32, T),
+            ptr(slots, "slots", dev, i32, T), ptr(inv_freq, "inv_freq", dev, f32), rot,
             1 if interleaved else 0, ptr(q_weight, "q_weight", dev, dt, D), ptr(k_weight, "k_weight", dev, dt, D),
             eps)
     st = ptr(status, "status", dev, i32)
-    if q_out is not None and tuple(q_out.shape) != (T, hq, D):
+    if q_out is not None and q_out.shape != (T, hq, D):
         raise ValueError(f"q_out must be [{T}, {hq}, {D}], got {list(q_out.shape)}")
 
     def launch(handle):
         nonlocal q_out
         if q_out is None:
             q_out = torch.empty(T, hq, D, dtype=q_dtype, device=q.device)
-        rc = lib().pa_v2_qk_rope_append_fp8(*head, ptr(q_out, "q_out", dev), KV_DTYPES[q_dtype], *pools, pages,
+        rc = lib().pa_v2_qk_rope_append_fp8(*head, ptr(q_out, "q_out", dev), q_code, *pools, pages,
                                             page_size, st, handle)
         if rc != PA_OK:
             raise PaError(rc, "pa_v2_qk_rope_append_fp8")
@@ -1020,13 +1019,12 @@ def pa_v2_attention_fp8(q, k_pool, v_pool, k_exp, v_exp, indices, indptr, last_p
     int32, as in the tables, are needed with a tree_mask and a window.  Returns (out [T, Hq, D] of q's dtype, lse2
     [T, Hq] float32); rows behind the last token are not written."""
     dev = _device_index(q, "q")
-    pools = _pools_fp8(k_pool, v_pool, k_exp, v_exp, dev)
+    pools, (P, ps, hkv, pool_dim) = _pools_fp8(k_pool, v_pool, k_exp, v_exp, dev)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, head_dim]")
     if q.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("q must be float16 or bfloat16")
     T, hq, D = q.shape
-    P, ps, hkv, pool_dim = k_pool.shape
     if pool_dim != D:
         raise ValueError(f"pools must be [P, page_size, Hkv, {D}]")
     B, dt, i32, ptr = last_page_len.numel(), q.dtype, torch.int32, _step_ptr
