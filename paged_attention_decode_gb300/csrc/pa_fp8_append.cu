@@ -25,7 +25,7 @@
 //
 // 16384 tokens of 48 heads take 78 us of 54 (4.7 TB/s of 6.8): alone q takes 52 (5.2 TB/s)
 // and the runs 45, which wait for their data, a run's steps one after the other (8 us a
-// CTA, three CTAs an SM).  2048 tokens 20 us of 7, the same steps twice over.  Kept in shared
+// CTA, three CTAs an SM).  2048 tokens 19 us of 7: few rows for a run's steps to hide behind.  Kept in shared
 // memory between maximum and codes K costs q more than it saves (93 us); held in registers it
 // leaves two CTAs an SM (106); angles by every warp for itself spill (146); 64 registers for
 // four CTAs spill (118).
@@ -534,18 +534,18 @@ extern "C" pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, c
     cudaGetLastError();
     return PA_ECUDA;
   }
-  // Stretches and q tiles: short enough that the CTAs fill the GPU, and, while the stretches alone do not, the heads of
-  // one are shared out.
-  // Stretches short enough that the CTAs fill the GPU, and, while the stretches alone do not, the heads of one shared out.
+  // Stretches of as many tokens as leave two CTAs an SM for them all, a stretch's heads shared out in eights: with shorter
+  // ones a CTA's begin, a few loads one after the other, is most of its time (2048 tokens 19.1 us, with a third of the
+  // tokens 20.4), with longer ones runs wait behind one another (1024 requests of one token 20.3 us, twice the tokens 36).
   // For q as many warps as are resident, or, while the tokens alone do not give them work, several to a token.
   const int per = num_tokens / (kApCtas * sms);
-  p.stretch = per < 1 ? 1 : per < kApStretch ? per : kApStretch;
-  const int stretches = (num_tokens + p.stretch - 1) / p.stretch;
   p.kv_splits = (2 * num_kv_heads + kApWarps - 1) / kApWarps;
+  p.stretch = (int)std::min<int64_t>(std::max<int64_t>((int64_t)num_tokens * p.kv_splits / (2 * sms), 1), kApStretch);
+  const int stretches = (num_tokens + p.stretch - 1) / p.stretch;
   const int kv_ctas = stretches * p.kv_splits;
   // With many tokens q's CTAs come first and leave a third of each SM to the stretches', which wait for their data most of
   // the time, so that the two run side by side (16384 tokens 78 us; q last and on all of the SM 84); with few the
-  // stretches, which take longest, come first (777 tokens 7.1 us, last 8.5).
+  // stretches, which take longest, come first (777 tokens 6.4 us, last 8.0).
   const bool q_first = per >= kApStretch;
   const int q_most = (q_first ? kApCtas - 1 : kApCtas) * sms;
   const int resident = q_most * kApWarps, share = 4;  // heads that are worth a warp
