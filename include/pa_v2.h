@@ -872,7 +872,9 @@ pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, const void* 
  * chunk) write the pages that some token sees out in q_dtype first, exactly, and run pa_v2_tree_attention's kernels
  * over them, where the pages fit: 2^26 elements of K, 2^20 listed pages.  The workspace for such sizes is larger by
  * 270 MB and the tree attention's; calls with a workspace for other sizes, of at least its smaller part, and chains
- * in a window without positions take the other way.
+ * in a window without positions take the other way.  Lists that overlap (an indptr that falls at a request without
+ * tokens) and are together longer than that room, num_indices being shorter, are refused: PA_DEVICE_BAD_TREE, zeros
+ * and -inf for all.
  * PA_EINVAL: sinks without a window.  PA_EUNSUPPORTED: as pa_v2_tree_attention, and batch
  * above 2^20.  The workspace (pa_v2_attention_fp8_workspace's size, 16-byte
  * aligned) needs no initialisation; two calls sharing it must not overlap on

@@ -1240,6 +1240,7 @@ struct F8Wide {
   void* k;
   void* v;
   int64_t max_slots, max_pages;
+  bool last;            // no blocks of few rows follow: the listed pages are fewer, so only lists that overlap pass them
   uint32_t hkv_magic, hkv_shift;
 };
 constexpr int kWideThreads = 256;
@@ -1322,14 +1323,14 @@ __global__ void __launch_bounds__(kWideThreads) pa_v2_fp8_expand_kernel(const F8
     int64_t at = upto[0] - mine[0];
     for (int r = r0; r < r1; ++r) {
       const int32_t qo = p.qo_indptr[r];
-      w.qo_wide[r] = fits ? qo : 0;
+      w.qo_wide[r] = fits || w.last ? qo : 0;  // (not fitting, with empty tables, which are refused)
       w.qo_narrow[r] = fits ? 0 : qo;
       w.indptr[r] = fits ? (int32_t)at : 0;
       at += f8_pages(p, f8_req<kF8MaxRows>(p, r, false), r).pages;
     }
     if (threadIdx.x == 0) {
       const int32_t qo = p.qo_indptr[p.batch];
-      w.qo_wide[p.batch] = fits ? qo : 0;
+      w.qo_wide[p.batch] = fits || w.last ? qo : 0;
       w.qo_narrow[p.batch] = fits ? 0 : qo;
       w.indptr[p.batch] = fits ? (int32_t)total[0] : 0;
     }
@@ -1598,6 +1599,7 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
     w.v = base + l.v;
     w.max_slots = kWideSlots;
     w.max_pages = kWideElements / page_elements;
+    w.last = num_indices <= w.max_slots && num_indices <= w.max_pages;
     const FastDiv fk = FastDiv::make((uint32_t)num_kv_heads);
     w.hkv_magic = fk.magic;
     w.hkv_shift = fk.shift;
@@ -1612,8 +1614,7 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
                         kWideSlots, w.indptr, last_page_len, first_page_offset, batch, w.qo_wide, num_tokens, tree_mask,
                         mask_words, positions, window, sinks, sm_scale, out, lse2_out, base + l.tree, tree_bytes, status,
                         cuda_stream);
-    // the pages fit for sure: nothing is left for the blocks of few rows
-    if (ws != PA_OK || (num_indices <= kWideSlots && num_indices <= w.max_pages)) return ws;
+    if (ws != PA_OK || w.last) return ws;
     p.qo_indptr = w.qo_narrow;
   }
   p.workers = sms * (pick.threads / 32);

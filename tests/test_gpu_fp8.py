@@ -572,6 +572,28 @@ def test_attention_many_rows_of_more_pages_than_fit(ctx):
     _check_attn(c)
 
 
+@pytest.mark.parametrize("ctx,new", [(7900, 100), (7800, 200)])
+def test_attention_overlapping_lists_longer_than_the_room(ctx, new):
+    """One list for two requests, one without tokens between: 500 listed pages of 64 heads, 512 fit, 1000 do not.
+    2 * 100 rows on 3 requests are less than 97 each and need no room, 2 * 200 are more."""
+    c = _attn_case(82, [(ctx, new)], 64, 64, 128, 16, torch.float16)
+    n = len(c["ids"])
+    assert n <= 512 < 2 * n
+    ref = _attn_ref(c) if new == 100 else None
+    c.update(q=torch.cat((c["q"], c["q"])), pos=torch.cat((c["pos"], c["pos"])), indptr=i32([0, n, 0, n]),
+             lpl=c["lpl"].repeat(3), fpo=c["fpo"].repeat(3), qo=i32([0, new, new, 2 * new]))
+    st = status_word()
+    out = torch.full((2 * new, 64, 128), 7.0, dtype=torch.float16, device="cuda")
+    lse = torch.full((2 * new, 64), 7.0, device="cuda")
+    _run_attn(c, status=st, out=out, lse2_out=lse)
+    if ref:
+        assert int(st) == 0
+        _close((out[:new], lse[:new]), ref)
+        _close((out[new:], lse[new:]), ref)
+    else:
+        assert int(st) == pa.DEVICE_BAD_TREE and out.eq(0).all() and lse.eq(-math.inf).all()
+
+
 def test_attention_many_rows_bad_tables_and_graphs():
     def case():
         return _attn_case(91, [(50, 60), (20, 60), (33, 60)], 8, 2, 64, 16, torch.float16)
