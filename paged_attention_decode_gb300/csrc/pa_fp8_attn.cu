@@ -40,13 +40,14 @@
 // HBM), over 1K 13 us: starts (8 us: cold code, tables, pages, tiles, one after the other),
 // joining 2-3, the merge kernel 4.  More warps help while registers allow them (12 at 168
 // for one block of 8 rows: 26 -> 23 us over 32K; the wider blocks need 255); q in registers
-// up to 16 rows, 16 keys at a time for 32 rows (spills made 32 chains 161 us).  Measured and
-// not kept: the same code for a request's geometry called, not inlined (+2 us everywhere);
-// lanes as parts in the joining (equal).
+// up to 16 rows, in shared memory for 24.  Measured and not kept: blocks of 32 rows (spills); the
+// same code for a request's geometry called, not inlined (+2 us everywhere); lanes as parts in
+// the joining (equal).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -68,11 +69,11 @@ constexpr int kF8Tile = 32;       // keys of a unit
 constexpr int kF8Infos = 8;       // requests a warp's ring can have under way, a power of two
 constexpr float kF8Shift = 11.f;  // P is rounded relative to 2^kF8Shift at the row's offset,
 constexpr float kF8Lazy = 4.f;    // which follows the running maximum with a lag of up to kF8Lazy (log2 units)
-constexpr int kF8MaxRows = 32;    // query rows of a block, at most
+constexpr int kF8MaxRows = 24;    // query rows of a block, at most
 constexpr int kMergeWarps = 8;
 constexpr int kMergeFew = 16;     // parts that one warp folds alone
 constexpr int kMergeCtas = 2;     // per SM
-constexpr int kF8PartRows = 256;  // rows of a CTA's runs, at most: 12 warps of 8, 8 of 32
+constexpr int kF8PartRows = 192;  // rows of a CTA's runs, at most: 12 warps of 8, 8 of 24
 constexpr int64_t kF8Spread = 16;  // units of a run from which on heads are taken side by side
 constexpr int64_t kF8MaxUnits = 1ll << 40;  // units of one request, at most
 
@@ -81,7 +82,6 @@ struct F8Cfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kSide = kF8Tile * D;    // bytes of a stage's K, or V
   static constexpr bool kQSmem = NT > 2;       // q's fragments live in shared memory: 16 NT registers are too many
-  static constexpr int kMt = NT > 3 ? 1 : 2;   // 16-key halves of a tile that go through the softmax at once
   // 64 K registers: 168 a thread for 12 warps, 255 for 8
   static constexpr int kWarps = NT == 1 ? 12 : 8;
   static constexpr int kStages = (D == 128 ? 1 : 2) * (kQSmem || kWarps == 12 ? 2 : 3);
@@ -689,192 +689,186 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
     }
     if (!skip) {
       const uint32_t kb = smem_addr(ring + stage * 2 * C::kSide), vb = kb + C::kSide;
-      constexpr int MT = C::kMt;
-#pragma unroll 1
-      for (int pass = 0; pass < 2 / MT; ++pass) {
-        const int key0 = 16 * MT * pass;  // of the tile
-        // ---- S^T
-        float s[MT][NT][4];
+      // ---- S^T
+      float s[2][NT][4];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.f;
+        for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t x[MT][2][4];
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t x[2][2][4];
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(x[i][h][0]), "=r"(x[i][h][1]), "=r"(x[i][h][2]), "=r"(x[i][h][3])
-                           : "r"(kb + side_at<D>(key0 + 16 * i + 8 * h + g, t * (D / 64) + c))
-                           : "memory");
+          for (int h = 0; h < 2; ++h)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[i][h][0]), "=r"(x[i][h][1]), "=r"(x[i][h][2]), "=r"(x[i][h][3])
+                         : "r"(kb + side_at<D>(16 * i + 8 * h + g, t * (D / 64) + c))
+                         : "memory");
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int k = 4 * c + w;
-            uint32_t b[NT][2];
+        for (int w = 0; w < 4; ++w) {
+          const int k = 4 * c + w;
+          uint32_t b[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (C::kQSmem) {
-                const uint2 u = qs[(k * NT + nt) * 32 + lane];
-                b[nt][0] = u.x;
-                b[nt][1] = u.y;
-              } else {
-                b[nt][0] = qb[k][nt][0];
-                b[nt][1] = qb[k][nt][1];
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              const uint32_t a[4] = {codes_lo(x[i][0][w]), codes_lo(x[i][1][w]), codes_hi(x[i][0][w]),
-                                     codes_hi(x[i][1][w])};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) TC<__half>::mma(s[i][nt], a, b[nt][0], b[nt][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if (C::kQSmem) {
+              const uint2 u = qs[(k * NT + nt) * 32 + lane];
+              b[nt][0] = u.x;
+              b[nt][1] = u.y;
+            } else {
+              b[nt][0] = qb[k][nt][0];
+              b[nt][1] = qb[k][nt][1];
             }
           }
-        }
-        // ---- scores in log2 units, softmax
-        float ks[2 * MT];
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) ks[i] = meta[stage].k_scale[key0 + 8 * i + g];
-        // (each step for all columns before the next: 2 warps a scheduler do not hide one column's chain of shuffles)
-        float mt[NT][2];
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a[4] = {codes_lo(x[i][0][w]), codes_lo(x[i][1][w]), codes_hi(x[i][0][w]),
+                                   codes_hi(x[i][1][w])};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) TC<__half>::mma(s[i][nt], a, b[nt][0], b[nt][1]);
+          }
+        }
+      }
+      // ---- scores in log2 units, softmax
+      float ks[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ks[i] = meta[stage].k_scale[8 * i + g];
+      // (each step for all columns before the next: 2 warps a scheduler do not hide one column's chain of shuffles)
+      float mt[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+        if (!clear) {
+          see[0] = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t);
+          see[1] = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t + 1);
+        }
+        mt[nt][0] = mt[nt][1] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // token 16 i + 8 (k >> 1) + g, column 2 t + (k & 1)
+            const int q4 = 2 * i + (k >> 1);
+            float y = s[i][nt][k] * (ks[q4] * qf[nt][k & 1]);
+            if (!clear) y = see[k & 1] >> (8 * q4 + g) & 1u ? y : -INFINITY;
+            s[i][nt][k] = y;
+            mt[nt][k & 1] = fmaxf(mt[nt][k & 1], y);
+          }
+      }
+#pragma unroll
+      for (int x = 4; x <= 16; x <<= 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-          if (!clear) {
-            see[0] = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t) >> key0;
-            see[1] = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t + 1) >> key0;
-          }
-          mt[nt][0] = mt[nt][1] = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {  // token key0 + 16 i + 8 (k >> 1) + g, column 2 t + (k & 1)
-              const int q4 = 2 * i + (k >> 1);
-              float y = s[i][nt][k] * (ks[q4] * qf[nt][k & 1]);
-              if (!clear) y = see[k & 1] >> (8 * q4 + g) & 1u ? y : -INFINITY;
-              s[i][nt][k] = y;
-              mt[nt][k & 1] = fmaxf(mt[nt][k & 1], y);
-            }
+          mt[nt][0] = fmaxf(mt[nt][0], __shfl_xor_sync(0xffffffffu, mt[nt][0], x));
+          mt[nt][1] = fmaxf(mt[nt][1], __shfl_xor_sync(0xffffffffu, mt[nt][1], x));
         }
+      bool grow = false;
 #pragma unroll
-        for (int x = 4; x <= 16; x <<= 1)
+      for (int nt = 0; nt < NT; ++nt)
+        grow |= mt[nt][0] > m[nt][0] + kF8Lazy || mt[nt][1] > m[nt][1] + kF8Lazy;
+      if (__any_sync(0xffffffffu, grow)) {  // m = -inf at first: any finite maximum
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mt[nt][0] = fmaxf(mt[nt][0], __shfl_xor_sync(0xffffffffu, mt[nt][0], x));
-            mt[nt][1] = fmaxf(mt[nt][1], __shfl_xor_sync(0xffffffffu, mt[nt][1], x));
+        for (int nt = 0; nt < NT; ++nt) {
+          float scale[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const bool need = mt[nt][k] > m[nt][k] + kF8Lazy;
+            scale[k] = !need ? 1.f : m[nt][k] == -INFINITY ? 0.f : fast_exp2(m[nt][k] - mt[nt][k]);
+            if (need) m[nt][k] = mt[nt][k];
+            l[nt][k] *= scale[k];
           }
-        bool grow = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          grow |= mt[nt][0] > m[nt][0] + kF8Lazy || mt[nt][1] > m[nt][1] + kF8Lazy;
-        if (__any_sync(0xffffffffu, grow)) {  // m = -inf at first: any finite maximum
+          for (int c = 0; c < KS; ++c) {
+            o[c][nt][0] *= scale[0];
+            o[c][nt][1] *= scale[1];
+            o[c][nt][2] *= scale[0];
+            o[c][nt][3] *= scale[1];
+          }
+        }
+      }
+      uint32_t pb[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float off[2] = {(m[nt][0] == -INFINITY ? 0.f : m[nt][0]) - kF8Shift,
+                              (m[nt][1] == -INFINITY ? 0.f : m[nt][1]) - kF8Shift};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float e0 = fast_exp2(s[i][nt][2 * h] - off[0]), e1 = fast_exp2(s[i][nt][2 * h + 1] - off[1]);
+            l[nt][0] += e0;
+            l[nt][1] += e1;
+            pb[nt][2 * i + h] = TC<__half>::pack(e0, e1);
+          }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pb[nt][i] = transposed(pb[nt][i]);
+      // ---- O^T += V^T P^T, 16 dims at a time
+      uint32_t vs[4];  // tokens 8 i + 2 t, + 1
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        vs[i] = *reinterpret_cast<const uint32_t*>(&meta[stage].v_scale[8 * i + 2 * t]);
+      // what a row does not see must not meet its zero weight as a NaN: rows that nobody sees become zeros, and NaN
+      // codes of the others zeros that are put back below for the rows that see them
+      uint32_t vm[4] = {}, taint = 0;
+      if (!clear) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t u = some >> (8 * i + 2 * t);
+          vm[i] = (u & 1u ? 0x00ff00ffu : 0u) | (u & 2u ? 0xff00ff00u : 0u);
+        }
+      }
+      auto values = [&](bool safe) {
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+          uint32_t x[4];
+          ldsm_x4_trans(x, vb + side_at<D>(lane, c));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = __byte_perm(x[i], 0, 0x3120);
+            if (safe) {
+              x[i] &= vm[i];
+              const uint32_t nan = __vcmpeq4(x[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              taint |= nan;
+              x[i] &= ~nan;
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int k = 2 * h;
+            const uint32_t a[4] = {mul_f16(codes_lo(x[2 * h]), vs[k]), mul_f16(codes_hi(x[2 * h]), vs[k]),
+                                   mul_f16(codes_lo(x[2 * h + 1]), vs[k + 1]),
+                                   mul_f16(codes_hi(x[2 * h + 1]), vs[k + 1])};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) TC<__half>::mma(o[c][nt], a, pb[nt][k], pb[nt][k + 1]);
+          }
+        }
+      };
+      if (clear) {
+        values(false);
+      } else {
+        values(true);
+        if (__any_sync(0xffffffffu, taint != 0)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float scale[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const bool need = mt[nt][k] > m[nt][k] + kF8Lazy;
-              scale[k] = !need ? 1.f : m[nt][k] == -INFINITY ? 0.f : fast_exp2(m[nt][k] - mt[nt][k]);
-              if (need) m[nt][k] = mt[nt][k];
-              l[nt][k] *= scale[k];
-            }
+            const uint32_t see0 = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t);
+            const uint32_t see1 = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t + 1);
 #pragma unroll
             for (int c = 0; c < KS; ++c) {
-              o[c][nt][0] *= scale[0];
-              o[c][nt][1] *= scale[1];
-              o[c][nt][2] *= scale[0];
-              o[c][nt][3] *= scale[1];
-            }
-          }
-        }
-        uint32_t pb[NT][2 * MT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float off[2] = {(m[nt][0] == -INFINITY ? 0.f : m[nt][0]) - kF8Shift,
-                                (m[nt][1] == -INFINITY ? 0.f : m[nt][1]) - kF8Shift};
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float e0 = fast_exp2(s[i][nt][2 * h] - off[0]), e1 = fast_exp2(s[i][nt][2 * h + 1] - off[1]);
-              l[nt][0] += e0;
-              l[nt][1] += e1;
-              pb[nt][2 * i + h] = TC<__half>::pack(e0, e1);
-            }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2 * MT; ++i) pb[nt][i] = transposed(pb[nt][i]);
-        // ---- O^T += V^T P^T, 32 / MT dims at a time
-        uint32_t vs[2 * MT];  // tokens key0 + 8 i + 2 t, + 1
-#pragma unroll
-        for (int i = 0; i < 2 * MT; ++i)
-          vs[i] = *reinterpret_cast<const uint32_t*>(&meta[stage].v_scale[key0 + 8 * i + 2 * t]);
-        // what a row does not see must not meet its zero weight as a NaN: rows that nobody sees become zeros, and NaN
-        // codes of the others zeros that are put back below for the rows that see them
-        uint32_t vm[2 * MT] = {}, taint = 0;
-        if (!clear) {
-#pragma unroll
-          for (int i = 0; i < 2 * MT; ++i) {
-            const uint32_t u = some >> (key0 + 8 * i + 2 * t);
-            vm[i] = (u & 1u ? 0x00ff00ffu : 0u) | (u & 2u ? 0xff00ff00u : 0u);
-          }
-        }
-        auto values = [&](bool safe) {
-#pragma unroll
-          for (int cc = 0; cc < KS * MT / 2; ++cc) {
-            uint32_t x[4];  // 16 dims of 32 keys, or 32 dims of 16 keys
-            if (MT == 2) ldsm_x4_trans(x, vb + side_at<D>(lane, cc));
-            else ldsm_x4_trans(x, vb + side_at<D>(key0 + (lane & 15), 2 * cc + (lane >> 4)));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[i] = __byte_perm(x[i], 0, 0x3120);
-              if (safe) {
-                x[i] &= vm[i % (2 * MT)];
-                const uint32_t nan = __vcmpeq4(x[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                taint |= nan;
-                x[i] &= ~nan;
-              }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int c = MT == 2 ? cc : 2 * cc + h, k = MT == 2 ? 2 * h : 0;
-              const uint32_t a[4] = {mul_f16(codes_lo(x[2 * h]), vs[k]), mul_f16(codes_hi(x[2 * h]), vs[k]),
-                                     mul_f16(codes_lo(x[2 * h + 1]), vs[k + 1]),
-                                     mul_f16(codes_hi(x[2 * h + 1]), vs[k + 1])};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) TC<__half>::mma(o[c][nt], a, pb[nt][k], pb[nt][k + 1]);
-            }
-          }
-        };
-        if (clear) {
-          values(false);
-        } else {
-          values(true);
-          if (__any_sync(0xffffffffu, taint != 0)) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint32_t see0 = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t);
-              const uint32_t see1 = __shfl_sync(0xffffffffu, mine_bits, 8 * nt + 2 * t + 1);
-#pragma unroll
-              for (int c = 0; c < KS; ++c) {
 #pragma unroll 1
-                for (int k = key0; k < key0 + 16 * MT; ++k) {
-                  uint16_t pair;  // dims 16 c + 2 g, + 1 of token k
-                  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(pair) : "r"(vb + side_at<D>(k, c) + 2 * g) : "memory");
-                  const bool n0 = (pair & 0x7f) == 0x7f, n1 = (pair >> 8 & 0x7f) == 0x7f;
-                  if (see0 >> k & 1u) {
-                    if (n0) o[c][nt][0] = NAN;
-                    if (n1) o[c][nt][2] = NAN;
-                  }
-                  if (see1 >> k & 1u) {
-                    if (n0) o[c][nt][1] = NAN;
-                    if (n1) o[c][nt][3] = NAN;
-                  }
+              for (int k = 0; k < kF8Tile; ++k) {
+                uint16_t pair;  // dims 16 c + 2 g, + 1 of token k
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(pair) : "r"(vb + side_at<D>(k, c) + 2 * g) : "memory");
+                const bool n0 = (pair & 0x7f) == 0x7f, n1 = (pair >> 8 & 0x7f) == 0x7f;
+                if (see0 >> k & 1u) {
+                  if (n0) o[c][nt][0] = NAN;
+                  if (n1) o[c][nt][2] = NAN;
+                }
+                if (see1 >> k & 1u) {
+                  if (n0) o[c][nt][1] = NAN;
+                  if (n1) o[c][nt][3] = NAN;
                 }
               }
             }
@@ -1229,7 +1223,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, kMergeCtas) pa_v2_fp8_merge_
 // A prompt's chunk meets each key with hundreds of query rows, in blocks of kRows: the tensor cores bound it, and the warp's
 // ones at that.  So the pages that some token sees are written out once in q's 16-bit type (exactly: an element is a
 // binary16 number of 4 significant bits, and a bfloat16 one) and the tree attention runs over them, tcgen05 products and
-// all: 4 x 256 tokens over 8K take 209 us (expansion 50, attention 153) where blocks of 32 rows took 815.  Around the
+// all: 4 x 256 tokens over 8K take 209 us (expansion 50, attention 153) where blocks of few rows took 815.  Around the
 // border, 128 rows over 1K and 8K tokens: one request 26 and 43 us (blocks: 23 and 49), eight 50 and 164 (51 and 222);
 // 68 rows: 25 and 41 (21 and 41), 48 and 160 (44 and 171).
 struct F8Wide {
@@ -1403,13 +1397,17 @@ F8Pick pick_f8(bool tma) {
   return {tma ? pa_v2_attention_fp8_kernel<D, NT, true> : pa_v2_attention_fp8_kernel<D, NT, false>, C::kRows,
           C::kOffMeta + (int)(C::kWarps * C::kStages * sizeof(F8Meta)) + 1024, 32 * C::kWarps};
 }
+// Rows of a block.  One of 24 rows takes 1.2 times one of 16 where a warp meets many (32 requests over 8K: 20 rows 160
+// us, as two blocks 247; 64 rows 440 and 474; but 32 rows 300 and 250), and where it meets few, the units one after the
+// other are what a call takes, and narrow blocks make more and shorter ones (20 rows over 1K 17.7 us and 14.2, 64 rows of 8
+// requests over 1K 35 and 31; 32 requests over 512, just below the limit, 20 rows 34 and 36, 64 rows 64 and 57).
+// Blocks of 32 rows spill (32 rows over 8K 254 us, 64 rows 479).
 template <int D>
-F8Pick pick_f8(int64_t rows, bool tma) {
-  return rows <= 8    ? pick_f8<D, 1>(tma)
-         : rows <= 16 ? pick_f8<D, 2>(tma)
-         : rows <= 24 ? pick_f8<D, 3>(tma)
-                      : pick_f8<D, 4>(tma);
+F8Pick pick_f8(int64_t rows, bool few, bool tma) {
+  if (rows <= 8) return pick_f8<D, 1>(tma);
+  return rows <= 16 || few || 5 * ((rows + 15) / 16) <= 6 * ((rows + 23) / 24) ? pick_f8<D, 2>(tma) : pick_f8<D, 3>(tma);
 }
+constexpr int64_t kF8Few = 4;  // tiles of keys per warp, up to which few
 
 bool f8_aligned(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }
 
@@ -1574,7 +1572,11 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
   p.scale_log2 = scale_log2;
   p.window = window;
   p.sinks = sinks;
-  const F8Pick pick = head_dim == 64 ? pick_f8<64>(rows, tma) : pick_f8<128>(rows, tma);
+  // the keys that are listed, or that windows show, at most
+  int64_t keys = std::min(num_indices, (int64_t)1 << 40) * page_size;
+  if (window > 0) keys = std::min(keys, ((int64_t)window + sinks) * batch + num_tokens);
+  const bool few = keys <= kF8Few * kF8Tile * 8 * sms / num_kv_heads;
+  const F8Pick pick = head_dim == 64 ? pick_f8<64>(rows, few, tma) : pick_f8<128>(rows, few, tma);
   if (!prepare_kernel(reinterpret_cast<const void*>(pick.fn), pick.smem)) return PA_ECUDA;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t rc = cudaSuccess;
