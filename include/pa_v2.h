@@ -870,8 +870,8 @@ pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, const void* 
  * P = exp(s) enters the second product rounded to f16 (to q_dtype where a request has many query rows); scores,
  * statistics and sums are f32.  Calls of more than 96 query rows per KV head and request on average (a prompt's
  * chunk) write the pages that some token sees out in q_dtype first, exactly, and run pa_v2_tree_attention's kernels
- * over them, where the pages fit: 2^26 elements of K, 2^20 listed pages.  The workspace for such sizes is larger by
- * 270 MB and the tree attention's; calls with a workspace for other sizes, of at least its smaller part, and chains
+ * over them, where the pages fit: 2^28 elements of K, 2^20 listed pages.  The workspace for such sizes is larger by
+ * 1.08 GB and the tree attention's; calls with a workspace for other sizes, of at least its smaller part, and chains
  * in a window without positions take the other way.  Lists that overlap (an indptr that falls at a request without
  * tokens) and are together longer than that room, num_indices being shorter, are refused: PA_DEVICE_BAD_TREE, zeros
  * and -inf for all.

@@ -1224,8 +1224,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps, kMergeCtas) pa_v2_fp8_merge_
 // ones at that.  So the pages that some token sees are written out once in q's 16-bit type (exactly: an element is a
 // binary16 number of 4 significant bits, and a bfloat16 one) and the tree attention runs over them, tcgen05 products and
 // all: 4 x 256 tokens over 8K take 209 us (expansion 50, attention 153) where blocks of few rows took 815.  Around the
-// border, 128 rows over 1K and 8K tokens: one request 26 and 43 us (blocks: 23 and 49), eight 50 and 164 (51 and 222);
-// 68 rows: 25 and 41 (21 and 41), 48 and 160 (44 and 171).
+// border, 100 rows over 1K, 8K and 32K tokens: 26, 44 and 95 us (blocks 19, 39 and 114), 32 requests over 1K 114 (132);
+// 68 rows 26, 42 and 93 (19, 33 and 79) and 110 (90).
 struct F8Wide {
   int32_t* qo_wide;     // qo_indptr for the tree attention, all zero when the pages do not fit
   int32_t* qo_narrow;   // and for the blocks of few rows, all zero when they do
@@ -1239,7 +1239,7 @@ struct F8Wide {
 };
 constexpr int kWideThreads = 256;
 constexpr int kWideChunks = 256;              // 16-byte pieces of a side that a warp takes at once
-constexpr int64_t kWideElements = 1ll << 26;  // of k, and of v
+constexpr int64_t kWideElements = 1ll << 28;  // of k, and of v: 262144 tokens of 8 heads of 128
 constexpr int64_t kWideSlots = 1ll << 20;
 constexpr int64_t kWideRows = 96;             // query rows of a KV head: more of them take this way
 

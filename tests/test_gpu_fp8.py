@@ -564,32 +564,58 @@ def test_attention_many_rows_nothing_hidden_and_nan_where_it_is_seen(page_size, 
     assert nan.any() and torch.equal(out.isnan(), nan) and ((out - ro).abs() <= to)[~nan].all()
 
 
-@pytest.mark.parametrize("ctx", [7000, 8300])
-def test_attention_many_rows_of_more_pages_than_fit(ctx):
-    """64 KV heads: 512 pages of 16 tokens fit the workspace; a table with room for more leaves it to the device."""
-    c = _attn_case(81, [(ctx, 100)], 64, 64, 128, 16, torch.float16)
-    c["ids"] = torch.cat((c["ids"], torch.zeros(600, dtype=I32)))
-    _check_attn(c)
+def _long_lists(slots, new, seed=82):
+    """One request of 64 KV heads whose list repeats 41 pages; 2048 pages of 16 tokens fit the workspace."""
+    c = _attn_case(seed, [(16 * 41 - new, new)], 64, 64, 128, 16, torch.float16)
+    ids = c["ids"].repeat(-(-slots // 41))[-slots:]      # (the last ones as they were)
+    first = 16 * slots - new
+    rows = (ids.long()[:, None] * 16 + torch.arange(16)).flatten().tolist()
+    c.update(ids=ids, indptr=i32([0, slots]), seen=[rows[:first + i + 1] for i in range(new)],
+             pos=torch.arange(first, first + new, dtype=I32))
+    return c
 
 
-@pytest.mark.parametrize("ctx,new", [(7900, 100), (7800, 200)])
-def test_attention_overlapping_lists_longer_than_the_room(ctx, new):
-    """One list for two requests, one without tokens between: 500 listed pages of 64 heads, 512 fit, 1000 do not.
-    2 * 100 rows on 3 requests are less than 97 each and need no room, 2 * 200 are more."""
-    c = _attn_case(82, [(ctx, new)], 64, 64, 128, 16, torch.float16)
-    n = len(c["ids"])
-    assert n <= 512 < 2 * n
-    ref = _attn_ref(c) if new == 100 else None
-    c.update(q=torch.cat((c["q"], c["q"])), pos=torch.cat((c["pos"], c["pos"])), indptr=i32([0, n, 0, n]),
+def _some_of(c):
+    """The definition's results of some tokens and heads, and what picks them."""
+    some, heads = [0, 57, 99], slice(None, None, 31)
+    part = dict(c, q=c["q"][some][:, heads], seen=[c["seen"][i] for i in some],
+                **{n: c[n][:, :, heads] for n in ("kp", "vp")}, **{n: c[n][:, heads] for n in ("ke", "ve")})
+    return _attn_ref(part), lambda got: [x[some][:, heads] for x in got]
+
+
+@pytest.mark.parametrize("slots,padding", [(1500, 0), (1900, 300), (2048, 1), (2049, 0), (2300, 300)])
+def test_attention_many_rows_of_lists_around_the_room(slots, padding):
+    """Lists that the host knows to fit, that the device finds to fit, and that do not: the blocks of few rows take
+    those, as they do all calls with a workspace without that room."""
+    c = _long_lists(slots, 100)
+    c["ids"] = torch.cat((c["ids"], torch.zeros(padding, dtype=I32)))
+    st = status_word()
+    out, lse = _run_attn(c, status=st)
+    assert int(st) == 0
+    small = _run_attn(c, workspace=pa.attention_fp8_workspace(1, 1, 64, 64, 128))
+    if slots > 2048:
+        assert torch.equal(out, small[0]) and torch.equal(lse, small[1])
+    ref, pick = _some_of(c)
+    for got in ((out, lse), small):
+        _close(pick(got), ref)
+
+
+@pytest.mark.parametrize("slots,new", [(1100, 100), (1100, 200)])
+def test_attention_overlapping_lists_longer_than_the_room(slots, new):
+    """One list for two requests, one without tokens between.  2 * 100 rows on 3 requests are less than 97 each and
+    need no room, 2 * 200 are more."""
+    c = _long_lists(slots, new)
+    ref, pick = _some_of(c)
+    c.update(q=torch.cat((c["q"], c["q"])), pos=torch.cat((c["pos"], c["pos"])), indptr=i32([0, slots, 0, slots]),
              lpl=c["lpl"].repeat(3), fpo=c["fpo"].repeat(3), qo=i32([0, new, new, 2 * new]))
     st = status_word()
     out = torch.full((2 * new, 64, 128), 7.0, dtype=torch.float16, device="cuda")
     lse = torch.full((2 * new, 64), 7.0, device="cuda")
     _run_attn(c, status=st, out=out, lse2_out=lse)
-    if ref:
+    if new == 100:
         assert int(st) == 0
-        _close((out[:new], lse[:new]), ref)
-        _close((out[new:], lse[new:]), ref)
+        for half in (slice(0, new), slice(new, None)):
+            _close(pick((out[half], lse[half])), ref)
     else:
         assert int(st) == pa.DEVICE_BAD_TREE and out.eq(0).all() and lse.eq(-math.inf).all()
 
