@@ -1223,9 +1223,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps, kMergeCtas) pa_v2_fp8_merge_
 // A prompt's chunk meets each key with hundreds of query rows, in blocks of kRows: the tensor cores bound it, and the warp's
 // ones at that.  So the pages that some token sees are written out once in q's 16-bit type (exactly: an element is a
 // binary16 number of 4 significant bits, and a bfloat16 one) and the tree attention runs over them, tcgen05 products and
-// all: 4 x 256 tokens over 8K take 209 us (expansion 50, attention 153) where blocks of few rows took 815.  Around the
-// border, 100 rows over 1K, 8K and 32K tokens: 26, 44 and 95 us (blocks 19, 39 and 114), 32 requests over 1K 114 (132);
-// 68 rows 26, 42 and 93 (19, 33 and 79) and 110 (90).
+// all: 4 x 256 tokens over 8K take 197 us (expansion 38, attention 153) where blocks of few rows took 815.  Around the
+// border, 100 rows over 1K, 8K and 32K tokens: 24, 40 and 87 us (blocks 19, 39 and 114), 32 requests over 1K 106 (132);
+// 68 rows 24, 39 and 83 (19, 33 and 79) and 101 (90).
 struct F8Wide {
   int32_t* qo_wide;     // qo_indptr for the tree attention, all zero when the pages do not fit
   int32_t* qo_narrow;   // and for the blocks of few rows, all zero when they do
@@ -1238,7 +1238,8 @@ struct F8Wide {
   uint32_t hkv_magic, hkv_shift;
 };
 constexpr int kWideThreads = 256;
-constexpr int kWideChunks = 256;              // 16-byte pieces of a side that a warp takes at once
+constexpr int kWideCtas = 6;                  // per SM
+constexpr int kWideChunks = 512;              // 8-byte pieces of a side that a warp takes at once
 constexpr int64_t kWideElements = 1ll << 28;  // of k, and of v: 262144 tokens of 8 heads of 128
 constexpr int64_t kWideSlots = 1ll << 20;
 constexpr int64_t kWideRows = 96;             // query rows of a KV head: more of them take this way
@@ -1254,27 +1255,27 @@ __device__ __forceinline__ F8Pages f8_pages(const F8Params& p, const F8Req& g, i
           g.win0 / p.page_size};
 }
 
-// 16 codes times 2^e as T.
+// 8 codes times 2^e as T: a lane's 16 bytes, so that a warp writes whole lines (16 codes a lane, 32 bytes in two stores,
+// 209 us for 4 x 256 tokens over 8K and 287 for 25 over 128K, so 197 and 237).
 template <typename T>
-__device__ __forceinline__ void widen(const uint4& c, int e, uint4 (&out)[2]) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  uint32_t y[8];
+__device__ __forceinline__ uint4 widen(const uint2& c, int e) {
+  const uint32_t w[2] = {c.x, c.y};
+  uint32_t y[4];
   const float f = power_of_two(min(max(e, PA_V2_FP8_EXP_MIN), PA_V2_FP8_EXP_MAX));
   const __half2 h = __float2half2_rn(f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     y[2 * i] = mul_f16(codes_lo(w[i]), *reinterpret_cast<const uint32_t*>(&h));
     y[2 * i + 1] = mul_f16(codes_hi(w[i]), *reinterpret_cast<const uint32_t*>(&h));
   }
   if (std::is_same<T, __nv_bfloat16>::value) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
       y[i] = TC<__nv_bfloat16>::pack(x.x, x.y);
     }
   }
-  out[0] = make_uint4(y[0], y[1], y[2], y[3]);
-  out[1] = make_uint4(y[4], y[5], y[6], y[7]);
+  return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
 template <typename T, int D>
@@ -1332,7 +1333,7 @@ __global__ void __launch_bounds__(kWideThreads) pa_v2_fp8_expand_kernel(const F8
   if (!fits) return;
   // a run of slots' parts of 4096 elements for every warp (whole slots left most warps of 2K slots without one: 85 us)
   const int64_t page_elements = (int64_t)p.page_size * p.hkv * D;
-  const int chunks = (int)(page_elements / 16), parts = (chunks + kWideChunks - 1) / kWideChunks;
+  const int chunks = (int)(page_elements / 8), parts = (chunks + kWideChunks - 1) / kWideChunks;
   const int64_t workers = (int64_t)gridDim.x * W, run = div_units(total[0] * parts + workers - 1, workers);
   const int64_t begin = ((int64_t)blockIdx.x * W + warp) * run, behind = min(begin + run, total[0] * parts);
   if (begin >= behind) return;
@@ -1363,24 +1364,18 @@ __global__ void __launch_bounds__(kWideThreads) pa_v2_fp8_expand_kernel(const F8
     const int64_t id = page0 + (s < n.a ? s : s - max(n.a, n.b) + n.a);
     if (lane == 0 && c0 == 0) w.table[slot] = copied ? (int32_t)id : -1;
     if (!copied) continue;
-    const uint4* k = reinterpret_cast<const uint4*>(p.k_pool + page * page_elements);
-    const uint4* v = reinterpret_cast<const uint4*>(p.v_pool + page * page_elements);
+    const uint2* k = reinterpret_cast<const uint2*>(p.k_pool + page * page_elements);
+    const uint2* v = reinterpret_cast<const uint2*>(p.v_pool + page * page_elements);
     uint4* ko = reinterpret_cast<uint4*>(static_cast<T*>(w.k) + id * page_elements);
     uint4* vo = reinterpret_cast<uint4*>(static_cast<T*>(w.v) + id * page_elements);
     const int8_t* ke = p.k_exp + (int64_t)page * p.hkv;
     const int8_t* ve = p.v_exp + (int64_t)page * p.hkv;
 #pragma unroll 4
     for (int c = c0 + lane; c < c1; c += 32) {
-      const uint32_t row = (uint32_t)c / (D / 16);  // of the page's rows and heads
+      const uint32_t row = (uint32_t)c / (D / 8);  // of the page's rows and heads
       const uint32_t head = row - fast_div(row, w.hkv_magic, w.hkv_shift) * p.hkv;
-      const uint4 x = __ldg(k + c), y = __ldg(v + c);
-      uint4 a[2], b[2];
-      widen<T>(x, __ldg(ke + head), a);
-      widen<T>(y, __ldg(ve + head), b);
-      ko[2 * c] = a[0];
-      ko[2 * c + 1] = a[1];
-      vo[2 * c] = b[0];
-      vo[2 * c + 1] = b[1];
+      ko[c] = widen<T>(__ldg(k + c), __ldg(ke + head));
+      vo[c] = widen<T>(__ldg(v + c), __ldg(ve + head));
     }
   }
 }
@@ -1607,7 +1602,7 @@ extern "C" pa_status pa_v2_attention_fp8(const void* q, int32_t q_dtype, const v
     w.hkv_shift = fk.shift;
     auto expand = p.q_bf16 ? (head_dim == 64 ? pa_v2_fp8_expand_kernel<__nv_bfloat16, 64> : pa_v2_fp8_expand_kernel<__nv_bfloat16, 128>)
                            : (head_dim == 64 ? pa_v2_fp8_expand_kernel<__half, 64> : pa_v2_fp8_expand_kernel<__half, 128>);
-    rc = launch_dependent(expand, dim3(sms * 6), dim3(kWideThreads), 0, stream, p, w);
+    rc = launch_dependent(expand, dim3(sms * kWideCtas), dim3(kWideThreads), 0, stream, p, w);
     if (rc != cudaSuccess) {
       cudaGetLastError();
       return PA_ECUDA;
