@@ -520,6 +520,54 @@ def test_attention_nan_reaches_the_rows_that_see_it_and_no_other(page_size, hq, 
         assert lse[t, :hq // 2].isnan().all() == (hit[0] in rows)
 
 
+# -- blocks of 24 rows: 33 to 72 query rows per KV head (or 17 to 24) where a warp meets many keys, or a list could hold them
+
+def _listed_more(c, hkv, page_size):
+    """The same with a longer index array: more than four tiles of 32 keys for each of eight warps of up to 160 SMs."""
+    pad = 4 * 32 * 8 * 160 // hkv // page_size + 1
+    return dict(c, ids=torch.cat((c["ids"], torch.zeros(pad, dtype=I32))))
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("page_size,D", [(16, 128), (5, 64), (64, 64), (1, 128), (7, 128)])
+@pytest.mark.parametrize("reqs", [[(517, 9), (3, 10), (77, 15), (0, 0), (33, 16)], [(900, 5)], [(40, 14), (0, 13)]])
+def test_attention_blocks_of_24_rows(reqs, page_size, D, tree):
+    rng = random.Random(D)
+    trees = [R.random_tree(rng, n) for _, n in reqs] if tree else None
+    c = _attn_case(21, reqs, 8, 2, D, page_size, torch.bfloat16 if tree else torch.float16, trees=trees)
+    _check_attn(_listed_more(c, 2, page_size))
+
+
+@pytest.mark.parametrize("page_size,D", [(16, 64), (5, 64), (16, 128)])
+@pytest.mark.parametrize("window,sinks,tree", [(200, 5, False), (210, 0, False), (190, 20, True)])
+def test_attention_blocks_of_24_rows_under_windows(window, sinks, tree, page_size, D):
+    rng = random.Random(window)
+    reqs = [(rng.choice([0, 3, 190, 200, 333, 700]), rng.choice([1, 5, 9])) for _ in range(30)]
+    reqs[3], reqs[7] = (205, 5), (700, 6)
+    trees = [R.random_tree(rng, n, 0.3) for _, n in reqs] if tree else None
+    group = max(g for g in (4, 5, 6) if 17 <= -(-sum(n for _, n in reqs) // 30) * g <= 24)
+    c = _attn_case(22, reqs, 32 * group, 32, D, page_size, torch.float16, window, sinks, trees=trees, give_back=True)
+    _check_attn(_listed_more(c, 32, page_size))
+
+
+@pytest.mark.parametrize("page_size", [16, 5])
+def test_attention_blocks_of_24_rows_nan_only_where_it_is_seen(page_size):
+    rng = random.Random(3)
+    reqs = [(100, 12), (40, 11)]
+    c = _attn_case(23, reqs, 8, 2, 128, page_size, torch.bfloat16, trees=[R.random_tree(rng, n, 0.3) for _, n in reqs])
+    hit = sorted({rows[k] for rows in c["seen"] for k in (0, len(rows) // 2, -1)})[1:]  # (in new tokens that some see)
+    shown = set.intersection(*map(set, c["seen"][:12])) | set.intersection(*map(set, c["seen"][12:]))
+    hit = [row for row in hit if row not in shown]
+    for j, row in enumerate(hit):
+        c["vp"].view(torch.uint8).flatten(0, 1)[row, j % 2, (7 * j) % 128] = 0x7f if j % 3 else 0xff
+    out = _run_attn(_listed_more(c, 2, page_size))[0].cpu().double()
+    flat = c["vp"].float().isnan().flatten(0, 1)
+    nan = torch.stack([flat[rows].any(0).repeat_interleave(4, 0) for rows in c["seen"]])
+    assert nan.any() and not nan.all() and torch.equal(out.isnan(), nan)
+    ro, _, to, _ = _attn_ref(dict(c, vp=c["vp"].float().nan_to_num(0.0).to(E4M3)))
+    assert ((out - ro).abs() <= to)[~nan].all()
+
+
 # -- more than 96 query rows per KV head: pages written out in q's type, the tree attention over them
 
 MANY = [([(300, 60)], 8, 2, 0, 0), ([(0, 130)], 4, 2, 0, 0), ([(500, 70), (33, 50), (7, 0), (0, 61)], 8, 2, 0, 0),
