@@ -520,6 +520,27 @@ def test_attention_nan_reaches_the_rows_that_see_it_and_no_other(page_size, hq, 
         assert lse[t, :hq // 2].isnan().all() == (hit[0] in rows)
 
 
+@pytest.mark.parametrize("page_size", [16, 5])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (30, 2)])
+@pytest.mark.parametrize("hq,n", [(8, 1), (8, 4), (8, 12), (4, 40), (8, 60)])
+def test_attention_a_nan_key_reaches_all_of_the_rows_that_see_it_and_nothing_else(page_size, window, sinks, hq, n):
+    """Every element of the rows that see it, and not one of the others, whose results are those without it."""
+    rng = random.Random(n)
+    reqs = [(100, n), (40, n)]
+    c = _attn_case(14, reqs, hq, 2, 128, page_size, torch.bfloat16, window, sinks,
+                   trees=[R.random_tree(rng, n, 0.3) for _ in reqs])
+    ro, rl, to, tl = _attn_ref(c)
+    for hit in sorted({rows[k] for rows in c["seen"][::max(1, n // 3)] for k in (0, len(rows) // 2, -1)}):
+        d = dict(c, kp=c["kp"].clone())
+        d["kp"].view(torch.uint8).flatten(0, 1)[hit, 1, 77] = 0xff
+        out, lse = (x.cpu().double() for x in _run_attn(d))
+        nan = torch.zeros(ro.shape, dtype=torch.bool)
+        for t, rows in enumerate(c["seen"]):
+            nan[t, hq // 2:] = hit in rows
+        assert nan.any() and not nan.all() and torch.equal(out.isnan(), nan) and torch.equal(lse.isnan(), nan[..., 0])
+        assert ((out - ro).abs() <= to)[~nan].all() and ((lse - rl).abs() <= tl)[~nan[..., 0]].all()
+
+
 # -- blocks of 24 rows: 33 to 72 query rows per KV head (or 17 to 24) where a warp meets many keys, or a list could hold them
 
 def _listed_more(c, hkv, page_size):
