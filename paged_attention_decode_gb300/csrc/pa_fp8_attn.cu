@@ -8,9 +8,10 @@
 // in registers (exactly), q is f16 times a power of two of its row (exact but for
 // elements 2^-24 of the row's largest and below), and the exponents, -15 .. 7, keep every
 // 2^ev vc a binary16 number: both products of m16n8k16 have exact operands but for P,
-// which is rounded to f16 once, 2^kF8Shift at the row's offset so that weights down to
-// 2^-35 of the largest survive (2^-11 each, where the f16 or bf16 output rounds by 2^-11 or
-// 2^-8 anyhow); scores, statistics and sums are f32.
+// which is rounded to f16 once, 2^kF8Shift at the row's offset: by 2^-11 of a weight down to
+// 2^-25 of the offset's, where f16 is normal (the f16 or bf16 output rounds by 2^-11 or 2^-8
+// anyhow), and by 2^-36 of the offset's below, 2^20 keys of it together 2^-16 of the largest
+// value; scores, statistics and sums, of weights before that rounding, are f32.
 //
 // Work.  The query rows of a KV head (n * G pairs of new token and head) are taken in
 // blocks of 8 NT; one block against one tile of 32 pool rows (page order) is a unit.  The

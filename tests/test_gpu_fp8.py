@@ -778,6 +778,31 @@ def test_attention_small_weights_still_count():
     assert 0.003 < float(out[0, 0, 0]) < 0.005
 
 
+@pytest.mark.parametrize("weight", [24, 28, 31, 34])
+def test_attention_weights_below_the_normal_halves(weight):
+    """One key at each request's begin far above 2047 others of weight 2^-24 .. 2^-34 each, all of the result since its own
+    value is zero.  P is a half 2^11 at the row's offset: below 2^-25 of it a subnormal one, off by half a step of 2^-24,
+    2^-36 of the offset.  16 requests of 64 heads over the same pages: runs of more than 30 tiles a warp."""
+    B, H, D, N = 16, 64, 64, 2047
+    c = _attn_case(25, [(N, 1)], H, H, D, 16, torch.float16)
+    kp = torch.zeros(c["kp"].shape)
+    kp[int(c["ids"][0]), 3, :, 0] = 256.0
+    vp = torch.full_like(kp, 448.0)
+    vp[int(c["ids"][0]), 3] = 0.0
+    c.update(kp=kp.to(E4M3), vp=vp.to(E4M3), ke=torch.full_like(c["ke"], -4), ve=torch.full_like(c["ve"], 7), scale=1.0)
+    c["q"] = torch.zeros_like(c["q"])
+    c["q"][..., 0] = weight * math.log(2.0) / 16.0
+    one = {n: c[n][:, :, :1] for n in ("kp", "vp")} | {n: c[n][:, :1] for n in ("ke", "ve")}
+    ro, rl, to, tl = _attn_ref(dict(c, q=c["q"][:, :1], **one))
+    to = to + N * 2.0 ** -36 * 57344.0
+    assert (to < ro.abs() / 2).all()
+    many = dict(c, q=c["q"].repeat(B, 1, 1), ids=c["ids"].repeat(B), indptr=i32(128 * r for r in range(B + 1)),
+                lpl=c["lpl"].repeat(B), fpo=c["fpo"].repeat(B), qo=i32(range(B + 1)), pos=c["pos"].repeat(B))
+    out, lse = (x.cpu().double() for x in _run_attn(many))
+    assert ((out - ro).abs() <= to).all(), (float((out - ro).abs().max()), float(to.max()))
+    assert ((lse - rl).abs() <= tl).all()
+
+
 @pytest.mark.parametrize("dtype", DT)
 def test_attention_ends_of_the_ranges(dtype):
     """Exponents from end to end, out of range ones, codes from the smallest to the largest, large and tiny rows of q."""
