@@ -568,10 +568,13 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // the row's largest element to [2^13, 2^14)
+      // the row's largest element to [2^13, 2^14); rows that f16 holds as they are are not made smaller, and what is
+      // given back to the scores stays finite, so that one of zero stays zero at every scale
       int e = 13;
       if (top > 0.f && top <= 3.4028234e38f) e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
-      const float up = power_of_two(13 - e), down = power_of_two(e - 13) * p.scale_log2;
+      if (e <= 15) e = min(e, 13);
+      const float up = power_of_two(13 - e);
+      const float down = fminf(fmaxf(power_of_two(e - 13) * p.scale_log2, -3.4028234e38f), 3.4028234e38f);
       qf[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
       qf[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
 #pragma unroll
@@ -750,7 +753,7 @@ __global__ void __launch_bounds__(32 * F8Cfg<D, NT>::kWarps, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {  // token 16 i + 8 (k >> 1) + g, column 2 t + (k & 1)
             const int q4 = 2 * i + (k >> 1);
-            float y = s[i][nt][k] * (ks[q4] * qf[nt][k & 1]);
+            float y = s[i][nt][k] * ks[q4] * qf[nt][k & 1];  // (2^ek first: both factors together could overflow)
             if (!clear) y = see[k & 1] >> (8 * q4 + g) & 1u ? y : -INFINITY;
             s[i][nt][k] = y;
             mt[nt][k & 1] = fmaxf(mt[nt][k & 1], y);

@@ -803,6 +803,19 @@ def test_attention_weights_below_the_normal_halves(weight):
     assert ((lse - rl).abs() <= tl).all()
 
 
+@pytest.mark.parametrize("dtype,size,scale", [(torch.float16, 1.0, 1e38), (torch.float16, 30000.0, 1e38),
+                                              (torch.float16, 65504.0, -2e38), (torch.bfloat16, 60000.0, 2.3e38),
+                                              (torch.bfloat16, 2.0 ** 100, 1e38)])
+@pytest.mark.parametrize("n", [1, 3, 60])
+def test_attention_scores_of_zero_at_the_largest_scales(dtype, size, scale, n):
+    """A scale that f32 and its logarithm's base hold, rows of q however large, keys of zero: every score is zero."""
+    c = _attn_case(26, [(100, n), (3, n)], 8, 2, 128, 16, dtype)
+    c["q"] = torch.full_like(c["q"], size)
+    c["q"][:, :, ::2] = -1.0
+    c["kp"], c["scale"] = torch.zeros(c["kp"].shape).to(E4M3), scale
+    _close(_run_attn(c), _attn_ref(dict(c, scale=1.0)))
+
+
 @pytest.mark.parametrize("dtype", DT)
 def test_attention_ends_of_the_ranges(dtype):
     """Exponents from end to end, out of range ones, codes from the smallest to the largest, large and tiny rows of q."""
