@@ -838,8 +838,13 @@ pa_status pa_v2_tree_attention_sinks(const void* q, const void* k_pool, const vo
  *    448 * 2^PA_V2_FP8_EXP_MAX to that, infinities and NaN to NaN.
  * The other entries of the page keep their codes: no token lies there.  A token
  * with a negative slot is padding, one with a slot past the pool is skipped and
- * recorded (PA_DEVICE_BAD_SLOT); either ends a run, so padding lies behind the
- * last token.  Slots must be distinct, q_out must not overlap an input.
+ * recorded (PA_DEVICE_BAD_SLOT).  Either ends a run, so padding lies behind a
+ * request's last token: where skipped tokens alone stand between two tokens of a
+ * page, k and v of the later one, and of the tokens of its page behind it, are
+ * not stored and the same bit is recorded (q_out is written).  Two tokens of a
+ * page with one of another page between them are the caller's error: the page's
+ * codes and exponents are undefined.  Slots must be distinct, q_out must not
+ * overlap an input.
  * Arguments, types and refusals as pa_v2_qk_rope_append, dtype that of q, k and
  * v; page_size up to 256, num_tokens * num_kv_heads below 2^31 (PA_EUNSUPPORTED above). */
 pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,

@@ -10,7 +10,8 @@
 //
 // The new tokens of one page are a run of neighbours in the call, so one warp sees all of
 // them for a head and side and decides the exponent alone: no atomics, no second
-// launch, the same result in every call.  Where the exponent of a begun page grows, that
+// launch, the same result in every call.  A run that skipped tokens split from an earlier one
+// of its page is refused.  Where the exponent of a begun page grows, that
 // warp also rescales the page's earlier codes.  A code is a 4-bit number times a power of
 // two, so that step is exact except for codes that turn subnormal.
 //
@@ -323,6 +324,20 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) pa_v2_qk_rope_append_fp8_
   for (; starts; starts &= starts - 1) {
     const int at = __ffs(starts), t = w0 + at - 1;
     const int32_t page = page_of(at);
+    // Skipped tokens before it, and before those one of the same page: that one's run has decided the page, beside it
+    // this one would race for its exponent and codes.  It is refused (the same for all of the CTA's threads).
+    if (slot_of[at - 1] < 0) {
+      int32_t last = -1;  // the page of the nearest token before that is not skipped
+      for (int i = t - 2; i >= 0 && last < 0; i -= 32) {
+        const int32_t s = i >= lane ? __ldg(p.slots + i - lane) : -1;
+        const uint32_t live = __ballot_sync(0xffffffffu, s >= 0 && s < p.num_rows);
+        if (live) last = (int32_t)fast_div((uint32_t)__shfl_sync(0xffffffffu, s, __ffs(live) - 1), p.ps_magic, p.ps_shift);
+      }
+      if (last == page) {
+        if (task0 == 0 && threadIdx.x == 0) report(p.status, PA_DEVICE_BAD_SLOT);
+        continue;
+      }
+    }
     // the run: how many tokens, and the least entry
     int len = 1, least = INT_MAX;
     for (int i = 0;; i += 32) {

@@ -945,7 +945,8 @@ def pa_v2_qk_rope_append_fp8(q, k, v, positions, slots, inv_freq, k_pool, v_pool
 
     As pa_v2_qk_rope_append, with k_pool and v_pool [P, page_size, Hkv, D] float8_e4m3fn and k_exp and v_exp [P, Hkv]
     int8, the exponents of each page and KV head (an element is code * 2^exponent); the tokens of one page must be
-    neighbours in the call.  Returns q_out [T, Hq, D] in q_dtype (q's dtype by default, or float32)."""
+    neighbours in the call (those that skipped tokens cut off from the page's first are not stored and recorded in
+    status).  Returns q_out [T, Hq, D] in q_dtype (q's dtype by default, or float32)."""
     dev = _device_index(q, "q")
     pools, (pages, page_size, pool_heads, pool_dim) = _pools_fp8(k_pool, v_pool, k_exp, v_exp, dev)
     dt, i32, f32, ptr = q.dtype, torch.int32, torch.float32, _step_ptr

@@ -234,6 +234,73 @@ def test_append_padding_and_bad_slots_are_skipped():
     _check_append(c, out, cache)
 
 
+def _refused(slots, rows, page_size):
+    """Which tokens skipped ones cut off from an earlier token of their page."""
+    out, before, last = [], False, -1          # of the nearest earlier token that is not skipped: refused, its number
+    for t, s in enumerate(slots.tolist()):
+        out.append(False)
+        if 0 <= s < rows:
+            same = last >= 0 and int(slots[last]) // page_size == s // page_size
+            out[-1] = before = same and (before or t > last + 1)
+            last = t
+    return torch.tensor(out)
+
+
+def _check_append_refusing(c, **kw):
+    """A call whose skipped tokens split pages: what is cut off is not stored and recorded, all else is as without it."""
+    ps = c["kp"].shape[1]
+    rows = c["kp"].shape[0] * ps
+    cut = _refused(c["slots"], rows, ps)
+    st = status_word()
+    out, cache = _run_append(c, status=st, **kw)
+    assert int(st) == (pa.DEVICE_BAD_SLOT if cut.any() or (c["slots"] >= rows).any() else 0)
+    _check_append(dict(c, slots=torch.where(cut, -1, c["slots"])), out, cache)
+    want, mag = R.rope_ref(c["q"][cut], c["qw"], c["eps"], c["pos"][cut], c["freq"], False)
+    got = out.cpu().double()[cut]
+    fi = torch.finfo(out.dtype)
+    assert ((got - want).abs() <= R.rope_tolerance(want, mag, out.dtype) + fi.eps / 2 * fi.smallest_normal).all()
+    return cut
+
+
+@pytest.mark.parametrize("gap", [1, 2, 31, 32, 33, 70, 500])
+@pytest.mark.parametrize("skipped", [-1, -2 ** 31, 2 ** 31 - 1])
+def test_append_skipped_tokens_between_tokens_of_a_page(gap, skipped):
+    """Two tokens of a page, skipped ones, two more: the page's first run alone is stored, whatever lies between."""
+    c = _append_case(9, [(3, 2 + gap + 2), (40, 3)], 1024 // 4, 4, 2, 64, 64, torch.float16, True)
+    c["slots"][2:2 + gap] = skipped
+    if 2 + gap + 2 > 253:
+        c["slots"][2 + gap:4 + gap] = c["slots"][:2] + 10       # (of the same page, which ends before them)
+    cut = _check_append_refusing(c)
+    assert cut.nonzero().flatten().tolist() == [2 + gap, 3 + gap]
+
+
+@pytest.mark.parametrize("page_size", [1, 2, 5, 16, 64, 256])
+@pytest.mark.parametrize("T,share", [(40, 0.2), (700, 0.1), (700, 0.9), (1200, 0.3)])
+def test_append_skipped_tokens_anywhere(page_size, T, share):
+    """Long calls, stretches of one token and of more, random tokens of every page skipped, as padding or past the pool."""
+    g = torch.Generator().manual_seed(T + page_size)
+    c = _append_case(T, [(5, T // 2), (page_size // 2, T - T // 2)], page_size, 4, 2, 64, 16, torch.bfloat16, False)
+    rows = c["kp"].shape[0] * page_size
+    drop, past = torch.rand(T, generator=g) < share, torch.rand(T, generator=g) < 0.3
+    c["slots"] = torch.where(drop, torch.where(past, rows + 3, -1), c["slots"]).to(I32)
+    cut = _check_append_refusing(c)
+    assert cut.any() == (page_size > 2)
+
+
+@pytest.mark.parametrize("width", [1, 7, 33, 100])
+def test_append_requests_padded_to_one_width(width):
+    """A row of `width` tokens a request, the last ones padding: nothing is cut off."""
+    lens = [1, width, max(1, width // 2), 0, width, 1]
+    c = _append_case(width, [(7 * r, n) for r, n in enumerate(lens)], 16, 4, 2, 64, 64, torch.float16, True)
+    parts = torch.split(torch.arange(sum(lens)), lens)
+    at = torch.cat([torch.cat((p, torch.zeros(width - len(p), dtype=torch.long))) for p in parts])
+    live = torch.cat([torch.arange(width) < n for n in lens])
+    for n in ("q", "k", "v", "pos", "slots"):
+        c[n] = c[n][at]
+    c["slots"] = torch.where(live, c["slots"], -1).to(I32)
+    assert not _check_append_refusing(c).any()
+
+
 def test_append_tokens_of_a_page_in_any_order():
     c = _append_case(4, [(2, 30)], 16, 4, 2, 64, 64, torch.bfloat16, True)
     perm = torch.tensor([5, 3, 13, 0, 1, 2, 4, 6, 7, 8, 9, 10, 11, 12] + [29 - i for i in range(16)])
