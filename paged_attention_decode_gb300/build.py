@@ -20,7 +20,7 @@ LIB_NAME = "libpa_v2.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 BUILD_DIR = os.path.join(ROOT, "_build")
 
-SOURCES = ["pa_plan.cpp", "pa_cascade.cpp", "pa_partial.cu", "pa_partial_simt.cu", "pa_partial_tc.cu",
+SOURCES = ["pa_plan.cpp", "pa_cascade.cpp", "pa_prepare.cpp", "pa_partial.cu", "pa_partial_simt.cu", "pa_partial_tc.cu",
            "pa_partial_tc_cascade.cu", "pa_merge.cu", "pa_noalloc.cu", "pa_select.cu", "pa_host_step.cpp", "pa_partial_extra.cu",
            "pa_partial_extra_tc.cu", "pa_partial_extra_tc05.cu", "pa_tables.cu", "pa_qk_rope.cu", "pa_tree.cu",
            "pa_tree_window.cu", "pa_tree_sinks.cu", "pa_fp8_append.cu", "pa_fp8_attn.cu"]

@@ -25,26 +25,6 @@
 
 namespace pa {
 
-bool prepare_kernel(const void* fn, size_t smem) {
-  constexpr int kMaxDevices = 64;
-  constexpr int kMaxKernels = 128;
-  static std::mutex mu;
-  static const void* done[kMaxDevices][kMaxKernels] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
-  std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < kMaxKernels; ++i) {
-    if (done[dev][i] == fn) return true;
-    if (done[dev][i] == nullptr) {
-      if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return false;
-      done[dev][i] = fn;
-      return true;
-    }
-  }
-  return false;
-}
-
 namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
