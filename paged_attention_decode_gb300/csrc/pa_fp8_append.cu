@@ -321,23 +321,23 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) pa_v2_qk_rope_append_fp8_
   // (a lane a token of the stretch: kApStretch <= 32)
   const int32_t lane_page = lane < w1 - w0 ? page_of(lane + 1) : -1;
   uint32_t starts = __ballot_sync(0xffffffffu, lane_page >= 0 && page_of(lane) != lane_page);
+  // Skipped tokens before a start, and before those a token of the same page: that one's run has decided the page, and
+  // beside it this one would race for its exponent and codes.  It is refused.
+  for (uint32_t gaps = starts & __ballot_sync(0xffffffffu, slot_of[lane & (kApStretch - 1)] < 0); gaps; gaps &= gaps - 1) {
+    const int at = __ffs(gaps);
+    int32_t last = -1;  // the page of the nearest token before that is not skipped
+    for (int i = w0 + at - 3; i >= 0 && last < 0; i -= 32) {
+      const int32_t s = i >= lane ? __ldg(p.slots + i - lane) : -1;
+      const uint32_t live = __ballot_sync(0xffffffffu, s >= 0 && s < p.num_rows);
+      if (live) last = (int32_t)fast_div((uint32_t)__shfl_sync(0xffffffffu, s, __ffs(live) - 1), p.ps_magic, p.ps_shift);
+    }
+    if (last != page_of(at)) continue;
+    starts &= ~(1u << (at - 1));
+    if (task0 == 0 && threadIdx.x == 0) report(p.status, PA_DEVICE_BAD_SLOT);
+  }
   for (; starts; starts &= starts - 1) {
     const int at = __ffs(starts), t = w0 + at - 1;
     const int32_t page = page_of(at);
-    // Skipped tokens before it, and before those one of the same page: that one's run has decided the page, beside it
-    // this one would race for its exponent and codes.  It is refused (the same for all of the CTA's threads).
-    if (slot_of[at - 1] < 0) {
-      int32_t last = -1;  // the page of the nearest token before that is not skipped
-      for (int i = t - 2; i >= 0 && last < 0; i -= 32) {
-        const int32_t s = i >= lane ? __ldg(p.slots + i - lane) : -1;
-        const uint32_t live = __ballot_sync(0xffffffffu, s >= 0 && s < p.num_rows);
-        if (live) last = (int32_t)fast_div((uint32_t)__shfl_sync(0xffffffffu, s, __ffs(live) - 1), p.ps_magic, p.ps_shift);
-      }
-      if (last == page) {
-        if (task0 == 0 && threadIdx.x == 0) report(p.status, PA_DEVICE_BAD_SLOT);
-        continue;
-      }
-    }
     // the run: how many tokens, and the least entry
     int len = 1, least = INT_MAX;
     for (int i = 0;; i += 32) {
