@@ -671,6 +671,46 @@ def test_attention_many_rows(reqs, hq, hkv, window, sinks, page_size, D, tree, d
     _check_attn(_attn_case(61 + window, reqs, hq, hkv, D, page_size, dtype, window, sinks, trees=trees, give_back=True))
 
 
+@pytest.mark.parametrize("page_size,D", [(16, 128), (5, 64), (64, 64), (256, 128)])
+@pytest.mark.parametrize("window", [0, 33])
+def test_attention_many_rows_from_a_first_offset(page_size, D, window):
+    """Lists that begin inside a page, as a trimmed table's do, whole or with a window that hides their first rows."""
+    reqs, fpos = [(300, 60), (2, 70), (700, 50)], [page_size - 1, page_size // 2, 1 % page_size]
+    c = _attn_case(62, reqs, 8, 2, D, page_size, torch.bfloat16, window, fpos=fpos, give_back=True)
+    _check_attn(c)
+
+
+@pytest.mark.parametrize("window", [40, 300])
+@pytest.mark.parametrize("tree", [False, True])
+def test_sliding_tables_feed_the_attention_of_many_rows(window, tree):
+    """pa_v2_build_tables_sliding's tables of a prompt's chunks and of wide trees, beside a request without tokens."""
+    rng = random.Random(window)
+    cached, new, ps, hq, hkv, D, width = [700, 33, 0, 90], [99, 140, 112, 0], 16, 8, 2, 64, 50
+    g = torch.Generator().manual_seed(window + tree)
+    P, T = 4 * width + 3, sum(new)
+    table = torch.randperm(P, generator=g)[:4 * width].reshape(4, width).to(I32)
+    parents = [R.random_tree(rng, n) for n in new] if tree else None
+    pools = [(torch.randn(P, ps, hkv, D, generator=g) * 64).clamp(-448, 448).to(E4M3) for _ in range(2)]
+    exps = [torch.randint(-8, -3, (P, hkv), generator=g).to(torch.int8) for _ in range(2)]
+    q = torch.randn(T, hq, D, generator=g).half()
+    t = pa.StepTables.empty(4, 4 * width, T, 5 if tree else 0)
+    st = status_word()
+    pa.pa_v2_build_tables(i32(cached).cuda(), i32(new).cuda(), table.cuda(), ps, t, sliding_window=window, status=st,
+                          parents=i32(p for ps_ in parents for p in ps_).cuda() if tree else None)
+    got = pa.pa_v2_attention_fp8(q.cuda(), *[x.cuda() for x in pools + exps], t.indices, t.indptr, t.last_page_len,
+                                 t.first_page_offset, t.qo_indptr, D ** -0.5, tree_mask=t.tree_mask,
+                                 positions=t.positions, sliding_window=window, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0 and int(t.first_page_offset[0]) > 0
+    seen = []
+    for r in range(4):
+        for i in range(new[r]):
+            line = R.ancestors(parents[r], i) if tree else None
+            seen.append(F.seen_rows(table[r], ps, 0, cached[r] + new[r], new[r], i, window, 0,
+                                    set(line[:window]) if tree else None, len(line) - 1 if tree else i))
+    _close(got, F.attention_ref(q, F.values(pools[0], exps[0]), F.values(pools[1], exps[1]), seen, D ** -0.5))
+
+
 @pytest.mark.parametrize("page_size", [16, 5])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3)])
 def test_attention_many_rows_nothing_hidden_and_nan_where_it_is_seen(page_size, window, sinks):
