@@ -845,8 +845,13 @@ pa_status pa_v2_tree_attention_sinks(const void* q, const void* k_pool, const vo
  * page with one of another page between them are the caller's error: the page's
  * codes and exponents are undefined.  Slots must be distinct, q_out must not
  * overlap an input.
+ * A page's exponent does not fall when a token is overwritten: a draft that is
+ * rejected later has raised it for good where it was the largest, and the codes of
+ * the tokens before it keep the bits that they lost, until entry 0 is written again.
  * Arguments, types and refusals as pa_v2_qk_rope_append, dtype that of q, k and
- * v; page_size up to 256, num_tokens * num_kv_heads below 2^31 (PA_EUNSUPPORTED above). */
+ * v; page_size up to 256, num_tokens * num_kv_heads below 2^31 (PA_EUNSUPPORTED above).
+ * pa_v2_attention_fp8 reads q in f16 or bf16: an f32 q_out (the only one with f32
+ * inputs) is for a reader of the caller's, or is rounded to one of them in between. */
 pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                                    int64_t v_stride, int32_t dtype, int32_t num_tokens, int32_t num_qo_heads,
                                    int32_t num_kv_heads, int32_t head_dim, const int32_t* positions,
@@ -877,7 +882,13 @@ pa_status pa_v2_qk_rope_append_fp8(const void* q, int64_t q_stride, const void* 
  * chunk) write the pages that some token sees out in q_dtype first, exactly, and run pa_v2_tree_attention's kernels
  * over them, where the pages fit: 2^28 elements of K, 2^20 listed pages.  The workspace for such sizes is larger by
  * 1.08 GB and the tree attention's; calls with a workspace for other sizes, of at least its smaller part, and chains
- * in a window without positions take the other way.  Lists that overlap (an indptr that falls at a request without
+ * in a window without positions take the other way, whose results are as good but which takes up to four times as long.
+ * The size follows the average and not the most: one for more requests can be smaller.  A program whose calls differ
+ * takes the largest of their sizes, which serves them all.  The average also decides for a batch whose requests differ: a
+ * prompt's chunk beside many single tokens takes two to four times as long as the two in calls of their own (512 tokens
+ * over 8K beside 63 single ones over 1K-32K 697 us, apart 127 and 189; 2048 tokens 2230, apart 393 and 189), so they
+ * belong in calls of their own.
+ * Lists that overlap (an indptr that falls at a request without
  * tokens) and are together longer than that room, num_indices being shorter, are refused: PA_DEVICE_BAD_TREE, zeros
  * and -inf for all.
  * PA_EINVAL: sinks without a window.  PA_EUNSUPPORTED: as pa_v2_tree_attention, and batch

@@ -26,7 +26,10 @@
 //
 // 16384 tokens of 48 heads take 78 us of 54 (4.7 TB/s of 6.8): alone q takes 52 (5.2 TB/s)
 // and the runs 45, which wait for their data, a run's steps one after the other (8 us a
-// CTA, three CTAs an SM).  2048 tokens 19 us of 7: few rows for a run's steps to hide behind.  Kept in shared
+// CTA, three CTAs an SM).  2048 tokens 19 us of 7, 1024 of as many requests 20 of 3.4: few rows for a run's steps
+// to hide behind, or many runs one after the other.  Pages longer than a stretch leave CTAs without a run, and of 256 tokens
+// (128 KB of angles) one CTA fits an SM instead of three: 16384 tokens 97, 134 and 199 us with pages of 64, 128 and
+// 256, 2048 tokens 33, 35 and 29, 64 requests of one token 5.9, 5.9 and 6.5 (5.7 with pages of 16).  Kept in shared
 // memory between maximum and codes K costs q more than it saves (93 us); held in registers it
 // leaves two CTAs an SM (106); angles by every warp for itself spill (146); 64 registers for
 // four CTAs spill (118).

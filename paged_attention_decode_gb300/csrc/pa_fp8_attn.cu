@@ -33,12 +33,12 @@
 // one byte permutation apart from the two A registers it becomes.  P^T goes from the
 // accumulator's layout to the B operand's by movmatrix.
 //
-// What bounds it (GB300, 32 query heads on 8 KV heads, D = 128, page size 16, replayed):
-// 64 ragged requests of 1K-32K, one token each, 214-229 us, 5.9-6.2 TB/s of 6.8 measured:
-// HBM; 33 % of the issue slots.  32 chains of 5 tokens in a window of 4096 with 4 sinks
-// 77 us of 29: 20 of 24 columns of products, two warps a scheduler that wait for one
-// another's shuffles and conversions half of the time.  One token over 32K 26 us (10 of
-// HBM), over 1K 13 us: starts (8 us: cold code, tables, pages, tiles, one after the other),
+// What bounds it (GB300, 32 query heads on 8 KV heads, D = 128, page size 16, replayed over
+// three sets of inputs in turn): 64 ragged requests of 1K-32K, one token each, 214-229 us,
+// 5.9-6.2 TB/s of 6.8 measured: HBM; 52 % of the issue slots.  32 chains of 5 tokens in a
+// window of 4096 with 4 sinks 78 us of 29: 20 of 24 columns of products, two warps a scheduler
+// that wait for one another's shuffles and conversions, 35 % of the issue slots.  One token over
+// 32K 25 us (10 of HBM), over 1K 13 us: starts (8 us: cold code, tables, pages, tiles, one after the other),
 // joining 2-3, the merge kernel 4.  More warps help while registers allow them (12 at 168
 // for one block of 8 rows: 26 -> 23 us over 32K; the wider blocks need 255); q in registers
 // up to 16 rows, in shared memory for 24.  Measured and not kept: blocks of 32 rows (spills); the
@@ -1227,9 +1227,15 @@ __global__ void __launch_bounds__(32 * kMergeWarps, kMergeCtas) pa_v2_fp8_merge_
 // A prompt's chunk meets each key with hundreds of query rows, in blocks of kRows: the tensor cores bound it, and the warp's
 // ones at that.  So the pages that some token sees are written out once in q's 16-bit type (exactly: an element is a
 // binary16 number of 4 significant bits, and a bfloat16 one) and the tree attention runs over them, tcgen05 products and
-// all: 4 x 256 tokens over 8K take 197 us (expansion 38, attention 153) where blocks of few rows took 815.  Around the
-// border, 100 rows over 1K, 8K and 32K tokens: 24, 40 and 87 us (blocks 19, 39 and 114), 32 requests over 1K 106 (132);
-// 68 rows 24, 39 and 83 (19, 33 and 79) and 101 (90).
+// all: 4 x 256 tokens over 8K take 197 us (expansion 36, attention 153) where blocks of few rows took 815.  The rule counts
+// rows, averaged over the requests, and not keys, so that it loses on one side of the border and gains on the other: 100 rows
+// of one request over 1K, 8K and 32K tokens 25, 44 and 87 us (96 rows, in blocks: 19, 38 and 95), 100 rows of each of 32
+// requests over 1K 106 (in blocks 132); 68 rows this way 24, 39 and 83 (in blocks 19, 33 and 79), of 32 requests 101 (90).
+//
+// The tree attention rounds P to the pages' type, which is q's: with bf16 by 2^-8 of each weight, where the blocks of few
+// rows round it by 2^-11.  Against 64 bits the outputs' relative error is then 0.0021 where their own rounding alone gives
+// 0.0017.  Pages in f16 for a bf16 q would keep the 2^-11, but q's rows would each need a power of two that the tree
+// attention's scores do not have.
 struct F8Wide {
   int32_t* qo_wide;     // qo_indptr for the tree attention, all zero when the pages do not fit
   int32_t* qo_narrow;   // and for the blocks of few rows, all zero when they do

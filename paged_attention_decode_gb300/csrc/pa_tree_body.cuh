@@ -110,7 +110,8 @@ struct TreeCfg {
 
 // P is rounded to 16 bits relative to 2^kShift at the row's offset, and the offset follows the running maximum
 // with a lag of up to kLazy (log2 units).  bf16 has f32's range and takes a wide lag.  f16 holds nothing below
-// 2^-24: the shift keeps weights down to 2^-35 of the largest (a long context can hold thousands of those), and
+// 2^-24: the shift keeps weights down to 2^-35 of the largest (a long context can hold thousands of those), those
+// below 2^-25 as subnormal halves, off by up to 2^-36 of the largest, and
 // 2^(kShift + kLazy) stays below its largest value.  One 16-bit term: a second one for what the rounding drops would
 // be a second product of P and V, half as much tensor work again; the outputs' relative error is 1.1 to 1.4 times
 // that of f32 weights (bf16 0.0023 against 0.0017, f16 0.00024 to 0.00028 against 0.00021).

@@ -946,7 +946,8 @@ def pa_v2_qk_rope_append_fp8(q, k, v, positions, slots, inv_freq, k_pool, v_pool
     As pa_v2_qk_rope_append, with k_pool and v_pool [P, page_size, Hkv, D] float8_e4m3fn and k_exp and v_exp [P, Hkv]
     int8, the exponents of each page and KV head (an element is code * 2^exponent); the tokens of one page must be
     neighbours in the call (those that skipped tokens cut off from the page's first are not stored and recorded in
-    status).  Returns q_out [T, Hq, D] in q_dtype (q's dtype by default, or float32)."""
+    status).  Returns q_out [T, Hq, D] in q_dtype (q's dtype by default, or float32, which pa_v2_attention_fp8 does not
+    read: round it to float16 or bfloat16 first)."""
     dev = _device_index(q, "q")
     pools, (pages, page_size, pool_heads, pool_dim) = _pools_fp8(k_pool, v_pool, k_exp, v_exp, dev)
     dt, i32, f32, ptr = q.dtype, torch.int32, torch.float32, _step_ptr
@@ -989,7 +990,8 @@ def pa_v2_qk_rope_append_fp8(q, k, v, positions, slots, inv_freq, k_pool, v_pool
 
 def pa_v2_attention_fp8_workspace(num_tokens: int, batch: int, num_qo_heads: int, num_kv_heads: int, head_dim: int,
                                   device: int | None = None) -> int:
-    """Bytes of device scratch pa_v2_attention_fp8 needs for these sizes."""
+    """Bytes of device scratch that a pa_v2_attention_fp8 call of these sizes makes use of; more is fine, and less, down to
+    the size for single tokens, is slower for many query rows per request."""
     dev = torch.cuda.current_device() if device is None else device
     out = ctypes.c_int64()
     rc = lib().pa_v2_attention_fp8_workspace(dev, num_tokens, batch, num_qo_heads, num_kv_heads, head_dim,
@@ -1001,7 +1003,12 @@ def pa_v2_attention_fp8_workspace(num_tokens: int, batch: int, num_qo_heads: int
 
 def attention_fp8_workspace(num_tokens: int, batch: int, num_qo_heads: int, num_kv_heads: int, head_dim: int,
                             device="cuda") -> torch.Tensor:
-    """A workspace tensor for pa_v2_attention_fp8 calls of up to these sizes."""
+    """A workspace tensor for pa_v2_attention_fp8 calls of these sizes.
+
+    It serves calls of fewer tokens or requests as well.  But where num_tokens / batch (rounded up) times the query heads
+    per KV head passes 96, a call wants 1.08 GB more for the written-out pages; without that room, as in a workspace made
+    for more requests of fewer tokens each, it gives the same result in up to four times the time.  A program whose calls
+    differ keeps a tensor of the largest of their pa_v2_attention_fp8_workspace."""
     dev = torch.device(device)
     index = dev.index if dev.index is not None else torch.cuda.current_device()
     n = pa_v2_attention_fp8_workspace(num_tokens, batch, num_qo_heads, num_kv_heads, head_dim, index)
